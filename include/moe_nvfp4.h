@@ -378,6 +378,123 @@ moe_status hadamard_rotate_bf16(const uint16_t* src, int64_t rows, int64_t cols,
                                 const float* signs, int64_t block, uint16_t* dst, int64_t ld_dst,
                                 void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* MXFP4: the 4-bit floating-point format that gfx950's matrix cores multiply
+ * directly (OCP Microscaling Formats v1.0: E2M1 elements, one E8M0 scale per
+ * 32 consecutive elements of a row, no global scale).
+ *
+ *  Block      byte b stands for the scale 2^(b - 127), b = 255 for NaN;
+ *             value = e2m1(code) * 2^(b - 127).  Quantization of a block with
+ *             largest magnitude amax: b = floor(log2(amax)) - 2 + 127, clamped
+ *             to [0, 254] (0 for a zero block); code = E2M1 RNE-even of
+ *             x * 2^(127 - b), saturating at 6, sign bit = sign bit of x.  A
+ *             block that holds a NaN or an infinity gets b = 255 and zero
+ *             codes: all of it stands for NaN, and every product that reads it
+ *             is NaN.
+ *  Rows       Activations [rows, cols], cols % 32 == 0, are stored with rows
+ *             padded to Cp = round_up(cols, 256) columns: codes [rows, Cp/2]
+ *             (element 2j in bits 3:0 of byte j, element 2j+1 in bits 7:4) and
+ *             scales [rows, Cp/32]; the padding is zero codes under scale 0.
+ *  Weights    [N, K], K % 32 == 0, any N >= 1, are packed once into the
+ *             operand fragments of the 32x32x64 scaled MFMA: with G =
+ *             ceil(N / 32) and KK = ceil(K / 256), codes [G, KK, 4, 64, 16] bytes
+ *             and scales [G, KK, 64, 4] bytes.  Lane 32 f + 8 q + 4 h + j of
+ *             (g, c) belongs to row 32 g + 16 h + 4 q + j; its 16-byte piece s
+ *             (and scale byte s) is block 8 c + 4 f + s of that row.  Rows past
+ *             N and blocks past K are zero codes under scale 0.
+ * dtype arguments: 0 = BF16, 1 = FP32.  Results are deterministic. */
+
+/* x [rows, ld] (ld >= cols) -> codes, scales in the padded row form above.
+ * x 16-byte aligned with ld * sizeof(element) % 16 == 0; codes 16-byte
+ * aligned; rows * Cp < 2^35. */
+moe_status mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                          uint8_t* codes, uint8_t* scales, void* stream);
+/* The values that the codes stand for, out [rows, ld_out] (exact in both
+ * types).  out 16-byte aligned with ld_out * sizeof(element) % 16 == 0. */
+moe_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                            int32_t out_dtype, void* out, int64_t ld_out, void* stream);
+
+/* Offline quantization of `batch` BF16 matrices [batch, N, K] (contiguous) to
+ * packed weights, one matrix after another.  max_scale [batch] INT32 (or NULL)
+ * receives each matrix's largest scale byte.  w 16-byte, codes 16-byte,
+ * max_scale 4-byte aligned. */
+moe_status mxfp4_quantize_weights(const uint16_t* w_bf16, int64_t batch, int64_t N, int64_t K,
+                                  uint8_t* codes, uint8_t* scales, int32_t* max_scale, void* stream);
+/* Canonical MXFP4 weights (codes [batch, N, K/2] and scales [batch, N, K/32],
+ * row-major, unpadded) to packed weights, and the exact inverse.  Code arrays
+ * 16-byte aligned; the arrays must not overlap. */
+moe_status mxfp4_pack_weights(const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t N, int64_t K,
+                              uint8_t* packed_codes, uint8_t* packed_scales, int32_t* max_scale, void* stream);
+moe_status mxfp4_unpack_weights(const uint8_t* packed_codes, const uint8_t* packed_scales, int64_t batch,
+                                int64_t N, int64_t K, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* y[t, n] = sum_k x[t, k] * w[n, k] over the values that the codes stand for:
+ * products exact, FP32 accumulation.  x_codes/x_scales [T, K] in the padded row
+ * form, w packed [N, K]; y [T, ldy] (ldy >= N) in out_dtype (BF16
+ * round-to-nearest-even).  Code arrays 16-byte, scale arrays 4-byte, y 4-byte
+ * (BF16: 2-byte) aligned.  T * Kp / 2 < 2^32 bytes (Kp = round_up(K, 256)) and
+ * T <= 2097120.  workspace: mxfp4_linear_workspace_bytes(T, K, N) bytes
+ * (0 possible: workspace may then be NULL), 256-byte aligned. */
+size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K, int64_t N);
+moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t K,
+                        const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int32_t out_dtype, void* y,
+                        int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The routed experts' FFN in MXFP4 W4A4; the counterpart of
+ * moe_nvfp4_grouped_ffn between moe_route and moe_combine:
+ *
+ *   for each expert e and each pair p in sorted_pair_ids[offsets[e]..):
+ *     t = p / k;  g = x[t] . W_gate[e]^T, u = x[t] . W_up[e]^T
+ *     h = silu(g) * u in FP32, quantized to MXFP4
+ *     f = h . W_down[e]^T;  pair row p = topk_w[p] * f
+ *
+ * x_codes/x_scales [T, H] in the padded row form (mxfp4_quantize); w13 packed
+ * [E][2I, H] (gate rows, then up rows), w2 packed [E][H, I], w2_max_scale [E]
+ * as mxfp4_quantize_weights writes it.  pair_out [T*k, H] FP16 and pair_scale
+ * [T*k] are pair rows in the form of the header comment (moe_combine,
+ * moe_combine_block read them), with E = floor(log2 |w_p|) + 1 +
+ * ceil(log2(36 I)) + bh + bw - 269 clamped to [-126, 113], bh the largest scale
+ * byte of the pair's h and bw = w2_max_scale[e]: |w_p f| < 2^(E + 15).
+ * H % 32 == 0, I % 32 == 0, 1 <= k <= E <= 256, T * k < 2^31; x codes
+ * (T*Hp/2 bytes) and h codes (T*k*Ip/2 bytes) under 4 GiB.  Code arrays and
+ * pair_out 16-byte, scale arrays, pair_scale and w2_max_scale 4-byte aligned;
+ * workspace mxfp4_ffn_workspace_bytes(...) bytes, 256-byte aligned.  Pairs not
+ * listed in sorted_pair_ids are not written. */
+size_t mxfp4_ffn_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
+moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t H,
+                             const uint8_t* w13_codes, const uint8_t* w13_scales, const uint8_t* w2_codes,
+                             const uint8_t* w2_scales, const int32_t* w2_max_scale, int64_t E, int64_t I, int64_t k,
+                             const int32_t* expert_offsets, const int32_t* sorted_pair_ids, const float* topk_w,
+                             uint16_t* pair_out, float* pair_scale, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* RMS norms around a block, fused with what stands next to them.  All sums in
+ * FP32; one rounding to BF16 per result.
+ *
+ *  moe_norm_in:   n[t] = bf16(x[t] / rms(x[t]) * w),  rms(v) = sqrt(mean(v^2) + eps)
+ *  moe_norm_out:  z[t] = y[t] / rms(y[t]) * w_post    (w_post NULL: z = y)
+ *                 r_out[t] = bf16(r[t] + residual_scale * gate * z[t])
+ *                 n[t] = bf16(r_out[t] / rms(r_out[t]) * w_next)   (w_next NULL: none)
+ *
+ * n is computed from the BF16 r_out that is stored.  If codes is not NULL, n is
+ * also written in MXFP4 (the padded row form; bit-identical to mxfp4_quantize of
+ * n) and n itself may be NULL; this needs H % 32 == 0.  x, r, r_out, n, weights
+ * and gate are BF16, y is BF16 or FP32 (y_dtype).  gate (NULL: 1) has element
+ * (t, c) at gate[t * gate_row_stride + c * gate_col_stride], gate_col_stride 0
+ * (one value a token) or 1.  Any H from 1 to 16384 and any row strides >= H;
+ * 16-byte accesses are used when H % 8 == 0 and every pointer and row stride is a
+ * multiple of 16 bytes.  Pointers aligned to their element, codes to 4 bytes.
+ * r_out may be r, and n may be x (in place, same strides); other outputs must
+ * not overlap inputs. */
+moe_status moe_norm_in(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, const uint16_t* w, float eps,
+                       uint16_t* n, int64_t ldn, uint8_t* codes, uint8_t* scales, void* stream);
+moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, int64_t ldy, const uint16_t* r,
+                        int64_t ldr, const uint16_t* w_post, const uint16_t* gate, int64_t gate_row_stride,
+                        int64_t gate_col_stride, float residual_scale, const uint16_t* w_next, float eps,
+                        uint16_t* r_out, int64_t ldro, uint16_t* n, int64_t ldn, uint8_t* codes, uint8_t* scales,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -61,6 +61,19 @@ SIGNATURES = {
     "hadamard_rotate_bf16": (_i32, [_p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p]),
     "moe_nvfp4_prepack_weights": (_i32, [_p, _p, _i64, _i64, _i64, _i32, _p, _p, _p]),
     "moe_nvfp4_unpack_weights": (_i32, [_p, _p, _i64, _i64, _i64, _i32, _p, _p, _p]),
+    "mxfp4_quantize": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _p]),
+    "mxfp4_dequantize": (_i32, [_p, _p, _i64, _i64, _i32, _p, _i64, _p]),
+    "mxfp4_quantize_weights": (_i32, [_p, _i64, _i64, _i64, _p, _p, _p, _p]),
+    "mxfp4_pack_weights": (_i32, [_p, _p, _i64, _i64, _i64, _p, _p, _p, _p]),
+    "mxfp4_unpack_weights": (_i32, [_p, _p, _i64, _i64, _i64, _p, _p, _p]),
+    "mxfp4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "mxfp4_linear": (_i32, [_p, _p, _i64, _i64, _p, _p, _i64, _i32, _p, _i64, _p, _sz, _p]),
+    "mxfp4_ffn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "mxfp4_grouped_ffn": (_i32, [_p, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p,
+                                 _sz, _p]),
+    "moe_norm_in": (_i32, [_p, _i64, _i64, _i64, _p, _f32, _p, _i64, _p, _p, _p]),
+    "moe_norm_out": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _f32, _p, _f32, _p, _i64, _p,
+                            _i64, _p, _p, _p]),
 }
 
 

@@ -12,12 +12,14 @@
 #include <mutex>
 #include <string>
 
-#include "../../include/moe_nvfp4.h"
+#include "api_check.h"
 #include "launch.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace moe {
 
 moe_status fail(moe_status st, const char* fmt, ...) {
   char buf[512];
@@ -29,11 +31,6 @@ moe_status fail(moe_status st, const char* fmt, ...) {
   return st;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-// The current device must be gfx950; checked once per device id.
 moe_status check_device() {
   static std::mutex mu;
   static int ok_state[64] = {0};  // 0 unknown, 1 ok, -1 bad
@@ -59,6 +56,16 @@ moe_status launched(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(MOE_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
   return MOE_OK;
 }
+
+}  // namespace moe
+
+namespace {
+
+using moe::aligned;
+using moe::check_device;
+using moe::fail;
+using moe::launched;
+using moe::round_up;
 
 // ---- FFN workspace layout
 struct FfnWs {

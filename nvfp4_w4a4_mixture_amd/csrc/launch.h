@@ -104,4 +104,68 @@ int64_t hadamard_max_cols();
 hipError_t launch_hadamard_rotate(const uint16_t* src, int64_t rows, int64_t cols, int64_t ld_src, const float* signs,
                                   int64_t b, uint16_t* dst, int64_t ld_dst, hipStream_t st);
 
+// ---- MXFP4 (blocks of 32 E2M1 elements, E8M0 scales); rows are padded to whole column groups
+constexpr int64_t mx_padded(int64_t cols) { return (cols + 255) / 256 * 256; }
+
+// Arguments of an MXFP4 product.
+struct MxArgs {
+  const uint8_t* a_codes;   // activations [rows, KK * 128]
+  const uint8_t* a_scales;  // [rows, KK * 8]
+  const uint8_t* w_codes;   // packed weights (experts one after another)
+  const uint8_t* w_scales;
+  int64_t T;   // tokens
+  int64_t KK;  // column groups of 256 in the reduction
+  int64_t N;   // weight rows (per expert)
+  int64_t G;   // groups of 32 weight rows (per expert)
+  int k;
+  const int32_t* offsets;
+  const int32_t* sorted;
+  const float* topk_w;
+  const int32_t* w_max;  // down: largest weight scale byte per expert
+  int lg36I;             // down: ceil(log2(36 I))
+  uint8_t* h_codes;      // gate_up output [T*k, ldh], scales [T*k, ldh / 16]
+  uint8_t* h_scales;
+  int64_t ldh;  // bytes of one h row
+  void* out;    // linear: BF16 or FP32 [T, ldo]; down: FP16 pair rows [T*k, ldo]
+  int64_t ldo;
+  int out_f32;
+  float* pair_scale;
+};
+
+hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                              uint8_t* scales, hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
+                                void* out, int64_t ld, hipStream_t st);
+hipError_t launch_mx_quantize_weights(const uint16_t* w, int64_t batch, int64_t N, int64_t K, uint8_t* codes,
+                                      uint8_t* scales, int32_t* max_scale, hipStream_t st);
+// canonical -> packed (pack) or back; max_scale (pack only) may be null
+hipError_t launch_mx_relayout(uint8_t* codes, uint8_t* scales, int64_t batch, int64_t N, int64_t K, uint8_t* pcodes,
+                              uint8_t* pscales, int32_t* max_scale, bool pack, hipStream_t st);
+hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st);
+hipError_t launch_mx_gate_up(const MxArgs& a, int64_t E, hipStream_t st);
+hipError_t launch_mx_down(const MxArgs& a, int64_t E, hipStream_t st);
+
+// Norms around a block; x is the row to norm (norm_in) or the block output y (norm_out).
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  int y_f32;
+  int64_t T, H, Hp;        // Hp: columns the row's lanes cover (padded when it is quantised)
+  const uint16_t* w_post;  // norm_out: null = no norm of y
+  const uint16_t* gate;    // null = 1; element (t, c) at t * gate_rs + c * gate_cs
+  int64_t gate_rs, gate_cs;
+  const uint16_t* r;
+  int64_t ldr;
+  float scale, eps;
+  uint16_t* r_out;
+  int64_t ldro;
+  const uint16_t* w;  // weight of the norm that follows; null = none
+  uint16_t* n;        // null = only the codes
+  int64_t ldn;
+  uint8_t* codes;  // null = not quantised
+  uint8_t* scales;
+};
+int64_t norm_max_cols();
+hipError_t launch_norm(const NormArgs& a, bool post, bool vec, hipStream_t st);
+
 }  // namespace moe

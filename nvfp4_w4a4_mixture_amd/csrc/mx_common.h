@@ -1,0 +1,90 @@
+// Device helpers of the MXFP4 kernels (OCP Microscaling: blocks of 32 E2M1
+// elements with one E8M0 scale).
+//
+// E8M0 byte b stands for 2^(b - 127), b = 255 for NaN.  A block's byte is
+// floor(log2(amax)) - 2 + 127 (2 = the exponent of the largest E2M1 value, 6),
+// so amax / scale lies in [4, 8) and what exceeds 6 saturates.
+//
+// Operand fragments.  The scaled FP4 MFMA of 32 x 32 x 64 takes, per lane l,
+// 32 elements (16 bytes) of row l % 32: one MX block, with that block's scale
+// byte in one of the four bytes of a scale register.  The order of the blocks
+// along K is free as long as both operands agree; here the 256 columns of one
+// column group (8 blocks) are four MFMA steps, and lane half f = l / 32 takes
+// block 4 f + s at step s.  A lane's four blocks of a column group are then 64
+// consecutive bytes of codes, and their scale bytes one dword.
+//
+// Result rows.  Lane l holds column l % 32 of the result and, in register
+// 4 q + j, row 8 q + 4 (l / 32) + j.  Weights are the row operand, and packed
+// so that MFMA row 8 q + 4 h + j is weight row 16 h + 4 q + j of its group of
+// 32: a lane then holds 16 consecutive output features of one token.
+#pragma once
+
+#include "device_common.h"
+
+namespace moe {
+
+constexpr int kMxBlock = 32;    // elements per scale
+constexpr int kMxGroupCols = 256;  // columns of one column group
+constexpr int kMxGroupRows = 32;   // rows of one packed row group
+// bytes of one packed (row group, column group): codes and scales
+constexpr int kMxFragCodes = 4096;
+constexpr int kMxFragScales = 256;
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// Scale byte of a block from the largest |x| of it, given as float bits with
+// the sign cleared (as integers these order like the values, infinities above
+// every number and NaN above infinity).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// 2^(127 - byte), the exact factor that takes x to its element; 0 for a NaN block.
+__device__ __forceinline__ float mx_inverse_scale(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0u : (254u - byte) << 23);
+}
+
+// 2^(byte - 127), NaN for byte 255
+__device__ __forceinline__ float mx_scale_value(uint32_t byte) {
+  const uint32_t bits = byte == 0u ? 0x00400000u : (byte == 255u ? 0x7FC00000u : byte << 23);
+  return __uint_as_float(bits);
+}
+
+// Eight codes (one dword) of x[0..7] under a block's scale byte.  A NaN block has zero codes.
+__device__ __forceinline__ uint32_t mx_encode8(const float* x, uint32_t byte) {
+  const float inv = mx_inverse_scale(byte);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = x[i] * inv;
+  const uint32_t d = e2m1_encode8(v);
+  return byte == 255u ? 0u : d;
+}
+
+// BF16 bits of a float, round to nearest even; NaN stays NaN
+__device__ __forceinline__ uint32_t bf16_bits_rne(float f) {
+  const uint32_t u = __float_as_uint(f);
+  const uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+  return (u & 0x7FFFFFFFu) > 0x7F800000u ? (u >> 16) | 0x40u : r;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// One scaled FP4 MFMA step: c += A . B over 64 columns; S = step = scale byte.
+template <int S>
+__device__ __forceinline__ float16_t mx_mfma(i32x4_t a, i32x4_t b, float16_t c, int sa, int sb) {
+  const i32x8_t a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  const i32x8_t b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, S, sa, S, sb);
+}
+
+// Lane (of 64) and byte of the packed layout for weight row `row` and block `blk` (of 32 columns):
+// codes  ((g * KK + c) * 4 + s) * 1024 + lane * 16, scales (g * KK + c) * 256 + lane * 4 + s.
+__host__ __device__ __forceinline__ int mx_packed_lane(int64_t row, int64_t blk) {
+  const int r = (int)(row & 31), f = (int)((blk >> 2) & 1);
+  const int h = r >> 4, q = (r >> 2) & 3, j = r & 3;
+  return 32 * f + 8 * q + 4 * h + j;
+}
+
+}  // namespace moe

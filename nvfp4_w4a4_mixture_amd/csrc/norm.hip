@@ -1,0 +1,188 @@
+// RMS norms before and after a block, fused with the block's gate, residual
+// scale and residual, and with the MXFP4 quantisation of what the next product
+// reads.
+#include "launch.h"
+#include "mx_common.h"
+
+namespace moe {
+
+namespace {
+
+// Sum over the row's waves, in a fixed order; every thread gets it.
+template <int NW>
+__device__ __forceinline__ float row_sum(float v, float* lds, int w) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  if (NW == 1) return v;
+  if ((threadIdx.x & 63) == 0) lds[w] = v;
+  __syncthreads();
+  float s = lds[0];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) s += lds[i];
+  return s;
+}
+
+// Eight elements at column c of a row of H: 16-byte accesses in the vector
+// form, element by element (and only the ones below H) in the other.
+template <bool VEC>
+__device__ __forceinline__ void load8_bf16(const uint16_t* p, int c, int H, float* f) {
+  if (VEC) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < H) v = *reinterpret_cast<const uint4*>(p + c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < H ? bf16_to_f32(p[c + i]) : 0.0f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8_f32(const float* p, int c, int H, float* f) {
+  if (VEC) {
+    float4 a = make_float4(0, 0, 0, 0), b = a;
+    if (c < H) {
+      a = *reinterpret_cast<const float4*>(p + c);
+      b = *reinterpret_cast<const float4*>(p + c + 4);
+    }
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < H ? p[c + i] : 0.0f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uint32_t* b) {
+  if (VEC) {
+    if (c < H)
+      *reinterpret_cast<uint4*>(p + c) =
+          make_uint4(b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < H) p[c + i] = (uint16_t)b[i];
+  }
+}
+
+}  // namespace
+
+// NW waves per row, V chunks of 8 columns per lane; the row stays in registers
+// between the passes.  POST: the row is y, and the first norm, gate, residual
+// scale and residual give r'; otherwise the row is x itself.
+template <int NW, int V, bool POST, bool VEC>
+__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
+  constexpr int kRows = 4 / NW;  // rows per workgroup of 256 threads
+  __shared__ float lds[2][4];
+  const int w = (threadIdx.x >> 6) % NW, t = threadIdx.x % (64 * NW);
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (64 * NW);
+  if (NW == 1 && row >= a.T) return;  // with several waves a row is a workgroup
+  const int H = (int)a.H;
+  float x[V][8];
+  if (POST) {
+    float sq = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * 64 * NW + t) * 8;
+      if (a.y_f32)
+        load8_f32<VEC>(static_cast<const float*>(a.x) + row * a.ldx, c, H, x[v]);
+      else
+        load8_bf16<VEC>(static_cast<const uint16_t*>(a.x) + row * a.ldx, c, H, x[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq = fmaf(x[v][i], x[v][i], sq);
+    }
+    float inv = 1.0f;
+    if (a.w_post) inv = rsqrtf(row_sum<NW>(sq, lds[0], w) / (float)H + a.eps);
+    const float g_row = a.gate && a.gate_cs == 0 ? bf16_to_f32(a.gate[row * a.gate_rs]) : 1.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * 64 * NW + t) * 8;
+      float wv[8], rv[8], gv[8];
+      uint32_t o[8];
+      if (a.w_post) load8_bf16<VEC>(a.w_post, c, H, wv);
+      if (a.gate && a.gate_cs != 0) load8_bf16<VEC>(a.gate + row * a.gate_rs, c, H, gv);
+      load8_bf16<VEC>(a.r + row * a.ldr, c, H, rv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float z = x[v][i];
+        if (a.w_post) z = z * inv * wv[i];
+        if (a.gate) z *= a.gate_cs != 0 ? gv[i] : g_row;
+        o[i] = bf16_bits_rne(fmaf(a.scale, z, rv[i]));
+        x[v][i] = bf16_to_f32(o[i]);  // the next norm reads the residual that is kept
+      }
+      store8_bf16<VEC>(a.r_out + row * a.ldro, c, H, o);
+    }
+    if (!a.w) return;
+  }
+  float sq = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * 64 * NW + t) * 8;
+    if (!POST) load8_bf16<VEC>(static_cast<const uint16_t*>(a.x) + row * a.ldx, c, H, x[v]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(x[v][i], x[v][i], sq);
+  }
+  const float inv = rsqrtf(row_sum<NW>(sq, lds[1], w) / (float)H + a.eps);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * 64 * NW + t) * 8;
+    float wv[8];
+    uint32_t o[8];
+    load8_bf16<VEC>(a.w, c, H, wv);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[i] = c + i < H ? bf16_bits_rne(x[v][i] * inv * wv[i]) : 0u;
+      m = max(m, (o[i] & 0x7FFFu) << 16);
+    }
+    if (a.n) store8_bf16<VEC>(a.n + row * a.ldn, c, H, o);
+    if (a.codes) {  // H % 32 == 0: a quad of lanes holds one block
+      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+      const uint32_t byte = mx_scale_byte(m);
+      float q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = bf16_to_f32(o[i]);
+      if (c < a.Hp) {
+        reinterpret_cast<uint32_t*>(a.codes)[(row * a.Hp + c) / 8] = mx_encode8(q, byte);
+        if ((t & 3) == 0) a.scales[(row * a.Hp + c) / 32] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+namespace {
+
+template <int NW, int V, bool POST>
+void launch_norm_as(const NormArgs& a, bool vec, hipStream_t st) {
+  const dim3 grid((unsigned)((a.T * NW + 3) / 4));
+  if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, true>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((norm_kernel<NW, V, POST, false>), grid, dim3(256), 0, st, a);
+}
+
+template <bool POST>
+void launch_norm_shape(const NormArgs& a, bool vec, hipStream_t st) {
+  const int64_t cols = a.Hp;  // columns that a row's lanes cover (the padded row when it is quantised)
+  if (cols <= 512) launch_norm_as<1, 1, POST>(a, vec, st);
+  else if (cols <= 1024) launch_norm_as<1, 2, POST>(a, vec, st);
+  else if (cols <= 2048) launch_norm_as<4, 1, POST>(a, vec, st);
+  else if (cols <= 4096) launch_norm_as<4, 2, POST>(a, vec, st);
+  else if (cols <= 6144) launch_norm_as<4, 3, POST>(a, vec, st);
+  else if (cols <= 8192) launch_norm_as<4, 4, POST>(a, vec, st);
+  else launch_norm_as<4, 8, POST>(a, vec, st);
+}
+
+}  // namespace
+
+int64_t norm_max_cols() { return 16384; }
+
+hipError_t launch_norm(const NormArgs& a, bool post, bool vec, hipStream_t st) {
+  if (post) launch_norm_shape<true>(a, vec, st);
+  else launch_norm_shape<false>(a, vec, st);
+  return hipGetLastError();
+}
+
+}  // namespace moe

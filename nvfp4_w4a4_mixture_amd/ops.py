@@ -20,7 +20,10 @@ __all__ = ["moe_route", "moe_route_quantize", "nvfp4_quantize_act", "nvfp4_quant
            "moe_combine_reap", "reap_prune_select", "moe_gather_experts", "moe_shared_workspace_bytes", "moe_shared_expert",
            "moe_shared_gate_up", "moe_shared_down", "moe_combine_block", "hadamard_rotate_bf16",
            "moe_nvfp4_prepack_weights", "moe_nvfp4_unpack_weights",
-           "moe_route_workspace_bytes", "moe_ffn_workspace_bytes", "moe_ffn_stage_workspace_bytes", "RouteOut"]
+           "moe_route_workspace_bytes", "moe_ffn_workspace_bytes", "moe_ffn_stage_workspace_bytes", "RouteOut",
+           "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_quantize_weights", "mxfp4_pack_weights", "mxfp4_unpack_weights",
+           "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn",
+           "moe_norm_in", "moe_norm_out"]
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -494,3 +497,257 @@ def moe_nvfp4_prepack_weights(codes: torch.Tensor, scales: torch.Tensor, kind: i
 def moe_nvfp4_unpack_weights(codes: torch.Tensor, packed_scales: torch.Tensor, kind: int, stream=None):
     """Exact inverse of moe_nvfp4_prepack_weights."""
     return _relayout("moe_nvfp4_unpack_weights", codes, packed_scales, kind, False, stream)
+
+
+# ---- MXFP4 operators
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _rows(t: torch.Tensor, name: str, dtypes=(torch.bfloat16,)) -> int:
+    """Checks a [rows, cols] GPU matrix with unit column stride; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU device")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.numel() > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, cols] with unit column stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _mx_padded(cols: int) -> int:
+    return -(-cols // 256) * 256
+
+
+def _mx_rows(rows: int, cols: int, device, codes, scales):
+    """The codes and scales of [rows, cols] in the padded row form: given ones checked, missing ones allocated."""
+    c = _mx_padded(cols)
+    if codes is None:
+        codes = torch.empty((rows, c // 2), dtype=torch.uint8, device=device)
+    else:
+        _need(codes, "codes", torch.uint8, (rows, c // 2))
+    if scales is None:
+        scales = torch.empty((rows, c // 32), dtype=torch.uint8, device=device)
+    else:
+        _need(scales, "scales", torch.uint8, (rows, c // 32))
+    return codes, scales
+
+
+def _need_mx_rows(codes, scales, name: str, cols: int) -> int:
+    c = _mx_padded(cols)
+    _need(codes, f"{name}_codes", torch.uint8)
+    if codes.dim() != 2 or codes.shape[1] != c // 2:
+        raise ValueError(f"{name}_codes must be [rows, {c // 2}] for {cols} columns, got {tuple(codes.shape)}")
+    _need(scales, f"{name}_scales", torch.uint8, (codes.shape[0], c // 32))
+    return codes.shape[0]
+
+
+def _mx_weight_shapes(N: int, K: int):
+    g, kk = -(-N // 32), -(-K // 256)
+    return (g, kk, 4, 64, 16), (g, kk, 64, 4)
+
+
+def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """x [rows, cols] BF16 or FP32 -> (codes [rows, Cp/2], scales [rows, Cp/32]), Cp = cols rounded up to 256."""
+    ld = _rows(x, "x", (torch.bfloat16, torch.float32))
+    rows, cols = x.shape
+    codes, scales = _mx_rows(rows, cols, x.device, codes, scales)
+    st = lib().mxfp4_quantize(_p(x), _DTYPE[x.dtype], rows, cols, ld, _p(codes), _p(scales), _stream(stream))
+    check(st, "mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out_dtype: torch.dtype = torch.bfloat16,
+                     out=None, stream=None) -> torch.Tensor:
+    """The values that the codes stand for, [rows, cols] in BF16 or FP32 (exact in both)."""
+    rows = _need_mx_rows(codes, scales, "x", cols)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device)
+    ld = _rows(out, "out", (torch.bfloat16, torch.float32))
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"out must have shape {(rows, cols)}, got {tuple(out.shape)}")
+    st = lib().mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _DTYPE[out.dtype], _p(out), ld, _stream(stream))
+    check(st, "mxfp4_dequantize")
+    return out
+
+
+def mxfp4_quantize_weights(w_bf16: torch.Tensor, stream=None):
+    """w_bf16 [batch, N, K] -> packed (codes [batch, G, KK, 4, 64, 16], scales [batch, G, KK, 64, 4]) and the largest
+    scale byte of each matrix [batch] INT32."""
+    _need(w_bf16, "w_bf16", torch.bfloat16)
+    if w_bf16.dim() != 3:
+        raise ValueError("w_bf16 must be [batch, N, K]")
+    b, n, k = w_bf16.shape
+    cs, ss = _mx_weight_shapes(n, k)
+    dev = w_bf16.device
+    codes = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
+    scales = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
+    max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
+    st = lib().mxfp4_quantize_weights(_p(w_bf16), b, n, k, _p(codes), _p(scales), _p(max_scale), _stream(stream))
+    check(st, "mxfp4_quantize_weights")
+    return codes, scales, max_scale
+
+
+def mxfp4_pack_weights(codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """Canonical (codes [batch, N, K/2], scales [batch, N, K/32]) -> what mxfp4_quantize_weights returns."""
+    _need(codes, "codes", torch.uint8)
+    if codes.dim() != 3:
+        raise ValueError("codes must be [batch, N, K/2]")
+    b, n, kh = codes.shape
+    if kh % 16:
+        raise ValueError("K must be a multiple of 32")
+    _need(scales, "scales", torch.uint8, (b, n, kh // 16))
+    cs, ss = _mx_weight_shapes(n, 2 * kh)
+    dev = codes.device
+    pc = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
+    ps = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
+    max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
+    st = lib().mxfp4_pack_weights(_p(codes), _p(scales), b, n, 2 * kh, _p(pc), _p(ps), _p(max_scale), _stream(stream))
+    check(st, "mxfp4_pack_weights")
+    return pc, ps, max_scale
+
+
+def mxfp4_unpack_weights(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, stream=None):
+    """Packed weights of [batch, N, K] -> canonical (codes [batch, N, K/2], scales [batch, N, K/32])."""
+    cs, ss = _mx_weight_shapes(N, K)
+    b = codes.shape[0]
+    _need(codes, "codes", torch.uint8, (b, *cs))
+    _need(scales, "scales", torch.uint8, (b, *ss))
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    oc = torch.empty((b, N, K // 2), dtype=torch.uint8, device=codes.device)
+    os_ = torch.empty((b, N, K // 32), dtype=torch.uint8, device=codes.device)
+    st = lib().mxfp4_unpack_weights(_p(codes), _p(scales), b, N, K, _p(oc), _p(os_), _stream(stream))
+    check(st, "mxfp4_unpack_weights")
+    return oc, os_
+
+
+def mxfp4_linear_workspace_bytes(T: int, K: int, N: int) -> int:
+    return int(lib().mxfp4_linear_workspace_bytes(T, K, N))
+
+
+def mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.dtype = torch.bfloat16, y=None,
+                 workspace=None, stream=None) -> torch.Tensor:
+    """y [T, N] = x W^T for quantized x (mxfp4_quantize) and packed weights w_codes [G, KK, 4, 64, 16]."""
+    if w_codes.dim() != 5:
+        raise ValueError("w_codes must be [G, KK, 4, 64, 16]")
+    K = 256 * w_codes.shape[1]  # the padded width: the padding is zero on both sides
+    T = _need_mx_rows(x_codes, x_scales, "x", K)
+    cs, ss = _mx_weight_shapes(N, K)
+    _need(w_codes, "w_codes", torch.uint8, cs)
+    _need(w_scales, "w_scales", torch.uint8, ss)
+    if y is None:
+        y = torch.empty((T, N), dtype=out_dtype, device=x_codes.device)
+    ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
+    if tuple(y.shape) != (T, N):
+        raise ValueError(f"y must have shape {(T, N)}, got {tuple(y.shape)}")
+    nbytes = mxfp4_linear_workspace_bytes(T, K, N)
+    ws = _workspace(nbytes, x_codes.device, workspace) if nbytes or workspace is not None else None
+    st = lib().mxfp4_linear(_p(x_codes), _p(x_scales), T, K, _p(w_codes), _p(w_scales), N, _DTYPE[y.dtype], _p(y), ldy,
+                            _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    check(st, "mxfp4_linear")
+    return y
+
+
+def mxfp4_ffn_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
+    return int(lib().mxfp4_ffn_workspace_bytes(T, k, E, H, I))
+
+
+def mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_scales, w2_max_scale, H: int, I: int,
+                      k: int, expert_offsets, sorted_pair_ids, topk_w, pair_out=None, pair_scale=None, workspace=None,
+                      stream=None):
+    """The routed experts' FFN in MXFP4: (pair_out, pair_scale), what moe_combine and moe_combine_block read."""
+    T = _need_mx_rows(x_codes, x_scales, "x", H)
+    E = w13_codes.shape[0]
+    cs, ss = _mx_weight_shapes(2 * I, H)
+    _need(w13_codes, "w13_codes", torch.uint8, (E, *cs))
+    _need(w13_scales, "w13_scales", torch.uint8, (E, *ss))
+    cs, ss = _mx_weight_shapes(H, I)
+    _need(w2_codes, "w2_codes", torch.uint8, (E, *cs))
+    _need(w2_scales, "w2_scales", torch.uint8, (E, *ss))
+    _need(w2_max_scale, "w2_max_scale", torch.int32, (E,))
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
+    _need(topk_w, "topk_w", torch.float32, (T, k))
+    dev = x_codes.device
+    pair_out, pair_scale, _ = _pair_outputs(T * k, H, dev, pair_out, pair_scale, None)
+    ws = _workspace(mxfp4_ffn_workspace_bytes(T, k, E, H, I), dev, workspace)
+    st = lib().mxfp4_grouped_ffn(_p(x_codes), _p(x_scales), T, H, _p(w13_codes), _p(w13_scales), _p(w2_codes),
+                                 _p(w2_scales), _p(w2_max_scale), E, I, k, _p(expert_offsets), _p(sorted_pair_ids),
+                                 _p(topk_w), _p(pair_out), _p(pair_scale), _p(ws), ws.numel(), _stream(stream))
+    check(st, "mxfp4_grouped_ffn")
+    return pair_out, pair_scale
+
+
+# ---- norms around the block
+
+
+def _norm_outputs(T: int, H: int, device, n, quantize: bool, codes, scales):
+    """Output n (False: none) and, if asked for, its codes and scales."""
+    if n is None:
+        n = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+    elif n is False:
+        n = None
+    ldn = H
+    if n is not None:
+        ldn = _rows(n, "n")
+        if tuple(n.shape) != (T, H):
+            raise ValueError(f"n must have shape {(T, H)}, got {tuple(n.shape)}")
+    if quantize or codes is not None or scales is not None:
+        codes, scales = _mx_rows(T, H, device, codes, scales)
+    return n, ldn, codes, scales
+
+
+def moe_norm_in(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, n=None, quantize: bool = False, codes=None,
+                scales=None, stream=None):
+    """n = bf16(x / rms(x) * w).  quantize=True (or codes/scales given): (n, codes, scales), the MXFP4 form of n
+    from the same pass; n=False then skips the BF16 result."""
+    ldx = _rows(x, "x")
+    T, H = x.shape
+    _need(w, "w", torch.bfloat16, (H,))
+    n, ldn, codes, scales = _norm_outputs(T, H, x.device, n, quantize, codes, scales)
+    st = lib().moe_norm_in(_p(x), T, H, ldx, _p(w), eps, _p(n), ldn, _p(codes), _p(scales), _stream(stream))
+    check(st, "moe_norm_in")
+    return n if codes is None else (n, codes, scales)
+
+
+def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch.Tensor] = None,
+                 w_next: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                 residual_scale: float = 1.0, eps: float = 1e-6, out=None, n=None, quantize: bool = False, codes=None,
+                 scales=None, stream=None):
+    """r' = bf16(residual + residual_scale * gate * (y / rms(y) * w_post)); with w_next also n = bf16(r' / rms(r') * w_next).
+
+    w_post None: y is not normed.  gate: None, or BF16 [T, 1], [1, H] or [T, H].  Returns r', or (r', n), or
+    (r', n, codes, scales) when n is quantized to MXFP4 as well (n=False then skips the BF16 n)."""
+    ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
+    T, H = y.shape
+    ldr = _rows(residual, "residual")
+    if tuple(residual.shape) != (T, H):
+        raise ValueError(f"residual must have shape {(T, H)}, got {tuple(residual.shape)}")
+    for name, w in (("w_post", w_post), ("w_next", w_next)):
+        if w is not None:
+            _need(w, name, torch.bfloat16, (H,))
+    grs = gcs = 0
+    if gate is not None:
+        _need(gate, "gate", torch.bfloat16, contiguous=False)
+        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, H):
+            raise ValueError(f"gate must be [T, 1], [1, H] or [T, H], got {tuple(gate.shape)}")
+        gcs = 0 if gate.shape[1] == 1 else gate.stride(1)
+        grs = 0 if gate.shape[0] == 1 else gate.stride(0)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    ldo = _rows(out, "out")
+    if tuple(out.shape) != (T, H):
+        raise ValueError(f"out must have shape {(T, H)}, got {tuple(out.shape)}")
+    ldn = H
+    if w_next is not None:
+        n, ldn, codes, scales = _norm_outputs(T, H, y.device, n, quantize, codes, scales)
+    elif quantize or codes is not None or scales is not None or n is not None:
+        raise ValueError("n and its quantization need w_next")
+    st = lib().moe_norm_out(_p(y), _DTYPE[y.dtype], T, H, ldy, _p(residual), ldr, _p(w_post), _p(gate), grs, gcs,
+                            residual_scale, _p(w_next), eps, _p(out), ldo, _p(n), ldn, _p(codes), _p(scales),
+                            _stream(stream))
+    check(st, "moe_norm_out")
+    if w_next is None:
+        return out
+    return (out, n) if codes is None else (out, n, codes, scales)
