@@ -51,12 +51,14 @@ moe_status check_weights(const char* fn, int64_t batch, int64_t N, int64_t K) {
 }
 
 struct MxFfnWs {
-  size_t h_codes, h_scales, total;
+  size_t tiles, h_codes, h_scales, total;
 };
 
-MxFfnWs mx_ffn_ws(int64_t T, int64_t k, int64_t I) {
+MxFfnWs mx_ffn_ws(int64_t T, int64_t k, int64_t E, int64_t I) {
   MxFfnWs w{};
   size_t o = 0;
+  w.tiles = o;
+  o = round_up(o + (size_t)(moe::mx_max_mtiles(T, k, E) + 1) * 16, 256);
   w.h_codes = o;
   o = round_up(o + (size_t)(T * k) * (size_t)(mx_padded(I) / 2), 256);
   w.h_scales = o;
@@ -177,12 +179,13 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
   a.out = y;
   a.ldo = ldy;
   a.out_f32 = out_dtype;
+  a.out_vec = aligned(y, 16) && (ldy * (out_dtype ? 4 : 2)) % 16 == 0;
   return launched(moe::launch_mx_linear(a, (hipStream_t)stream), fn);
 }
 
 size_t mxfp4_ffn_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   if (T < 0 || k < 1 || E < 1 || H < 1 || I < 1) return 0;
-  return mx_ffn_ws(T, k, I).total;
+  return mx_ffn_ws(T, k, E, I).total;
 }
 
 moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t H,
@@ -210,7 +213,7 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
       !aligned(x_scales, 4) || !aligned(w13_scales, 4) || !aligned(w2_scales, 4) || !aligned(pair_scale, 4) ||
       !aligned(w2_max_scale, 4) || !aligned(expert_offsets, 4) || !aligned(sorted_pair_ids, 4) || !aligned(topk_w, 4))
     return fail(MOE_ERR_ALIGN, "%s: code arrays and pair_out must be 16-byte, the other arrays 4-byte aligned", fn);
-  const MxFfnWs L = mx_ffn_ws(T, k, I);
+  const MxFfnWs L = mx_ffn_ws(T, k, E, I);
   if (!workspace || workspace_bytes < L.total) return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, L.total);
   if (!aligned(workspace, 256)) return fail(MOE_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
   if (moe_status s = check_device()) return s;
@@ -232,6 +235,7 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
   a.h_codes = ws + L.h_codes;
   a.h_scales = ws + L.h_scales;
   a.ldh = mx_padded(I) / 2;
+  a.tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
   if (moe_status s = launched(moe::launch_mx_gate_up(a, E, (hipStream_t)stream), fn)) return s;
   a.a_codes = a.h_codes;
   a.a_scales = a.h_scales;

@@ -157,6 +157,297 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   }
 }
 
+// Tiled product: four waves share a tile of 256 weight rows by kTok tokens
+// through LDS, double buffered by column groups of 256.  Weights arrive in
+// fragment order, so a wave reads them back as they lie; a token's 128 bytes of
+// a column group are eight 16-byte chunks, stored exchanged by the row's low
+// three bits so that the eight lanes of one LDS cycle touch all banks.
+//
+// Wave (wm, wx) of WM x (4 / WM) holds GW weight groups by GX token groups of
+// 32 in accumulators.  One column group is four MFMA steps; the fragments of
+// the next step are read while the current one multiplies, and the barrier
+// that hands over the buffers stands between the third and the fourth step, so
+// that the fourth covers the first reads of the next buffer.
+template <int WM, int GW, int GX>
+struct MxTile {
+  static constexpr int kWX = 4 / WM;
+  static constexpr int kSlots = WM * GW;       // weight groups of a tile
+  static constexpr int kTok = kWX * GX * 32;   // tokens of a tile
+  static constexpr int kWBytes = kSlots * kMxFragCodes;
+  static constexpr int kStage = kWBytes + kTok * 128;
+  static constexpr int kLds = 2 * kStage;
+};
+
+template <int MODE, int WM, int GW, int GX>
+__global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
+  using S = MxTile<WM, GW, GX>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, l = tid & 63, n = l & 31, f = l >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w % WM, wx = w / WM;
+
+  // ---- which tile: each XCD takes one contiguous run of the tile order
+  const int64_t nw = a.n_wtiles;
+  const int64_t mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : a.tiles[0];
+  const int64_t total = mtiles * nw, chunk = (total + 7) / 8;
+  const int64_t at = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+  if ((int64_t)(blockIdx.x >> 3) >= chunk || at >= total) return;
+  int e = 0;
+  int64_t first = 0, rows = a.T, span = mtiles, q = at;
+  if (MODE != kLinear) {
+    const int32_t* t = a.tiles + 4 + (at / nw) * 4;  // {expert, its first m-tile, its m-tiles}
+    e = t[0];
+    q = at - (int64_t)t[1] * nw;
+    span = t[2];
+    first = a.offsets[e];
+    rows = a.offsets[e + 1] - first;
+  }
+  // blocks of up to four token tiles by all weight tiles, tokens fastest
+  const int64_t blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min((int64_t)4, span - 4 * blk);
+  const int64_t wt = rem / tc, t0 = (4 * blk + rem - wt * tc) * S::kTok;
+  const int cnt = (int)min((int64_t)S::kTok, rows - t0);
+  first += t0;
+
+  // weight group of slot s (of kSlots)
+  auto group = [&](int s) -> int64_t {
+    if (MODE == kGateUp) {  // a wave holds gate groups and the up groups of the same h columns
+      const int64_t half = a.G / 2, hb = wt * (S::kSlots / 2) + (s / GW) * (GW / 2) + s % (GW / 2);
+      return min(hb, half - 1) + (s % GW >= GW / 2 ? half : 0);
+    }
+    return min(wt * S::kSlots + s, a.G - 1);
+  };
+
+  // ---- DMA sources: this wave's weight slots and token rows
+  constexpr int kWSlots = S::kSlots / 4, kXDma = S::kTok / 32;
+  const uint8_t* wsrc[kWSlots];
+#pragma unroll
+  for (int i = 0; i < kWSlots; ++i)
+    wsrc[i] = a.w_codes + ((int64_t)e * a.G + group(w * kWSlots + i)) * a.KK * kMxFragCodes;
+  auto act_row = [&](int t) -> int64_t {  // activation row of the tile's token t (rows past the end repeat the last)
+    const int64_t pos = first + min(t, cnt - 1);
+    return MODE == kGateUp ? a.sorted[pos] / a.k : pos;
+  };
+  uint32_t xoff[kXDma];
+#pragma unroll
+  for (int i = 0; i < kXDma; ++i) {
+    const int r = (w * kXDma + i) * 8 + (l >> 3);
+    xoff[i] = (uint32_t)(act_row(r) * (a.KK * 128)) + (uint32_t)(((l & 7) ^ (r & 7)) * 16);
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
+  const uint32_t woff = (uint32_t)l * 16u;
+  auto dma = [&](int64_t c) {
+    const uint32_t buf = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(c & 1) * (uint32_t)S::kStage);
+#pragma unroll
+    for (int i = 0; i < kWSlots; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        dma16_async(wsrc[i] + c * kMxFragCodes + s * 1024, woff, buf + (uint32_t)((w * kWSlots + i) * 4096 + s * 1024));
+    const uint8_t* xc = a.a_codes + c * 128;
+#pragma unroll
+    for (int i = 0; i < kXDma; ++i)
+      dma16_async(xc, xoff[i], buf + (uint32_t)(S::kWBytes + (w * kXDma + i) * 1024));
+  };
+
+  // ---- scales: one dword per lane, group and column group, in registers
+  const uint8_t* wsp[GW];
+  const uint8_t* xsp[GX];
+#pragma unroll
+  for (int i = 0; i < GW; ++i)
+    wsp[i] = a.w_scales + ((int64_t)e * a.G + group(wm * GW + i)) * a.KK * kMxFragScales + l * 4;
+#pragma unroll
+  for (int i = 0; i < GX; ++i) xsp[i] = a.a_scales + act_row((wx * GX + i) * 32 + n) * (a.KK * 8) + f * 4;
+  int sw[GW], sx[GX], nsw[GW], nsx[GX];
+  auto load_scales = [&](int64_t c, int* pw, int* px) {
+#pragma unroll
+    for (int i = 0; i < GW; ++i) pw[i] = *reinterpret_cast<const int*>(wsp[i] + c * kMxFragScales);
+#pragma unroll
+    for (int i = 0; i < GX; ++i) px[i] = *reinterpret_cast<const int*>(xsp[i] + c * 8);
+  };
+
+  // ---- fragments
+  const int xrow0 = wx * GX * 32 + n;  // rows of the GX groups are 32 apart: the same low three bits
+  auto read = [&](int64_t c, int s, i32x4_t* fw, i32x4_t* fx) {
+    const unsigned char* buf = smem + (c & 1) * S::kStage;
+#pragma unroll
+    for (int i = 0; i < GW; ++i)
+      fw[i] = *reinterpret_cast<const i32x4_t*>(buf + (wm * GW + i) * 4096 + s * 1024 + l * 16);
+#pragma unroll
+    for (int i = 0; i < GX; ++i)
+      fx[i] = *reinterpret_cast<const i32x4_t*>(buf + S::kWBytes + (xrow0 + 32 * i) * 128 + (((4 * f + s) ^ (n & 7)) * 16));
+  };
+
+  float16_t acc[GW][GX];
+#pragma unroll
+  for (int i = 0; i < GW; ++i)
+#pragma unroll
+    for (int j = 0; j < GX; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  uint32_t bh[GX];
+#pragma unroll
+  for (int j = 0; j < GX; ++j) bh[j] = 0;
+
+#define MX_STEP(SEL, FW, FX, SW, SX)                                                  \
+  _Pragma("unroll") for (int i = 0; i < GW; ++i) _Pragma("unroll") for (int j = 0; j < GX; ++j) \
+      acc[i][j] = mx_mfma<SEL>(FW[i], FX[j], acc[i][j], SW[i], SX[j]);
+
+  i32x4_t fw0[GW], fx0[GX], fw1[GW], fx1[GX];
+  dma(0);
+  load_scales(0, sw, sx);
+  wait_vmcnt<0>();
+  barrier_after_lds();
+  read(0, 0, fw0, fx0);
+  if (a.KK > 1) {
+    load_scales(1, nsw, nsx);
+    dma(1);
+  }
+  for (int64_t c = 0; c < a.KK; ++c) {
+    if (MODE == kDown) {
+#pragma unroll
+      for (int j = 0; j < GX; ++j) bh[j] = max(bh[j], max_byte((uint32_t)sx[j]));
+    }
+    read(c, 1, fw1, fx1);
+    MX_STEP(0, fw0, fx0, sw, sx)
+    read(c, 2, fw0, fx0);
+    MX_STEP(1, fw1, fx1, sw, sx)
+    read(c, 3, fw1, fx1);
+    MX_STEP(2, fw0, fx0, sw, sx)
+    int lw[GW], lx[GX];  // the fourth step's bytes, so that sw and sx can take the next group's
+#pragma unroll
+    for (int i = 0; i < GW; ++i) lw[i] = (int)((uint32_t)sw[i] >> 24);
+#pragma unroll
+    for (int j = 0; j < GX; ++j) lx[j] = (int)((uint32_t)sx[j] >> 24);
+    if (c + 1 < a.KK) {
+      wait_vmcnt<0>();
+      barrier_after_lds();
+      read(c + 1, 0, fw0, fx0);
+#pragma unroll
+      for (int i = 0; i < GW; ++i) sw[i] = nsw[i];
+#pragma unroll
+      for (int j = 0; j < GX; ++j) sx[j] = nsx[j];
+      if (c + 2 < a.KK) {
+        load_scales(c + 2, nsw, nsx);
+        dma(c + 2);
+      }
+    }
+    MX_STEP(0, fw1, fx1, lw, lx)
+  }
+#undef MX_STEP
+
+  // ---- epilogue: a lane holds 16 consecutive features (half f of a group) of token n
+#pragma unroll
+  for (int j = 0; j < GX; ++j) {
+    const int tok = (wx * GX + j) * 32 + n;
+    const int64_t row = first + tok;
+    const bool in = tok < cnt;
+    if constexpr (MODE == kGateUp) {
+#pragma unroll
+      for (int i = 0; i < GW / 2; ++i) {
+        float h[16];
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          h[r] = silu(acc[i][j][r]) * acc[i + GW / 2][j][r];
+          m = max(m, abs_bits(h[r]));
+        }
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        const uint32_t byte = mx_scale_byte(m);
+        const int64_t hb = wt * (S::kSlots / 2) + wm * (GW / 2) + i;
+        if (in && hb < a.G / 2) {
+          *reinterpret_cast<uint2*>(a.h_codes + row * a.ldh + hb * 16 + f * 8) =
+              make_uint2(mx_encode8(h, byte), mx_encode8(h + 8, byte));
+          if (f == 0) a.h_scales[row * (a.ldh / 16) + hb] = (uint8_t)byte;
+        }
+      }
+    } else {
+      float wp = 1.0f, inv = 1.0f;
+      int64_t out = row;
+      if constexpr (MODE == kDown) {
+        const uint32_t b = max(bh[j], (uint32_t)__shfl_xor((int)bh[j], 32));
+        if (in) {
+          out = a.sorted[row];
+          wp = a.topk_w[out];
+          const int E = pair_exponent(wp, b, a.w_max[e], a.lg36I);
+          inv = __uint_as_float((uint32_t)(127 - E) << 23);
+          if (wt == 0 && wm == 0 && f == 0) a.pair_scale[out] = __uint_as_float((uint32_t)(127 + E) << 23);
+        }
+      }
+      if (!in) continue;
+#pragma unroll
+      for (int i = 0; i < GW; ++i) {
+        const int64_t g = wt * S::kSlots + wm * GW + i;
+        if (g >= a.G) continue;
+        const int64_t col = g * 32 + f * 16;
+        if constexpr (MODE == kDown) {
+          half8_t v[2];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r >> 3][r & 7] = (_Float16)((wp * acc[i][j][r]) * inv);
+          half8_t* p = reinterpret_cast<half8_t*>(static_cast<_Float16*>(a.out) + out * a.ldo + col);
+          p[0] = v[0];
+          p[1] = v[1];
+        } else {
+          const bool whole = a.out_vec && col + 16 <= a.N;
+          if (a.out_f32) {
+            float* p = static_cast<float*>(a.out) + out * a.ldo + col;
+            if (whole) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                reinterpret_cast<float4*>(p)[r] =
+                    make_float4(acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (col + r < a.N) p[r] = acc[i][j][r];
+            }
+          } else {
+            uint16_t* p = static_cast<uint16_t*>(a.out) + out * a.ldo + col;
+            uint32_t b[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) b[r] = bf16_bits_rne(acc[i][j][r]);
+            if (whole) {
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                reinterpret_cast<uint4*>(p)[r] =
+                    make_uint4(b[8 * r] | (b[8 * r + 1] << 16), b[8 * r + 2] | (b[8 * r + 3] << 16),
+                               b[8 * r + 4] | (b[8 * r + 5] << 16), b[8 * r + 6] | (b[8 * r + 7] << 16));
+            } else {
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (col + r < a.N) p[r] = (uint16_t)b[r];
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// The m-tiles of every expert: tiles[0] their number; from tiles[4] on, four
+// words each: {expert, the expert's first m-tile, its m-tiles, 0}.
+__global__ __launch_bounds__(256) void mx_schedule_kernel(const int32_t* __restrict__ offsets, int E, int tok,
+                                                          int32_t* __restrict__ tiles) {
+  __shared__ int32_t sum[256];
+  const int e = threadIdx.x;
+  const int n = e < E ? (offsets[e + 1] - offsets[e] + tok - 1) / tok : 0;
+  sum[e] = n;
+  __syncthreads();
+  for (int d = 1; d < 256; d <<= 1) {
+    const int v = e >= d ? sum[e - d] : 0;
+    __syncthreads();
+    sum[e] += v;
+    __syncthreads();
+  }
+  const int s0 = sum[e] - n;
+  if (e == 255) tiles[0] = sum[255];
+  for (int i = 0; i < n; ++i) {
+    int32_t* t = tiles + 4 + (int64_t)(s0 + i) * 4;
+    t[0] = e;
+    t[1] = s0;
+    t[2] = n;
+    t[3] = 0;
+  }
+}
+
 // Rows of h past I (a row is padded to a whole column group) are zero blocks.
 __global__ __launch_bounds__(256) void mx_zero_pad_kernel(uint8_t* codes, uint8_t* scales, int64_t rows, int64_t ldh,
                                                           int64_t I) {
@@ -168,22 +459,61 @@ __global__ __launch_bounds__(256) void mx_zero_pad_kernel(uint8_t* codes, uint8_
   scales[r * (ldh / 16) + b] = 0;
 }
 
-hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
+namespace {
+
+using MxBig = MxTile<2, 4, 4>;  // 256 weight rows by 256 tokens
+
+// Tokens (linear) or mean pairs per expert from which the tiled kernel is used.
+constexpr int64_t kTiledFrom = 64;
+
+template <int MODE>
+hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
+  auto* k = &mx_tiled_kernel<MODE, 2, 4, 4>;
+  if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), MxBig::kLds)) return e;
+  const int64_t grid = (max_mtiles * a.n_wtiles + 7) / 8 * 8;
+  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), MxBig::kLds, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool mx_experts_tiled(int64_t T, int64_t k, int64_t E) { return T * k >= kTiledFrom * E; }
+
+int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E) {
+  const int64_t pairs = T * k;
+  return pairs / MxBig::kTok + (pairs < E ? pairs : E);
+}
+
+hipError_t launch_mx_linear(MxArgs a, hipStream_t st) {
+  if (a.T >= kTiledFrom) {
+    a.n_wtiles = (a.G + MxBig::kSlots - 1) / MxBig::kSlots;
+    return launch_tiled<kLinear>(a, (a.T + MxBig::kTok - 1) / MxBig::kTok, st);
+  }
   hipLaunchKernelGGL((mx_stream_kernel<kLinear, 1, 8>), dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512), 0,
                      st, a);
   return hipGetLastError();
 }
 
-hipError_t launch_mx_gate_up(const MxArgs& a, int64_t E, hipStream_t st) {
+hipError_t launch_mx_gate_up(MxArgs a, int64_t E, hipStream_t st) {
   const int64_t I = a.N / 2, pad = a.ldh / 16 - I / 32, npairs = a.T * a.k;
   if (pad > 0)
     hipLaunchKernelGGL(mx_zero_pad_kernel, dim3((unsigned)((npairs * pad + 255) / 256)), dim3(256), 0, st, a.h_codes,
                        a.h_scales, npairs, a.ldh, I);
+  if (mx_experts_tiled(a.T, a.k, E)) {
+    hipLaunchKernelGGL(mx_schedule_kernel, dim3(1), dim3(256), 0, st, a.offsets, (int)E, MxBig::kTok, a.tiles);
+    a.n_wtiles = (a.G / 2 + MxBig::kSlots / 2 - 1) / (MxBig::kSlots / 2);
+    return launch_tiled<kGateUp>(a, mx_max_mtiles(a.T, a.k, E), st);
+  }
   hipLaunchKernelGGL((mx_stream_kernel<kGateUp, 2, 4>), dim3((unsigned)(a.G / 2), (unsigned)E), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-hipError_t launch_mx_down(const MxArgs& a, int64_t E, hipStream_t st) {
+// Reads the schedule that launch_mx_gate_up made.
+hipError_t launch_mx_down(MxArgs a, int64_t E, hipStream_t st) {
+  if (mx_experts_tiled(a.T, a.k, E)) {
+    a.n_wtiles = (a.G + MxBig::kSlots - 1) / MxBig::kSlots;
+    return launch_tiled<kDown>(a, mx_max_mtiles(a.T, a.k, E), st);
+  }
   hipLaunchKernelGGL((mx_stream_kernel<kDown, 2, 4>), dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st,
                      a);
   return hipGetLastError();
