@@ -7,6 +7,11 @@ namespace moe {
 
 namespace {
 
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+
 enum { kLinear = 0, kGateUp = 1, kDown = 2 };
 
 // Scale of a pair row: an exponent E with |w_p f| < 2^(E + 15) for every
@@ -157,26 +162,36 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   }
 }
 
-// Tiled product: four waves share a tile of 256 weight rows by kTok tokens
-// through LDS, double buffered by column groups of 256.  Weights arrive in
-// fragment order, so a wave reads them back as they lie; a token's 128 bytes of
-// a column group are eight 16-byte chunks, stored exchanged by the row's low
-// three bits so that the eight lanes of one LDS cycle touch all banks.
+// Tiled product: four waves share a tile of kSlots * 32 weight rows by kTok
+// tokens through LDS.  A stage is half a column group (128 columns, two MFMA
+// steps); a ring of four stages is filled by global -> LDS DMA three stages
+// ahead.  Weights arrive in fragment order, so a wave reads them back as they
+// lie.  A token's 64 bytes of a stage are four 16-byte chunks, stored exchanged
+// by mx_swizzle(row), so that the lanes of one LDS cycle touch all banks.
+// Scale dwords (a whole column group's) come by DMA too: the loop then has no
+// load that the compiler would wait for, and every wait is one written here.
 //
 // Wave (wm, wx) of WM x (4 / WM) holds GW weight groups by GX token groups of
-// 32 in accumulators.  One column group is four MFMA steps; the fragments of
-// the next step are read while the current one multiplies, and the barrier
-// that hands over the buffers stands between the third and the fourth step, so
-// that the fourth covers the first reads of the next buffer.
+// 32 in accumulators.  The fragments of the next MFMA step are read while the
+// current one multiplies; the barrier that hands over a stage stands between
+// its two steps, so that the second covers the first reads of the next stage.
 template <int WM, int GW, int GX>
 struct MxTile {
   static constexpr int kWX = 4 / WM;
   static constexpr int kSlots = WM * GW;       // weight groups of a tile
   static constexpr int kTok = kWX * GX * 32;   // tokens of a tile
-  static constexpr int kWBytes = kSlots * kMxFragCodes;
-  static constexpr int kStage = kWBytes + kTok * 128;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kRing = 4;
+  static constexpr int kWBytes = kSlots * 2048;
+  static constexpr int kStage = kWBytes + kTok * 64;
+  static constexpr int kUnits = kSlots + kTok / 32;  // scale dwords: 256 bytes a group of 32 rows
+  static constexpr int kLds = kRing * kStage + 2 * kUnits * 256;
+  // DMA instructions per wave: weights and tokens of a stage, scales of a column group
+  static constexpr int kWDma = kSlots / 2, kXDma = kTok / 64, kSDma = (kUnits + 3) / 4;
 };
+
+// Exchange of the four chunks of LDS row r (64 bytes): distinct for the rows that share a bank
+// group, both over 8 rows (128 bytes a cycle) and over 16.
+__device__ __forceinline__ int mx_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
 template <int MODE, int WM, int GW, int GX>
 __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
@@ -217,63 +232,87 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
     return min(wt * S::kSlots + s, a.G - 1);
   };
 
-  // ---- DMA sources: this wave's weight slots and token rows
-  constexpr int kWSlots = S::kSlots / 4, kXDma = S::kTok / 32;
-  const uint8_t* wsrc[kWSlots];
-#pragma unroll
-  for (int i = 0; i < kWSlots; ++i)
-    wsrc[i] = a.w_codes + ((int64_t)e * a.G + group(w * kWSlots + i)) * a.KK * kMxFragCodes;
   auto act_row = [&](int t) -> int64_t {  // activation row of the tile's token t (rows past the end repeat the last)
     const int64_t pos = first + min(t, cnt - 1);
     return MODE == kGateUp ? a.sorted[pos] / a.k : pos;
   };
-  uint32_t xoff[kXDma];
-#pragma unroll
-  for (int i = 0; i < kXDma; ++i) {
-    const int r = (w * kXDma + i) * 8 + (l >> 3);
-    xoff[i] = (uint32_t)(act_row(r) * (a.KK * 128)) + (uint32_t)(((l & 7) ^ (r & 7)) * 16);
-  }
+
+  // ---- DMA sources: this wave's share of the weight pieces, token rows and scales
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
-  const uint32_t woff = (uint32_t)l * 16u;
-  auto dma = [&](int64_t c) {
-    const uint32_t buf = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(c & 1) * (uint32_t)S::kStage);
+  const uint8_t* wsrc[S::kWDma];
+  uint32_t xoff[S::kXDma];
+  const uint8_t* ssrc[S::kSDma];
+  uint32_t soff[S::kSDma], sstep[S::kSDma];
 #pragma unroll
-    for (int i = 0; i < kWSlots; ++i)
+  for (int i = 0; i < S::kWDma; ++i) {
+    const int piece = w * S::kWDma + i;  // (slot, piece of the stage)
+    wsrc[i] = a.w_codes + ((int64_t)e * a.G + group(piece >> 1)) * a.KK * kMxFragCodes + (piece & 1) * 1024;
+  }
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        dma16_async(wsrc[i] + c * kMxFragCodes + s * 1024, woff, buf + (uint32_t)((w * kWSlots + i) * 4096 + s * 1024));
-    const uint8_t* xc = a.a_codes + c * 128;
+  for (int i = 0; i < S::kXDma; ++i) {
+    const int r = (w * S::kXDma + i) * 16 + (l >> 2), q = (l & 3) ^ mx_swizzle(r);  // q = 2 half + piece
+    xoff[i] = (uint32_t)(act_row(r) * (a.KK * 128)) + (uint32_t)((4 * (q >> 1) + (q & 1)) * 16);
+  }
 #pragma unroll
-    for (int i = 0; i < kXDma; ++i)
-      dma16_async(xc, xoff[i], buf + (uint32_t)(S::kWBytes + (w * kXDma + i) * 1024));
+  for (int i = 0; i < S::kSDma; ++i) {
+    const int u = min(w * S::kSDma + i, S::kUnits - 1);
+    if (u < S::kSlots) {
+      ssrc[i] = a.w_scales + ((int64_t)e * a.G + group(u)) * a.KK * kMxFragScales;
+      soff[i] = (uint32_t)l * 4u;
+      sstep[i] = kMxFragScales;
+    } else {
+      ssrc[i] = a.a_scales;
+      soff[i] = (uint32_t)(act_row((u - S::kSlots) * 32 + n) * (a.KK * 8)) + (uint32_t)f * 4u;
+      sstep[i] = 8;
+    }
+  }
+  // Part `part` of GW parts of a stage's DMA (with the scales of its column group if it is the first half).
+  auto dma = [&](int st, int part) {
+    const int64_t c = st >> 1;
+    const uint32_t buf = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(st & 3) * (uint32_t)S::kStage);
+    if (part == 0 && (st & 1) == 0) {
+      const uint32_t sb = __builtin_amdgcn_readfirstlane(
+          lds0 + (uint32_t)(S::kRing * S::kStage) + ((uint32_t)c & 1u) * (uint32_t)(S::kUnits * 256));
+#pragma unroll
+      for (int i = 0; i < S::kSDma; ++i)
+        dma4_async(ssrc[i] + c * sstep[i], soff[i], sb + (uint32_t)min(w * S::kSDma + i, S::kUnits - 1) * 256u);
+    }
+#pragma unroll
+    for (int i = 0; i < S::kWDma; ++i)
+      if (i * GW / S::kWDma == part)
+        dma16_async(wsrc[i] + c * kMxFragCodes + (st & 1) * 2048, (uint32_t)l * 16u,
+                    buf + (uint32_t)((w * S::kWDma + i) * 1024));
+    const uint8_t* xc = a.a_codes + c * 128 + (st & 1) * 32;
+#pragma unroll
+    for (int i = 0; i < S::kXDma; ++i)
+      if (i * GW / S::kXDma == part)
+        dma16_async(xc, xoff[i], buf + (uint32_t)(S::kWBytes + (w * S::kXDma + i) * 1024));
   };
 
-  // ---- scales: one dword per lane, group and column group, in registers
-  const uint8_t* wsp[GW];
-  const uint8_t* xsp[GX];
-#pragma unroll
-  for (int i = 0; i < GW; ++i)
-    wsp[i] = a.w_scales + ((int64_t)e * a.G + group(wm * GW + i)) * a.KK * kMxFragScales + l * 4;
-#pragma unroll
-  for (int i = 0; i < GX; ++i) xsp[i] = a.a_scales + act_row((wx * GX + i) * 32 + n) * (a.KK * 8) + f * 4;
-  int sw[GW], sx[GX], nsw[GW], nsx[GX];
-  auto load_scales = [&](int64_t c, int* pw, int* px) {
-#pragma unroll
-    for (int i = 0; i < GW; ++i) pw[i] = *reinterpret_cast<const int*>(wsp[i] + c * kMxFragScales);
-#pragma unroll
-    for (int i = 0; i < GX; ++i) px[i] = *reinterpret_cast<const int*>(xsp[i] + c * 8);
+  // ---- fragments and scales from LDS
+  struct Frags {
+    i32x4_t w[GW], x[GX];
   };
-
-  // ---- fragments
-  const int xrow0 = wx * GX * 32 + n;  // rows of the GX groups are 32 apart: the same low three bits
-  auto read = [&](int64_t c, int s, i32x4_t* fw, i32x4_t* fx) {
-    const unsigned char* buf = smem + (c & 1) * S::kStage;
+  struct Scales {
+    int w[GW], x[GX];
+  };
+  const int xlane = (wx * GX * 32 + n) * 64, sw_n = mx_swizzle(n);  // a wave's token groups are 32 rows apart
+  auto read_x = [&](int st, int p, Frags& fr) {
+    const unsigned char* buf = smem + (st & 3) * S::kStage + S::kWBytes + xlane + (((2 * f + p) ^ sw_n) * 16);
 #pragma unroll
-    for (int i = 0; i < GW; ++i)
-      fw[i] = *reinterpret_cast<const i32x4_t*>(buf + (wm * GW + i) * 4096 + s * 1024 + l * 16);
+    for (int i = 0; i < GX; ++i) fr.x[i] = *reinterpret_cast<const i32x4_t*>(buf + i * 2048);
+  };
+  auto read_w = [&](int st, int p, Frags& fr) {
+    const unsigned char* buf = smem + (st & 3) * S::kStage + (wm * GW * 2 + p) * 1024 + l * 16;
 #pragma unroll
-    for (int i = 0; i < GX; ++i)
-      fx[i] = *reinterpret_cast<const i32x4_t*>(buf + S::kWBytes + (xrow0 + 32 * i) * 128 + (((4 * f + s) ^ (n & 7)) * 16));
+    for (int i = 0; i < GW; ++i) fr.w[i] = *reinterpret_cast<const i32x4_t*>(buf + i * 2048);
+  };
+  auto read_scales = [&](int c, Scales& s) {
+    const unsigned char* buf = smem + S::kRing * S::kStage + (c & 1) * (S::kUnits * 256) + l * 4;
+#pragma unroll
+    for (int i = 0; i < GW; ++i) s.w[i] = *reinterpret_cast<const int*>(buf + (wm * GW + i) * 256);
+#pragma unroll
+    for (int i = 0; i < GX; ++i) s.x[i] = *reinterpret_cast<const int*>(buf + (S::kSlots + wx * GX + i) * 256);
   };
 
   float16_t acc[GW][GX];
@@ -287,52 +326,66 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
 #pragma unroll
   for (int j = 0; j < GX; ++j) bh[j] = 0;
 
-#define MX_STEP(SEL, FW, FX, SW, SX)                                                  \
-  _Pragma("unroll") for (int i = 0; i < GW; ++i) _Pragma("unroll") for (int j = 0; j < GX; ++j) \
-      acc[i][j] = mx_mfma<SEL>(FW[i], FX[j], acc[i][j], SW[i], SX[j]);
-
-  i32x4_t fw0[GW], fx0[GX], fw1[GW], fx1[GX];
-  dma(0);
-  load_scales(0, sw, sx);
-  wait_vmcnt<0>();
-  barrier_after_lds();
-  read(0, 0, fw0, fx0);
-  if (a.KK > 1) {
-    load_scales(1, nsw, nsx);
-    dma(1);
-  }
-  for (int64_t c = 0; c < a.KK; ++c) {
+  // One MFMA step on `fr`, reading `nx` = piece np of stage nst under it (the
+  // token fragments with the first row of products, the weights' with the
+  // second) and, with DMA, issuing the DMA of stage dst.  The steps hold no
+  // branches: products have no side effects, and the compiler would move them
+  // past a branch to where their result is used.
+  auto step = [&](auto sel, auto with_dma, const Frags& fr, const Scales& sc, Frags& nx, int nst, int np, int dst) {
+#pragma unroll
+    for (int i = 0; i < GW; ++i) {
+      if (i == 0) read_x(nst, np, nx);
+      if (i == 1) read_w(nst, np, nx);
+      if constexpr (decltype(with_dma)::value != 0) dma(dst, i);
+#pragma unroll
+      for (int j = 0; j < GX; ++j) acc[i][j] = mx_mfma<decltype(sel)::value>(fr.w[i], fr.x[j], acc[i][j], sc.w[i], sc.x[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  Frags f0, f1;
+  Scales sc;
+  // Column group c, issuing the DMA of the stages four ahead (DMA).  Each
+  // hand-over waits until the next stage is in LDS, leaving W1 (W2) later DMA
+  // instructions in flight, and until no wave reads the present one any more.
+  auto group_cols = [&](int c, auto with_dma, auto w1, auto w2) {
+    const int st = 2 * c;
     if (MODE == kDown) {
 #pragma unroll
-      for (int j = 0; j < GX; ++j) bh[j] = max(bh[j], max_byte((uint32_t)sx[j]));
+      for (int j = 0; j < GX; ++j) bh[j] = max(bh[j], max_byte((uint32_t)sc.x[j]));
     }
-    read(c, 1, fw1, fx1);
-    MX_STEP(0, fw0, fx0, sw, sx)
-    read(c, 2, fw0, fx0);
-    MX_STEP(1, fw1, fx1, sw, sx)
-    read(c, 3, fw1, fx1);
-    MX_STEP(2, fw0, fx0, sw, sx)
-    int lw[GW], lx[GX];  // the fourth step's bytes, so that sw and sx can take the next group's
+    step(Const<0>(), Const<0>(), f0, sc, f1, st, 1, 0);
+    wait_vmcnt<decltype(w1)::value>();
+    barrier_after_lds();
+    step(Const<1>(), with_dma, f1, sc, f0, st + 1, 0, st + 4);
+    step(Const<2>(), Const<0>(), f0, sc, f1, st + 1, 1, 0);
+    Scales last;  // the fourth step's bytes
 #pragma unroll
-    for (int i = 0; i < GW; ++i) lw[i] = (int)((uint32_t)sw[i] >> 24);
+    for (int i = 0; i < GW; ++i) last.w[i] = (int)((uint32_t)sc.w[i] >> 24);
 #pragma unroll
-    for (int j = 0; j < GX; ++j) lx[j] = (int)((uint32_t)sx[j] >> 24);
-    if (c + 1 < a.KK) {
-      wait_vmcnt<0>();
-      barrier_after_lds();
-      read(c + 1, 0, fw0, fx0);
+    for (int j = 0; j < GX; ++j) last.x[j] = (int)((uint32_t)sc.x[j] >> 24);
+    wait_vmcnt<decltype(w2)::value>();
+    barrier_after_lds();
+    // past the last group these read buffers that are not used
+    read_scales(c + 1, sc);
+    step(Const<0>(), with_dma, f1, last, f0, st + 2, 0, st + 5);
+  };
+  constexpr int kHalf = S::kWDma + S::kXDma, kTwo = 2 * kHalf + S::kSDma;  // DMA of an odd stage; of two stages
+  const int KK = (int)a.KK;
 #pragma unroll
-      for (int i = 0; i < GW; ++i) sw[i] = nsw[i];
+  for (int st = 0; st < 4; ++st)
+    if (st < 2 * KK) {
 #pragma unroll
-      for (int j = 0; j < GX; ++j) sx[j] = nsx[j];
-      if (c + 2 < a.KK) {
-        load_scales(c + 2, nsw, nsx);
-        dma(c + 2);
-      }
+      for (int p = 0; p < GW; ++p) dma(st, p);
     }
-    MX_STEP(0, fw1, fx1, lw, lx)
-  }
-#undef MX_STEP
+  if (KK > 1) wait_vmcnt<kTwo + kHalf>();  // all but the first stage
+  else wait_vmcnt<0>();
+  barrier_after_lds();
+  read_scales(0, sc);
+  read_x(0, 0, f0);
+  read_w(0, 0, f0);
+  for (int c = 0; c + 2 < KK; ++c) group_cols(c, Const<1>(), Const<kTwo>(), Const<kTwo>());
+  if (KK > 1) group_cols(KK - 2, Const<0>(), Const<kTwo>(), Const<kHalf>());
+  group_cols(KK - 1, Const<0>(), Const<0>(), Const<0>());
 
   // ---- epilogue: a lane holds 16 consecutive features (half f of a group) of token n
 #pragma unroll
