@@ -175,12 +175,12 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 // 32 in accumulators.  The fragments of the next MFMA step are read while the
 // current one multiplies; the barrier that hands over a stage stands between
 // its two steps, so that the second covers the first reads of the next stage.
-template <int WM, int GW, int GX>
+template <int WM, int GW, int GX, int RING>
 struct MxTile {
   static constexpr int kWX = 4 / WM;
   static constexpr int kSlots = WM * GW;       // weight groups of a tile
   static constexpr int kTok = kWX * GX * 32;   // tokens of a tile
-  static constexpr int kRing = 4;
+  static constexpr int kRing = RING;
   static constexpr int kWBytes = kSlots * 2048;
   static constexpr int kStage = kWBytes + kTok * 64;
   static constexpr int kUnits = kSlots + kTok / 32;  // scale dwords: 256 bytes a group of 32 rows
@@ -193,9 +193,9 @@ struct MxTile {
 // group, both over 8 rows (128 bytes a cycle) and over 16.
 __device__ __forceinline__ int mx_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
-template <int MODE, int WM, int GW, int GX>
-__global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
-  using S = MxTile<WM, GW, GX>;
+template <int MODE, int WM, int GW, int GX, int RING, int WGS>
+__global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
+  using S = MxTile<WM, GW, GX, RING>;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, n = l & 31, f = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -266,10 +266,10 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
       sstep[i] = 8;
     }
   }
-  // Part `part` of GW parts of a stage's DMA (with the scales of its column group if it is the first half).
+  // Part `part` of 2 GW parts of a stage's DMA (the first with the scales of its column group if it is the first half).
   auto dma = [&](int st, int part) {
     const int64_t c = st >> 1;
-    const uint32_t buf = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(st & 3) * (uint32_t)S::kStage);
+    const uint32_t buf = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(st % RING) * (uint32_t)S::kStage);
     if (part == 0 && (st & 1) == 0) {
       const uint32_t sb = __builtin_amdgcn_readfirstlane(
           lds0 + (uint32_t)(S::kRing * S::kStage) + ((uint32_t)c & 1u) * (uint32_t)(S::kUnits * 256));
@@ -277,15 +277,16 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
       for (int i = 0; i < S::kSDma; ++i)
         dma4_async(ssrc[i] + c * sstep[i], soff[i], sb + (uint32_t)min(w * S::kSDma + i, S::kUnits - 1) * 256u);
     }
+    constexpr int kAll = S::kWDma + S::kXDma;
 #pragma unroll
     for (int i = 0; i < S::kWDma; ++i)
-      if (i * GW / S::kWDma == part)
+      if (i * 2 * GW / kAll == part)
         dma16_async(wsrc[i] + c * kMxFragCodes + (st & 1) * 2048, (uint32_t)l * 16u,
                     buf + (uint32_t)((w * S::kWDma + i) * 1024));
     const uint8_t* xc = a.a_codes + c * 128 + (st & 1) * 32;
 #pragma unroll
     for (int i = 0; i < S::kXDma; ++i)
-      if (i * GW / S::kXDma == part)
+      if ((S::kWDma + i) * 2 * GW / kAll == part)
         dma16_async(xc, xoff[i], buf + (uint32_t)(S::kWBytes + (w * S::kXDma + i) * 1024));
   };
 
@@ -298,12 +299,12 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
   };
   const int xlane = (wx * GX * 32 + n) * 64, sw_n = mx_swizzle(n);  // a wave's token groups are 32 rows apart
   auto read_x = [&](int st, int p, Frags& fr) {
-    const unsigned char* buf = smem + (st & 3) * S::kStage + S::kWBytes + xlane + (((2 * f + p) ^ sw_n) * 16);
+    const unsigned char* buf = smem + (st % RING) * S::kStage + S::kWBytes + xlane + (((2 * f + p) ^ sw_n) * 16);
 #pragma unroll
     for (int i = 0; i < GX; ++i) fr.x[i] = *reinterpret_cast<const i32x4_t*>(buf + i * 2048);
   };
   auto read_w = [&](int st, int p, Frags& fr) {
-    const unsigned char* buf = smem + (st & 3) * S::kStage + (wm * GW * 2 + p) * 1024 + l * 16;
+    const unsigned char* buf = smem + (st % RING) * S::kStage + (wm * GW * 2 + p) * 1024 + l * 16;
 #pragma unroll
     for (int i = 0; i < GW; ++i) fr.w[i] = *reinterpret_cast<const i32x4_t*>(buf + i * 2048);
   };
@@ -328,15 +329,18 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
 
   // One MFMA step on `fr`, reading `nx` = piece np of stage nst under it (the
   // token fragments with the first row of products, the weights' with the
-  // second) and, with DMA, issuing the DMA of stage dst.  The steps hold no
-  // branches: products have no side effects, and the compiler would move them
-  // past a branch to where their result is used.
-  auto step = [&](auto sel, auto with_dma, const Frags& fr, const Scales& sc, Frags& nx, int nst, int np, int dst) {
+  // second) and issuing half `half` (0, 1; 2 = none) of the DMA of stage dst,
+  // one instruction or so a row: the memory pipe takes a 1 KB DMA in no less
+  // than 16 cycles, and waves that issue theirs in a burst wait for each other.
+  // The steps hold no branches: products have no side effects, and the compiler
+  // would move them past a branch to where their result is used.
+  auto step = [&](auto sel, auto half, const Frags& fr, const Scales& sc, Frags& nx, int nst, int np, int dst) {
+    constexpr int kHalf = decltype(half)::value;
 #pragma unroll
     for (int i = 0; i < GW; ++i) {
       if (i == 0) read_x(nst, np, nx);
       if (i == 1) read_w(nst, np, nx);
-      if constexpr (decltype(with_dma)::value != 0) dma(dst, i);
+      if constexpr (kHalf < 2) dma(dst, kHalf * GW + i);
 #pragma unroll
       for (int j = 0; j < GX; ++j) acc[i][j] = mx_mfma<decltype(sel)::value>(fr.w[i], fr.x[j], acc[i][j], sc.w[i], sc.x[j]);
       __builtin_amdgcn_sched_barrier(0);
@@ -344,20 +348,24 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
   };
   Frags f0, f1;
   Scales sc;
-  // Column group c, issuing the DMA of the stages four ahead (DMA).  Each
-  // hand-over waits until the next stage is in LDS, leaving W1 (W2) later DMA
-  // instructions in flight, and until no wave reads the present one any more.
-  auto group_cols = [&](int c, auto with_dma, auto w1, auto w2) {
+  // Column group c.  The DMA of the stage RING ahead of one is issued in two
+  // halves, in the two steps after its hand-over; D0, D1 and D2 say whether
+  // there is such a stage for the hand-overs before, inside and at the end of
+  // this group.  A hand-over waits until the next stage is in LDS, leaving W1
+  // (W2) later DMA instructions in flight, and until no wave reads the present
+  // one any more.
+  auto group_cols = [&](int c, auto d0, auto d1, auto d2, auto w1, auto w2) {
+    constexpr int kD0 = decltype(d0)::value, kD1 = decltype(d1)::value, kD2 = decltype(d2)::value;
     const int st = 2 * c;
     if (MODE == kDown) {
 #pragma unroll
       for (int j = 0; j < GX; ++j) bh[j] = max(bh[j], max_byte((uint32_t)sc.x[j]));
     }
-    step(Const<0>(), Const<0>(), f0, sc, f1, st, 1, 0);
+    step(Const<0>(), Const<(kD0 ? 1 : 2)>(), f0, sc, f1, st, 1, st - 1 + RING);
     wait_vmcnt<decltype(w1)::value>();
     barrier_after_lds();
-    step(Const<1>(), with_dma, f1, sc, f0, st + 1, 0, st + 4);
-    step(Const<2>(), Const<0>(), f0, sc, f1, st + 1, 1, 0);
+    step(Const<1>(), Const<(kD1 ? 0 : 2)>(), f1, sc, f0, st + 1, 0, st + RING);
+    step(Const<2>(), Const<(kD1 ? 1 : 2)>(), f0, sc, f1, st + 1, 1, st + RING);
     Scales last;  // the fourth step's bytes
 #pragma unroll
     for (int i = 0; i < GW; ++i) last.w[i] = (int)((uint32_t)sc.w[i] >> 24);
@@ -367,25 +375,33 @@ __global__ __launch_bounds__(256, 1) void mx_tiled_kernel(MxArgs a) {
     barrier_after_lds();
     // past the last group these read buffers that are not used
     read_scales(c + 1, sc);
-    step(Const<0>(), with_dma, f1, last, f0, st + 2, 0, st + 5);
+    step(Const<0>(), Const<(kD2 ? 0 : 2)>(), f1, last, f0, st + 2, 0, st + 1 + RING);
   };
-  constexpr int kHalf = S::kWDma + S::kXDma, kTwo = 2 * kHalf + S::kSDma;  // DMA of an odd stage; of two stages
+  // DMA instructions of an odd stage, an even one (with scales), both
+  constexpr int kOdd = S::kWDma + S::kXDma, kEven = kOdd + S::kSDma, kTwo = kOdd + kEven;
   const int KK = (int)a.KK;
+  using No = Const<0>;
+  using Yes = Const<1>;
 #pragma unroll
-  for (int st = 0; st < 4; ++st)
+  for (int st = 0; st < RING; ++st)
     if (st < 2 * KK) {
 #pragma unroll
-      for (int p = 0; p < GW; ++p) dma(st, p);
+      for (int p = 0; p < (st == RING - 1 ? GW : 2 * GW); ++p) dma(st, p);  // the last one's second half: first step
     }
-  if (KK > 1) wait_vmcnt<kTwo + kHalf>();  // all but the first stage
+  if (KK > 1) wait_vmcnt<RING == 4 ? kTwo : kOdd>();  // at least the first stage
   else wait_vmcnt<0>();
   barrier_after_lds();
   read_scales(0, sc);
   read_x(0, 0, f0);
   read_w(0, 0, f0);
-  for (int c = 0; c + 2 < KK; ++c) group_cols(c, Const<1>(), Const<kTwo>(), Const<kTwo>());
-  if (KK > 1) group_cols(KK - 2, Const<0>(), Const<kTwo>(), Const<kHalf>());
-  group_cols(KK - 1, Const<0>(), Const<0>(), Const<0>());
+  if constexpr (RING == 4) {
+    for (int c = 0; c + 2 < KK; ++c) group_cols(c, Yes(), Yes(), Yes(), Const<kTwo>(), Const<kTwo>());
+    if (KK > 1) group_cols(KK - 2, Yes(), No(), No(), Const<kTwo>(), Const<kOdd>());
+  } else {
+    for (int c = 0; c + 2 < KK; ++c) group_cols(c, Yes(), Yes(), Yes(), Const<kEven>(), Const<kOdd>());
+    if (KK > 1) group_cols(KK - 2, Yes(), Yes(), No(), Const<kEven>(), Const<kOdd>());
+  }
+  group_cols(KK - 1, No(), No(), No(), Const<0>(), Const<0>());
 
   // ---- epilogue: a lane holds 16 consecutive features (half f of a group) of token n
 #pragma unroll
@@ -514,14 +530,18 @@ __global__ __launch_bounds__(256) void mx_zero_pad_kernel(uint8_t* codes, uint8_
 
 namespace {
 
-using MxBig = MxTile<2, 4, 4>;  // 256 weight rows by 256 tokens
+#ifndef CFG
+#define CFG 2, 4, 2, 3
+#define CFGW 2
+#endif
+using MxBig = MxTile<CFG>;  // 256 weight rows by 128 tokens, two workgroups a CU
 
 // Tokens (linear) or mean pairs per expert from which the tiled kernel is used.
 constexpr int64_t kTiledFrom = 64;
 
 template <int MODE>
 hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
-  auto* k = &mx_tiled_kernel<MODE, 2, 4, 4>;
+  auto* k = &mx_tiled_kernel<MODE, CFG, CFGW>;
   if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), MxBig::kLds)) return e;
   const int64_t grid = (max_mtiles * a.n_wtiles + 7) / 8 * 8;
   hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), MxBig::kLds, st, a);
