@@ -453,8 +453,9 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
  * as mxfp4_quantize_weights writes it.  pair_out [T*k, H] FP16 and pair_scale
  * [T*k] are pair rows in the form of the header comment (moe_combine,
  * moe_combine_block read them), with E = floor(log2 |w_p|) + 1 +
- * ceil(log2(36 I)) + bh + bw - 269 clamped to [-126, 113], bh the largest scale
- * byte of the pair's h and bw = w2_max_scale[e]: |w_p f| < 2^(E + 15).
+ * ceil(log2(36 I)) + bh + bw - 269 clamped to [max(0, floor(log2 |w_p|)) - 126,
+ * 113], bh the largest scale byte of the pair's h and bw = w2_max_scale[e]:
+ * |w_p f| < 2^(E + 15).
  * H % 32 == 0, I % 32 == 0, 1 <= k <= E <= 256, T * k < 2^31; x codes
  * (T*Hp/2 bytes) and h codes (T*k*Ip/2 bytes) under 4 GiB.  Code arrays and
  * pair_out 16-byte, scale arrays, pair_scale and w2_max_scale 4-byte aligned;

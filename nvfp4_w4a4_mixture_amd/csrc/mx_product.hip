@@ -18,11 +18,22 @@ enum { kLinear = 0, kGateUp = 1, kDown = 2 };
 // operand.  |f| <= I * 6^2 * 2^(bh - 127) * 2^(bw - 127) for the largest scale
 // byte bh of the h row and bw of the expert's down weights, 36 I <= 2^lg, and
 // |w_p| < 2^(ew + 1).  FP16's normal range reaches 29 binades below 2^15, so a
-// loose bound costs no precision.  Clamped so that 2^E and 2^-E are normal.
+// loose bound costs no precision.  Clamped so that 2^E, 2^-E and w_p 2^-E are
+// normal or zero (a row of zeros has a bound far below its weight).
 __device__ __forceinline__ int pair_exponent(float wp, uint32_t bh, int bw, int lg) {
   const int ew = (int)((__float_as_uint(wp) >> 23) & 255u) - 127;
   const int e = ew + 1 + lg + (int)bh + bw - 254 - 15;
-  return min(max(e, -126), 113);
+  return min(max(e, max(ew, 0) - 126), 113);
+}
+
+// Two values rounded to nearest even in 16 bits, the first in the low half
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
 __device__ __forceinline__ uint32_t max_byte(uint32_t d) {
@@ -127,16 +138,16 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
         reinterpret_cast<uint16_t*>(a.h_codes + row * a.ldh)[blk * 8 + p] = (uint16_t)mx_encode8(h, byte);
         if (p == 0) a.h_scales[row * (a.ldh / 16) + blk] = (uint8_t)byte;
       } else {
-        float wp = 1.0f, inv = 1.0f;
+        float factor = 1.0f;
         int64_t out = row;
         if constexpr (MODE == kDown) {
           out = a.sorted[row];
-          wp = a.topk_w[out];
+          const float wp = a.topk_w[out];
           uint32_t b = hmax[0][tok];
 #pragma unroll
           for (int q = 1; q < NW; ++q) b = max(b, hmax[q][tok]);
           const int E = pair_exponent(wp, b, a.w_max[e], a.lg36I);
-          inv = __uint_as_float((uint32_t)(127 - E) << 23);
+          factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
           if (blockIdx.x == 0 && p == 0) a.pair_scale[out] = __uint_as_float((uint32_t)(127 + E) << 23);
         }
 #pragma unroll
@@ -148,7 +159,7 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
             const int64_t col = gi * 32 + 4 * p + j;
             if (col >= a.N) continue;
             if constexpr (MODE == kDown)
-              reinterpret_cast<_Float16*>(a.out)[out * a.ldo + col] = (_Float16)((wp * v[i][j]) * inv);
+              reinterpret_cast<_Float16*>(a.out)[out * a.ldo + col] = (_Float16)(factor * v[i][j]);
             else if (a.out_f32)
               static_cast<float*>(a.out)[out * a.ldo + col] = v[i][j];
             else
@@ -185,6 +196,9 @@ struct MxTile {
   static constexpr int kStage = kWBytes + kTok * 64;
   static constexpr int kUnits = kSlots + kTok / 32;  // scale dwords: 256 bytes a group of 32 rows
   static constexpr int kLds = kRing * kStage + 2 * kUnits * 256;
+  // epilogue: a row of 16-bit results in LDS, offset by 16 bytes against bank conflicts; then the output rows
+  static constexpr int kOutRow = kSlots * 64 + 16;
+  static_assert(kTok * (kOutRow + 4) <= kLds, "the epilogue's tile fits the ring");
   // DMA instructions per wave: weights and tokens of a stage, scales of a column group
   static constexpr int kWDma = kSlots / 2, kXDma = kTok / 64, kSDma = (kUnits + 3) / 4;
 };
@@ -403,6 +417,7 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
   }
   group_cols(KK - 1, No(), No(), No(), Const<0>(), Const<0>());
 
+  int* out_row = reinterpret_cast<int*>(smem + S::kTok * S::kOutRow);
   // ---- epilogue: a lane holds 16 consecutive features (half f of a group) of token n
 #pragma unroll
   for (int j = 0; j < GX; ++j) {
@@ -428,65 +443,68 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
           if (f == 0) a.h_scales[row * (a.ldh / 16) + hb] = (uint8_t)byte;
         }
       }
-    } else {
-      float wp = 1.0f, inv = 1.0f;
-      int64_t out = row;
-      if constexpr (MODE == kDown) {
-        const uint32_t b = max(bh[j], (uint32_t)__shfl_xor((int)bh[j], 32));
-        if (in) {
-          out = a.sorted[row];
-          wp = a.topk_w[out];
-          const int E = pair_exponent(wp, b, a.w_max[e], a.lg36I);
-          inv = __uint_as_float((uint32_t)(127 - E) << 23);
-          if (wt == 0 && wm == 0 && f == 0) a.pair_scale[out] = __uint_as_float((uint32_t)(127 + E) << 23);
-        }
-      }
+    } else if (MODE == kLinear && a.out_f32) {
       if (!in) continue;
 #pragma unroll
       for (int i = 0; i < GW; ++i) {
-        const int64_t g = wt * S::kSlots + wm * GW + i;
-        if (g >= a.G) continue;
-        const int64_t col = g * 32 + f * 16;
-        if constexpr (MODE == kDown) {
-          half8_t v[2];
+        const int64_t col = (wt * S::kSlots + wm * GW + i) * 32 + f * 16;
+        float* p = static_cast<float*>(a.out) + row * a.ldo + col;
+        if (a.out_vec && col + 16 <= a.N) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r >> 3][r & 7] = (_Float16)((wp * acc[i][j][r]) * inv);
-          half8_t* p = reinterpret_cast<half8_t*>(static_cast<_Float16*>(a.out) + out * a.ldo + col);
-          p[0] = v[0];
-          p[1] = v[1];
+          for (int r = 0; r < 4; ++r)
+            reinterpret_cast<float4*>(p)[r] =
+                make_float4(acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]);
         } else {
-          const bool whole = a.out_vec && col + 16 <= a.N;
-          if (a.out_f32) {
-            float* p = static_cast<float*>(a.out) + out * a.ldo + col;
-            if (whole) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                reinterpret_cast<float4*>(p)[r] =
-                    make_float4(acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]);
-            } else {
-#pragma unroll
-              for (int r = 0; r < 16; ++r)
-                if (col + r < a.N) p[r] = acc[i][j][r];
-            }
-          } else {
-            uint16_t* p = static_cast<uint16_t*>(a.out) + out * a.ldo + col;
-            uint32_t b[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) b[r] = bf16_bits_rne(acc[i][j][r]);
-            if (whole) {
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-                reinterpret_cast<uint4*>(p)[r] =
-                    make_uint4(b[8 * r] | (b[8 * r + 1] << 16), b[8 * r + 2] | (b[8 * r + 3] << 16),
-                               b[8 * r + 4] | (b[8 * r + 5] << 16), b[8 * r + 6] | (b[8 * r + 7] << 16));
-            } else {
-#pragma unroll
-              for (int r = 0; r < 16; ++r)
-                if (col + r < a.N) p[r] = (uint16_t)b[r];
-            }
+          for (int r = 0; r < 16; ++r)
+            if (col + r < a.N) p[r] = acc[i][j][r];
+        }
+      }
+    } else {
+      // 16-bit results go through LDS (the ring is no longer needed), so that
+      // every row leaves as one run of kSlots * 64 bytes
+      float factor = 1.0f;
+      if constexpr (MODE == kDown) {
+        const uint32_t b = max(bh[j], (uint32_t)__shfl_xor((int)bh[j], 32));
+        if (in) {
+          const int out = a.sorted[row];
+          const float wp = a.topk_w[out];
+          const int E = pair_exponent(wp, b, a.w_max[e], a.lg36I);
+          factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
+          if (wm == 0 && f == 0) {
+            out_row[tok] = out;
+            if (wt == 0) a.pair_scale[out] = __uint_as_float((uint32_t)(127 + E) << 23);
           }
         }
       }
+#pragma unroll
+      for (int i = 0; i < GW; ++i) {
+        uint32_t v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          v[r] = MODE == kDown ? f16_pair(factor * acc[i][j][2 * r], factor * acc[i][j][2 * r + 1])
+                               : bf16_pair(acc[i][j][2 * r], acc[i][j][2 * r + 1]);
+        uint4* p = reinterpret_cast<uint4*>(smem + tok * S::kOutRow + (wm * GW + i) * 64 + f * 32);
+        p[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        p[1] = make_uint4(v[4], v[5], v[6], v[7]);
+      }
+    }
+  }
+  if (MODE == kGateUp || (MODE == kLinear && a.out_f32)) return;
+  barrier_after_lds();
+  constexpr int kLanes = S::kSlots * 4, kRows = 64 / kLanes;  // lanes that write a row, rows a wave writes at a time
+  const int64_t col = wt * S::kSlots * 32 + (l % kLanes) * 8;
+  if (col >= a.N) return;
+  for (int t = w * kRows + l / kLanes; t < cnt; t += 4 * kRows) {
+    const uint4 v = *reinterpret_cast<const uint4*>(smem + t * S::kOutRow + (l % kLanes) * 16);
+    uint16_t* p = static_cast<uint16_t*>(a.out) + (MODE == kDown ? (int64_t)out_row[t] : first + t) * a.ldo + col;
+    if (MODE == kDown || (a.out_vec && col + 8 <= a.N)) {
+      *reinterpret_cast<uint4*>(p) = v;
+    } else {
+      const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (col + r < a.N) p[r] = (uint16_t)(d[r >> 1] >> (16 * (r & 1)));
     }
   }
 }

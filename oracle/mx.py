@@ -127,4 +127,5 @@ def pair_exponent(w: np.ndarray, h_byte: np.ndarray, w2_byte: np.ndarray, I: int
     """Exponent E of a pair row's scale 2**E (the header's rule); h_byte the row's largest, w2_byte the expert's."""
     _, e = np.frexp(np.asarray(w, np.float32))
     lg = int(np.ceil(np.log2(36 * I)))
-    return np.clip((e - 1) + 1 + lg + h_byte.astype(np.int64) + w2_byte.astype(np.int64) - 269, -126, 113)
+    low = np.maximum(e - 1, 0) - 126  # w 2**-E stays finite
+    return np.minimum(np.maximum((e - 1) + 1 + lg + h_byte.astype(np.int64) + w2_byte.astype(np.int64) - 269, low), 113)
