@@ -312,15 +312,13 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
     int w[GW], x[GX];
   };
   const int xlane = (wx * GX * 32 + n) * 64, sw_n = mx_swizzle(n);  // a wave's token groups are 32 rows apart
-  auto read_x = [&](int st, int p, Frags& fr) {
-    const unsigned char* buf = smem + (st % RING) * S::kStage + S::kWBytes + xlane + (((2 * f + p) ^ sw_n) * 16);
-#pragma unroll
-    for (int i = 0; i < GX; ++i) fr.x[i] = *reinterpret_cast<const i32x4_t*>(buf + i * 2048);
-  };
-  auto read_w = [&](int st, int p, Frags& fr) {
-    const unsigned char* buf = smem + (st % RING) * S::kStage + (wm * GW * 2 + p) * 1024 + l * 16;
-#pragma unroll
-    for (int i = 0; i < GW; ++i) fr.w[i] = *reinterpret_cast<const i32x4_t*>(buf + i * 2048);
+  // Fragment r of piece p of stage st: the GX token fragments, then the GW weight fragments.
+  auto read = [&](int st, int p, int r, Frags& fr) {
+    const unsigned char* buf = smem + (st % RING) * S::kStage;
+    if (r < GX)
+      fr.x[r] = *reinterpret_cast<const i32x4_t*>(buf + S::kWBytes + xlane + (((2 * f + p) ^ sw_n) * 16) + r * 2048);
+    else
+      fr.w[r - GX] = *reinterpret_cast<const i32x4_t*>(buf + (wm * GW * 2 + p) * 1024 + l * 16 + (r - GX) * 2048);
   };
   auto read_scales = [&](int c, Scales& s) {
     const unsigned char* buf = smem + S::kRing * S::kStage + (c & 1) * (S::kUnits * 256) + l * 4;
@@ -341,23 +339,29 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
 #pragma unroll
   for (int j = 0; j < GX; ++j) bh[j] = 0;
 
-  // One MFMA step on `fr`, reading `nx` = piece np of stage nst under it (the
-  // token fragments with the first row of products, the weights' with the
-  // second) and issuing half `half` (0, 1; 2 = none) of the DMA of stage dst,
-  // one instruction or so a row: the memory pipe takes a 1 KB DMA in no less
-  // than 16 cycles, and waves that issue theirs in a burst wait for each other.
-  // The steps hold no branches: products have no side effects, and the compiler
-  // would move them past a branch to where their result is used.
+  // One MFMA step on `fr`, reading `nx` = piece np of stage nst under it and
+  // issuing half `half` (0, 1; 2 = none) of the DMA of stage dst.  Reads and DMA
+  // are dealt out between the products, which leave the issue slots free: the
+  // LDS takes 8 cycles for a fragment of one wave and the memory pipe 16 for a
+  // 1 KB DMA, so that waves that issue theirs in a burst wait for each other
+  // with the matrix cores idle.  The last quarter of a step has no reads: a
+  // barrier may follow, and waits for them.  The steps hold no branches:
+  // products have no side effects, and the compiler would move them past a
+  // branch to where their result is used.
   auto step = [&](auto sel, auto half, const Frags& fr, const Scales& sc, Frags& nx, int nst, int np, int dst) {
-    constexpr int kHalf = decltype(half)::value;
+    constexpr int kHalf = decltype(half)::value, kReads = GW + GX, kSpan = 3 * GW * GX / 4;
 #pragma unroll
     for (int i = 0; i < GW; ++i) {
-      if (i == 0) read_x(nst, np, nx);
-      if (i == 1) read_w(nst, np, nx);
-      if constexpr (kHalf < 2) dma(dst, kHalf * GW + i);
 #pragma unroll
-      for (int j = 0; j < GX; ++j) acc[i][j] = mx_mfma<decltype(sel)::value>(fr.w[i], fr.x[j], acc[i][j], sc.w[i], sc.x[j]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < GX; ++j) {
+        acc[i][j] = mx_mfma<decltype(sel)::value>(fr.w[i], fr.x[j], acc[i][j], sc.w[i], sc.x[j]);
+#pragma unroll
+        for (int k = 0; k < kReads; ++k)
+          if (k * kSpan / kReads == i * GX + j) read(nst, np, k, nx);
+        if constexpr (kHalf < 2)
+          if (j == GX / 2) dma(dst, kHalf * GW + i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
   Frags f0, f1;
@@ -406,8 +410,8 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
   else wait_vmcnt<0>();
   barrier_after_lds();
   read_scales(0, sc);
-  read_x(0, 0, f0);
-  read_w(0, 0, f0);
+#pragma unroll
+  for (int k = 0; k < GW + GX; ++k) read(0, 0, k, f0);
   if constexpr (RING == 4) {
     for (int c = 0; c + 2 < KK; ++c) group_cols(c, Yes(), Yes(), Yes(), Const<kTwo>(), Const<kTwo>());
     if (KK > 1) group_cols(KK - 2, Yes(), No(), No(), Const<kTwo>(), Const<kOdd>());
