@@ -186,11 +186,12 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 // 32 in accumulators.  The fragments of the next MFMA step are read while the
 // current one multiplies; the barrier that hands over a stage stands between
 // its two steps, so that the second covers the first reads of the next stage.
-template <int WM, int GW, int GX, int RING>
+template <int NW, int WM, int GW, int GX, int RING>
 struct MxTile {
-  static constexpr int kWX = 4 / WM;
+  static constexpr int kWX = NW / WM;
   static constexpr int kSlots = WM * GW;       // weight groups of a tile
   static constexpr int kTok = kWX * GX * 32;   // tokens of a tile
+  static constexpr int kWaves = NW;
   static constexpr int kRing = RING;
   static constexpr int kWBytes = kSlots * 2048;
   static constexpr int kStage = kWBytes + kTok * 64;
@@ -200,16 +201,16 @@ struct MxTile {
   static constexpr int kOutRow = kSlots * 64 + 16;
   static_assert(kTok * (kOutRow + 4) <= kLds, "the epilogue's tile fits the ring");
   // DMA instructions per wave: weights and tokens of a stage, scales of a column group
-  static constexpr int kWDma = kSlots / 2, kXDma = kTok / 64, kSDma = (kUnits + 3) / 4;
+  static constexpr int kWDma = 2 * kSlots / NW, kXDma = kTok / 16 / NW, kSDma = (kUnits + NW - 1) / NW;
 };
 
 // Exchange of the four chunks of LDS row r (64 bytes): distinct for the rows that share a bank
 // group, both over 8 rows (128 bytes a cycle) and over 16.
 __device__ __forceinline__ int mx_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
-template <int MODE, int WM, int GW, int GX, int RING, int WGS>
-__global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
-  using S = MxTile<WM, GW, GX, RING>;
+template <int MODE, int NW, int WM, int GW, int GX, int RING, int WGS>
+__global__ __launch_bounds__(NW * 64, WGS) void mx_tiled_kernel(MxArgs a) {
+  using S = MxTile<NW, WM, GW, GX, RING>;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, n = l & 31, f = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -347,9 +348,17 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
   // with the matrix cores idle.  The last quarter of a step has no reads: a
   // barrier may follow, and waits for them.  The steps hold no branches:
   // products have no side effects, and the compiler would move them past a
-  // branch to where their result is used.
-  auto step = [&](auto sel, auto half, const Frags& fr, const Scales& sc, Frags& nx, int nst, int np, int dst) {
+  // branch to where their result is used.  A wave whose tokens are all past the
+  // end (live = 0) only does its share of the DMA: its SIMD is the other wave's.
+  auto step = [&](auto live, auto sel, auto half, const Frags& fr, const Scales& sc, Frags& nx, int nst, int np, int dst) {
     constexpr int kHalf = decltype(half)::value, kReads = GW + GX, kSpan = 3 * GW * GX / 4;
+    if constexpr (decltype(live)::value == 0) {
+      if constexpr (kHalf < 2) {
+#pragma unroll
+        for (int i = 0; i < GW; ++i) dma(dst, kHalf * GW + i);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < GW; ++i) {
 #pragma unroll
@@ -366,60 +375,71 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
   };
   Frags f0, f1;
   Scales sc;
-  // Column group c.  The DMA of the stage RING ahead of one is issued in two
-  // halves, in the two steps after its hand-over; D0, D1 and D2 say whether
-  // there is such a stage for the hand-overs before, inside and at the end of
-  // this group.  A hand-over waits until the next stage is in LDS, leaving W1
-  // (W2) later DMA instructions in flight, and until no wave reads the present
-  // one any more.
-  auto group_cols = [&](int c, auto d0, auto d1, auto d2, auto w1, auto w2) {
-    constexpr int kD0 = decltype(d0)::value, kD1 = decltype(d1)::value, kD2 = decltype(d2)::value;
+  // DMA instructions of a stage; an even one has kSDma more, its column group's scales
+  constexpr int kPlain = S::kWDma + S::kXDma;
+  // Column group c; t of the groups after it count, later ones are as many as
+  // it takes (t >= (RING + 1) / 2).  The DMA of the stage RING ahead of one is
+  // issued in two halves, in the two steps after its hand-over: here those of
+  // the hand-overs before, inside and at the end of this group, as far as there
+  // are such stages.  A hand-over waits until the next stage is in LDS, leaving
+  // the later ones (up to RING - 2) in flight, and until no wave reads the
+  // present one any more.
+  auto group_cols = [&](auto live, int c, auto after) {
+    constexpr int t = decltype(after)::value;
+    constexpr bool kD0 = 2 * t + 2 >= RING, kD1 = 2 * t + 1 >= RING, kD2 = 2 * t >= RING;
+    constexpr int n1 = 2 * t < RING - 2 ? 2 * t : RING - 2, w1 = n1 * kPlain + (n1 + 1) / 2 * S::kSDma;
+    constexpr int m2 = t > 0 ? 2 * t - 1 : 0, n2 = m2 < RING - 2 ? m2 : RING - 2, w2 = n2 * kPlain + n2 / 2 * S::kSDma;
     const int st = 2 * c;
     if (MODE == kDown) {
 #pragma unroll
       for (int j = 0; j < GX; ++j) bh[j] = max(bh[j], max_byte((uint32_t)sc.x[j]));
     }
-    step(Const<0>(), Const<(kD0 ? 1 : 2)>(), f0, sc, f1, st, 1, st - 1 + RING);
-    wait_vmcnt<decltype(w1)::value>();
+    step(live, Const<0>(), Const<(kD0 ? 1 : 2)>(), f0, sc, f1, st, 1, st - 1 + RING);
+    wait_vmcnt<w1>();
     barrier_after_lds();
-    step(Const<1>(), Const<(kD1 ? 0 : 2)>(), f1, sc, f0, st + 1, 0, st + RING);
-    step(Const<2>(), Const<(kD1 ? 1 : 2)>(), f0, sc, f1, st + 1, 1, st + RING);
+    step(live, Const<1>(), Const<(kD1 ? 0 : 2)>(), f1, sc, f0, st + 1, 0, st + RING);
+    step(live, Const<2>(), Const<(kD1 ? 1 : 2)>(), f0, sc, f1, st + 1, 1, st + RING);
     Scales last;  // the fourth step's bytes
 #pragma unroll
     for (int i = 0; i < GW; ++i) last.w[i] = (int)((uint32_t)sc.w[i] >> 24);
 #pragma unroll
     for (int j = 0; j < GX; ++j) last.x[j] = (int)((uint32_t)sc.x[j] >> 24);
-    wait_vmcnt<decltype(w2)::value>();
+    wait_vmcnt<w2>();
     barrier_after_lds();
     // past the last group these read buffers that are not used
-    read_scales(c + 1, sc);
-    step(Const<0>(), Const<(kD2 ? 0 : 2)>(), f1, last, f0, st + 2, 0, st + 1 + RING);
+    if constexpr (decltype(live)::value != 0) read_scales(c + 1, sc);
+    step(live, Const<0>(), Const<(kD2 ? 0 : 2)>(), f1, last, f0, st + 2, 0, st + 1 + RING);
   };
-  // DMA instructions of an odd stage, an even one (with scales), both
-  constexpr int kOdd = S::kWDma + S::kXDma, kEven = kOdd + S::kSDma, kTwo = kOdd + kEven;
   const int KK = (int)a.KK;
   using No = Const<0>;
   using Yes = Const<1>;
+  constexpr int kLong = (RING + 1) / 2;
 #pragma unroll
   for (int st = 0; st < RING; ++st)
     if (st < 2 * KK) {
 #pragma unroll
       for (int p = 0; p < (st == RING - 1 ? GW : 2 * GW); ++p) dma(st, p);  // the last one's second half: first step
     }
-  if (KK > 1) wait_vmcnt<RING == 4 ? kTwo : kOdd>();  // at least the first stage
+  // the first stage is in LDS; of the RING - 1 later ones all but the half-issued last may be in flight
+  if (2 * KK >= RING) wait_vmcnt<(RING - 2) * kPlain + (RING - 2) / 2 * S::kSDma>();
   else wait_vmcnt<0>();
   barrier_after_lds();
-  read_scales(0, sc);
+  auto tail = [&](auto self, auto live, auto after) {
+    constexpr int t = decltype(after)::value;
+    if (KK > t) group_cols(live, KK - 1 - t, after);
+    if constexpr (t > 0) self(self, live, Const<t - 1>());
+  };
+  auto all_cols = [&](auto live) {
+    if constexpr (decltype(live)::value != 0) {
+      read_scales(0, sc);
 #pragma unroll
-  for (int k = 0; k < GW + GX; ++k) read(0, 0, k, f0);
-  if constexpr (RING == 4) {
-    for (int c = 0; c + 2 < KK; ++c) group_cols(c, Yes(), Yes(), Yes(), Const<kTwo>(), Const<kTwo>());
-    if (KK > 1) group_cols(KK - 2, Yes(), No(), No(), Const<kTwo>(), Const<kOdd>());
-  } else {
-    for (int c = 0; c + 2 < KK; ++c) group_cols(c, Yes(), Yes(), Yes(), Const<kEven>(), Const<kOdd>());
-    if (KK > 1) group_cols(KK - 2, Yes(), Yes(), No(), Const<kEven>(), Const<kOdd>());
-  }
-  group_cols(KK - 1, No(), No(), No(), Const<0>(), Const<0>());
+      for (int k = 0; k < GW + GX; ++k) read(0, 0, k, f0);
+    }
+    for (int c = 0; c + kLong < KK; ++c) group_cols(live, c, Const<kLong>());
+    tail(tail, live, Const<kLong - 1>());
+  };
+  if (wx * GX * 32 < cnt) all_cols(Yes());
+  else all_cols(No());
 
   int* out_row = reinterpret_cast<int*>(smem + S::kTok * S::kOutRow);
   // ---- epilogue: a lane holds 16 consecutive features (half f of a group) of token n
@@ -499,7 +519,7 @@ __global__ __launch_bounds__(256, WGS) void mx_tiled_kernel(MxArgs a) {
   constexpr int kLanes = S::kSlots * 4, kRows = 64 / kLanes;  // lanes that write a row, rows a wave writes at a time
   const int64_t col = wt * S::kSlots * 32 + (l % kLanes) * 8;
   if (col >= a.N) return;
-  for (int t = w * kRows + l / kLanes; t < cnt; t += 4 * kRows) {
+  for (int t = w * kRows + l / kLanes; t < cnt; t += NW * kRows) {
     const uint4 v = *reinterpret_cast<const uint4*>(smem + t * S::kOutRow + (l % kLanes) * 16);
     uint16_t* p = static_cast<uint16_t*>(a.out) + (MODE == kDown ? (int64_t)out_row[t] : first + t) * a.ldo + col;
     if (MODE == kDown || (a.out_vec && col + 8 <= a.N)) {
@@ -553,20 +573,23 @@ __global__ __launch_bounds__(256) void mx_zero_pad_kernel(uint8_t* codes, uint8_
 namespace {
 
 #ifndef CFG
-#define CFG 2, 4, 2, 3
+#define CFG 8, 4, 2, 4, 4
 #define CFGW 2
 #endif
-using MxBig = MxTile<CFG>;  // 256 weight rows by 128 tokens, two workgroups a CU
+using MxBig = MxTile<CFG>;  // 256 weight rows by 256 tokens
 
 // Tokens (linear) or mean pairs per expert from which the tiled kernel is used.
-constexpr int64_t kTiledFrom = 64;
+#ifndef TFROM
+#define TFROM 64
+#endif
+constexpr int64_t kTiledFrom = TFROM;
 
 template <int MODE>
 hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
   auto* k = &mx_tiled_kernel<MODE, CFG, CFGW>;
   if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), MxBig::kLds)) return e;
   const int64_t grid = (max_mtiles * a.n_wtiles + 7) / 8 * 8;
-  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), MxBig::kLds, st, a);
+  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * MxBig::kWaves), MxBig::kLds, st, a);
   return hipGetLastError();
 }
 

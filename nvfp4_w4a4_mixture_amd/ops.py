@@ -9,6 +9,7 @@ non-OK status.  Every step of the layer runs in the library's HIP kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -500,19 +501,41 @@ def moe_nvfp4_unpack_weights(codes: torch.Tensor, packed_scales: torch.Tensor, k
 
 
 # ---- MXFP4 operators
+#
+# Single-token calls last a few microseconds on the device, so the host side counts: a check that passes is a few
+# attribute reads (_ok), and pointers and the stream go to the library as plain integers.
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+
+
+def _ok(t, name: str, dtype: torch.dtype, shape) -> None:
+    """_need, with the passing case first."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, dtypes=(torch.bfloat16,)) -> int:
     """Checks a [rows, cols] GPU matrix with unit column stride; returns its row stride."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.numel() > 0 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be [rows, cols] with unit column stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{name} must be [rows, cols] with unit column stride")
+    return ld if rows > 1 else max(cols, 1)
 
 
 def _mx_padded(cols: int) -> int:
@@ -523,23 +546,24 @@ def _mx_rows(rows: int, cols: int, device, codes, scales):
     """The codes and scales of [rows, cols] in the padded row form: given ones checked, missing ones allocated."""
     c = _mx_padded(cols)
     if codes is None:
-        codes = torch.empty((rows, c // 2), dtype=torch.uint8, device=device)
+        codes = torch.empty((rows, c // 2), dtype=_U8, device=device)
     else:
-        _need(codes, "codes", torch.uint8, (rows, c // 2))
+        _ok(codes, "codes", _U8, (rows, c // 2))
     if scales is None:
-        scales = torch.empty((rows, c // 32), dtype=torch.uint8, device=device)
+        scales = torch.empty((rows, c // 32), dtype=_U8, device=device)
     else:
-        _need(scales, "scales", torch.uint8, (rows, c // 32))
+        _ok(scales, "scales", _U8, (rows, c // 32))
     return codes, scales
 
 
 def _need_mx_rows(codes, scales, name: str, cols: int) -> int:
     c = _mx_padded(cols)
-    _need(codes, f"{name}_codes", torch.uint8)
-    if codes.dim() != 2 or codes.shape[1] != c // 2:
-        raise ValueError(f"{name}_codes must be [rows, {c // 2}] for {cols} columns, got {tuple(codes.shape)}")
-    _need(scales, f"{name}_scales", torch.uint8, (codes.shape[0], c // 32))
-    return codes.shape[0]
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError(f"{name}_codes must be a tensor [rows, {c // 2}]")
+    rows = codes.shape[0]
+    _ok(codes, f"{name}_codes", _U8, (rows, c // 2))
+    _ok(scales, f"{name}_scales", _U8, (rows, c // 32))
+    return rows
 
 
 def _mx_weight_shapes(N: int, K: int):
@@ -552,7 +576,7 @@ def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
     ld = _rows(x, "x", (torch.bfloat16, torch.float32))
     rows, cols = x.shape
     codes, scales = _mx_rows(rows, cols, x.device, codes, scales)
-    st = lib().mxfp4_quantize(_p(x), _DTYPE[x.dtype], rows, cols, ld, _p(codes), _p(scales), _stream(stream))
+    st = lib().mxfp4_quantize(_ptr(x), _DTYPE[x.dtype], rows, cols, ld, _ptr(codes), _ptr(scales), _raw_stream(stream, x))
     check(st, "mxfp4_quantize")
     return codes, scales
 
@@ -566,7 +590,7 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out_d
     ld = _rows(out, "out", (torch.bfloat16, torch.float32))
     if tuple(out.shape) != (rows, cols):
         raise ValueError(f"out must have shape {(rows, cols)}, got {tuple(out.shape)}")
-    st = lib().mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _DTYPE[out.dtype], _p(out), ld, _stream(stream))
+    st = lib().mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _DTYPE[out.dtype], _ptr(out), ld, _raw_stream(stream, codes))
     check(st, "mxfp4_dequantize")
     return out
 
@@ -583,7 +607,7 @@ def mxfp4_quantize_weights(w_bf16: torch.Tensor, stream=None):
     codes = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
     scales = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
     max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
-    st = lib().mxfp4_quantize_weights(_p(w_bf16), b, n, k, _p(codes), _p(scales), _p(max_scale), _stream(stream))
+    st = lib().mxfp4_quantize_weights(_ptr(w_bf16), b, n, k, _ptr(codes), _ptr(scales), _ptr(max_scale), _raw_stream(stream, w_bf16))
     check(st, "mxfp4_quantize_weights")
     return codes, scales, max_scale
 
@@ -596,13 +620,13 @@ def mxfp4_pack_weights(codes: torch.Tensor, scales: torch.Tensor, stream=None):
     b, n, kh = codes.shape
     if kh % 16:
         raise ValueError("K must be a multiple of 32")
-    _need(scales, "scales", torch.uint8, (b, n, kh // 16))
+    _ok(scales, "scales", torch.uint8, (b, n, kh // 16))
     cs, ss = _mx_weight_shapes(n, 2 * kh)
     dev = codes.device
     pc = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
     ps = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
     max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
-    st = lib().mxfp4_pack_weights(_p(codes), _p(scales), b, n, 2 * kh, _p(pc), _p(ps), _p(max_scale), _stream(stream))
+    st = lib().mxfp4_pack_weights(_ptr(codes), _ptr(scales), b, n, 2 * kh, _ptr(pc), _ptr(ps), _ptr(max_scale), _raw_stream(stream, codes))
     check(st, "mxfp4_pack_weights")
     return pc, ps, max_scale
 
@@ -611,17 +635,18 @@ def mxfp4_unpack_weights(codes: torch.Tensor, scales: torch.Tensor, N: int, K: i
     """Packed weights of [batch, N, K] -> canonical (codes [batch, N, K/2], scales [batch, N, K/32])."""
     cs, ss = _mx_weight_shapes(N, K)
     b = codes.shape[0]
-    _need(codes, "codes", torch.uint8, (b, *cs))
-    _need(scales, "scales", torch.uint8, (b, *ss))
+    _ok(codes, "codes", torch.uint8, (b, *cs))
+    _ok(scales, "scales", torch.uint8, (b, *ss))
     if K % 32:
         raise ValueError("K must be a multiple of 32")
     oc = torch.empty((b, N, K // 2), dtype=torch.uint8, device=codes.device)
     os_ = torch.empty((b, N, K // 32), dtype=torch.uint8, device=codes.device)
-    st = lib().mxfp4_unpack_weights(_p(codes), _p(scales), b, N, K, _p(oc), _p(os_), _stream(stream))
+    st = lib().mxfp4_unpack_weights(_ptr(codes), _ptr(scales), b, N, K, _ptr(oc), _ptr(os_), _raw_stream(stream, codes))
     check(st, "mxfp4_unpack_weights")
     return oc, os_
 
 
+@functools.lru_cache(maxsize=4096)
 def mxfp4_linear_workspace_bytes(T: int, K: int, N: int) -> int:
     return int(lib().mxfp4_linear_workspace_bytes(T, K, N))
 
@@ -634,8 +659,8 @@ def mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.
     K = 256 * w_codes.shape[1]  # the padded width: the padding is zero on both sides
     T = _need_mx_rows(x_codes, x_scales, "x", K)
     cs, ss = _mx_weight_shapes(N, K)
-    _need(w_codes, "w_codes", torch.uint8, cs)
-    _need(w_scales, "w_scales", torch.uint8, ss)
+    _ok(w_codes, "w_codes", torch.uint8, cs)
+    _ok(w_scales, "w_scales", torch.uint8, ss)
     if y is None:
         y = torch.empty((T, N), dtype=out_dtype, device=x_codes.device)
     ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
@@ -643,12 +668,13 @@ def mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.
         raise ValueError(f"y must have shape {(T, N)}, got {tuple(y.shape)}")
     nbytes = mxfp4_linear_workspace_bytes(T, K, N)
     ws = _workspace(nbytes, x_codes.device, workspace) if nbytes or workspace is not None else None
-    st = lib().mxfp4_linear(_p(x_codes), _p(x_scales), T, K, _p(w_codes), _p(w_scales), N, _DTYPE[y.dtype], _p(y), ldy,
-                            _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    st = lib().mxfp4_linear(_ptr(x_codes), _ptr(x_scales), T, K, _ptr(w_codes), _ptr(w_scales), N, _DTYPE[y.dtype], _ptr(y), ldy,
+                            _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, x_codes))
     check(st, "mxfp4_linear")
     return y
 
 
+@functools.lru_cache(maxsize=4096)
 def mxfp4_ffn_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
     return int(lib().mxfp4_ffn_workspace_bytes(T, k, E, H, I))
 
@@ -660,21 +686,21 @@ def mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_sca
     T = _need_mx_rows(x_codes, x_scales, "x", H)
     E = w13_codes.shape[0]
     cs, ss = _mx_weight_shapes(2 * I, H)
-    _need(w13_codes, "w13_codes", torch.uint8, (E, *cs))
-    _need(w13_scales, "w13_scales", torch.uint8, (E, *ss))
+    _ok(w13_codes, "w13_codes", torch.uint8, (E, *cs))
+    _ok(w13_scales, "w13_scales", torch.uint8, (E, *ss))
     cs, ss = _mx_weight_shapes(H, I)
-    _need(w2_codes, "w2_codes", torch.uint8, (E, *cs))
-    _need(w2_scales, "w2_scales", torch.uint8, (E, *ss))
-    _need(w2_max_scale, "w2_max_scale", torch.int32, (E,))
-    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
-    _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
-    _need(topk_w, "topk_w", torch.float32, (T, k))
+    _ok(w2_codes, "w2_codes", torch.uint8, (E, *cs))
+    _ok(w2_scales, "w2_scales", torch.uint8, (E, *ss))
+    _ok(w2_max_scale, "w2_max_scale", torch.int32, (E,))
+    _ok(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _ok(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
+    _ok(topk_w, "topk_w", torch.float32, (T, k))
     dev = x_codes.device
     pair_out, pair_scale, _ = _pair_outputs(T * k, H, dev, pair_out, pair_scale, None)
     ws = _workspace(mxfp4_ffn_workspace_bytes(T, k, E, H, I), dev, workspace)
-    st = lib().mxfp4_grouped_ffn(_p(x_codes), _p(x_scales), T, H, _p(w13_codes), _p(w13_scales), _p(w2_codes),
-                                 _p(w2_scales), _p(w2_max_scale), E, I, k, _p(expert_offsets), _p(sorted_pair_ids),
-                                 _p(topk_w), _p(pair_out), _p(pair_scale), _p(ws), ws.numel(), _stream(stream))
+    st = lib().mxfp4_grouped_ffn(_ptr(x_codes), _ptr(x_scales), T, H, _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes),
+                                 _ptr(w2_scales), _ptr(w2_max_scale), E, I, k, _ptr(expert_offsets), _ptr(sorted_pair_ids),
+                                 _ptr(topk_w), _ptr(pair_out), _ptr(pair_scale), _ptr(ws), ws.numel(), _raw_stream(stream, x_codes))
     check(st, "mxfp4_grouped_ffn")
     return pair_out, pair_scale
 
@@ -704,9 +730,9 @@ def moe_norm_in(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, n=None, qua
     from the same pass; n=False then skips the BF16 result."""
     ldx = _rows(x, "x")
     T, H = x.shape
-    _need(w, "w", torch.bfloat16, (H,))
+    _ok(w, "w", torch.bfloat16, (H,))
     n, ldn, codes, scales = _norm_outputs(T, H, x.device, n, quantize, codes, scales)
-    st = lib().moe_norm_in(_p(x), T, H, ldx, _p(w), eps, _p(n), ldn, _p(codes), _p(scales), _stream(stream))
+    st = lib().moe_norm_in(_ptr(x), T, H, ldx, _ptr(w), eps, _ptr(n), ldn, _ptr(codes), _ptr(scales), _raw_stream(stream, x))
     check(st, "moe_norm_in")
     return n if codes is None else (n, codes, scales)
 
@@ -726,7 +752,7 @@ def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch
         raise ValueError(f"residual must have shape {(T, H)}, got {tuple(residual.shape)}")
     for name, w in (("w_post", w_post), ("w_next", w_next)):
         if w is not None:
-            _need(w, name, torch.bfloat16, (H,))
+            _ok(w, name, torch.bfloat16, (H,))
     grs = gcs = 0
     if gate is not None:
         _need(gate, "gate", torch.bfloat16, contiguous=False)
@@ -744,9 +770,9 @@ def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch
         n, ldn, codes, scales = _norm_outputs(T, H, y.device, n, quantize, codes, scales)
     elif quantize or codes is not None or scales is not None or n is not None:
         raise ValueError("n and its quantization need w_next")
-    st = lib().moe_norm_out(_p(y), _DTYPE[y.dtype], T, H, ldy, _p(residual), ldr, _p(w_post), _p(gate), grs, gcs,
-                            residual_scale, _p(w_next), eps, _p(out), ldo, _p(n), ldn, _p(codes), _p(scales),
-                            _stream(stream))
+    st = lib().moe_norm_out(_ptr(y), _DTYPE[y.dtype], T, H, ldy, _ptr(residual), ldr, _ptr(w_post), _ptr(gate), grs, gcs,
+                            residual_scale, _ptr(w_next), eps, _ptr(out), ldo, _ptr(n), ldn, _ptr(codes), _ptr(scales),
+                            _raw_stream(stream, y))
     check(st, "moe_norm_out")
     if w_next is None:
         return out
