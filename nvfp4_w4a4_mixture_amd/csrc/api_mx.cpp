@@ -51,14 +51,16 @@ moe_status check_weights(const char* fn, int64_t batch, int64_t N, int64_t K) {
 }
 
 struct MxFfnWs {
-  size_t tiles, h_codes, h_scales, total;
+  size_t tiles[2], h_codes, h_scales, total;
 };
 
 MxFfnWs mx_ffn_ws(int64_t T, int64_t k, int64_t E, int64_t I) {
   MxFfnWs w{};
   size_t o = 0;
-  w.tiles = o;
-  o = round_up(o + (size_t)(moe::mx_max_mtiles(T, k, E) + 1) * 16, 256);
+  for (size_t& t : w.tiles) {
+    t = o;
+    o = round_up(o + (size_t)(moe::mx_max_mtiles(T, k, E) + 1) * 16, 256);
+  }
   w.h_codes = o;
   o = round_up(o + (size_t)(T * k) * (size_t)(mx_padded(I) / 2), 256);
   w.h_scales = o;
@@ -235,21 +237,22 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
   a.h_codes = ws + L.h_codes;
   a.h_scales = ws + L.h_scales;
   a.ldh = mx_padded(I) / 2;
-  a.tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
-  if (moe_status s = launched(moe::launch_mx_gate_up(a, E, (hipStream_t)stream), fn)) return s;
-  a.a_codes = a.h_codes;
-  a.a_scales = a.h_scales;
-  a.w_codes = w2_codes;
-  a.w_scales = w2_scales;
-  a.KK = mx_padded(I) / 256;
-  a.N = H;
-  a.G = H / 32;
-  a.w_max = w2_max_scale;
-  a.lg36I = ceil_log2(36 * I);
-  a.out = pair_out;
-  a.ldo = H;
-  a.pair_scale = pair_scale;
-  return launched(moe::launch_mx_down(a, E, (hipStream_t)stream), fn);
+  a.tiles = reinterpret_cast<int32_t*>(ws + L.tiles[0]);
+  moe::MxArgs d = a;
+  d.a_codes = a.h_codes;
+  d.a_scales = a.h_scales;
+  d.w_codes = w2_codes;
+  d.w_scales = w2_scales;
+  d.KK = mx_padded(I) / 256;
+  d.N = H;
+  d.G = H / 32;
+  d.w_max = w2_max_scale;
+  d.lg36I = ceil_log2(36 * I);
+  d.out = pair_out;
+  d.ldo = H;
+  d.pair_scale = pair_scale;
+  d.tiles = reinterpret_cast<int32_t*>(ws + L.tiles[1]);
+  return launched(moe::launch_mx_experts(a, d, E, (hipStream_t)stream), fn);
 }
 
 // ---- norms

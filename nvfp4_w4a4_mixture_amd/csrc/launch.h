@@ -132,7 +132,7 @@ struct MxArgs {
   int out_vec;  // linear: out rows start on 16-byte boundaries
   float* pair_scale;
   int32_t* tiles;     // experts: the m-tile schedule of the tiled kernel
-  int64_t n_wtiles;   // weight tiles (set by the launchers)
+  int64_t n_wtiles;   // weight tiles of the tiled kernel (set at its launch)
 };
 
 hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
@@ -144,9 +144,8 @@ hipError_t launch_mx_quantize_weights(const uint16_t* w, int64_t batch, int64_t 
 // canonical -> packed (pack) or back; max_scale (pack only) may be null
 hipError_t launch_mx_relayout(uint8_t* codes, uint8_t* scales, int64_t batch, int64_t N, int64_t K, uint8_t* pcodes,
                               uint8_t* pscales, int32_t* max_scale, bool pack, hipStream_t st);
-hipError_t launch_mx_linear(MxArgs a, hipStream_t st);
-hipError_t launch_mx_gate_up(MxArgs a, int64_t E, hipStream_t st);
-hipError_t launch_mx_down(MxArgs a, int64_t E, hipStream_t st);
+hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st);
+hipError_t launch_mx_experts(MxArgs gate_up, MxArgs down, int64_t E, hipStream_t st);
 // an upper bound on the experts' m-tiles
 int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E);
 

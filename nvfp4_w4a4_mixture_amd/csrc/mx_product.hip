@@ -40,6 +40,14 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t d) {
   return max(max(d & 255u, (d >> 8) & 255u), max((d >> 16) & 255u, d >> 24));
 }
 
+// The blocks of h row `row` past I, up to its padded width, are zero; thread `p` of `n` takes every n-th.
+__device__ __forceinline__ void zero_h_pad(const MxArgs& a, int64_t row, int p, int n) {
+  for (int64_t b = a.G / 2 + p; b < a.ldh / 16; b += n) {
+    *reinterpret_cast<uint4*>(a.h_codes + row * a.ldh + b * 16) = make_uint4(0, 0, 0, 0);
+    a.h_scales[row * (a.ldh / 16) + b] = 0;
+  }
+}
+
 }  // namespace
 
 // Streaming product: few tokens per weight row, so the weights' bytes bound it.
@@ -52,17 +60,22 @@ template <int MODE, int R, int NW>
 __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   __shared__ float part[NW][R][16][64];
   __shared__ uint32_t hmax[NW][32];
-  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, n = l & 31, f = l >> 5;
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, n = l & 31, f = l >> 5;
   const int e = MODE == kLinear ? 0 : blockIdx.y;
+  const int KK = (int)a.KK;
   int64_t lo = 0, hi = a.T;
   if (MODE != kLinear) {
     lo = a.offsets[e];
     hi = a.offsets[e + 1];
   }
-  int64_t g[R];
+  const uint8_t* wc[R];
+  const uint8_t* ws[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    g[i] = MODE == kGateUp ? (int64_t)blockIdx.x + i * (a.G / 2) : min((int64_t)blockIdx.x * R + i, a.G - 1);
+  for (int i = 0; i < R; ++i) {
+    const int64_t g = MODE == kGateUp ? (int64_t)blockIdx.x + i * (a.G / 2) : min((int64_t)blockIdx.x * R + i, a.G - 1);
+    wc[i] = a.w_codes + ((int64_t)e * a.G + g) * a.KK * kMxFragCodes;
+    ws[i] = a.w_scales + ((int64_t)e * a.G + g) * a.KK * kMxFragScales;
+  }
 
   for (int64_t t0 = lo + (MODE == kLinear ? (int64_t)blockIdx.y * 32 : 0); t0 < hi; t0 += 32) {
     const int cnt = (int)min((int64_t)32, hi - t0);
@@ -76,16 +89,14 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
     uint32_t bh = 0;
-    for (int64_t c = w; c < a.KK; c += NW) {
-      i32x4_t xf[4], wf[R][4];
-      int ws[R];
+    for (int64_t c = w; c < KK; c += NW) {
+      i32x4_t wf[R][4], xf[4];
+      int sw[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int64_t tile = ((int64_t)e * a.G + g[i]) * a.KK + c;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          wf[i][s] = reinterpret_cast<const i32x4_t*>(a.w_codes + tile * kMxFragCodes)[s * 64 + l];
-        ws[i] = reinterpret_cast<const int*>(a.w_scales + tile * kMxFragScales)[l];
+        for (int s = 0; s < 4; ++s) wf[i][s] = reinterpret_cast<const i32x4_t*>(wc[i] + c * kMxFragCodes)[s * 64 + l];
+        sw[i] = reinterpret_cast<const int*>(ws[i] + c * kMxFragScales)[l];
       }
 #pragma unroll
       for (int s = 0; s < 4; ++s) xf[s] = reinterpret_cast<const i32x4_t*>(xc + c * 128)[s];
@@ -93,20 +104,20 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
       if (MODE == kDown) bh = max(bh, max_byte((uint32_t)sx));
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        acc[i] = mx_mfma<0>(wf[i][0], xf[0], acc[i], ws[i], sx);
-        acc[i] = mx_mfma<1>(wf[i][1], xf[1], acc[i], ws[i], sx);
-        acc[i] = mx_mfma<2>(wf[i][2], xf[2], acc[i], ws[i], sx);
-        acc[i] = mx_mfma<3>(wf[i][3], xf[3], acc[i], ws[i], sx);
+        acc[i] = mx_mfma<0>(wf[i][0], xf[0], acc[i], sw[i], sx);
+        acc[i] = mx_mfma<1>(wf[i][1], xf[1], acc[i], sw[i], sx);
+        acc[i] = mx_mfma<2>(wf[i][2], xf[2], acc[i], sw[i], sx);
+        acc[i] = mx_mfma<3>(wf[i][3], xf[3], acc[i], sw[i], sx);
       }
+    }
+    if (MODE == kDown) {
+      bh = max(bh, (uint32_t)__shfl_xor((int)bh, 32));
+      if (f == 0) hmax[w][n] = bh;
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) part[w][i][r][l] = acc[i][r];
-    if (MODE == kDown) {
-      bh = max(bh, (uint32_t)__shfl_xor((int)bh, 32));
-      if (f == 0) hmax[w][n] = bh;
-    }
     __syncthreads();
     // thread (tok, p): features 4 p .. 4 p + 3 of one token
     const int tok = tid >> 3, p = tid & 7;
@@ -115,20 +126,20 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float s = part[0][i][4 * (p & 3) + j][32 * (p >> 2) + tok];
+        for (int q = 0; q < 4; ++q) {
+          float s = part[0][i][4 * (p & 3) + q][32 * (p >> 2) + tok];
 #pragma unroll
-          for (int q = 1; q < NW; ++q) s += part[q][i][4 * (p & 3) + j][32 * (p >> 2) + tok];
-          v[i][j] = s;
+          for (int k = 1; k < NW; ++k) s += part[k][i][4 * (p & 3) + q][32 * (p >> 2) + tok];
+          v[i][q] = s;
         }
       const int64_t row = t0 + tok;
       if constexpr (MODE == kGateUp) {
         float h[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[j] = silu(v[0][j]) * v[1][j];
-          m = max(m, abs_bits(h[j]));
+        for (int q = 0; q < 4; ++q) {
+          h[q] = silu(v[0][q]) * v[1][q];
+          m = max(m, abs_bits(h[q]));
         }
         m = max(m, (uint32_t)__shfl_xor((int)m, 1));
         m = max(m, (uint32_t)__shfl_xor((int)m, 2));
@@ -137,6 +148,7 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
         const int64_t blk = blockIdx.x;
         reinterpret_cast<uint16_t*>(a.h_codes + row * a.ldh)[blk * 8 + p] = (uint16_t)mx_encode8(h, byte);
         if (p == 0) a.h_scales[row * (a.ldh / 16) + blk] = (uint8_t)byte;
+        if (blk == 0) zero_h_pad(a, row, p, 8);
       } else {
         float factor = 1.0f;
         int64_t out = row;
@@ -145,25 +157,25 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
           const float wp = a.topk_w[out];
           uint32_t b = hmax[0][tok];
 #pragma unroll
-          for (int q = 1; q < NW; ++q) b = max(b, hmax[q][tok]);
+          for (int k = 1; k < NW; ++k) b = max(b, hmax[k][tok]);
           const int E = pair_exponent(wp, b, a.w_max[e], a.lg36I);
           factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
           if (blockIdx.x == 0 && p == 0) a.pair_scale[out] = __uint_as_float((uint32_t)(127 + E) << 23);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          const int64_t gi = (int64_t)blockIdx.x * R + i;
-          if (gi >= a.G) continue;
+          const int64_t col = ((int64_t)blockIdx.x * R + i) * 32 + 4 * p;
+          if (MODE == kDown) {  // N % 32 == 0 and the rows are aligned
+            if (col < a.N)
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out * a.ldo + col) =
+                  make_uint2(f16_pair(factor * v[i][0], factor * v[i][1]), f16_pair(factor * v[i][2], factor * v[i][3]));
+          } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t col = gi * 32 + 4 * p + j;
-            if (col >= a.N) continue;
-            if constexpr (MODE == kDown)
-              reinterpret_cast<_Float16*>(a.out)[out * a.ldo + col] = (_Float16)(factor * v[i][j]);
-            else if (a.out_f32)
-              static_cast<float*>(a.out)[out * a.ldo + col] = v[i][j];
-            else
-              static_cast<uint16_t*>(a.out)[out * a.ldo + col] = (uint16_t)bf16_bits_rne(v[i][j]);
+            for (int q = 0; q < 4; ++q) {
+              if (col + q >= a.N) break;
+              if (a.out_f32) static_cast<float*>(a.out)[out * a.ldo + col + q] = v[i][q];
+              else static_cast<uint16_t*>(a.out)[out * a.ldo + col + q] = (uint16_t)bf16_pair(v[i][q], 0.0f);
+            }
           }
         }
       }
@@ -186,13 +198,14 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 // 32 in accumulators.  The fragments of the next MFMA step are read while the
 // current one multiplies; the barrier that hands over a stage stands between
 // its two steps, so that the second covers the first reads of the next stage.
-template <int NW, int WM, int GW, int GX, int RING>
+template <int NW, int WM, int GW_, int GX_, int RING_>
 struct MxTile {
+  static constexpr int kWM = WM, GW = GW_, GX = GX_;
   static constexpr int kWX = NW / WM;
   static constexpr int kSlots = WM * GW;       // weight groups of a tile
   static constexpr int kTok = kWX * GX * 32;   // tokens of a tile
   static constexpr int kWaves = NW;
-  static constexpr int kRing = RING;
+  static constexpr int kRing = RING_;
   static constexpr int kWBytes = kSlots * 2048;
   static constexpr int kStage = kWBytes + kTok * 64;
   static constexpr int kUnits = kSlots + kTok / 32;  // scale dwords: 256 bytes a group of 32 rows
@@ -208,9 +221,9 @@ struct MxTile {
 // group, both over 8 rows (128 bytes a cycle) and over 16.
 __device__ __forceinline__ int mx_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
-template <int MODE, int NW, int WM, int GW, int GX, int RING, int WGS>
-__global__ __launch_bounds__(NW * 64, WGS) void mx_tiled_kernel(MxArgs a) {
-  using S = MxTile<NW, WM, GW, GX, RING>;
+template <int MODE, class S>
+__global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
+  constexpr int NW = S::kWaves, WM = S::kWM, GW = S::GW, GX = S::GX, RING = S::kRing;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, n = l & 31, f = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -467,6 +480,7 @@ __global__ __launch_bounds__(NW * 64, WGS) void mx_tiled_kernel(MxArgs a) {
           if (f == 0) a.h_scales[row * (a.ldh / 16) + hb] = (uint8_t)byte;
         }
       }
+      if (wt == 0 && wm == 0 && in) zero_h_pad(a, row, f, 2);
     } else if (MODE == kLinear && a.out_f32) {
       if (!in) continue;
 #pragma unroll
@@ -533,108 +547,131 @@ __global__ __launch_bounds__(NW * 64, WGS) void mx_tiled_kernel(MxArgs a) {
   }
 }
 
-// The m-tiles of every expert: tiles[0] their number; from tiles[4] on, four
-// words each: {expert, the expert's first m-tile, its m-tiles, 0}.
-__global__ __launch_bounds__(256) void mx_schedule_kernel(const int32_t* __restrict__ offsets, int E, int tok,
-                                                          int32_t* __restrict__ tiles) {
-  __shared__ int32_t sum[256];
-  const int e = threadIdx.x;
+// The m-tiles of every expert, for the two stages (block 0: gate_up, 1: down),
+// whose tiles may differ in tokens: tiles[0] their number; from tiles[4] on,
+// four words each: {expert, the expert's first m-tile, its m-tiles, 0}.  Thread
+// e counts expert e's tiles, a scan gives the first ones, and then tiles are
+// dealt to the threads, which find a tile's expert by bisection.
+__global__ __launch_bounds__(256) void mx_schedule_kernel(const int32_t* __restrict__ offsets, int E, int tok0,
+                                                          int tok1, int32_t* tiles0, int32_t* tiles1) {
+  const int tok = blockIdx.x == 0 ? tok0 : tok1;
+  int32_t* tiles = blockIdx.x == 0 ? tiles0 : tiles1;
+  __shared__ int32_t start[257], wave_sum[4];
+  const int e = threadIdx.x, l = e & 63;
   const int n = e < E ? (offsets[e + 1] - offsets[e] + tok - 1) / tok : 0;
-  sum[e] = n;
+  int sum = n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(sum, d);
+    if (l >= d) sum += v;
+  }
+  if (l == 63) wave_sum[e >> 6] = sum;
   __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
-    const int v = e >= d ? sum[e - d] : 0;
-    __syncthreads();
-    sum[e] += v;
-    __syncthreads();
+  for (int w = 0; w < (e >> 6); ++w) sum += wave_sum[w];
+  start[e + 1] = sum;
+  if (e == 0) start[0] = 0;
+  __syncthreads();
+  const int total = start[256];
+  if (e == 0) tiles[0] = total;
+  for (int i = e; i < total; i += 256) {
+    int lo = 0, hi = 256;  // start[lo] <= i < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    *reinterpret_cast<int4*>(tiles + 4 + (int64_t)i * 4) = make_int4(lo, start[lo], start[lo + 1] - start[lo], 0);
   }
-  const int s0 = sum[e] - n;
-  if (e == 255) tiles[0] = sum[255];
-  for (int i = 0; i < n; ++i) {
-    int32_t* t = tiles + 4 + (int64_t)(s0 + i) * 4;
-    t[0] = e;
-    t[1] = s0;
-    t[2] = n;
-    t[3] = 0;
-  }
-}
-
-// Rows of h past I (a row is padded to a whole column group) are zero blocks.
-__global__ __launch_bounds__(256) void mx_zero_pad_kernel(uint8_t* codes, uint8_t* scales, int64_t rows, int64_t ldh,
-                                                          int64_t I) {
-  const int64_t blocks = ldh / 16 - I / 32;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * blocks) return;
-  const int64_t r = i / blocks, b = I / 32 + (i - r * blocks);
-  *reinterpret_cast<uint4*>(codes + r * ldh + b * 16) = make_uint4(0, 0, 0, 0);
-  scales[r * (ldh / 16) + b] = 0;
 }
 
 namespace {
 
-#ifndef CFG
-#define CFG 8, 4, 2, 4, 4
-#define CFGW 2
-#endif
-using MxBig = MxTile<CFG>;  // 256 weight rows by 256 tokens
+using Mx128x64 = MxTile<4, 2, 2, 1, 4>;   // weight rows by tokens
+using Mx128x128 = MxTile<4, 2, 2, 2, 4>;
+using Mx256x128 = MxTile<4, 2, 4, 2, 3>;  // 78 KB of LDS: two workgroups a CU
+using Mx256x256 = MxTile<8, 4, 2, 4, 4>;
 
-// Tokens (linear) or mean pairs per expert from which the tiled kernel is used.
-#ifndef TFROM
-#define TFROM 64
-#endif
-constexpr int64_t kTiledFrom = TFROM;
+template <int MODE, class S>
+hipError_t launch_tiled(MxArgs a, int64_t E, hipStream_t st) {
+  auto* k = &mx_tiled_kernel<MODE, S>;
+  if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), S::kLds)) return e;
+  const int64_t rows = MODE == kGateUp ? a.G / 2 : a.G, per = MODE == kGateUp ? S::kSlots / 2 : S::kSlots;
+  a.n_wtiles = (rows + per - 1) / per;
+  int64_t mtiles = (a.T + S::kTok - 1) / S::kTok;
+  if (MODE != kLinear) {
+    const int64_t pairs = a.T * a.k;  // an upper bound: the schedule knows the number
+    mtiles = pairs / S::kTok + (pairs < E ? pairs : E);
+  }
+  const int64_t grid = (mtiles * a.n_wtiles + 7) / 8 * 8;
+  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * S::kWaves), S::kLds, st, a);
+  return hipGetLastError();
+}
 
 template <int MODE>
-hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
-  auto* k = &mx_tiled_kernel<MODE, CFG, CFGW>;
-  if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), MxBig::kLds)) return e;
-  const int64_t grid = (max_mtiles * a.n_wtiles + 7) / 8 * 8;
-  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * MxBig::kWaves), MxBig::kLds, st, a);
+hipError_t launch_stream(const MxArgs& a, int64_t E, hipStream_t st) {
+  if constexpr (MODE == kLinear)
+    hipLaunchKernelGGL((mx_stream_kernel<MODE, 1, 8>), dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512), 0, st,
+                       a);
+  else
+    hipLaunchKernelGGL((mx_stream_kernel<MODE, 2, 4>), dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st, a);
   return hipGetLastError();
+}
+
+enum Shape { kStream, k128x64, k128x128, k256x128, k256x256 };
+
+template <int MODE>
+hipError_t launch_shape(Shape s, const MxArgs& a, int64_t E, hipStream_t st) {
+  switch (s) {
+    case kStream: return launch_stream<MODE>(a, E, st);
+    case k128x64: return launch_tiled<MODE, Mx128x64>(a, E, st);
+    case k128x128:
+      if constexpr (MODE == kLinear) return launch_tiled<MODE, Mx128x128>(a, E, st);
+      return hipErrorInvalidValue;
+    case k256x128: return launch_tiled<MODE, Mx256x128>(a, E, st);
+    case k256x256: return launch_tiled<MODE, Mx256x256>(a, E, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+int shape_tokens(Shape s) { return s == k128x64 ? 64 : s == k256x256 ? 256 : 128; }
+
+Shape linear_shape(const MxArgs& a) {
+  const int64_t cus = 256;
+  auto tiles = [&](int64_t rows, int64_t tok) { return (a.G + rows / 32 - 1) / (rows / 32) * ((a.T + tok - 1) / tok); };
+  if (a.T <= 32 || tiles(32, 32) <= cus) return kStream;
+  if (tiles(256, 256) >= cus * 3 / 4) return k256x256;
+  if (tiles(256, 128) >= cus * 3 / 4) return k256x128;
+  if (tiles(128, 128) >= cus / 2) return k128x128;
+  return k128x64;
+}
+
+Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
+  if (pairs <= 32 * E && (pairs < E ? pairs : E) * (rows / 32) <= 2048) return kStream;
+  const int64_t tiles = (pairs / 128 + (pairs < E ? pairs : E) / 2) * ((rows + 255) / 256);
+  if (pairs <= 32 * E || tiles < 256) return k128x64;
+  return pairs < 512 * E || KK < 16 ? k256x128 : k256x256;
 }
 
 }  // namespace
 
-bool mx_experts_tiled(int64_t T, int64_t k, int64_t E) { return T * k >= kTiledFrom * E; }
-
 int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E) {
   const int64_t pairs = T * k;
-  return pairs / MxBig::kTok + (pairs < E ? pairs : E);
+  return pairs / Mx128x64::kTok + (pairs < E ? pairs : E);
 }
 
-hipError_t launch_mx_linear(MxArgs a, hipStream_t st) {
-  if (a.T >= kTiledFrom) {
-    a.n_wtiles = (a.G + MxBig::kSlots - 1) / MxBig::kSlots;
-    return launch_tiled<kLinear>(a, (a.T + MxBig::kTok - 1) / MxBig::kTok, st);
-  }
-  hipLaunchKernelGGL((mx_stream_kernel<kLinear, 1, 8>), dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512), 0,
-                     st, a);
-  return hipGetLastError();
-}
+hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) { return launch_shape<kLinear>(linear_shape(a), a, 1, st); }
 
-hipError_t launch_mx_gate_up(MxArgs a, int64_t E, hipStream_t st) {
-  const int64_t I = a.N / 2, pad = a.ldh / 16 - I / 32, npairs = a.T * a.k;
-  if (pad > 0)
-    hipLaunchKernelGGL(mx_zero_pad_kernel, dim3((unsigned)((npairs * pad + 255) / 256)), dim3(256), 0, st, a.h_codes,
-                       a.h_scales, npairs, a.ldh, I);
-  if (mx_experts_tiled(a.T, a.k, E)) {
-    hipLaunchKernelGGL(mx_schedule_kernel, dim3(1), dim3(256), 0, st, a.offsets, (int)E, MxBig::kTok, a.tiles);
-    a.n_wtiles = (a.G / 2 + MxBig::kSlots / 2 - 1) / (MxBig::kSlots / 2);
-    return launch_tiled<kGateUp>(a, mx_max_mtiles(a.T, a.k, E), st);
+hipError_t launch_mx_experts(MxArgs gate_up, MxArgs down, int64_t E, hipStream_t st) {
+  const int64_t pairs = gate_up.T * gate_up.k;
+  const Shape s0 = experts_shape(pairs, E, gate_up.N, gate_up.KK),
+              s1 = experts_shape(pairs, E, down.N, down.KK);
+  if (s0 != kStream || s1 != kStream) {
+    hipLaunchKernelGGL(mx_schedule_kernel, dim3(2), dim3(256), 0, st, gate_up.offsets, (int)E, shape_tokens(s0),
+                       shape_tokens(s1), gate_up.tiles, down.tiles);
+    if (hipError_t e = hipGetLastError()) return e;
   }
-  hipLaunchKernelGGL((mx_stream_kernel<kGateUp, 2, 4>), dim3((unsigned)(a.G / 2), (unsigned)E), dim3(256), 0, st, a);
-  return hipGetLastError();
-}
-
-// Reads the schedule that launch_mx_gate_up made.
-hipError_t launch_mx_down(MxArgs a, int64_t E, hipStream_t st) {
-  if (mx_experts_tiled(a.T, a.k, E)) {
-    a.n_wtiles = (a.G + MxBig::kSlots - 1) / MxBig::kSlots;
-    return launch_tiled<kDown>(a, mx_max_mtiles(a.T, a.k, E), st);
-  }
-  hipLaunchKernelGGL((mx_stream_kernel<kDown, 2, 4>), dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st,
-                     a);
-  return hipGetLastError();
+  if (hipError_t e = launch_shape<kGateUp>(s0, gate_up, E, st)) return e;
+  return launch_shape<kDown>(s1, down, E, st);
 }
 
 }  // namespace moe
