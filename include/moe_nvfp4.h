@@ -406,7 +406,7 @@ moe_status hadamard_rotate_bf16(const uint16_t* src, int64_t rows, int64_t cols,
 
 /* x [rows, ld] (ld >= cols) -> codes, scales in the padded row form above.
  * x 16-byte aligned with ld * sizeof(element) % 16 == 0; codes 16-byte
- * aligned; rows * Cp < 2^35. */
+ * aligned; rows * Cp < 2^35 - 2^15. */
 moe_status mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,
                           uint8_t* codes, uint8_t* scales, void* stream);
 /* The values that the codes stand for, out [rows, ld_out] (exact in both

@@ -24,7 +24,7 @@ bool dtype_ok(int32_t d) { return d == 0 || d == 1; }
 // rows * padded columns of 4-bit elements fit one launch of 8 elements a thread
 bool rows_fit(int64_t rows, int64_t cols) {
   return rows < kMaxDim && cols < kMaxDim &&
-         (unsigned __int128)rows * (uint64_t)(mx_padded(cols) / 8) < (unsigned __int128)kMaxThreads - 256;
+         (unsigned __int128)rows * (uint64_t)(mx_padded(cols) / 8) < (unsigned __int128)kMaxThreads - 4096;
 }
 
 moe_status check_rows(const char* fn, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, const void* x,

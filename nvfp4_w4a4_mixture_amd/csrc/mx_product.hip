@@ -238,12 +238,12 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   int e = 0;
   int64_t first = 0, rows = a.T, span = mtiles, q = at;
   if (MODE != kLinear) {
-    const int32_t* t = a.tiles + 4 + (at / nw) * 4;  // {expert, its first m-tile, its m-tiles}
-    e = t[0];
-    q = at - (int64_t)t[1] * nw;
-    span = t[2];
-    first = a.offsets[e];
-    rows = a.offsets[e + 1] - first;
+    const int4 t = reinterpret_cast<const int4*>(a.tiles)[1 + at / nw];
+    e = t.x;
+    q = at - (int64_t)t.y * nw;
+    first = t.z;
+    rows = t.w - first;
+    span = (rows + S::kTok - 1) / S::kTok;
   }
   // blocks of up to four token tiles by all weight tiles, tokens fastest
   const int64_t blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min((int64_t)4, span - 4 * blk);
@@ -342,6 +342,16 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     for (int i = 0; i < GX; ++i) s.x[i] = *reinterpret_cast<const int*>(buf + (S::kSlots + wx * GX + i) * 256);
   };
 
+  // what the epilogue needs of the pairs, loaded ahead of the products
+  int pair[GX];
+  float pair_w[GX];
+  if constexpr (MODE == kDown) {
+#pragma unroll
+    for (int j = 0; j < GX; ++j) {
+      pair[j] = a.sorted[first + min((wx * GX + j) * 32 + n, cnt - 1)];
+      pair_w[j] = a.topk_w[pair[j]];
+    }
+  }
   float16_t acc[GW][GX];
 #pragma unroll
   for (int i = 0; i < GW; ++i)
@@ -505,13 +515,11 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
       if constexpr (MODE == kDown) {
         const uint32_t b = max(bh[j], (uint32_t)__shfl_xor((int)bh[j], 32));
         if (in) {
-          const int out = a.sorted[row];
-          const float wp = a.topk_w[out];
-          const int E = pair_exponent(wp, b, a.w_max[e], a.lg36I);
-          factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
+          const int E = pair_exponent(pair_w[j], b, a.w_max[e], a.lg36I);
+          factor = pair_w[j] * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
           if (wm == 0 && f == 0) {
-            out_row[tok] = out;
-            if (wt == 0) a.pair_scale[out] = __uint_as_float((uint32_t)(127 + E) << 23);
+            out_row[tok] = pair[j];
+            if (wt == 0) a.pair_scale[pair[j]] = __uint_as_float((uint32_t)(127 + E) << 23);
           }
         }
       }
@@ -549,7 +557,8 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 
 // The m-tiles of every expert, for the two stages (block 0: gate_up, 1: down),
 // whose tiles may differ in tokens: tiles[0] their number; from tiles[4] on,
-// four words each: {expert, the expert's first m-tile, its m-tiles, 0}.  Thread
+// four words each: {expert, the expert's first m-tile, its first pair, the end of
+// its pairs}.  Thread
 // e counts expert e's tiles, a scan gives the first ones, and then tiles are
 // dealt to the threads, which find a tile's expert by bisection.
 __global__ __launch_bounds__(256) void mx_schedule_kernel(const int32_t* __restrict__ offsets, int E, int tok0,
@@ -580,7 +589,7 @@ __global__ __launch_bounds__(256) void mx_schedule_kernel(const int32_t* __restr
       if (start[mid] <= i) lo = mid;
       else hi = mid;
     }
-    *reinterpret_cast<int4*>(tiles + 4 + (int64_t)i * 4) = make_int4(lo, start[lo], start[lo + 1] - start[lo], 0);
+    *reinterpret_cast<int4*>(tiles + 4 + (int64_t)i * 4) = make_int4(lo, start[lo], offsets[lo], offsets[lo + 1]);
   }
 }
 

@@ -27,58 +27,80 @@ __device__ __forceinline__ void load8(const float* p, float* f) {
 // Four neighbouring lanes share one block of 32: each reads 8 elements (16 or
 // 32 bytes), the block's amax is two exchanges within the quad, and each writes
 // one dword of codes.  Columns past `cols` (up to the padded row) are zero
-// blocks with scale byte 0.  Memory bound: 2 (4) + 17/32 bytes an element.
+// blocks with scale byte 0.  A thread has kChunks loads in flight.  Memory
+// bound: 2 (4) + 17/32 bytes an element.
+constexpr int kChunks = 4;
+
 template <typename X>
-__global__ __launch_bounds__(256) void mx_quantize_kernel(const X* __restrict__ x, int64_t rows, int cols,
-                                                          int64_t ld, int chunks, uint32_t* __restrict__ codes,
+__global__ __launch_bounds__(256) void mx_quantize_kernel(const X* __restrict__ x, uint32_t n, uint32_t cols,
+                                                          int64_t ld, uint32_t chunks, uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // chunk of 8 elements of the padded rows
-  if (i >= rows * chunks) return;                            // chunks % 32 == 0: a quad is in or out as one
-  const int64_t r = i / chunks;
-  const int c = (int)(i - r * chunks);
-  float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (c * 8 < cols) load8(x + r * ld + (int64_t)c * 8, f);
-  uint32_t m = 0;
+  const uint32_t i0 = blockIdx.x * (256u * kChunks) + threadIdx.x;  // chunk of 8 elements of the padded rows
+  float f[kChunks][8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = max(m, abs_bits(f[k]));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-  const uint32_t byte = mx_scale_byte(m);
-  codes[i] = mx_encode8(f, byte);
-  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+  for (int v = 0; v < kChunks; ++v) {
+    const uint32_t i = i0 + 256u * v, r = i / chunks, c = (i - r * chunks) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[v][k] = 0.0f;
+    if (i < n && c < cols) load8(x + r * ld + c, f[v]);
+  }
+#pragma unroll
+  for (int v = 0; v < kChunks; ++v) {
+    const uint32_t i = i0 + 256u * v;
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, abs_bits(f[v][k]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+    const uint32_t byte = mx_scale_byte(m);
+    if (i < n) {  // n % 32 == 0: a quad is in or out as one
+      codes[i] = mx_encode8(f[v], byte);
+      if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+    }
+  }
 }
 
-// The values that codes stand for.  Thread = 8 elements.
+// The values that codes stand for.  A thread takes 8 elements, kChunks times.
 template <bool F32>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __restrict__ codes,
-                                                            const uint8_t* __restrict__ scales, int64_t rows,
-                                                            int chunks, int chunks_padded, void* __restrict__ out,
-                                                            int64_t ld) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * chunks) return;
-  const int64_t r = i / chunks;
-  const int c = (int)(i - r * chunks);
-  const int64_t src = r * chunks_padded + c;
-  const uint32_t d = codes[src];
-  const float s = mx_scale_value(scales[src >> 2]);
-  float f[8];
+                                                            const uint8_t* __restrict__ scales, uint32_t n,
+                                                            uint32_t chunks, uint32_t chunks_padded,
+                                                            void* __restrict__ out, int64_t ld) {
+  const uint32_t i0 = blockIdx.x * (256u * kChunks) + threadIdx.x;
+  uint32_t d[kChunks], byte[kChunks];
+  int64_t at[kChunks];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t code = (d >> (4 * k)) & 15u, m = code & 7u;
-    // 0, .5, 1, 1.5, 2, 3, 4, 6: exponent m / 2, mantissa bit m % 2
-    const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-    f[k] = ((code & 8u) ? -a : a) * s;
+  for (int v = 0; v < kChunks; ++v) {
+    const uint32_t i = i0 + 256u * v, r = i / chunks, c = i - r * chunks;
+    const int64_t src = (int64_t)r * chunks_padded + c;
+    at[v] = r * ld + (int64_t)c * 8;
+    if (i < n) {
+      d[v] = codes[src];
+      byte[v] = scales[src >> 2];
+    }
   }
-  const int64_t o = r * ld + (int64_t)c * 8;
-  if (F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
-    p[0] = make_float4(f[0], f[1], f[2], f[3]);
-    p[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {  // exact: two significant bits, and BF16 has FP32's exponents (down to 2^-133)
-    uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = (__float_as_uint(f[2 * k]) >> 16) | (__float_as_uint(f[2 * k + 1]) & 0xFFFF0000u);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int v = 0; v < kChunks; ++v) {
+    if (i0 + 256u * v >= n) break;
+    const float s = mx_scale_value(byte[v]);
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t code = (d[v] >> (4 * k)) & 15u, m = code & 7u;
+      // 0, .5, 1, 1.5, 2, 3, 4, 6: exponent m / 2, mantissa bit m % 2
+      const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
+      f[k] = ((code & 8u) ? -a : a) * s;
+    }
+    if (F32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at[v]);
+      p[0] = make_float4(f[0], f[1], f[2], f[3]);
+      p[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {  // exact: two significant bits, and BF16 has FP32's exponents (down to 2^-133)
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = (__float_as_uint(f[2 * k]) >> 16) | (__float_as_uint(f[2 * k + 1]) & 0xFFFF0000u);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at[v]) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -162,31 +184,30 @@ __global__ void mx_zero_ints_kernel(int* p, int64_t n) {
   if (i < n) p[i] = 0;
 }
 
+// rows * padded columns / 8 < 2^32 (checked by the caller)
 hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                               uint8_t* scales, hipStream_t st) {
-  const int64_t chunks = mx_padded(cols) / 8;
-  const dim3 grid((unsigned)((rows * chunks + 255) / 256));
+  const uint32_t chunks = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
+  const dim3 grid((unsigned)(((uint64_t)n + 256 * kChunks - 1) / (256 * kChunks)));
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   if (f32)
-    hipLaunchKernelGGL(mx_quantize_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), rows,
-                       (int)cols, ld, (int)chunks, c, scales);
+    hipLaunchKernelGGL(mx_quantize_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), n, (uint32_t)cols,
+                       ld, chunks, c, scales);
   else
-    hipLaunchKernelGGL(mx_quantize_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(x), rows,
-                       (int)cols, ld, (int)chunks, c, scales);
+    hipLaunchKernelGGL(mx_quantize_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(x), n,
+                       (uint32_t)cols, ld, chunks, c, scales);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
                                 void* out, int64_t ld, hipStream_t st) {
-  const int64_t chunks = cols / 8;
-  const dim3 grid((unsigned)((rows * chunks + 255) / 256));
+  const uint32_t chunks = (uint32_t)(cols / 8), padded = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
+  const dim3 grid((unsigned)(((uint64_t)n + 256 * kChunks - 1) / (256 * kChunks)));
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   if (f32)
-    hipLaunchKernelGGL(mx_dequantize_kernel<true>, grid, dim3(256), 0, st, c, scales, rows, (int)chunks,
-                       (int)(mx_padded(cols) / 8), out, ld);
+    hipLaunchKernelGGL(mx_dequantize_kernel<true>, grid, dim3(256), 0, st, c, scales, n, chunks, padded, out, ld);
   else
-    hipLaunchKernelGGL(mx_dequantize_kernel<false>, grid, dim3(256), 0, st, c, scales, rows, (int)chunks,
-                       (int)(mx_padded(cols) / 8), out, ld);
+    hipLaunchKernelGGL(mx_dequantize_kernel<false>, grid, dim3(256), 0, st, c, scales, n, chunks, padded, out, ld);
   return hipGetLastError();
 }
 

@@ -22,37 +22,43 @@ __device__ __forceinline__ float row_sum(float v, float* lds, int w) {
   return s;
 }
 
-// Eight elements at column c of a row of H: 16-byte accesses in the vector
-// form, element by element (and only the ones below H) in the other.
+// Eight BF16 (FP32) elements at column c of a row of H, as they lie in memory:
+// 16-byte accesses in the vector form, element by element (and only the ones
+// below H) in the other.  Elements past H are zero.
 template <bool VEC>
-__device__ __forceinline__ void load8_bf16(const uint16_t* p, int c, int H, float* f) {
+__device__ __forceinline__ uint4 load8_bf16(const uint16_t* p, int c, int H) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
   if (VEC) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (c < H) v = *reinterpret_cast<const uint4*>(p + c);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    if (c < H) return *reinterpret_cast<const uint4*>(p + c);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < H ? bf16_to_f32(p[c + i]) : 0.0f;
+    for (int i = 0; i < 8; ++i)
+      if (c + i < H) w[i >> 1] |= (uint32_t)p[c + i] << (16 * (i & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
 template <bool VEC>
 __device__ __forceinline__ void load8_f32(const float* p, int c, int H, float* f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = 0.0f;
   if (VEC) {
-    float4 a = make_float4(0, 0, 0, 0), b = a;
     if (c < H) {
-      a = *reinterpret_cast<const float4*>(p + c);
-      b = *reinterpret_cast<const float4*>(p + c + 4);
+      const float4 a = *reinterpret_cast<const float4*>(p + c), b = *reinterpret_cast<const float4*>(p + c + 4);
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < H ? p[c + i] : 0.0f;
+    for (int i = 0; i < 8; ++i)
+      if (c + i < H) f[i] = p[c + i];
   }
 }
 template <bool VEC>
@@ -72,8 +78,10 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uin
 
 // NW waves per row, V chunks of 8 columns per lane; the row stays in registers
 // between the passes.  POST: the row is y, and the first norm, gate, residual
-// scale and residual give r'; otherwise the row is x itself.
-template <int NW, int V, bool POST, bool VEC>
+// scale and residual give r'; otherwise the row is x itself.  Everything the
+// row needs is loaded before the first sum, so that one memory latency covers
+// it; the sums are FP32, in a fixed order.
+template <int NW, int V, bool POST, bool YF32, bool VEC>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
   constexpr int kRows = 4 / NW;  // rows per workgroup of 256 threads
   __shared__ float lds[2][4];
@@ -81,30 +89,48 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (64 * NW);
   if (NW == 1 && row >= a.T) return;  // with several waves a row is a workgroup
   const int H = (int)a.H;
+  const bool follow = !POST || a.w != nullptr;
   float x[V][8];
-  if (POST) {
-    float sq = 0.0f;
+  uint4 rr[V], wp[V], wn[V], gg[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * 64 * NW + t) * 8;
-      if (a.y_f32)
-        load8_f32<VEC>(static_cast<const float*>(a.x) + row * a.ldx, c, H, x[v]);
-      else
-        load8_bf16<VEC>(static_cast<const uint16_t*>(a.x) + row * a.ldx, c, H, x[v]);
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * 64 * NW + t) * 8;
+    if constexpr (YF32) load8_f32<VEC>(static_cast<const float*>(a.x) + row * a.ldx, c, H, x[v]);
+    else unpack8(load8_bf16<VEC>(static_cast<const uint16_t*>(a.x) + row * a.ldx, c, H), x[v]);
+    if constexpr (POST) rr[v] = load8_bf16<VEC>(a.r + row * a.ldr, c, H);
+  }
+  if constexpr (POST) {
+    if (a.gate && a.gate_cs != 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(x[v][i], x[v][i], sq);
+      for (int v = 0; v < V; ++v) gg[v] = load8_bf16<VEC>(a.gate + row * a.gate_rs, (v * 64 * NW + t) * 8, H);
     }
-    float inv = 1.0f;
-    if (a.w_post) inv = rsqrtf(row_sum<NW>(sq, lds[0], w) / (float)H + a.eps);
+    if (a.w_post) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) wp[v] = load8_bf16<VEC>(a.w_post, (v * 64 * NW + t) * 8, H);
+    }
+  }
+  if (follow) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) wn[v] = load8_bf16<VEC>(a.w, (v * 64 * NW + t) * 8, H);
+  }
+  if constexpr (POST) {
     const float g_row = a.gate && a.gate_cs == 0 ? bf16_to_f32(a.gate[row * a.gate_rs]) : 1.0f;
+    float inv = 1.0f;
+    if (a.w_post) {
+      float sq = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sq = fmaf(x[v][i], x[v][i], sq);
+      inv = rsqrtf(row_sum<NW>(sq, lds[0], w) / (float)H + a.eps);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * 64 * NW + t) * 8;
       float wv[8], rv[8], gv[8];
       uint32_t o[8];
-      if (a.w_post) load8_bf16<VEC>(a.w_post, c, H, wv);
-      if (a.gate && a.gate_cs != 0) load8_bf16<VEC>(a.gate + row * a.gate_rs, c, H, gv);
-      load8_bf16<VEC>(a.r + row * a.ldr, c, H, rv);
+      unpack8(rr[v], rv);
+      if (a.w_post) unpack8(wp[v], wv);
+      if (a.gate && a.gate_cs != 0) unpack8(gg[v], gv);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float z = x[v][i];
@@ -113,25 +139,22 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
         o[i] = bf16_bits_rne(fmaf(a.scale, z, rv[i]));
         x[v][i] = bf16_to_f32(o[i]);  // the next norm reads the residual that is kept
       }
-      store8_bf16<VEC>(a.r_out + row * a.ldro, c, H, o);
+      store8_bf16<VEC>(a.r_out + row * a.ldro, (v * 64 * NW + t) * 8, H, o);
     }
-    if (!a.w) return;
+    if (!follow) return;
   }
   float sq = 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = (v * 64 * NW + t) * 8;
-    if (!POST) load8_bf16<VEC>(static_cast<const uint16_t*>(a.x) + row * a.ldx, c, H, x[v]);
+  for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) sq = fmaf(x[v][i], x[v][i], sq);
-  }
   const float inv = rsqrtf(row_sum<NW>(sq, lds[1], w) / (float)H + a.eps);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * 64 * NW + t) * 8;
     float wv[8];
     uint32_t o[8];
-    load8_bf16<VEC>(a.w, c, H, wv);
+    unpack8(wn[v], wv);
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -159,8 +182,15 @@ namespace {
 template <int NW, int V, bool POST>
 void launch_norm_as(const NormArgs& a, bool vec, hipStream_t st) {
   const dim3 grid((unsigned)((a.T * NW + 3) / 4));
-  if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, true>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((norm_kernel<NW, V, POST, false>), grid, dim3(256), 0, st, a);
+  if constexpr (POST) {
+    if (a.y_f32) {
+      if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, true>), grid, dim3(256), 0, st, a);
+      else hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, false>), grid, dim3(256), 0, st, a);
+      return;
+    }
+  }
+  if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, true>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, false>), grid, dim3(256), 0, st, a);
 }
 
 template <bool POST>
