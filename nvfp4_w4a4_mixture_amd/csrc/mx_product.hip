@@ -326,20 +326,21 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     int w[GW], x[GX];
   };
   const int xlane = (wx * GX * 32 + n) * 64, sw_n = mx_swizzle(n);  // a wave's token groups are 32 rows apart
-  // Fragment r of piece p of stage st: the GX token fragments, then the GW weight fragments.
-  auto read = [&](int st, int p, int r, Frags& fr) {
+  // Fragment r of piece p of stage st: the token fragments (lx of them), then the GW weight fragments.
+  auto read = [&](int st, int p, int r, int lx, Frags& fr) {
     const unsigned char* buf = smem + (st % RING) * S::kStage;
-    if (r < GX)
+    if (r < lx)
       fr.x[r] = *reinterpret_cast<const i32x4_t*>(buf + S::kWBytes + xlane + (((2 * f + p) ^ sw_n) * 16) + r * 2048);
     else
-      fr.w[r - GX] = *reinterpret_cast<const i32x4_t*>(buf + (wm * GW * 2 + p) * 1024 + l * 16 + (r - GX) * 2048);
+      fr.w[r - lx] = *reinterpret_cast<const i32x4_t*>(buf + (wm * GW * 2 + p) * 1024 + l * 16 + (r - lx) * 2048);
   };
-  auto read_scales = [&](int c, Scales& s) {
+  auto read_scales = [&](int c, int lx, Scales& s) {
+    if (lx == 0) return;
     const unsigned char* buf = smem + S::kRing * S::kStage + (c & 1) * (S::kUnits * 256) + l * 4;
 #pragma unroll
     for (int i = 0; i < GW; ++i) s.w[i] = *reinterpret_cast<const int*>(buf + (wm * GW + i) * 256);
 #pragma unroll
-    for (int i = 0; i < GX; ++i) s.x[i] = *reinterpret_cast<const int*>(buf + (S::kSlots + wx * GX + i) * 256);
+    for (int i = 0; i < lx; ++i) s.x[i] = *reinterpret_cast<const int*>(buf + (S::kSlots + wx * GX + i) * 256);
   };
 
   // what the epilogue needs of the pairs, loaded ahead of the products
@@ -371,11 +372,13 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   // with the matrix cores idle.  The last quarter of a step has no reads: a
   // barrier may follow, and waits for them.  The steps hold no branches:
   // products have no side effects, and the compiler would move them past a
-  // branch to where their result is used.  A wave whose tokens are all past the
-  // end (live = 0) only does its share of the DMA: its SIMD is the other wave's.
+  // branch to where their result is used.  Token groups past the end are left out
+  // (live of GX remain): a wave with none only does its share of the DMA, and
+  // its SIMD is the other wave's.
   auto step = [&](auto live, auto sel, auto half, const Frags& fr, const Scales& sc, Frags& nx, int nst, int np, int dst) {
-    constexpr int kHalf = decltype(half)::value, kReads = GW + GX, kSpan = 3 * GW * GX / 4;
-    if constexpr (decltype(live)::value == 0) {
+    constexpr int LX = decltype(live)::value, kHalf = decltype(half)::value;
+    constexpr int kReads = GW + LX, kSpan = 3 * GW * LX / 4;
+    if constexpr (LX == 0) {
       if constexpr (kHalf < 2) {
 #pragma unroll
         for (int i = 0; i < GW; ++i) dma(dst, kHalf * GW + i);
@@ -385,13 +388,13 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < GW; ++i) {
 #pragma unroll
-      for (int j = 0; j < GX; ++j) {
+      for (int j = 0; j < LX; ++j) {
         acc[i][j] = mx_mfma<decltype(sel)::value>(fr.w[i], fr.x[j], acc[i][j], sc.w[i], sc.x[j]);
 #pragma unroll
         for (int k = 0; k < kReads; ++k)
-          if (k * kSpan / kReads == i * GX + j) read(nst, np, k, nx);
+          if (k * kSpan / kReads == i * LX + j) read(nst, np, k, LX, nx);
         if constexpr (kHalf < 2)
-          if (j == GX / 2) dma(dst, kHalf * GW + i);
+          if (j == LX / 2) dma(dst, kHalf * GW + i);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -415,7 +418,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     const int st = 2 * c;
     if (MODE == kDown) {
 #pragma unroll
-      for (int j = 0; j < GX; ++j) bh[j] = max(bh[j], max_byte((uint32_t)sc.x[j]));
+      for (int j = 0; j < decltype(live)::value; ++j) bh[j] = max(bh[j], max_byte((uint32_t)sc.x[j]));
     }
     step(live, Const<0>(), Const<(kD0 ? 1 : 2)>(), f0, sc, f1, st, 1, st - 1 + RING);
     wait_vmcnt<w1>();
@@ -426,16 +429,14 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < GW; ++i) last.w[i] = (int)((uint32_t)sc.w[i] >> 24);
 #pragma unroll
-    for (int j = 0; j < GX; ++j) last.x[j] = (int)((uint32_t)sc.x[j] >> 24);
+    for (int j = 0; j < decltype(live)::value; ++j) last.x[j] = (int)((uint32_t)sc.x[j] >> 24);
     wait_vmcnt<w2>();
     barrier_after_lds();
     // past the last group these read buffers that are not used
-    if constexpr (decltype(live)::value != 0) read_scales(c + 1, sc);
+    read_scales(c + 1, decltype(live)::value, sc);
     step(live, Const<0>(), Const<(kD2 ? 0 : 2)>(), f1, last, f0, st + 2, 0, st + 1 + RING);
   };
   const int KK = (int)a.KK;
-  using No = Const<0>;
-  using Yes = Const<1>;
   constexpr int kLong = (RING + 1) / 2;
 #pragma unroll
   for (int st = 0; st < RING; ++st)
@@ -453,16 +454,21 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     if constexpr (t > 0) self(self, live, Const<t - 1>());
   };
   auto all_cols = [&](auto live) {
-    if constexpr (decltype(live)::value != 0) {
-      read_scales(0, sc);
+    constexpr int LX = decltype(live)::value;
+    read_scales(0, LX, sc);
+    if constexpr (LX > 0) {
 #pragma unroll
-      for (int k = 0; k < GW + GX; ++k) read(0, 0, k, f0);
+      for (int k = 0; k < GW + LX; ++k) read(0, 0, k, LX, f0);
     }
     for (int c = 0; c + kLong < KK; ++c) group_cols(live, c, Const<kLong>());
     tail(tail, live, Const<kLong - 1>());
   };
-  if (wx * GX * 32 < cnt) all_cols(Yes());
-  else all_cols(No());
+  const int groups = (cnt - wx * GX * 32 + 31) / 32;  // of this wave's tokens
+  if (groups >= GX) all_cols(Const<GX>());
+  else if (GX > 3 && groups == 3) all_cols(Const<(GX > 3 ? 3 : 0)>());
+  else if (GX > 2 && groups == 2) all_cols(Const<(GX > 2 ? 2 : 0)>());
+  else if (GX > 1 && groups == 1) all_cols(Const<(GX > 1 ? 1 : 0)>());
+  else all_cols(Const<0>());
 
   int* out_row = reinterpret_cast<int*>(smem + S::kTok * S::kOutRow);
   // ---- epilogue: a lane holds 16 consecutive features (half f of a group) of token n
@@ -658,7 +664,7 @@ Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   if (pairs <= 32 * E && (pairs < E ? pairs : E) * (rows / 32) <= 2048) return kStream;
   const int64_t tiles = (pairs / 128 + (pairs < E ? pairs : E) / 2) * ((rows + 255) / 256);
   if (pairs <= 32 * E || tiles < 256) return k128x64;
-  return pairs < 512 * E || KK < 16 ? k256x128 : k256x256;
+  return pairs < 128 * E || KK < 16 ? k256x128 : k256x256;
 }
 
 }  // namespace

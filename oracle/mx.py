@@ -37,11 +37,10 @@ def scale_byte(amax: np.ndarray) -> np.ndarray:
 def _round_codes(v: np.ndarray) -> np.ndarray:
     """Nearest E2M1 code of each v (float64), ties to the even code, saturating; sign bit from v."""
     mags = formats.E2M1_VALUES[:8]
-    d = np.abs(np.abs(v)[..., None] - mags)
-    best = d.min(-1, keepdims=True)
-    near = d == best  # one or two candidates; of two neighbours exactly one code is even
-    even = near & (np.arange(8) % 2 == 0)
-    pick = np.where(even.any(-1), even.argmax(-1), near.argmax(-1))
+    mid = (mags[:-1] + mags[1:]) / 2
+    a = np.abs(v)
+    below, upto = np.searchsorted(mid, a, "left"), np.searchsorted(mid, a, "right")  # they differ on a tie only
+    pick = np.where(below % 2 == 0, below, upto)  # of two neighbours exactly one code is even
     return (pick | (np.signbit(v).astype(np.int64) << 3)).astype(np.uint8)
 
 
