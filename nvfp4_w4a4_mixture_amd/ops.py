@@ -8,7 +8,6 @@ non-OK status.  Every step of the layer runs in the library's HIP kernels.
 
 from __future__ import annotations
 
-import ctypes
 import functools
 from typing import NamedTuple, Optional
 
@@ -27,13 +26,18 @@ __all__ = ["moe_route", "moe_route_quantize", "nvfp4_quantize_act", "nvfp4_quant
            "moe_norm_in", "moe_norm_out"]
 
 
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+# Single-token calls last a few microseconds on the device, so the host side counts: pointers and the stream go to the
+# library as plain integers, and a check that passes is a few attribute reads.
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _p(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, contiguous: bool = True) -> None:
@@ -41,7 +45,7 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, contiguous
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -463,7 +467,7 @@ def hadamard_rotate_bf16(src: torch.Tensor, signs: Optional[torch.Tensor], block
         out = torch.empty(src.shape, dtype=torch.bfloat16, device=src.device)
     _need(out, "out", torch.bfloat16, tuple(src.shape), contiguous=False)
     o2 = out.reshape(-1, cols) if out.dim() != 2 else out
-    if o2.data_ptr() != out.data_ptr() or (out.dim() != 2 and not out.is_contiguous()):
+    if o2.data_p() != out.data_ptr() or (out.dim() != 2 and not out.is_contiguous()):
         raise ValueError("out must be 2-D or contiguous")
     if signs is not None:
         _need(signs, "signs", torch.float32, (cols,))
@@ -501,26 +505,15 @@ def moe_nvfp4_unpack_weights(codes: torch.Tensor, packed_scales: torch.Tensor, k
 
 
 # ---- MXFP4 operators
-#
-# Single-token calls last a few microseconds on the device, so the host side counts: a check that passes is a few
-# attribute reads (_ok), and pointers and the stream go to the library as plain integers.
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
-_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+_U8 = torch.uint8
 
 
 def _ok(t, name: str, dtype: torch.dtype, shape) -> None:
     """_need, with the passing case first."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
         _need(t, name, dtype, shape)
-
-
-def _raw_stream(stream, t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
-
-
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, dtypes=(torch.bfloat16,)) -> int:
@@ -576,7 +569,7 @@ def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
     ld = _rows(x, "x", (torch.bfloat16, torch.float32))
     rows, cols = x.shape
     codes, scales = _mx_rows(rows, cols, x.device, codes, scales)
-    st = lib().mxfp4_quantize(_ptr(x), _DTYPE[x.dtype], rows, cols, ld, _ptr(codes), _ptr(scales), _raw_stream(stream, x))
+    st = lib().mxfp4_quantize(_p(x), _DTYPE[x.dtype], rows, cols, ld, _p(codes), _p(scales), _stream(stream))
     check(st, "mxfp4_quantize")
     return codes, scales
 
@@ -590,7 +583,7 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out_d
     ld = _rows(out, "out", (torch.bfloat16, torch.float32))
     if tuple(out.shape) != (rows, cols):
         raise ValueError(f"out must have shape {(rows, cols)}, got {tuple(out.shape)}")
-    st = lib().mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _DTYPE[out.dtype], _ptr(out), ld, _raw_stream(stream, codes))
+    st = lib().mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _DTYPE[out.dtype], _p(out), ld, _stream(stream))
     check(st, "mxfp4_dequantize")
     return out
 
@@ -607,7 +600,7 @@ def mxfp4_quantize_weights(w_bf16: torch.Tensor, stream=None):
     codes = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
     scales = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
     max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
-    st = lib().mxfp4_quantize_weights(_ptr(w_bf16), b, n, k, _ptr(codes), _ptr(scales), _ptr(max_scale), _raw_stream(stream, w_bf16))
+    st = lib().mxfp4_quantize_weights(_p(w_bf16), b, n, k, _p(codes), _p(scales), _p(max_scale), _stream(stream))
     check(st, "mxfp4_quantize_weights")
     return codes, scales, max_scale
 
@@ -626,7 +619,7 @@ def mxfp4_pack_weights(codes: torch.Tensor, scales: torch.Tensor, stream=None):
     pc = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
     ps = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
     max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
-    st = lib().mxfp4_pack_weights(_ptr(codes), _ptr(scales), b, n, 2 * kh, _ptr(pc), _ptr(ps), _ptr(max_scale), _raw_stream(stream, codes))
+    st = lib().mxfp4_pack_weights(_p(codes), _p(scales), b, n, 2 * kh, _p(pc), _p(ps), _p(max_scale), _stream(stream))
     check(st, "mxfp4_pack_weights")
     return pc, ps, max_scale
 
@@ -641,7 +634,7 @@ def mxfp4_unpack_weights(codes: torch.Tensor, scales: torch.Tensor, N: int, K: i
         raise ValueError("K must be a multiple of 32")
     oc = torch.empty((b, N, K // 2), dtype=torch.uint8, device=codes.device)
     os_ = torch.empty((b, N, K // 32), dtype=torch.uint8, device=codes.device)
-    st = lib().mxfp4_unpack_weights(_ptr(codes), _ptr(scales), b, N, K, _ptr(oc), _ptr(os_), _raw_stream(stream, codes))
+    st = lib().mxfp4_unpack_weights(_p(codes), _p(scales), b, N, K, _p(oc), _p(os_), _stream(stream))
     check(st, "mxfp4_unpack_weights")
     return oc, os_
 
@@ -668,8 +661,8 @@ def mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.
         raise ValueError(f"y must have shape {(T, N)}, got {tuple(y.shape)}")
     nbytes = mxfp4_linear_workspace_bytes(T, K, N)
     ws = _workspace(nbytes, x_codes.device, workspace) if nbytes or workspace is not None else None
-    st = lib().mxfp4_linear(_ptr(x_codes), _ptr(x_scales), T, K, _ptr(w_codes), _ptr(w_scales), N, _DTYPE[y.dtype], _ptr(y), ldy,
-                            _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, x_codes))
+    st = lib().mxfp4_linear(_p(x_codes), _p(x_scales), T, K, _p(w_codes), _p(w_scales), N, _DTYPE[y.dtype], _p(y), ldy,
+                            _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     check(st, "mxfp4_linear")
     return y
 
@@ -698,9 +691,9 @@ def mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_sca
     dev = x_codes.device
     pair_out, pair_scale, _ = _pair_outputs(T * k, H, dev, pair_out, pair_scale, None)
     ws = _workspace(mxfp4_ffn_workspace_bytes(T, k, E, H, I), dev, workspace)
-    st = lib().mxfp4_grouped_ffn(_ptr(x_codes), _ptr(x_scales), T, H, _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes),
-                                 _ptr(w2_scales), _ptr(w2_max_scale), E, I, k, _ptr(expert_offsets), _ptr(sorted_pair_ids),
-                                 _ptr(topk_w), _ptr(pair_out), _ptr(pair_scale), _ptr(ws), ws.numel(), _raw_stream(stream, x_codes))
+    st = lib().mxfp4_grouped_ffn(_p(x_codes), _p(x_scales), T, H, _p(w13_codes), _p(w13_scales), _p(w2_codes),
+                                 _p(w2_scales), _p(w2_max_scale), E, I, k, _p(expert_offsets), _p(sorted_pair_ids),
+                                 _p(topk_w), _p(pair_out), _p(pair_scale), _p(ws), ws.numel(), _stream(stream))
     check(st, "mxfp4_grouped_ffn")
     return pair_out, pair_scale
 
@@ -732,7 +725,7 @@ def moe_norm_in(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, n=None, qua
     T, H = x.shape
     _ok(w, "w", torch.bfloat16, (H,))
     n, ldn, codes, scales = _norm_outputs(T, H, x.device, n, quantize, codes, scales)
-    st = lib().moe_norm_in(_ptr(x), T, H, ldx, _ptr(w), eps, _ptr(n), ldn, _ptr(codes), _ptr(scales), _raw_stream(stream, x))
+    st = lib().moe_norm_in(_p(x), T, H, ldx, _p(w), eps, _p(n), ldn, _p(codes), _p(scales), _stream(stream))
     check(st, "moe_norm_in")
     return n if codes is None else (n, codes, scales)
 
@@ -770,9 +763,9 @@ def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch
         n, ldn, codes, scales = _norm_outputs(T, H, y.device, n, quantize, codes, scales)
     elif quantize or codes is not None or scales is not None or n is not None:
         raise ValueError("n and its quantization need w_next")
-    st = lib().moe_norm_out(_ptr(y), _DTYPE[y.dtype], T, H, ldy, _ptr(residual), ldr, _ptr(w_post), _ptr(gate), grs, gcs,
-                            residual_scale, _ptr(w_next), eps, _ptr(out), ldo, _ptr(n), ldn, _ptr(codes), _ptr(scales),
-                            _raw_stream(stream, y))
+    st = lib().moe_norm_out(_p(y), _DTYPE[y.dtype], T, H, ldy, _p(residual), ldr, _p(w_post), _p(gate), grs, gcs,
+                            residual_scale, _p(w_next), eps, _p(out), ldo, _p(n), ldn, _p(codes), _p(scales),
+                            _stream(stream))
     check(st, "moe_norm_out")
     if w_next is None:
         return out
