@@ -535,18 +535,36 @@ def _mx_padded(cols: int) -> int:
     return -(-cols // 256) * 256
 
 
-def _mx_rows(rows: int, cols: int, device, codes, scales):
+def _out(t, name: str, like: torch.Tensor, dtype: torch.dtype, rows: int, cols: int):
+    """An output matrix and its row stride: a given one checked (any row stride), a missing one allocated."""
+    if t is None:
+        return like.new_empty((rows, cols), dtype=dtype), cols
+    ld = _rows(t, name, (dtype,))
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    return t, ld
+
+
+def _mx_rows(rows: int, cols: int, like: torch.Tensor, codes, scales):
     """The codes and scales of [rows, cols] in the padded row form: given ones checked, missing ones allocated."""
     c = _mx_padded(cols)
     if codes is None:
-        codes = torch.empty((rows, c // 2), dtype=_U8, device=device)
+        codes = like.new_empty((rows, c // 2), dtype=_U8)
     else:
         _ok(codes, "codes", _U8, (rows, c // 2))
     if scales is None:
-        scales = torch.empty((rows, c // 32), dtype=_U8, device=device)
+        scales = codes.new_empty((rows, c // 32))
     else:
         _ok(scales, "scales", _U8, (rows, c // 32))
     return codes, scales
+
+
+def _out_type(out_dtype: torch.dtype, out) -> torch.dtype:
+    """The type of the result: that of a given output, or the one asked for; BF16 or FP32."""
+    dtype = out_dtype if out is None else out.dtype
+    if dtype not in _DTYPE:
+        raise TypeError(f"the output type must be torch.bfloat16 or torch.float32, got {dtype}")
+    return dtype
 
 
 def _need_mx_rows(codes, scales, name: str, cols: int) -> int:
@@ -559,16 +577,17 @@ def _need_mx_rows(codes, scales, name: str, cols: int) -> int:
     return rows
 
 
-def _mx_weight_shapes(N: int, K: int):
+@functools.lru_cache(maxsize=4096)
+def _mx_weight_shapes(N: int, K: int, *batch: int):
     g, kk = -(-N // 32), -(-K // 256)
-    return (g, kk, 4, 64, 16), (g, kk, 64, 4)
+    return (*batch, g, kk, 4, 64, 16), (*batch, g, kk, 64, 4)
 
 
 def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
     """x [rows, cols] BF16 or FP32 -> (codes [rows, Cp/2], scales [rows, Cp/32]), Cp = cols rounded up to 256."""
     ld = _rows(x, "x", (torch.bfloat16, torch.float32))
     rows, cols = x.shape
-    codes, scales = _mx_rows(rows, cols, x.device, codes, scales)
+    codes, scales = _mx_rows(rows, cols, x, codes, scales)
     st = lib().mxfp4_quantize(_p(x), _DTYPE[x.dtype], rows, cols, ld, _p(codes), _p(scales), _stream(stream))
     check(st, "mxfp4_quantize")
     return codes, scales
@@ -578,11 +597,7 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out_d
                      out=None, stream=None) -> torch.Tensor:
     """The values that the codes stand for, [rows, cols] in BF16 or FP32 (exact in both)."""
     rows = _need_mx_rows(codes, scales, "x", cols)
-    if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device)
-    ld = _rows(out, "out", (torch.bfloat16, torch.float32))
-    if tuple(out.shape) != (rows, cols):
-        raise ValueError(f"out must have shape {(rows, cols)}, got {tuple(out.shape)}")
+    out, ld = _out(out, "out", codes, _out_type(out_dtype, out), rows, cols)
     st = lib().mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _DTYPE[out.dtype], _p(out), ld, _stream(stream))
     check(st, "mxfp4_dequantize")
     return out
@@ -652,13 +667,9 @@ def mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.
     K = 256 * w_codes.shape[1]  # the padded width: the padding is zero on both sides
     T = _need_mx_rows(x_codes, x_scales, "x", K)
     cs, ss = _mx_weight_shapes(N, K)
-    _ok(w_codes, "w_codes", torch.uint8, cs)
-    _ok(w_scales, "w_scales", torch.uint8, ss)
-    if y is None:
-        y = torch.empty((T, N), dtype=out_dtype, device=x_codes.device)
-    ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
-    if tuple(y.shape) != (T, N):
-        raise ValueError(f"y must have shape {(T, N)}, got {tuple(y.shape)}")
+    _ok(w_codes, "w_codes", _U8, cs)
+    _ok(w_scales, "w_scales", _U8, ss)
+    y, ldy = _out(y, "y", x_codes, _out_type(out_dtype, y), T, N)
     nbytes = mxfp4_linear_workspace_bytes(T, K, N)
     ws = _workspace(nbytes, x_codes.device, workspace) if nbytes or workspace is not None else None
     st = lib().mxfp4_linear(_p(x_codes), _p(x_scales), T, K, _p(w_codes), _p(w_scales), N, _DTYPE[y.dtype], _p(y), ldy,
@@ -678,19 +689,26 @@ def mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_sca
     """The routed experts' FFN in MXFP4: (pair_out, pair_scale), what moe_combine and moe_combine_block read."""
     T = _need_mx_rows(x_codes, x_scales, "x", H)
     E = w13_codes.shape[0]
-    cs, ss = _mx_weight_shapes(2 * I, H)
-    _ok(w13_codes, "w13_codes", torch.uint8, (E, *cs))
-    _ok(w13_scales, "w13_scales", torch.uint8, (E, *ss))
-    cs, ss = _mx_weight_shapes(H, I)
-    _ok(w2_codes, "w2_codes", torch.uint8, (E, *cs))
-    _ok(w2_scales, "w2_scales", torch.uint8, (E, *ss))
+    cs, ss = _mx_weight_shapes(2 * I, H, E)
+    _ok(w13_codes, "w13_codes", _U8, cs)
+    _ok(w13_scales, "w13_scales", _U8, ss)
+    cs, ss = _mx_weight_shapes(H, I, E)
+    _ok(w2_codes, "w2_codes", _U8, cs)
+    _ok(w2_scales, "w2_scales", _U8, ss)
     _ok(w2_max_scale, "w2_max_scale", torch.int32, (E,))
     _ok(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
     _ok(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
     _ok(topk_w, "topk_w", torch.float32, (T, k))
-    dev = x_codes.device
-    pair_out, pair_scale, _ = _pair_outputs(T * k, H, dev, pair_out, pair_scale, None)
-    ws = _workspace(mxfp4_ffn_workspace_bytes(T, k, E, H, I), dev, workspace)
+    if pair_out is None:
+        pair_out = x_codes.new_empty((T * k, H), dtype=torch.float16)
+    else:
+        _ok(pair_out, "pair_out", torch.float16, (T * k, H))
+    if pair_scale is None:
+        pair_scale = topk_w.new_empty((T * k,))
+    else:
+        _ok(pair_scale, "pair_scale", torch.float32, (T * k,))
+    nbytes = mxfp4_ffn_workspace_bytes(T, k, E, H, I)
+    ws = x_codes.new_empty((max(nbytes, 1),)) if workspace is None else workspace
     st = lib().mxfp4_grouped_ffn(_p(x_codes), _p(x_scales), T, H, _p(w13_codes), _p(w13_scales), _p(w2_codes),
                                  _p(w2_scales), _p(w2_max_scale), E, I, k, _p(expert_offsets), _p(sorted_pair_ids),
                                  _p(topk_w), _p(pair_out), _p(pair_scale), _p(ws), ws.numel(), _stream(stream))
@@ -701,19 +719,14 @@ def mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_sca
 # ---- norms around the block
 
 
-def _norm_outputs(T: int, H: int, device, n, quantize: bool, codes, scales):
+def _norm_outputs(like: torch.Tensor, T: int, H: int, n, quantize: bool, codes, scales):
     """Output n (False: none) and, if asked for, its codes and scales."""
-    if n is None:
-        n = torch.empty((T, H), dtype=torch.bfloat16, device=device)
-    elif n is False:
-        n = None
-    ldn = H
-    if n is not None:
-        ldn = _rows(n, "n")
-        if tuple(n.shape) != (T, H):
-            raise ValueError(f"n must have shape {(T, H)}, got {tuple(n.shape)}")
+    if n is False:
+        n, ldn = None, H
+    else:
+        n, ldn = _out(n, "n", like, torch.bfloat16, T, H)
     if quantize or codes is not None or scales is not None:
-        codes, scales = _mx_rows(T, H, device, codes, scales)
+        codes, scales = _mx_rows(T, H, like, codes, scales)
     return n, ldn, codes, scales
 
 
@@ -724,7 +737,7 @@ def moe_norm_in(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, n=None, qua
     ldx = _rows(x, "x")
     T, H = x.shape
     _ok(w, "w", torch.bfloat16, (H,))
-    n, ldn, codes, scales = _norm_outputs(T, H, x.device, n, quantize, codes, scales)
+    n, ldn, codes, scales = _norm_outputs(x, T, H, n, quantize, codes, scales)
     st = lib().moe_norm_in(_p(x), T, H, ldx, _p(w), eps, _p(n), ldn, _p(codes), _p(scales), _stream(stream))
     check(st, "moe_norm_in")
     return n if codes is None else (n, codes, scales)
@@ -741,26 +754,27 @@ def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch
     ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
     T, H = y.shape
     ldr = _rows(residual, "residual")
-    if tuple(residual.shape) != (T, H):
+    if residual.shape != (T, H):
         raise ValueError(f"residual must have shape {(T, H)}, got {tuple(residual.shape)}")
-    for name, w in (("w_post", w_post), ("w_next", w_next)):
-        if w is not None:
-            _ok(w, name, torch.bfloat16, (H,))
+    if w_post is not None:
+        _ok(w_post, "w_post", torch.bfloat16, (H,))
+    if w_next is not None:
+        _ok(w_next, "w_next", torch.bfloat16, (H,))
     grs = gcs = 0
     if gate is not None:
         _need(gate, "gate", torch.bfloat16, contiguous=False)
-        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, H):
-            raise ValueError(f"gate must be [T, 1], [1, H] or [T, H], got {tuple(gate.shape)}")
-        gcs = 0 if gate.shape[1] == 1 else gate.stride(1)
-        grs = 0 if gate.shape[0] == 1 else gate.stride(0)
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
-    ldo = _rows(out, "out")
-    if tuple(out.shape) != (T, H):
-        raise ValueError(f"out must have shape {(T, H)}, got {tuple(out.shape)}")
+        shape = gate.shape
+        if len(shape) != 2 or shape[0] not in (1, T) or shape[1] not in (1, H):
+            raise ValueError(f"gate must be [T, 1], [1, H] or [T, H], got {tuple(shape)}")
+        grs, gcs = gate.stride()
+        if shape[0] == 1:
+            grs = 0
+        if shape[1] == 1:
+            gcs = 0
+    out, ldo = _out(out, "out", y, torch.bfloat16, T, H)
     ldn = H
     if w_next is not None:
-        n, ldn, codes, scales = _norm_outputs(T, H, y.device, n, quantize, codes, scales)
+        n, ldn, codes, scales = _norm_outputs(y, T, H, n, quantize, codes, scales)
     elif quantize or codes is not None or scales is not None or n is not None:
         raise ValueError("n and its quantization need w_next")
     st = lib().moe_norm_out(_p(y), _DTYPE[y.dtype], T, H, ldy, _p(residual), ldr, _p(w_post), _p(gate), grs, gcs,
