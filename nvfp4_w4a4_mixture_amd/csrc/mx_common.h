@@ -69,6 +69,13 @@ __device__ __forceinline__ uint32_t bf16_bits_rne(float f) {
   return (u & 0x7FFFFFFFu) > 0x7F800000u ? (u >> 16) | 0x40u : r;
 }
 
+// A 16-byte store that does not stay in L2: for results larger than it, whose
+// lines would push out what is still read.
+__device__ __forceinline__ void store16_streaming(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const u32x4_t v = {a, b, c, d};
+  __builtin_nontemporal_store(v, static_cast<u32x4_t*>(p));
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // One scaled FP4 MFMA step: c += A . B over 64 columns; S = step = scale byte.

@@ -505,9 +505,9 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
         float* p = static_cast<float*>(a.out) + row * a.ldo + col;
         if (a.out_vec && col + 16 <= a.N) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            reinterpret_cast<float4*>(p)[r] =
-                make_float4(acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]);
+          for (int r = 0; r < 16; r += 4)
+            store16_streaming(p + r, __float_as_uint(acc[i][j][r]), __float_as_uint(acc[i][j][r + 1]),
+                              __float_as_uint(acc[i][j][r + 2]), __float_as_uint(acc[i][j][r + 3]));
         } else {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
@@ -551,7 +551,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     const uint4 v = *reinterpret_cast<const uint4*>(smem + t * S::kOutRow + (l % kLanes) * 16);
     uint16_t* p = static_cast<uint16_t*>(a.out) + (MODE == kDown ? (int64_t)out_row[t] : first + t) * a.ldo + col;
     if (MODE == kDown || (a.out_vec && col + 8 <= a.N)) {
-      *reinterpret_cast<uint4*>(p) = v;
+      store16_streaming(p, v.x, v.y, v.z, v.w);
     } else {
       const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -65,8 +65,7 @@ template <bool VEC>
 __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uint32_t* b) {
   if (VEC) {
     if (c < H)
-      *reinterpret_cast<uint4*>(p + c) =
-          make_uint4(b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16));
+      store16_streaming(p + c, b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
