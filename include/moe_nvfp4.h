@@ -433,7 +433,7 @@ moe_status mxfp4_unpack_weights(const uint8_t* packed_codes, const uint8_t* pack
  * form, w packed [N, K]; y [T, ldy] (ldy >= N) in out_dtype (BF16
  * round-to-nearest-even).  Code arrays 16-byte, scale arrays 4-byte, y 4-byte
  * (BF16: 2-byte) aligned.  T * Kp / 2 < 2^32 bytes (Kp = round_up(K, 256)) and
- * T <= 2097120.  workspace: mxfp4_linear_workspace_bytes(T, K, N) bytes
+ * T <= 2097120, N <= 2^27, ldy < 2^31, and under 2^22 tiles of 256 x 256.  workspace: mxfp4_linear_workspace_bytes(T, K, N) bytes
  * (0 possible: workspace may then be NULL), 256-byte aligned. */
 size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K, int64_t N);
 moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t K,
@@ -457,7 +457,8 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
  * 113], bh the largest scale byte of the pair's h and bw = w2_max_scale[e]:
  * |w_p f| < 2^(E + 15).
  * H % 32 == 0, I % 32 == 0, 1 <= k <= E <= 256, T * k < 2^31; x codes
- * (T*Hp/2 bytes) and h codes (T*k*Ip/2 bytes) under 4 GiB.  Code arrays and
+ * (T*Hp/2 bytes) and h codes (T*k*Ip/2 bytes) under 4 GiB, and (T*k/128 + E) *
+ * ceil(max(2I, H) / 256) < 2^22.  Code arrays and
  * pair_out 16-byte, scale arrays, pair_scale and w2_max_scale 4-byte aligned;
  * workspace mxfp4_ffn_workspace_bytes(...) bytes, 256-byte aligned.  Pairs not
  * listed in sorted_pair_ids are not written. */
@@ -483,7 +484,8 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
  * n) and n itself may be NULL; this needs H % 32 == 0.  x, r, r_out, n, weights
  * and gate are BF16, y is BF16 or FP32 (y_dtype).  gate (NULL: 1) has element
  * (t, c) at gate[t * gate_row_stride + c * gate_col_stride], gate_col_stride 0
- * (one value a token) or 1.  Any H from 1 to 16384 and any row strides >= H;
+ * (one value a token) or 1.  Any H from 1 to 16384 and any row strides from H to
+ * 2^31 - 1;
  * 16-byte accesses are used when H % 8 == 0 and every pointer and row stride is a
  * multiple of 16 bytes.  Pointers aligned to their element, codes to 4 bytes.
  * r_out may be r, and n may be x (in place, same strides); other outputs must

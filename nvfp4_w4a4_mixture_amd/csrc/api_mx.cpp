@@ -18,6 +18,7 @@ using moe::round_up;
 constexpr uint64_t kMaxThreads = (uint64_t)1 << 32;
 constexpr uint64_t kMaxOperand = (uint64_t)1 << 32;  // bytes that 32-bit offsets reach
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // of one launch (the kernels count them in 32 bits)
 
 bool dtype_ok(int32_t d) { return d == 0 || d == 1; }
 
@@ -139,6 +140,8 @@ static moe_status check_linear(int64_t T, int64_t K, int64_t N) {
   if (T < 0) return fail(MOE_ERR_SHAPE, "%s: T must be >= 0 (got %lld)", fn, (long long)T);
   if (moe_status s = check_weights(fn, 1, N, K)) return s;
   if (T > 2097120) return fail(MOE_ERR_SHAPE, "%s: T must be at most 2097120", fn);
+  if (N > ((int64_t)1 << 27) || ((T + 255) / 256) * ((N + 255) / 256) >= kMaxTiles)
+    return fail(MOE_ERR_SHAPE, "%s: N or the result is too large for one call", fn);
   if ((uint64_t)T * (uint64_t)(mx_padded(K) / 2) >= kMaxOperand)
     return fail(MOE_ERR_SHAPE, "%s: x codes must be under 4 GiB", fn);
   return MOE_OK;
@@ -157,7 +160,7 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
   const char* fn = "mxfp4_linear";
   if (!dtype_ok(out_dtype)) return fail(MOE_ERR_SHAPE, "%s: out_dtype must be 0 (BF16) or 1 (FP32)", fn);
   if (moe_status s = check_linear(T, K, N)) return s;
-  if (ldy < N) return fail(MOE_ERR_SHAPE, "%s: ldy must be >= N", fn);
+  if (ldy < N || ldy >= kMaxDim) return fail(MOE_ERR_SHAPE, "%s: ldy must be >= N and < 2^31", fn);
   if (T == 0) return MOE_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return fail(MOE_ERR_NULL, "%s: a required pointer is NULL", fn);
   if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
@@ -173,15 +176,14 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
   a.a_scales = x_scales;
   a.w_codes = w_codes;
   a.w_scales = w_scales;
-  a.T = T;
-  a.KK = mx_padded(K) / 256;
-  a.N = N;
-  a.G = (N + 31) / 32;
-  a.k = 1;
   a.out = y;
-  a.ldo = ldy;
-  a.out_f32 = out_dtype;
-  a.out_vec = aligned(y, 16) && (ldy * (out_dtype ? 4 : 2)) % 16 == 0;
+  a.KK = (int32_t)(mx_padded(K) / 256);
+  a.N = (int32_t)N;
+  a.G = (int32_t)((N + 31) / 32);
+  a.ldo = (int32_t)ldy;
+  a.T = (int32_t)T;
+  a.aux = (out_dtype ? moe::kMxOutF32 : 0) |
+          (aligned(y, 16) && (ldy * (out_dtype ? 4 : 2)) % 16 == 0 ? moe::kMxOutVec : 0);
   return launched(moe::launch_mx_linear(a, (hipStream_t)stream), fn);
 }
 
@@ -207,6 +209,8 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
     return fail(MOE_ERR_SHAPE, "%s: x codes must be under 4 GiB", fn);
   if ((uint64_t)(T * k) * (uint64_t)(mx_padded(I) / 2) >= kMaxOperand)
     return fail(MOE_ERR_SHAPE, "%s: h codes must be under 4 GiB", fn);
+  if ((T * k / 128 + E) * (((2 * I > H ? 2 * I : H) + 255) / 256) >= kMaxTiles)
+    return fail(MOE_ERR_SHAPE, "%s: too many tiles for one call", fn);
   if (T == 0) return MOE_OK;
   if (!x_codes || !x_scales || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !w2_max_scale ||
       !expert_offsets || !sorted_pair_ids || !topk_w || !pair_out || !pair_scale)
@@ -221,41 +225,46 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
   if (moe_status s = check_device()) return s;
 
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  moe::MxArgs a{};
+  moe::MxExperts x{};
+  x.T = T;
+  x.k = k;
+  x.E = E;
+  x.offsets = expert_offsets;
+  for (int i = 0; i < 2; ++i) x.tiles[i] = reinterpret_cast<int32_t*>(ws + L.tiles[i]);
+  moe::MxArgs& a = x.gate_up;
   a.a_codes = x_codes;
   a.a_scales = x_scales;
   a.w_codes = w13_codes;
   a.w_scales = w13_scales;
-  a.T = T;
-  a.KK = mx_padded(H) / 256;
-  a.N = 2 * I;
-  a.G = 2 * I / 32;
-  a.k = (int)k;
-  a.offsets = expert_offsets;
+  a.out = ws + L.h_codes;
+  a.out_scales = ws + L.h_scales;
   a.sorted = sorted_pair_ids;
-  a.topk_w = topk_w;
-  a.h_codes = ws + L.h_codes;
-  a.h_scales = ws + L.h_scales;
-  a.ldh = mx_padded(I) / 2;
-  a.tiles = reinterpret_cast<int32_t*>(ws + L.tiles[0]);
-  moe::MxArgs d = a;
-  d.a_codes = a.h_codes;
-  d.a_scales = a.h_scales;
+  a.KK = (int32_t)(mx_padded(H) / 256);
+  a.N = (int32_t)(2 * I);
+  a.G = (int32_t)(2 * I / 32);
+  a.ldo = (int32_t)(mx_padded(I) / 2);
+  a.aux = (int32_t)k;
+  moe::MxArgs& d = x.down;
+  d.a_codes = ws + L.h_codes;
+  d.a_scales = ws + L.h_scales;
   d.w_codes = w2_codes;
   d.w_scales = w2_scales;
-  d.KK = mx_padded(I) / 256;
-  d.N = H;
-  d.G = H / 32;
-  d.w_max = w2_max_scale;
-  d.lg36I = ceil_log2(36 * I);
   d.out = pair_out;
-  d.ldo = H;
-  d.pair_scale = pair_scale;
-  d.tiles = reinterpret_cast<int32_t*>(ws + L.tiles[1]);
-  return launched(moe::launch_mx_experts(a, d, E, (hipStream_t)stream), fn);
+  d.out_scales = pair_scale;
+  d.sorted = sorted_pair_ids;
+  d.topk_w = topk_w;
+  d.w_max = w2_max_scale;
+  d.KK = (int32_t)(mx_padded(I) / 256);
+  d.N = (int32_t)H;
+  d.G = (int32_t)(H / 32);
+  d.ldo = (int32_t)H;
+  d.aux = ceil_log2(36 * I);
+  return launched(moe::launch_mx_experts(x, (hipStream_t)stream), fn);
 }
 
 // ---- norms
+
+static bool stride_ok(int64_t ld, int64_t H) { return ld >= H && ld < kMaxDim; }
 
 static moe_status check_norm(const char* fn, int64_t T, int64_t H, float eps, const uint16_t* n, int64_t ldn,
                              const uint8_t* codes, const uint8_t* scales, bool norm_follows) {
@@ -265,7 +274,7 @@ static moe_status check_norm(const char* fn, int64_t T, int64_t H, float eps, co
   if ((uint64_t)T * 256 >= kMaxThreads) return fail(MOE_ERR_SHAPE, "%s: too many rows for one call", fn);
   if (!(eps >= 0.0f)) return fail(MOE_ERR_SHAPE, "%s: eps must be >= 0", fn);
   if (codes && H % 32 != 0) return fail(MOE_ERR_SHAPE, "%s: H must be a multiple of 32 to quantize", fn);
-  if (n && ldn < H) return fail(MOE_ERR_SHAPE, "%s: a row stride is smaller than H", fn);
+  if (n && !stride_ok(ldn, H)) return fail(MOE_ERR_SHAPE, "%s: a row stride is smaller than H or over 2^31", fn);
   if (T > 0 && norm_follows && !n && !codes) return fail(MOE_ERR_NULL, "%s: neither n nor codes is given", fn);
   if (T > 0 && (codes != nullptr) != (scales != nullptr)) return fail(MOE_ERR_NULL, "%s: codes and scales go together", fn);
   if (!aligned(n, 2) || !aligned(codes, 4)) return fail(MOE_ERR_ALIGN, "%s: n must be 2-byte, codes 4-byte aligned", fn);
@@ -278,25 +287,24 @@ moe_status moe_norm_in(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, con
                        uint16_t* n, int64_t ldn, uint8_t* codes, uint8_t* scales, void* stream) {
   const char* fn = "moe_norm_in";
   if (moe_status s = check_norm(fn, T, H, eps, n, ldn, codes, scales, true)) return s;
-  if (ldx < H) return fail(MOE_ERR_SHAPE, "%s: a row stride is smaller than H", fn);
+  if (!stride_ok(ldx, H)) return fail(MOE_ERR_SHAPE, "%s: a row stride is smaller than H or over 2^31", fn);
   if (T == 0) return MOE_OK;
   if (!x || !w) return fail(MOE_ERR_NULL, "%s: a required pointer is NULL", fn);
   if (!aligned(x, 2) || !aligned(w, 2)) return fail(MOE_ERR_ALIGN, "%s: BF16 arrays must be 2-byte aligned", fn);
   if (moe_status s = check_device()) return s;
   moe::NormArgs a{};
   a.x = x;
-  a.ldx = ldx;
-  a.T = T;
-  a.H = H;
-  a.Hp = codes ? mx_padded(H) : H;
-  a.eps = eps;
   a.w = w;
   a.n = n;
-  a.ldn = ldn;
   a.codes = codes;
   a.scales = scales;
+  a.ldx = (int32_t)ldx;
+  a.ldn = (int32_t)ldn;
+  a.H = (uint32_t)H;
+  a.Hp = (uint32_t)(codes ? mx_padded(H) : H);
+  a.eps = eps;
   const bool vec = H % 8 == 0 && vec16(x, ldx, 2) && vec16(w, 0, 2) && vec16(n, ldn, 2);
-  return launched(moe::launch_norm(a, false, vec, (hipStream_t)stream), fn);
+  return launched(moe::launch_norm(a, T, false, false, vec, (hipStream_t)stream), fn);
 }
 
 moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, int64_t ldy, const uint16_t* r,
@@ -307,8 +315,9 @@ moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, in
   const char* fn = "moe_norm_out";
   if (!dtype_ok(y_dtype)) return fail(MOE_ERR_SHAPE, "%s: y_dtype must be 0 (BF16) or 1 (FP32)", fn);
   if (moe_status s = check_norm(fn, T, H, eps, n, ldn, codes, scales, w_next != nullptr)) return s;
-  if (ldy < H || ldr < H || ldro < H) return fail(MOE_ERR_SHAPE, "%s: a row stride is smaller than H", fn);
-  if (gate && (gate_row_stride < 0 || (gate_col_stride != 0 && gate_col_stride != 1)))
+  if (!stride_ok(ldy, H) || !stride_ok(ldr, H) || !stride_ok(ldro, H))
+    return fail(MOE_ERR_SHAPE, "%s: a row stride is smaller than H or over 2^31", fn);
+  if (gate && (gate_row_stride < 0 || gate_row_stride >= kMaxDim || (gate_col_stride != 0 && gate_col_stride != 1)))
     return fail(MOE_ERR_SHAPE, "%s: gate strides must be >= 0 (rows) and 0 or 1 (columns)", fn);
   if (!w_next && (n || codes)) return fail(MOE_ERR_NULL, "%s: n and codes need w_next", fn);
   if (T == 0) return MOE_OK;
@@ -319,30 +328,28 @@ moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, in
   if (moe_status s = check_device()) return s;
   moe::NormArgs a{};
   a.x = y;
-  a.ldx = ldy;
-  a.y_f32 = y_dtype;
-  a.T = T;
-  a.H = H;
-  a.Hp = codes ? mx_padded(H) : H;
+  a.r = r;
   a.w_post = w_post;
   a.gate = gate;
-  a.gate_rs = gate_row_stride;
-  a.gate_cs = gate_col_stride;
-  a.r = r;
-  a.ldr = ldr;
-  a.scale = residual_scale;
-  a.eps = eps;
-  a.r_out = r_out;
-  a.ldro = ldro;
   a.w = w_next;
+  a.r_out = r_out;
   a.n = n;
-  a.ldn = ldn;
   a.codes = codes;
   a.scales = scales;
+  a.ldx = (int32_t)ldy;
+  a.ldr = (int32_t)ldr;
+  a.ldro = (int32_t)ldro;
+  a.ldn = (int32_t)ldn;
+  a.gate_rs = (int32_t)gate_row_stride;
+  a.H = (uint32_t)H;
+  a.Hp = (uint32_t)(codes ? mx_padded(H) : H);
+  a.gate_row = gate_col_stride == 0;
+  a.scale = residual_scale;
+  a.eps = eps;
   const bool vec = H % 8 == 0 && vec16(y, ldy, y_dtype ? 4 : 2) && vec16(r, ldr, 2) && vec16(r_out, ldro, 2) &&
                    vec16(w_post, 0, 2) && vec16(w_next, 0, 2) && vec16(n, ldn, 2) &&
                    (gate_col_stride == 0 || vec16(gate, gate_row_stride, 2));
-  return launched(moe::launch_norm(a, true, vec, (hipStream_t)stream), fn);
+  return launched(moe::launch_norm(a, T, true, y_dtype == 1, vec, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

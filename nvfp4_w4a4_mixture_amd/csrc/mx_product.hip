@@ -42,9 +42,9 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t d) {
 
 // The blocks of h row `row` past I, up to its padded width, are zero; thread `p` of `n` takes every n-th.
 __device__ __forceinline__ void zero_h_pad(const MxArgs& a, int64_t row, int p, int n) {
-  for (int64_t b = a.G / 2 + p; b < a.ldh / 16; b += n) {
-    *reinterpret_cast<uint4*>(a.h_codes + row * a.ldh + b * 16) = make_uint4(0, 0, 0, 0);
-    a.h_scales[row * (a.ldh / 16) + b] = 0;
+  for (int b = a.G / 2 + p; b < a.ldo / 16; b += n) {
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * a.ldo + b * 16) = make_uint4(0, 0, 0, 0);
+    static_cast<uint8_t*>(a.out_scales)[row * (a.ldo / 16) + b] = 0;
   }
 }
 
@@ -65,14 +65,14 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   const int KK = (int)a.KK;
   int64_t lo = 0, hi = a.T;
   if (MODE != kLinear) {
-    lo = a.offsets[e];
-    hi = a.offsets[e + 1];
+    lo = a.route[e];
+    hi = a.route[e + 1];
   }
   const uint8_t* wc[R];
   const uint8_t* ws[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t g = MODE == kGateUp ? (int64_t)blockIdx.x + i * (a.G / 2) : min((int64_t)blockIdx.x * R + i, a.G - 1);
+    const int g = MODE == kGateUp ? (int)blockIdx.x + i * (a.G / 2) : min((int)blockIdx.x * R + i, a.G - 1);
     wc[i] = a.w_codes + ((int64_t)e * a.G + g) * a.KK * kMxFragCodes;
     ws[i] = a.w_scales + ((int64_t)e * a.G + g) * a.KK * kMxFragScales;
   }
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   for (int64_t t0 = lo + (MODE == kLinear ? (int64_t)blockIdx.y * 32 : 0); t0 < hi; t0 += 32) {
     const int cnt = (int)min((int64_t)32, hi - t0);
     const int64_t pos = t0 + min(n, cnt - 1);  // lanes past the last token repeat it
-    const int64_t arow = MODE == kGateUp ? a.sorted[pos] / a.k : pos;
+    const int64_t arow = MODE == kGateUp ? a.sorted[pos] / a.aux : pos;
     const uint8_t* xc = a.a_codes + arow * (a.KK * 128) + f * 64;
     const uint8_t* xs = a.a_scales + arow * (a.KK * 8) + f * 4;
     float16_t acc[R];
@@ -146,8 +146,8 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
         m = max(m, (uint32_t)__shfl_xor((int)m, 4));
         const uint32_t byte = mx_scale_byte(m);
         const int64_t blk = blockIdx.x;
-        reinterpret_cast<uint16_t*>(a.h_codes + row * a.ldh)[blk * 8 + p] = (uint16_t)mx_encode8(h, byte);
-        if (p == 0) a.h_scales[row * (a.ldh / 16) + blk] = (uint8_t)byte;
+        reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + row * a.ldo)[blk * 8 + p] = (uint16_t)mx_encode8(h, byte);
+        if (p == 0) static_cast<uint8_t*>(a.out_scales)[row * (a.ldo / 16) + blk] = (uint8_t)byte;
         if (blk == 0) zero_h_pad(a, row, p, 8);
       } else {
         float factor = 1.0f;
@@ -158,13 +158,13 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
           uint32_t b = hmax[0][tok];
 #pragma unroll
           for (int k = 1; k < NW; ++k) b = max(b, hmax[k][tok]);
-          const int E = pair_exponent(wp, b, a.w_max[e], a.lg36I);
+          const int E = pair_exponent(wp, b, a.w_max[e], a.aux);
           factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
-          if (blockIdx.x == 0 && p == 0) a.pair_scale[out] = __uint_as_float((uint32_t)(127 + E) << 23);
+          if (blockIdx.x == 0 && p == 0) static_cast<float*>(a.out_scales)[out] = __uint_as_float((uint32_t)(127 + E) << 23);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          const int64_t col = ((int64_t)blockIdx.x * R + i) * 32 + 4 * p;
+          const int col = ((int)blockIdx.x * R + i) * 32 + 4 * p;
           if (MODE == kDown) {  // N % 32 == 0 and the rows are aligned
             if (col < a.N)
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out * a.ldo + col) =
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               if (col + q >= a.N) break;
-              if (a.out_f32) static_cast<float*>(a.out)[out * a.ldo + col + q] = v[i][q];
+              if (a.aux & kMxOutF32) static_cast<float*>(a.out)[out * a.ldo + col + q] = v[i][q];
               else static_cast<uint16_t*>(a.out)[out * a.ldo + col + q] = (uint16_t)bf16_pair(v[i][q], 0.0f);
             }
           }
@@ -229,32 +229,32 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w % WM, wx = w / WM;
 
-  // ---- which tile: each XCD takes one contiguous run of the tile order
-  const int64_t nw = a.n_wtiles;
-  const int64_t mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : a.tiles[0];
-  const int64_t total = mtiles * nw, chunk = (total + 7) / 8;
-  const int64_t at = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= chunk || at >= total) return;
-  int e = 0;
-  int64_t first = 0, rows = a.T, span = mtiles, q = at;
+  // ---- which tile: each XCD takes one contiguous run of the tile order (under 2^23 tiles)
+  const int nw = MODE == kGateUp ? (a.G / 2 + S::kSlots / 2 - 1) / (S::kSlots / 2) : (a.G + S::kSlots - 1) / S::kSlots;
+  const int mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : a.route[0];
+  const int total = mtiles * nw, chunk = (total + 7) / 8, slot = blockIdx.x >> 3;
+  const int at = (int)(blockIdx.x & 7) * chunk + slot;
+  if (slot >= chunk || at >= total) return;
+  int e = 0, rows = a.T, span = mtiles, q = at;
+  int64_t first = 0;
   if (MODE != kLinear) {
-    const int4 t = reinterpret_cast<const int4*>(a.tiles)[1 + at / nw];
+    const int4 t = reinterpret_cast<const int4*>(a.route)[1 + at / nw];
     e = t.x;
-    q = at - (int64_t)t.y * nw;
+    q = at - t.y * nw;
     first = t.z;
-    rows = t.w - first;
+    rows = t.w - t.z;
     span = (rows + S::kTok - 1) / S::kTok;
   }
   // blocks of up to four token tiles by all weight tiles, tokens fastest
-  const int64_t blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min((int64_t)4, span - 4 * blk);
-  const int64_t wt = rem / tc, t0 = (4 * blk + rem - wt * tc) * S::kTok;
-  const int cnt = (int)min((int64_t)S::kTok, rows - t0);
+  const int blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min(4, span - 4 * blk);
+  const int wt = rem / tc, t0 = (4 * blk + rem - wt * tc) * S::kTok;
+  const int cnt = min(S::kTok, rows - t0);
   first += t0;
 
   // weight group of slot s (of kSlots)
-  auto group = [&](int s) -> int64_t {
+  auto group = [&](int s) -> int {
     if (MODE == kGateUp) {  // a wave holds gate groups and the up groups of the same h columns
-      const int64_t half = a.G / 2, hb = wt * (S::kSlots / 2) + (s / GW) * (GW / 2) + s % (GW / 2);
+      const int half = a.G / 2, hb = wt * (S::kSlots / 2) + (s / GW) * (GW / 2) + s % (GW / 2);
       return min(hb, half - 1) + (s % GW >= GW / 2 ? half : 0);
     }
     return min(wt * S::kSlots + s, a.G - 1);
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 
   auto act_row = [&](int t) -> int64_t {  // activation row of the tile's token t (rows past the end repeat the last)
     const int64_t pos = first + min(t, cnt - 1);
-    return MODE == kGateUp ? a.sorted[pos] / a.k : pos;
+    return MODE == kGateUp ? a.sorted[pos] / a.aux : pos;
   };
 
   // ---- DMA sources: this wave's share of the weight pieces, token rows and scales
@@ -489,21 +489,21 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
         }
         m = max(m, (uint32_t)__shfl_xor((int)m, 32));
         const uint32_t byte = mx_scale_byte(m);
-        const int64_t hb = wt * (S::kSlots / 2) + wm * (GW / 2) + i;
+        const int hb = wt * (S::kSlots / 2) + wm * (GW / 2) + i;
         if (in && hb < a.G / 2) {
-          *reinterpret_cast<uint2*>(a.h_codes + row * a.ldh + hb * 16 + f * 8) =
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.ldo + hb * 16 + f * 8) =
               make_uint2(mx_encode8(h, byte), mx_encode8(h + 8, byte));
-          if (f == 0) a.h_scales[row * (a.ldh / 16) + hb] = (uint8_t)byte;
+          if (f == 0) static_cast<uint8_t*>(a.out_scales)[row * (a.ldo / 16) + hb] = (uint8_t)byte;
         }
       }
       if (wt == 0 && wm == 0 && in) zero_h_pad(a, row, f, 2);
-    } else if (MODE == kLinear && a.out_f32) {
+    } else if (MODE == kLinear && (a.aux & kMxOutF32)) {
       if (!in) continue;
 #pragma unroll
       for (int i = 0; i < GW; ++i) {
-        const int64_t col = (wt * S::kSlots + wm * GW + i) * 32 + f * 16;
+        const int col = (wt * S::kSlots + wm * GW + i) * 32 + f * 16;
         float* p = static_cast<float*>(a.out) + row * a.ldo + col;
-        if (a.out_vec && col + 16 <= a.N) {
+        if ((a.aux & kMxOutVec) && col + 16 <= a.N) {
 #pragma unroll
           for (int r = 0; r < 16; r += 4)
             store16_streaming(p + r, __float_as_uint(acc[i][j][r]), __float_as_uint(acc[i][j][r + 1]),
@@ -521,11 +521,11 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
       if constexpr (MODE == kDown) {
         const uint32_t b = max(bh[j], (uint32_t)__shfl_xor((int)bh[j], 32));
         if (in) {
-          const int E = pair_exponent(pair_w[j], b, a.w_max[e], a.lg36I);
+          const int E = pair_exponent(pair_w[j], b, a.w_max[e], a.aux);
           factor = pair_w[j] * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
           if (wm == 0 && f == 0) {
             out_row[tok] = pair[j];
-            if (wt == 0) a.pair_scale[pair[j]] = __uint_as_float((uint32_t)(127 + E) << 23);
+            if (wt == 0) static_cast<float*>(a.out_scales)[pair[j]] = __uint_as_float((uint32_t)(127 + E) << 23);
           }
         }
       }
@@ -542,15 +542,15 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
       }
     }
   }
-  if (MODE == kGateUp || (MODE == kLinear && a.out_f32)) return;
+  if (MODE == kGateUp || (MODE == kLinear && (a.aux & kMxOutF32))) return;
   barrier_after_lds();
   constexpr int kLanes = S::kSlots * 4, kRows = 64 / kLanes;  // lanes that write a row, rows a wave writes at a time
-  const int64_t col = wt * S::kSlots * 32 + (l % kLanes) * 8;
+  const int col = wt * S::kSlots * 32 + (l % kLanes) * 8;
   if (col >= a.N) return;
   for (int t = w * kRows + l / kLanes; t < cnt; t += NW * kRows) {
     const uint4 v = *reinterpret_cast<const uint4*>(smem + t * S::kOutRow + (l % kLanes) * 16);
     uint16_t* p = static_cast<uint16_t*>(a.out) + (MODE == kDown ? (int64_t)out_row[t] : first + t) * a.ldo + col;
-    if (MODE == kDown || (a.out_vec && col + 8 <= a.N)) {
+    if (MODE == kDown || ((a.aux & kMxOutVec) && col + 8 <= a.N)) {
       store16_streaming(p, v.x, v.y, v.z, v.w);
     } else {
       const uint32_t d[4] = {v.x, v.y, v.z, v.w};
@@ -606,18 +606,13 @@ using Mx128x128 = MxTile<4, 2, 2, 2, 4>;
 using Mx256x128 = MxTile<4, 2, 4, 2, 3>;  // 78 KB of LDS: two workgroups a CU
 using Mx256x256 = MxTile<8, 4, 2, 4, 4>;
 
+// max_mtiles: an upper bound on the m-tiles (the experts' schedule knows their number)
 template <int MODE, class S>
-hipError_t launch_tiled(MxArgs a, int64_t E, hipStream_t st) {
+hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
   auto* k = &mx_tiled_kernel<MODE, S>;
   if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), S::kLds)) return e;
   const int64_t rows = MODE == kGateUp ? a.G / 2 : a.G, per = MODE == kGateUp ? S::kSlots / 2 : S::kSlots;
-  a.n_wtiles = (rows + per - 1) / per;
-  int64_t mtiles = (a.T + S::kTok - 1) / S::kTok;
-  if (MODE != kLinear) {
-    const int64_t pairs = a.T * a.k;  // an upper bound: the schedule knows the number
-    mtiles = pairs / S::kTok + (pairs < E ? pairs : E);
-  }
-  const int64_t grid = (mtiles * a.n_wtiles + 7) / 8 * 8;
+  const int64_t grid = (max_mtiles * ((rows + per - 1) / per) + 7) / 8 * 8;
   hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * S::kWaves), S::kLds, st, a);
   return hipGetLastError();
 }
@@ -634,32 +629,25 @@ hipError_t launch_stream(const MxArgs& a, int64_t E, hipStream_t st) {
 
 enum Shape { kStream, k128x64, k128x128, k256x128, k256x256 };
 
-template <int MODE>
-hipError_t launch_shape(Shape s, const MxArgs& a, int64_t E, hipStream_t st) {
-  switch (s) {
-    case kStream: return launch_stream<MODE>(a, E, st);
-    case k128x64: return launch_tiled<MODE, Mx128x64>(a, E, st);
-    case k128x128:
-      if constexpr (MODE == kLinear) return launch_tiled<MODE, Mx128x128>(a, E, st);
-      return hipErrorInvalidValue;
-    case k256x128: return launch_tiled<MODE, Mx256x128>(a, E, st);
-    case k256x256: return launch_tiled<MODE, Mx256x256>(a, E, st);
-  }
-  return hipErrorInvalidValue;
-}
+int shape_tokens(Shape s) { return s == k128x64 ? Mx128x64::kTok : s == k256x256 ? Mx256x256::kTok : Mx256x128::kTok; }
 
-int shape_tokens(Shape s) { return s == k128x64 ? 64 : s == k256x256 ? 256 : 128; }
+// m-tiles of `tok` pairs that E experts can have at most
+int64_t most_mtiles(int64_t pairs, int64_t E, int64_t tok) { return pairs / tok + (pairs < E ? pairs : E); }
 
-Shape linear_shape(const MxArgs& a) {
+// The shape of a dense product.  The streaming kernel reads the weights once
+// per 32 tokens and spreads over all CUs at any size; a tile wants one for each
+// CU, the larger the fewer bytes a product moves.
+Shape linear_shape(int64_t T, int64_t G) {
   const int64_t cus = 256;
-  auto tiles = [&](int64_t rows, int64_t tok) { return (a.G + rows / 32 - 1) / (rows / 32) * ((a.T + tok - 1) / tok); };
-  if (a.T <= 32 || tiles(32, 32) <= cus) return kStream;
+  auto tiles = [&](int64_t rows, int64_t tok) { return (G + rows / 32 - 1) / (rows / 32) * ((T + tok - 1) / tok); };
+  if (T <= 32 || tiles(32, 32) <= cus) return kStream;
   if (tiles(256, 256) >= cus * 3 / 4) return k256x256;
   if (tiles(256, 128) >= cus * 3 / 4) return k256x128;
   if (tiles(128, 128) >= cus / 2) return k128x128;
   return k128x64;
 }
 
+// The shape of a stage of the experts' FFN over weights of `rows` rows.
 Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   if (pairs <= 32 * E && (pairs < E ? pairs : E) * (rows / 32) <= 2048) return kStream;
   const int64_t tiles = (pairs / 128 + (pairs < E ? pairs : E) / 2) * ((rows + 255) / 256);
@@ -667,26 +655,43 @@ Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   return pairs < 128 * E || KK < 16 ? k256x128 : k256x256;
 }
 
-}  // namespace
-
-int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E) {
-  const int64_t pairs = T * k;
-  return pairs / Mx128x64::kTok + (pairs < E ? pairs : E);
+template <int MODE>
+hipError_t launch_experts_stage(MxArgs a, Shape s, const MxExperts& x, const int32_t* tiles, hipStream_t st) {
+  a.route = s == kStream ? x.offsets : tiles;
+  const int64_t mtiles = most_mtiles(x.T * x.k, x.E, shape_tokens(s));
+  switch (s) {
+    case kStream: return launch_stream<MODE>(a, x.E, st);
+    case k128x64: return launch_tiled<MODE, Mx128x64>(a, mtiles, st);
+    case k256x256: return launch_tiled<MODE, Mx256x256>(a, mtiles, st);
+    default: return launch_tiled<MODE, Mx256x128>(a, mtiles, st);
+  }
 }
 
-hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) { return launch_shape<kLinear>(linear_shape(a), a, 1, st); }
+}  // namespace
 
-hipError_t launch_mx_experts(MxArgs gate_up, MxArgs down, int64_t E, hipStream_t st) {
-  const int64_t pairs = gate_up.T * gate_up.k;
-  const Shape s0 = experts_shape(pairs, E, gate_up.N, gate_up.KK),
-              s1 = experts_shape(pairs, E, down.N, down.KK);
+int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E) { return most_mtiles(T * k, E, Mx128x64::kTok); }
+
+hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
+  const int64_t T = a.T;
+  switch (linear_shape(T, a.G)) {
+    case kStream: return launch_stream<kLinear>(a, 1, st);
+    case k128x64: return launch_tiled<kLinear, Mx128x64>(a, (T + 63) / 64, st);
+    case k128x128: return launch_tiled<kLinear, Mx128x128>(a, (T + 127) / 128, st);
+    case k256x128: return launch_tiled<kLinear, Mx256x128>(a, (T + 127) / 128, st);
+    default: return launch_tiled<kLinear, Mx256x256>(a, (T + 255) / 256, st);
+  }
+}
+
+hipError_t launch_mx_experts(MxExperts x, hipStream_t st) {
+  const int64_t pairs = x.T * x.k;
+  const Shape s0 = experts_shape(pairs, x.E, x.gate_up.N, x.gate_up.KK), s1 = experts_shape(pairs, x.E, x.down.N, x.down.KK);
   if (s0 != kStream || s1 != kStream) {
-    hipLaunchKernelGGL(mx_schedule_kernel, dim3(2), dim3(256), 0, st, gate_up.offsets, (int)E, shape_tokens(s0),
-                       shape_tokens(s1), gate_up.tiles, down.tiles);
+    hipLaunchKernelGGL(mx_schedule_kernel, dim3(2), dim3(256), 0, st, x.offsets, (int)x.E, shape_tokens(s0),
+                       shape_tokens(s1), x.tiles[0], x.tiles[1]);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  if (hipError_t e = launch_shape<kGateUp>(s0, gate_up, E, st)) return e;
-  return launch_shape<kDown>(s1, down, E, st);
+  if (hipError_t e = launch_experts_stage<kGateUp>(x.gate_up, s0, x, x.tiles[0], st)) return e;
+  return launch_experts_stage<kDown>(x.down, s1, x, x.tiles[1], st);
 }
 
 }  // namespace moe

@@ -75,18 +75,16 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uin
 
 }  // namespace
 
-// NW waves per row, V chunks of 8 columns per lane; the row stays in registers
+// A workgroup is a row: NW waves, V chunks of 8 columns per lane; the row stays in registers
 // between the passes.  POST: the row is y, and the first norm, gate, residual
 // scale and residual give r'; otherwise the row is x itself.  Everything the
 // row needs is loaded before the first sum, so that one memory latency covers
 // it; the sums are FP32, in a fixed order.
 template <int NW, int V, bool POST, bool YF32, bool VEC>
-__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
-  constexpr int kRows = 4 / NW;  // rows per workgroup of 256 threads
+__global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
   __shared__ float lds[2][4];
-  const int w = (threadIdx.x >> 6) % NW, t = threadIdx.x % (64 * NW);
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (64 * NW);
-  if (NW == 1 && row >= a.T) return;  // with several waves a row is a workgroup
+  const int w = threadIdx.x >> 6, t = threadIdx.x;
+  const int64_t row = blockIdx.x;
   const int H = (int)a.H;
   const bool follow = !POST || a.w != nullptr;
   float x[V][8];
@@ -99,7 +97,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     if constexpr (POST) rr[v] = load8_bf16<VEC>(a.r + row * a.ldr, c, H);
   }
   if constexpr (POST) {
-    if (a.gate && a.gate_cs != 0) {
+    if (a.gate && !a.gate_row) {
 #pragma unroll
       for (int v = 0; v < V; ++v) gg[v] = load8_bf16<VEC>(a.gate + row * a.gate_rs, (v * 64 * NW + t) * 8, H);
     }
@@ -113,7 +111,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     for (int v = 0; v < V; ++v) wn[v] = load8_bf16<VEC>(a.w, (v * 64 * NW + t) * 8, H);
   }
   if constexpr (POST) {
-    const float g_row = a.gate && a.gate_cs == 0 ? bf16_to_f32(a.gate[row * a.gate_rs]) : 1.0f;
+    const float g_row = a.gate && a.gate_row ? bf16_to_f32(a.gate[row * a.gate_rs]) : 1.0f;
     float inv = 1.0f;
     if (a.w_post) {
       float sq = 0.0f;
@@ -129,12 +127,12 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
       uint32_t o[8];
       unpack8(rr[v], rv);
       if (a.w_post) unpack8(wp[v], wv);
-      if (a.gate && a.gate_cs != 0) unpack8(gg[v], gv);
+      if (a.gate && !a.gate_row) unpack8(gg[v], gv);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float z = x[v][i];
         if (a.w_post) z = z * inv * wv[i];
-        if (a.gate) z *= a.gate_cs != 0 ? gv[i] : g_row;
+        if (a.gate) z *= a.gate_row ? g_row : gv[i];
         o[i] = bf16_bits_rne(fmaf(a.scale, z, rv[i]));
         x[v][i] = bf16_to_f32(o[i]);  // the next norm reads the residual that is kept
       }
@@ -168,9 +166,9 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
       float q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) q[i] = bf16_to_f32(o[i]);
-      if (c < a.Hp) {
-        reinterpret_cast<uint32_t*>(a.codes)[(row * a.Hp + c) / 8] = mx_encode8(q, byte);
-        if ((t & 3) == 0) a.scales[(row * a.Hp + c) / 32] = (uint8_t)byte;
+      if (c < (int)a.Hp) {
+        reinterpret_cast<uint32_t*>(a.codes)[(row * (int)a.Hp + c) / 8] = mx_encode8(q, byte);
+        if ((t & 3) == 0) a.scales[(row * (int)a.Hp + c) / 32] = (uint8_t)byte;
       }
     }
   }
@@ -179,38 +177,39 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
 namespace {
 
 template <int NW, int V, bool POST>
-void launch_norm_as(const NormArgs& a, bool vec, hipStream_t st) {
-  const dim3 grid((unsigned)((a.T * NW + 3) / 4));
+void launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, bool vec, hipStream_t st) {
+  const dim3 grid((unsigned)T), block(64 * NW);
   if constexpr (POST) {
-    if (a.y_f32) {
-      if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, true>), grid, dim3(256), 0, st, a);
-      else hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, false>), grid, dim3(256), 0, st, a);
+    if (y_f32) {
+      if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, true>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, false>), grid, block, 0, st, a);
       return;
     }
   }
-  if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, true>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, false>), grid, dim3(256), 0, st, a);
+  if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, false>), grid, block, 0, st, a);
 }
 
+// The fewest lanes that hold a row in a few chunks each: a wave alone needs no barrier.
 template <bool POST>
-void launch_norm_shape(const NormArgs& a, bool vec, hipStream_t st) {
-  const int64_t cols = a.Hp;  // columns that a row's lanes cover (the padded row when it is quantised)
-  if (cols <= 512) launch_norm_as<1, 1, POST>(a, vec, st);
-  else if (cols <= 1024) launch_norm_as<1, 2, POST>(a, vec, st);
-  else if (cols <= 2048) launch_norm_as<4, 1, POST>(a, vec, st);
-  else if (cols <= 4096) launch_norm_as<4, 2, POST>(a, vec, st);
-  else if (cols <= 6144) launch_norm_as<4, 3, POST>(a, vec, st);
-  else if (cols <= 8192) launch_norm_as<4, 4, POST>(a, vec, st);
-  else launch_norm_as<4, 8, POST>(a, vec, st);
+void launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, bool vec, hipStream_t st) {
+  const int cols = (int)a.Hp;
+  if (cols <= 512) launch_norm_as<1, 1, POST>(a, T, y_f32, vec, st);
+  else if (cols <= 1024) launch_norm_as<1, 2, POST>(a, T, y_f32, vec, st);
+  else if (cols <= 2048) launch_norm_as<4, 1, POST>(a, T, y_f32, vec, st);
+  else if (cols <= 4096) launch_norm_as<4, 2, POST>(a, T, y_f32, vec, st);
+  else if (cols <= 6144) launch_norm_as<4, 3, POST>(a, T, y_f32, vec, st);
+  else if (cols <= 8192) launch_norm_as<4, 4, POST>(a, T, y_f32, vec, st);
+  else launch_norm_as<4, 8, POST>(a, T, y_f32, vec, st);
 }
 
 }  // namespace
 
 int64_t norm_max_cols() { return 16384; }
 
-hipError_t launch_norm(const NormArgs& a, bool post, bool vec, hipStream_t st) {
-  if (post) launch_norm_shape<true>(a, vec, st);
-  else launch_norm_shape<false>(a, vec, st);
+hipError_t launch_norm(const NormArgs& a, int64_t T, bool post, bool y_f32, bool vec, hipStream_t st) {
+  if (post) launch_norm_shape<true>(a, T, y_f32, vec, st);
+  else launch_norm_shape<false>(a, T, false, vec, st);
   return hipGetLastError();
 }
 

@@ -41,6 +41,9 @@ def _stream(stream) -> int:
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, contiguous: bool = True) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape)
+            and (not contiguous or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -510,12 +513,6 @@ _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 _U8 = torch.uint8
 
 
-def _ok(t, name: str, dtype: torch.dtype, shape) -> None:
-    """_need, with the passing case first."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
-        _need(t, name, dtype, shape)
-
-
 def _rows(t: torch.Tensor, name: str, dtypes=(torch.bfloat16,)) -> int:
     """Checks a [rows, cols] GPU matrix with unit column stride; returns its row stride."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
@@ -551,11 +548,11 @@ def _mx_rows(rows: int, cols: int, like: torch.Tensor, codes, scales):
     if codes is None:
         codes = like.new_empty((rows, c // 2), dtype=_U8)
     else:
-        _ok(codes, "codes", _U8, (rows, c // 2))
+        _need(codes, "codes", _U8, (rows, c // 2))
     if scales is None:
         scales = codes.new_empty((rows, c // 32))
     else:
-        _ok(scales, "scales", _U8, (rows, c // 32))
+        _need(scales, "scales", _U8, (rows, c // 32))
     return codes, scales
 
 
@@ -572,8 +569,8 @@ def _need_mx_rows(codes, scales, name: str, cols: int) -> int:
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise ValueError(f"{name}_codes must be a tensor [rows, {c // 2}]")
     rows = codes.shape[0]
-    _ok(codes, f"{name}_codes", _U8, (rows, c // 2))
-    _ok(scales, f"{name}_scales", _U8, (rows, c // 32))
+    _need(codes, f"{name}_codes", _U8, (rows, c // 2))
+    _need(scales, f"{name}_scales", _U8, (rows, c // 32))
     return rows
 
 
@@ -628,7 +625,7 @@ def mxfp4_pack_weights(codes: torch.Tensor, scales: torch.Tensor, stream=None):
     b, n, kh = codes.shape
     if kh % 16:
         raise ValueError("K must be a multiple of 32")
-    _ok(scales, "scales", torch.uint8, (b, n, kh // 16))
+    _need(scales, "scales", torch.uint8, (b, n, kh // 16))
     cs, ss = _mx_weight_shapes(n, 2 * kh)
     dev = codes.device
     pc = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
@@ -643,8 +640,8 @@ def mxfp4_unpack_weights(codes: torch.Tensor, scales: torch.Tensor, N: int, K: i
     """Packed weights of [batch, N, K] -> canonical (codes [batch, N, K/2], scales [batch, N, K/32])."""
     cs, ss = _mx_weight_shapes(N, K)
     b = codes.shape[0]
-    _ok(codes, "codes", torch.uint8, (b, *cs))
-    _ok(scales, "scales", torch.uint8, (b, *ss))
+    _need(codes, "codes", torch.uint8, (b, *cs))
+    _need(scales, "scales", torch.uint8, (b, *ss))
     if K % 32:
         raise ValueError("K must be a multiple of 32")
     oc = torch.empty((b, N, K // 2), dtype=torch.uint8, device=codes.device)
@@ -667,8 +664,8 @@ def mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.
     K = 256 * w_codes.shape[1]  # the padded width: the padding is zero on both sides
     T = _need_mx_rows(x_codes, x_scales, "x", K)
     cs, ss = _mx_weight_shapes(N, K)
-    _ok(w_codes, "w_codes", _U8, cs)
-    _ok(w_scales, "w_scales", _U8, ss)
+    _need(w_codes, "w_codes", _U8, cs)
+    _need(w_scales, "w_scales", _U8, ss)
     y, ldy = _out(y, "y", x_codes, _out_type(out_dtype, y), T, N)
     nbytes = mxfp4_linear_workspace_bytes(T, K, N)
     ws = _workspace(nbytes, x_codes.device, workspace) if nbytes or workspace is not None else None
@@ -690,23 +687,23 @@ def mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_sca
     T = _need_mx_rows(x_codes, x_scales, "x", H)
     E = w13_codes.shape[0]
     cs, ss = _mx_weight_shapes(2 * I, H, E)
-    _ok(w13_codes, "w13_codes", _U8, cs)
-    _ok(w13_scales, "w13_scales", _U8, ss)
+    _need(w13_codes, "w13_codes", _U8, cs)
+    _need(w13_scales, "w13_scales", _U8, ss)
     cs, ss = _mx_weight_shapes(H, I, E)
-    _ok(w2_codes, "w2_codes", _U8, cs)
-    _ok(w2_scales, "w2_scales", _U8, ss)
-    _ok(w2_max_scale, "w2_max_scale", torch.int32, (E,))
-    _ok(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
-    _ok(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
-    _ok(topk_w, "topk_w", torch.float32, (T, k))
+    _need(w2_codes, "w2_codes", _U8, cs)
+    _need(w2_scales, "w2_scales", _U8, ss)
+    _need(w2_max_scale, "w2_max_scale", torch.int32, (E,))
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
+    _need(topk_w, "topk_w", torch.float32, (T, k))
     if pair_out is None:
         pair_out = x_codes.new_empty((T * k, H), dtype=torch.float16)
     else:
-        _ok(pair_out, "pair_out", torch.float16, (T * k, H))
+        _need(pair_out, "pair_out", torch.float16, (T * k, H))
     if pair_scale is None:
         pair_scale = topk_w.new_empty((T * k,))
     else:
-        _ok(pair_scale, "pair_scale", torch.float32, (T * k,))
+        _need(pair_scale, "pair_scale", torch.float32, (T * k,))
     nbytes = mxfp4_ffn_workspace_bytes(T, k, E, H, I)
     ws = x_codes.new_empty((max(nbytes, 1),)) if workspace is None else workspace
     st = lib().mxfp4_grouped_ffn(_p(x_codes), _p(x_scales), T, H, _p(w13_codes), _p(w13_scales), _p(w2_codes),
@@ -736,7 +733,7 @@ def moe_norm_in(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, n=None, qua
     from the same pass; n=False then skips the BF16 result."""
     ldx = _rows(x, "x")
     T, H = x.shape
-    _ok(w, "w", torch.bfloat16, (H,))
+    _need(w, "w", torch.bfloat16, (H,))
     n, ldn, codes, scales = _norm_outputs(x, T, H, n, quantize, codes, scales)
     st = lib().moe_norm_in(_p(x), T, H, ldx, _p(w), eps, _p(n), ldn, _p(codes), _p(scales), _stream(stream))
     check(st, "moe_norm_in")
@@ -757,9 +754,9 @@ def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch
     if residual.shape != (T, H):
         raise ValueError(f"residual must have shape {(T, H)}, got {tuple(residual.shape)}")
     if w_post is not None:
-        _ok(w_post, "w_post", torch.bfloat16, (H,))
+        _need(w_post, "w_post", torch.bfloat16, (H,))
     if w_next is not None:
-        _ok(w_next, "w_next", torch.bfloat16, (H,))
+        _need(w_next, "w_next", torch.bfloat16, (H,))
     grs = gcs = 0
     if gate is not None:
         _need(gate, "gate", torch.bfloat16, contiguous=False)

@@ -76,6 +76,8 @@ def test_linear_refusals(L):
     assert lin(dt=1, y=ODD) == ALIGN
     assert lin(T=0, x=None, xs=None, y=None) == OK
     assert lin(T=1 << 20, K=8192) == SHAPE  # 4 GiB of x codes
+    assert lin(N=(1 << 27) + 1, ldy=1 << 28) == SHAPE and lin(T=1 << 20, N=1 << 21, ldy=1 << 21) == SHAPE
+    assert lin(ldy=1 << 31) == SHAPE
     if ws:
         assert lin(wsp=None) == WORKSPACE and lin(wsb=ws - 1) == WORKSPACE and lin(wsp=ODD) == ALIGN
 
@@ -100,6 +102,7 @@ def test_ffn_refusals(L):
     assert ffn(T=0, x=None) == OK
     assert ffn(T=1 << 21, H=4096) == SHAPE  # 4 GiB of x codes
     assert ffn(T=1 << 21, I=4096, H=32) == SHAPE  # 4 GiB of h codes
+    assert ffn(T=1 << 20, I=32, H=1 << 16) == SHAPE and ffn(T=1 << 18, I=32, H=1 << 18) == SHAPE  # too many tiles
 
 
 def test_norm_refusals(L):
@@ -113,13 +116,13 @@ def test_norm_refusals(L):
     nan = float("nan")
     for call in (nin, nout):
         refuses(call, x=[(None, NULL), (BYTE, ALIGN)], T=[(-1, SHAPE), (1 << 24, SHAPE)],
-                H=[(0, SHAPE), (16385, SHAPE), (40, SHAPE)], ldx=[(63, SHAPE)], eps=[(-1.0, SHAPE), (nan, SHAPE)],
-                n=[(BYTE, ALIGN)], ldn=[(63, SHAPE)], c=[(None, NULL), (ODD, ALIGN)], s=[(None, NULL)], w=[(BYTE, ALIGN)])
+                H=[(0, SHAPE), (16385, SHAPE), (40, SHAPE)], ldx=[(63, SHAPE), (1 << 31, SHAPE)], eps=[(-1.0, SHAPE), (nan, SHAPE)],
+                n=[(BYTE, ALIGN)], ldn=[(63, SHAPE), (1 << 31, SHAPE)], c=[(None, NULL), (ODD, ALIGN)], s=[(None, NULL)], w=[(BYTE, ALIGN)])
         assert call(n=None, c=None, s=None) == NULL
         assert call(T=0) == OK
     assert nin(w=None) == NULL
-    refuses(nout, dt=[(2, SHAPE)], r=[(None, NULL), (BYTE, ALIGN)], ldr=[(63, SHAPE)], ldro=[(63, SHAPE)],
-            ro=[(None, NULL)], grs=[(-1, SHAPE)], gcs=[(2, SHAPE)], wp=[(BYTE, ALIGN)], g=[(BYTE, ALIGN)], w=[(None, NULL)])
+    refuses(nout, dt=[(2, SHAPE)], r=[(None, NULL), (BYTE, ALIGN)], ldr=[(63, SHAPE), (1 << 31, SHAPE)], ldro=[(63, SHAPE)],
+            ro=[(None, NULL)], grs=[(-1, SHAPE), (1 << 31, SHAPE)], gcs=[(2, SHAPE)], wp=[(BYTE, ALIGN)], g=[(BYTE, ALIGN)], w=[(None, NULL)])
     assert nout(dt=1, x=ODD) == ALIGN
 
 
