@@ -470,7 +470,7 @@ def hadamard_rotate_bf16(src: torch.Tensor, signs: Optional[torch.Tensor], block
         out = torch.empty(src.shape, dtype=torch.bfloat16, device=src.device)
     _need(out, "out", torch.bfloat16, tuple(src.shape), contiguous=False)
     o2 = out.reshape(-1, cols) if out.dim() != 2 else out
-    if o2.data_p() != out.data_ptr() or (out.dim() != 2 and not out.is_contiguous()):
+    if o2.data_ptr() != out.data_ptr() or (out.dim() != 2 and not out.is_contiguous()):
         raise ValueError("out must be 2-D or contiguous")
     if signs is not None:
         _need(signs, "signs", torch.float32, (cols,))
