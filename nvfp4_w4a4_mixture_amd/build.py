@@ -1,4 +1,4 @@
-"""Build libmoe_nvfp4.so in-tree with hipcc for gfx950.
+"""Build libmoe_nvfp4.so in-tree with hipcc for gfx950, and the compiled part of its Python binding.
 
 Usage: ``python -m nvfp4_w4a4_mixture_amd.build`` (also called by
 ``__graft_entry__.build()``).  Every source is compiled on every call.
@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libmoe_nvfp4.so"
 SOURCES = ["quantize.hip", "route.hip", "ffn.hip", "combine.hip", "prune.hip", "shared.hip", "rotate.hip", "mx_quantize.hip",
            "mx_product.hip", "norm.hip", "api.cpp", "api_mx.cpp"]
+
+BINDING = os.path.join(PKG, "_binding.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -50,9 +53,28 @@ def _compile(src: str, build_dir: str = BUILD_DIR, defines=(), extra=()) -> str:
     return obj
 
 
+def build_binding() -> str:
+    """Compile csrc/py_binding.cpp against the installed torch and Python headers; returns its path."""
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [f"-I{d}" for d in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"])]
+    libs = cpp_extension.TORCH_LIB_PATH
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, os.path.join(CSRC, "py_binding.cpp"),
+           "-o", tmp, f"-L{libs}", "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling the binding failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    shutil.move(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, out_dir: str = OUT_DIR, build_dir: str = BUILD_DIR, defines=(),
           sanitize: bool = False) -> str:
-    """Compile every source and link ``<out_dir>/libmoe_nvfp4.so``; returns its path.
+    """Compile every source and link ``<out_dir>/libmoe_nvfp4.so``; returns its path.  The product
+    build (the default ``out_dir``) compiles the binding too.
 
     ``defines`` (NAME=VALUE strings) override compile-time tile parameters.  ``sanitize``
     instruments the host code with AddressSanitizer and UndefinedBehaviorSanitizer (the library
@@ -64,8 +86,11 @@ def build(verbose: bool = False, out_dir: str = OUT_DIR, build_dir: str = BUILD_
     extra = SANITIZE_HOST if sanitize else []
     os.makedirs(build_dir, exist_ok=True)
     os.makedirs(out_dir, exist_ok=True)
-    with ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding) if out_dir == OUT_DIR else None
         objs = list(ex.map(lambda src: _compile(src, build_dir, defines, extra), SOURCES))
+        if binding is not None:
+            binding.result()
     tmp = os.path.join(out_dir, LIB_NAME + ".tmp")
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *extra, *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

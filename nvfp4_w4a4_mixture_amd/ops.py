@@ -8,7 +8,7 @@ non-OK status.  Every step of the layer runs in the library's HIP kernels.
 
 from __future__ import annotations
 
-import functools
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -24,10 +24,6 @@ __all__ = ["moe_route", "moe_route_quantize", "nvfp4_quantize_act", "nvfp4_quant
            "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_quantize_weights", "mxfp4_pack_weights", "mxfp4_unpack_weights",
            "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn",
            "moe_norm_in", "moe_norm_out"]
-
-
-# Single-token calls last a few microseconds on the device, so the host side counts: pointers and the stream go to the
-# library as plain integers, and a check that passes is a few attribute reads.
 
 
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -320,13 +316,7 @@ def _need_pairs(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k: int
 
 def moe_combine(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k: int,
                 out_dtype: torch.dtype = torch.bfloat16, y=None, stream=None) -> torch.Tensor:
-    H = _need_pairs(pair_out, pair_scale, T, k)
-    code = {torch.bfloat16: 0, torch.float32: 1}[out_dtype]
-    if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=pair_out.device)
-    st = lib().moe_combine(_p(pair_out), _p(pair_scale), T, k, H, code, _p(y), _stream(stream))
-    check(st, "moe_combine")
-    return y
+    return _b.moe_combine(pair_out, pair_scale, T, k, _DTYPE[out_dtype], y, stream)
 
 
 def moe_combine_reap(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k: int, pair_sqnorm, topk_w,
@@ -507,97 +497,48 @@ def moe_nvfp4_unpack_weights(codes: torch.Tensor, packed_scales: torch.Tensor, k
     return _relayout("moe_nvfp4_unpack_weights", codes, packed_scales, kind, False, stream)
 
 
-# ---- MXFP4 operators
+# ---- MXFP4 operators and block norms: checks, allocation and the call are compiled (csrc/py_binding.cpp)
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
-_U8 = torch.uint8
 
 
-def _rows(t: torch.Tensor, name: str, dtypes=(torch.bfloat16,)) -> int:
-    """Checks a [rows, cols] GPU matrix with unit column stride; returns its row stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-        raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU device")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be [rows, cols] with unit column stride")
-    rows, cols = t.shape
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1 and rows > 0:
-        raise ValueError(f"{name} must be [rows, cols] with unit column stride")
-    return ld if rows > 1 else max(cols, 1)
+def _bound():
+    """The compiled binding, with the loaded library's entry points."""
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the compiled binding is not built; run `python -m nvfp4_w4a4_mixture_amd.build`") from e
+    names = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear_workspace_bytes", "mxfp4_linear",
+             "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine")
+    _binding.bind(check, _stream, *(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names))
+    return _binding
 
 
-def _mx_padded(cols: int) -> int:
-    return -(-cols // 256) * 256
+_b = _bound()
 
 
-def _out(t, name: str, like: torch.Tensor, dtype: torch.dtype, rows: int, cols: int):
-    """An output matrix and its row stride: a given one checked (any row stride), a missing one allocated."""
-    if t is None:
-        return like.new_empty((rows, cols), dtype=dtype), cols
-    ld = _rows(t, name, (dtype,))
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
-    return t, ld
-
-
-def _mx_rows(rows: int, cols: int, like: torch.Tensor, codes, scales):
-    """The codes and scales of [rows, cols] in the padded row form: given ones checked, missing ones allocated."""
-    c = _mx_padded(cols)
-    if codes is None:
-        codes = like.new_empty((rows, c // 2), dtype=_U8)
-    else:
-        _need(codes, "codes", _U8, (rows, c // 2))
-    if scales is None:
-        scales = codes.new_empty((rows, c // 32))
-    else:
-        _need(scales, "scales", _U8, (rows, c // 32))
-    return codes, scales
-
-
-def _out_type(out_dtype: torch.dtype, out) -> torch.dtype:
-    """The type of the result: that of a given output, or the one asked for; BF16 or FP32."""
+def _code(out_dtype: torch.dtype, out) -> int:
+    """0 (BF16) or 1 (FP32): the type of a given output, or the one asked for."""
     dtype = out_dtype if out is None else out.dtype
     if dtype not in _DTYPE:
         raise TypeError(f"the output type must be torch.bfloat16 or torch.float32, got {dtype}")
-    return dtype
+    return _DTYPE[dtype]
 
 
-def _need_mx_rows(codes, scales, name: str, cols: int) -> int:
-    c = _mx_padded(cols)
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
-        raise ValueError(f"{name}_codes must be a tensor [rows, {c // 2}]")
-    rows = codes.shape[0]
-    _need(codes, f"{name}_codes", _U8, (rows, c // 2))
-    _need(scales, f"{name}_scales", _U8, (rows, c // 32))
-    return rows
-
-
-@functools.lru_cache(maxsize=4096)
-def _mx_weight_shapes(N: int, K: int, *batch: int):
+def _mx_weight_shapes(N: int, K: int):
     g, kk = -(-N // 32), -(-K // 256)
-    return (*batch, g, kk, 4, 64, 16), (*batch, g, kk, 64, 4)
+    return (g, kk, 4, 64, 16), (g, kk, 64, 4)
 
 
 def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
     """x [rows, cols] BF16 or FP32 -> (codes [rows, Cp/2], scales [rows, Cp/32]), Cp = cols rounded up to 256."""
-    ld = _rows(x, "x", (torch.bfloat16, torch.float32))
-    rows, cols = x.shape
-    codes, scales = _mx_rows(rows, cols, x, codes, scales)
-    st = lib().mxfp4_quantize(_p(x), _DTYPE[x.dtype], rows, cols, ld, _p(codes), _p(scales), _stream(stream))
-    check(st, "mxfp4_quantize")
-    return codes, scales
+    return _b.mxfp4_quantize(x, codes, scales, stream)
 
 
 def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out_dtype: torch.dtype = torch.bfloat16,
                      out=None, stream=None) -> torch.Tensor:
     """The values that the codes stand for, [rows, cols] in BF16 or FP32 (exact in both)."""
-    rows = _need_mx_rows(codes, scales, "x", cols)
-    out, ld = _out(out, "out", codes, _out_type(out_dtype, out), rows, cols)
-    st = lib().mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _DTYPE[out.dtype], _p(out), ld, _stream(stream))
-    check(st, "mxfp4_dequantize")
-    return out
+    return _b.mxfp4_dequantize(codes, scales, cols, _code(out_dtype, out), out, stream)
 
 
 def mxfp4_quantize_weights(w_bf16: torch.Tensor, stream=None):
@@ -651,7 +592,6 @@ def mxfp4_unpack_weights(codes: torch.Tensor, scales: torch.Tensor, N: int, K: i
     return oc, os_
 
 
-@functools.lru_cache(maxsize=4096)
 def mxfp4_linear_workspace_bytes(T: int, K: int, N: int) -> int:
     return int(lib().mxfp4_linear_workspace_bytes(T, K, N))
 
@@ -659,23 +599,9 @@ def mxfp4_linear_workspace_bytes(T: int, K: int, N: int) -> int:
 def mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.dtype = torch.bfloat16, y=None,
                  workspace=None, stream=None) -> torch.Tensor:
     """y [T, N] = x W^T for quantized x (mxfp4_quantize) and packed weights w_codes [G, KK, 4, 64, 16]."""
-    if w_codes.dim() != 5:
-        raise ValueError("w_codes must be [G, KK, 4, 64, 16]")
-    K = 256 * w_codes.shape[1]  # the padded width: the padding is zero on both sides
-    T = _need_mx_rows(x_codes, x_scales, "x", K)
-    cs, ss = _mx_weight_shapes(N, K)
-    _need(w_codes, "w_codes", _U8, cs)
-    _need(w_scales, "w_scales", _U8, ss)
-    y, ldy = _out(y, "y", x_codes, _out_type(out_dtype, y), T, N)
-    nbytes = mxfp4_linear_workspace_bytes(T, K, N)
-    ws = _workspace(nbytes, x_codes.device, workspace) if nbytes or workspace is not None else None
-    st = lib().mxfp4_linear(_p(x_codes), _p(x_scales), T, K, _p(w_codes), _p(w_scales), N, _DTYPE[y.dtype], _p(y), ldy,
-                            _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
-    check(st, "mxfp4_linear")
-    return y
+    return _b.mxfp4_linear(x_codes, x_scales, w_codes, w_scales, N, _code(out_dtype, y), y, workspace, stream)
 
 
-@functools.lru_cache(maxsize=4096)
 def mxfp4_ffn_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
     return int(lib().mxfp4_ffn_workspace_bytes(T, k, E, H, I))
 
@@ -684,100 +610,26 @@ def mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_sca
                       k: int, expert_offsets, sorted_pair_ids, topk_w, pair_out=None, pair_scale=None, workspace=None,
                       stream=None):
     """The routed experts' FFN in MXFP4: (pair_out, pair_scale), what moe_combine and moe_combine_block read."""
-    T = _need_mx_rows(x_codes, x_scales, "x", H)
-    E = w13_codes.shape[0]
-    cs, ss = _mx_weight_shapes(2 * I, H, E)
-    _need(w13_codes, "w13_codes", _U8, cs)
-    _need(w13_scales, "w13_scales", _U8, ss)
-    cs, ss = _mx_weight_shapes(H, I, E)
-    _need(w2_codes, "w2_codes", _U8, cs)
-    _need(w2_scales, "w2_scales", _U8, ss)
-    _need(w2_max_scale, "w2_max_scale", torch.int32, (E,))
-    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
-    _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
-    _need(topk_w, "topk_w", torch.float32, (T, k))
-    if pair_out is None:
-        pair_out = x_codes.new_empty((T * k, H), dtype=torch.float16)
-    else:
-        _need(pair_out, "pair_out", torch.float16, (T * k, H))
-    if pair_scale is None:
-        pair_scale = topk_w.new_empty((T * k,))
-    else:
-        _need(pair_scale, "pair_scale", torch.float32, (T * k,))
-    nbytes = mxfp4_ffn_workspace_bytes(T, k, E, H, I)
-    ws = x_codes.new_empty((max(nbytes, 1),)) if workspace is None else workspace
-    st = lib().mxfp4_grouped_ffn(_p(x_codes), _p(x_scales), T, H, _p(w13_codes), _p(w13_scales), _p(w2_codes),
-                                 _p(w2_scales), _p(w2_max_scale), E, I, k, _p(expert_offsets), _p(sorted_pair_ids),
-                                 _p(topk_w), _p(pair_out), _p(pair_scale), _p(ws), ws.numel(), _stream(stream))
-    check(st, "mxfp4_grouped_ffn")
-    return pair_out, pair_scale
-
-
-# ---- norms around the block
-
-
-def _norm_outputs(like: torch.Tensor, T: int, H: int, n, quantize: bool, codes, scales):
-    """Output n (False: none) and, if asked for, its codes and scales."""
-    if n is False:
-        n, ldn = None, H
-    else:
-        n, ldn = _out(n, "n", like, torch.bfloat16, T, H)
-    if quantize or codes is not None or scales is not None:
-        codes, scales = _mx_rows(T, H, like, codes, scales)
-    return n, ldn, codes, scales
+    return _b.mxfp4_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_scales, w2_max_scale, H, I, k,
+                                expert_offsets, sorted_pair_ids, topk_w, pair_out, pair_scale, workspace,
+                                stream)
 
 
 def moe_norm_in(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, n=None, quantize: bool = False, codes=None,
                 scales=None, stream=None):
     """n = bf16(x / rms(x) * w).  quantize=True (or codes/scales given): (n, codes, scales), the MXFP4 form of n
     from the same pass; n=False then skips the BF16 result."""
-    ldx = _rows(x, "x")
-    T, H = x.shape
-    _need(w, "w", torch.bfloat16, (H,))
-    n, ldn, codes, scales = _norm_outputs(x, T, H, n, quantize, codes, scales)
-    st = lib().moe_norm_in(_p(x), T, H, ldx, _p(w), eps, _p(n), ldn, _p(codes), _p(scales), _stream(stream))
-    check(st, "moe_norm_in")
-    return n if codes is None else (n, codes, scales)
+    return _b.moe_norm_in(x, w, eps, n, quantize, codes, scales, stream)
 
 
 def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch.Tensor] = None,
                  w_next: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                  residual_scale: float = 1.0, eps: float = 1e-6, out=None, n=None, quantize: bool = False, codes=None,
                  scales=None, stream=None):
-    """r' = bf16(residual + residual_scale * gate * (y / rms(y) * w_post)); with w_next also n = bf16(r' / rms(r') * w_next).
+    """r' = bf16(residual + residual_scale * gate * (y / rms(y) * w_post)); with w_next also n = bf16(r' / rms(r') *
+    w_next).
 
     w_post None: y is not normed.  gate: None, or BF16 [T, 1], [1, H] or [T, H].  Returns r', or (r', n), or
     (r', n, codes, scales) when n is quantized to MXFP4 as well (n=False then skips the BF16 n)."""
-    ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
-    T, H = y.shape
-    ldr = _rows(residual, "residual")
-    if residual.shape != (T, H):
-        raise ValueError(f"residual must have shape {(T, H)}, got {tuple(residual.shape)}")
-    if w_post is not None:
-        _need(w_post, "w_post", torch.bfloat16, (H,))
-    if w_next is not None:
-        _need(w_next, "w_next", torch.bfloat16, (H,))
-    grs = gcs = 0
-    if gate is not None:
-        _need(gate, "gate", torch.bfloat16, contiguous=False)
-        shape = gate.shape
-        if len(shape) != 2 or shape[0] not in (1, T) or shape[1] not in (1, H):
-            raise ValueError(f"gate must be [T, 1], [1, H] or [T, H], got {tuple(shape)}")
-        grs, gcs = gate.stride()
-        if shape[0] == 1:
-            grs = 0
-        if shape[1] == 1:
-            gcs = 0
-    out, ldo = _out(out, "out", y, torch.bfloat16, T, H)
-    ldn = H
-    if w_next is not None:
-        n, ldn, codes, scales = _norm_outputs(y, T, H, n, quantize, codes, scales)
-    elif quantize or codes is not None or scales is not None or n is not None:
-        raise ValueError("n and its quantization need w_next")
-    st = lib().moe_norm_out(_p(y), _DTYPE[y.dtype], T, H, ldy, _p(residual), ldr, _p(w_post), _p(gate), grs, gcs,
-                            residual_scale, _p(w_next), eps, _p(out), ldo, _p(n), ldn, _p(codes), _p(scales),
-                            _stream(stream))
-    check(st, "moe_norm_out")
-    if w_next is None:
-        return out
-    return (out, n) if codes is None else (out, n, codes, scales)
+    return _b.moe_norm_out(y, residual, w_post, w_next, gate, residual_scale, eps, out, n, quantize, codes, scales,
+                           stream)

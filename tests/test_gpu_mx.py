@@ -293,3 +293,39 @@ def test_experts_no_tokens(ops):
     po, ps = run_experts(ops, np.zeros((0, H), np.uint16), bf16(z)[1], bf16(np.zeros((E * H, I)))[1], None,
                          np.zeros((0, k), np.float32), np.zeros(E + 1, np.int32), np.zeros(0, np.int32), E, k, H, I)
     assert po.numel() == 0 and ps.numel() == 0
+
+
+def test_binding_refusals(ops):
+    """What the binding refuses of tensors on the device, before anything is enqueued."""
+    x = torch.zeros((4, 288), dtype=torch.bfloat16, device="cuda")
+    c, s = ops.mxfp4_quantize(x)
+    wc, ws, top = ops.mxfp4_quantize_weights(torch.zeros((2, 40, 288), dtype=torch.bfloat16, device="cuda"))
+
+    def raises(kind, match, f):
+        with pytest.raises(kind, match=match):
+            f()
+
+    raises(TypeError, "codes must be torch.uint8, got torch.float32", lambda: ops.mxfp4_quantize(x, codes=c.float()))
+    raises(ValueError, r"codes must have shape \(4, 256\), got \(4, 128\)", lambda: ops.mxfp4_quantize(x, codes=c[:, :128]))
+    raises(ValueError, "unit column stride", lambda: ops.mxfp4_quantize(x.t()))
+    raises(ops.MoEError, "MOE_ERR_SHAPE.*multiple of 32", lambda: ops.mxfp4_quantize(x[:, :40]))
+    raises(ops.MoEError, "MOE_ERR_ALIGN", lambda: ops.mxfp4_quantize(x[:, 1:33]))
+    raises(TypeError, "output type", lambda: ops.mxfp4_dequantize(c, s, 288, torch.float16))
+    raises(ValueError, r"out must have shape \(4, 288\)", lambda: ops.mxfp4_dequantize(c, s, 288, out=x[:2]))
+    raises(ValueError, "w_codes must have shape", lambda: ops.mxfp4_linear(c, s, wc[0], ws[0], 72))
+    raises(ValueError, "x_codes must have shape", lambda: ops.mxfp4_linear(c[:, :128], s, wc[0], ws[0], 40))
+    raises(ValueError, "codes must be contiguous", lambda: ops.mxfp4_quantize(x, codes=c.t().contiguous().t()))
+    off, srt = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    tw = torch.zeros((4, 1), device="cuda")
+    bad = torch.zeros((4, 2), device="cuda")
+    w2 = ops.mxfp4_quantize_weights(torch.zeros((2, 288, 32), dtype=torch.bfloat16, device="cuda"))
+    w13 = ops.mxfp4_quantize_weights(torch.zeros((2, 64, 288), dtype=torch.bfloat16, device="cuda"))[:2]
+    raises(ValueError, "topk_w must have shape", lambda: ops.mxfp4_grouped_ffn(c, s, *w13, *w2, 288, 32, 1, off, srt, bad))
+    raises(ops.MoEError, "MOE_ERR_WORKSPACE",
+           lambda: ops.mxfp4_grouped_ffn(c, s, *w13, *w2, 288, 32, 1, off, srt, tw,
+                                         workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")))
+    raises(ValueError, "residual must have shape", lambda: ops.moe_norm_out(x, x[:2]))
+    raises(ValueError, r"gate must be \[T, 1\]", lambda: ops.moe_norm_out(x, x, gate=x[:2]))
+    raises(ValueError, "need w_next", lambda: ops.moe_norm_out(x, x, quantize=True))
+    raises(ops.MoEError, "MOE_ERR_NULL.*neither n nor codes", lambda: ops.moe_norm_in(x, x[0], n=False))
+    raises(ops.MoEError, "MOE_ERR_SHAPE.*row stride", lambda: ops.moe_norm_in(x[:1].expand(4, 288), x[0]))
