@@ -125,7 +125,7 @@ struct MxArgs {
   int32_t N;               // weight rows (per expert)
   int32_t G;               // groups of 32 weight rows (per expert)
   int32_t ldo;             // elements (gate_up: bytes) of an output row
-  int32_t T;               // linear: tokens
+  int32_t T;               // linear: tokens; experts, tiled: their number if each has one m-tile (route: offsets), or 0
   int32_t aux;             // gate_up: k; down: ceil(log2(36 I)); linear: bit 0 FP32 results, bit 1 rows on 16 bytes
 };
 static_assert(sizeof(MxArgs) <= 112, "see above");

@@ -1,5 +1,13 @@
 // Products of MXFP4 activations and packed MXFP4 weights on the scaled FP4
 // MFMA: the dense y = x W^T, and the two stages of the routed experts' FFN.
+//
+// With few tokens the weights' bytes bound a product, with many the matrix
+// cores.  A register-only loop of the 32x32x64 FP4 MFMA takes 32 cycles an
+// instruction; on operands of random bits the card lowers its clock to 1.6 GHz
+// under it (6.5 PFLOP/s; 8.5 at 2.1 GHz on zeros).  The tiled kernel on 4096 x
+// 16384 x 4096 reaches 4.6 PFLOP/s, 5.2 without its DMA, and 6.2 on zeros: what
+// remains is mostly power, and a shape that moves fewer bytes per product wins
+// over one that hides latencies better.
 #include "launch.h"
 #include "mx_common.h"
 
@@ -55,7 +63,10 @@ __device__ __forceinline__ void zero_h_pad(const MxArgs& a, int64_t row, int p, 
 // up group of the same h columns) and tiles of 32 tokens; its NW waves split
 // the columns and load their fragments straight from memory to registers (a
 // packed fragment is one contiguous kilobyte), and the partial sums meet in LDS
-// in a fixed order.
+// in a fixed order.  One token, 6144 x 6144: 5.2 us, of which a launch takes
+// about 2; 8 waves on 1 row group where 4 waves on 2 take 6.8 (too few
+// workgroups).  Token groups past the first would cost more here than in a
+// tile: a lane's 16 bytes of x come from 32 different rows.
 template <int MODE, int R, int NW>
 __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   __shared__ float part[NW][R][16][64];
@@ -231,25 +242,37 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 
   // ---- which tile: each XCD takes one contiguous run of the tile order (under 2^23 tiles)
   const int nw = MODE == kGateUp ? (a.G / 2 + S::kSlots / 2 - 1) / (S::kSlots / 2) : (a.G + S::kSlots - 1) / S::kSlots;
-  const int mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : a.route[0];
+  const bool one = MODE != kLinear && a.T != 0;  // an m-tile for each of T experts: route is their offsets
+  const int mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : (one ? a.T : a.route[0]);
   const int total = mtiles * nw, chunk = (total + 7) / 8, slot = blockIdx.x >> 3;
   const int at = (int)(blockIdx.x & 7) * chunk + slot;
   if (slot >= chunk || at >= total) return;
-  int e = 0, rows = a.T, span = mtiles, q = at;
+  int e = 0, wt, cnt;
   int64_t first = 0;
-  if (MODE != kLinear) {
-    const int4 t = reinterpret_cast<const int4*>(a.route)[1 + at / nw];
-    e = t.x;
-    q = at - t.y * nw;
-    first = t.z;
-    rows = t.w - t.z;
-    span = (rows + S::kTok - 1) / S::kTok;
+  if (one) {
+    // weight tiles outermost: the experts without pairs, which end here, are spread over the XCDs
+    wt = at / a.T;
+    e = at - wt * a.T;
+    first = a.route[e];
+    cnt = a.route[e + 1] - (int)first;
+    if (cnt == 0) return;
+  } else {
+    int rows = a.T, span = mtiles, q = at;
+    if (MODE != kLinear) {
+      const int4 t = reinterpret_cast<const int4*>(a.route)[1 + at / nw];
+      e = t.x;
+      q = at - t.y * nw;
+      first = t.z;
+      rows = t.w - t.z;
+      span = (rows + S::kTok - 1) / S::kTok;
+    }
+    // blocks of up to four token tiles by all weight tiles, tokens fastest
+    const int blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min(4, span - 4 * blk);
+    wt = rem / tc;
+    const int t0 = (4 * blk + rem - wt * tc) * S::kTok;
+    cnt = min(S::kTok, rows - t0);
+    first += t0;
   }
-  // blocks of up to four token tiles by all weight tiles, tokens fastest
-  const int blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min(4, span - 4 * blk);
-  const int wt = rem / tc, t0 = (4 * blk + rem - wt * tc) * S::kTok;
-  const int cnt = min(S::kTok, rows - t0);
-  first += t0;
 
   // weight group of slot s (of kSlots)
   auto group = [&](int s) -> int {
@@ -601,9 +624,17 @@ __global__ __launch_bounds__(256) void mx_schedule_kernel(const int32_t* __restr
 
 namespace {
 
-using Mx128x64 = MxTile<4, 2, 2, 1, 4>;   // weight rows by tokens
+// Weight rows by tokens.  The small tiles serve few tokens per expert, whose
+// bound is the weight stream, and grids too small for the large ones: at 256 x
+// 6144 x 6144 128 x 64 takes 11.8 us, 128 x 128 13.7 and 256 x 256 30; at 512
+// tokens 22, 17 and 33.  256 x 128 (78 KB of LDS, two workgroups a CU) hides
+// its epilogue and suits short reductions: 60.7 us at 8192 x 2048 x 6144, where
+// 256 x 256 takes 67.  256 x 256 moves two thirds of its bytes per product: 164
+// against 180 us at 8192 x 6144 x 6144.  Its eight waves of 64 x 128 measured
+// the same as four of 128 x 128.
+using Mx128x64 = MxTile<4, 2, 2, 1, 4>;
 using Mx128x128 = MxTile<4, 2, 2, 2, 4>;
-using Mx256x128 = MxTile<4, 2, 4, 2, 3>;  // 78 KB of LDS: two workgroups a CU
+using Mx256x128 = MxTile<4, 2, 4, 2, 3>;
 using Mx256x256 = MxTile<8, 4, 2, 4, 4>;
 
 // max_mtiles: an upper bound on the m-tiles (the experts' schedule knows their number)
@@ -647,7 +678,17 @@ Shape linear_shape(int64_t T, int64_t G) {
   return k128x64;
 }
 
-// The shape of a stage of the experts' FFN over weights of `rows` rows.
+// The shape of a stage of the experts' FFN over weights of `rows` rows; both
+// sides measured on 80 experts of 6144 x 2048, top-8, us of gate_up (down):
+//   mean pairs an expert      1.6        32         64         128        256        819
+//   streaming             164 (87)   289 (150)
+//   128 x 64              149 (76)   183 (103)  265 (121)  365 (179)
+//   256 x 128             157 (79)   179 (106)  193 (118)  275 (150)  386 (216)  959 (599)
+//   256 x 256             167 (91)   185 (117)  198 (130)  239 (156)  384 (240)  883 (599)
+// Small layers (16 experts of 1024 x 512) are latency bound: streaming, which
+// needs no schedule, takes 4.1 us at 2 pairs an expert where 128 x 64 takes 4.8,
+// and 128 x 64 stays ahead of 256 x 128 (6.4 against 8.9 us at 128) until the
+// larger tiles fill the chip.
 Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   if (pairs <= 32 * E && (pairs < E ? pairs : E) * (rows / 32) <= 2048) return kStream;
   const int64_t tiles = (pairs / 128 + (pairs < E ? pairs : E) / 2) * ((rows + 255) / 256);
@@ -655,10 +696,15 @@ Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   return pairs < 128 * E || KK < 16 ? k256x128 : k256x256;
 }
 
+// A token picks an expert once, so with this few tokens every expert's pairs fit one m-tile and no schedule is needed.
+bool one_mtile(Shape s, int64_t T) { return s != kStream && T <= shape_tokens(s); }
+
 template <int MODE>
 hipError_t launch_experts_stage(MxArgs a, Shape s, const MxExperts& x, const int32_t* tiles, hipStream_t st) {
-  a.route = s == kStream ? x.offsets : tiles;
-  const int64_t mtiles = most_mtiles(x.T * x.k, x.E, shape_tokens(s));
+  const bool one = one_mtile(s, x.T);
+  a.route = s == kStream || one ? x.offsets : tiles;
+  a.T = one ? (int32_t)x.E : 0;
+  const int64_t mtiles = one ? x.E : most_mtiles(x.T * x.k, x.E, shape_tokens(s));
   switch (s) {
     case kStream: return launch_stream<MODE>(a, x.E, st);
     case k128x64: return launch_tiled<MODE, Mx128x64>(a, mtiles, st);
@@ -685,7 +731,8 @@ hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
 hipError_t launch_mx_experts(MxExperts x, hipStream_t st) {
   const int64_t pairs = x.T * x.k;
   const Shape s0 = experts_shape(pairs, x.E, x.gate_up.N, x.gate_up.KK), s1 = experts_shape(pairs, x.E, x.down.N, x.down.KK);
-  if (s0 != kStream || s1 != kStream) {
+  auto scheduled = [&](Shape s) { return s != kStream && !one_mtile(s, x.T); };
+  if (scheduled(s0) || scheduled(s1)) {
     hipLaunchKernelGGL(mx_schedule_kernel, dim3(2), dim3(256), 0, st, x.offsets, (int)x.E, shape_tokens(s0),
                        shape_tokens(s1), x.tiles[0], x.tiles[1]);
     if (hipError_t e = hipGetLastError()) return e;

@@ -27,52 +27,44 @@ __device__ __forceinline__ void load8(const float* p, float* f) {
 // Four neighbouring lanes share one block of 32: each reads 8 elements (16 or
 // 32 bytes), the block's amax is two exchanges within the quad, and each writes
 // one dword of codes.  Columns past `cols` (up to the padded row) are zero
-// blocks with scale byte 0.  A thread has kChunks loads in flight.  Memory
-// bound: 2 (4) + 17/32 bytes an element.
-constexpr int kChunks = 4;
-
+// blocks with scale byte 0.  Memory bound: 2 (4) + 17/32 bytes an element;
+// 8192 x 6144 BF16 in 22 us (5.7 TB/s, what a copy reaches).  Four blocks of
+// loads a thread were no faster there, and slower on a few rows (4.6 against
+// 3.4 us for 16 x 6144).
 template <typename X>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const X* __restrict__ x, uint32_t n, uint32_t cols,
                                                           int64_t ld, uint32_t chunks, uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
-  const uint32_t i0 = blockIdx.x * (256u * kChunks) + threadIdx.x;  // chunk of 8 elements of the padded rows
-  float f[kChunks][8];
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;  // chunk of 8 elements of the padded rows
+  if (i >= n) return;                                  // n % 32 == 0: a quad is in or out as one
+  const uint32_t r = i / chunks, c = (i - r * chunks) * 8;
+  float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < cols) load8(x + r * ld + c, f);
+  uint32_t m = 0;
 #pragma unroll
-  for (int v = 0; v < kChunks; ++v) {
-    const uint32_t i = i0 + 256u * v, r = i / chunks, c = (i - r * chunks) * 8;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[v][k] = 0.0f;
-    if (i < n && c < cols) load8(x + r * ld + c, f[v]);
-  }
-#pragma unroll
-  for (int v = 0; v < kChunks; ++v) {
-    const uint32_t i = i0 + 256u * v;
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, abs_bits(f[v][k]));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-    const uint32_t byte = mx_scale_byte(m);
-    if (i < n) {  // n % 32 == 0: a quad is in or out as one
-      codes[i] = mx_encode8(f[v], byte);
-      if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
-    }
-  }
+  for (int k = 0; k < 8; ++k) m = max(m, abs_bits(f[k]));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+  const uint32_t byte = mx_scale_byte(m);
+  codes[i] = mx_encode8(f, byte);
+  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
-// The values that codes stand for.  A thread takes 8 elements, kChunks times.
-// Streaming stores: quantising 8192 x 6144 BF16 and reading it back takes 46 us
-// with them and 54 us without.
-template <bool F32>
+// The values that codes stand for.  A thread takes 8 elements, V times: from
+// some 2^20 chunks on four loads in flight are faster (8192 x 6144 BF16: 25 us
+// against 28), below that the workgroups are too few.  Streaming stores:
+// quantising 8192 x 6144 BF16 and reading it back takes 46 us with them and 54
+// us without.
+template <bool F32, int V>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales, uint32_t n,
                                                             uint32_t chunks, uint32_t chunks_padded,
                                                             void* __restrict__ out, int64_t ld) {
-  const uint32_t i0 = blockIdx.x * (256u * kChunks) + threadIdx.x;
-  uint32_t d[kChunks], byte[kChunks];
-  int64_t at[kChunks];
+  const uint32_t i0 = blockIdx.x * (256u * V) + threadIdx.x;
+  uint32_t d[V], byte[V];
+  int64_t at[V];
 #pragma unroll
-  for (int v = 0; v < kChunks; ++v) {
+  for (int v = 0; v < V; ++v) {
     const uint32_t i = i0 + 256u * v, r = i / chunks, c = i - r * chunks;
     const int64_t src = (int64_t)r * chunks_padded + c;
     at[v] = r * ld + (int64_t)c * 8;
@@ -82,7 +74,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
     }
   }
 #pragma unroll
-  for (int v = 0; v < kChunks; ++v) {
+  for (int v = 0; v < V; ++v) {
     if (i0 + 256u * v >= n) break;
     const float s = mx_scale_value(byte[v]);
     float f[8];
@@ -192,7 +184,7 @@ __global__ void mx_zero_ints_kernel(int* p, int64_t n) {
 hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                               uint8_t* scales, hipStream_t st) {
   const uint32_t chunks = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
-  const dim3 grid((unsigned)(((uint64_t)n + 256 * kChunks - 1) / (256 * kChunks)));
+  const dim3 grid((unsigned)(((uint64_t)n + 255) / 256));
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   if (f32)
     hipLaunchKernelGGL(mx_quantize_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), n, (uint32_t)cols,
@@ -203,15 +195,23 @@ hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t col
   return hipGetLastError();
 }
 
+namespace {
+template <bool F32, int V>
+void launch_dequantize_as(const uint8_t* codes, const uint8_t* scales, uint32_t n, uint32_t chunks, uint32_t padded,
+                          void* out, int64_t ld, hipStream_t st) {
+  hipLaunchKernelGGL((mx_dequantize_kernel<F32, V>), dim3((unsigned)(((uint64_t)n + 256 * V - 1) / (256 * V))), dim3(256),
+                     0, st, reinterpret_cast<const uint32_t*>(codes), scales, n, chunks, padded, out, ld);
+}
+}  // namespace
+
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
                                 void* out, int64_t ld, hipStream_t st) {
   const uint32_t chunks = (uint32_t)(cols / 8), padded = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
-  const dim3 grid((unsigned)(((uint64_t)n + 256 * kChunks - 1) / (256 * kChunks)));
-  const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
-  if (f32)
-    hipLaunchKernelGGL(mx_dequantize_kernel<true>, grid, dim3(256), 0, st, c, scales, n, chunks, padded, out, ld);
-  else
-    hipLaunchKernelGGL(mx_dequantize_kernel<false>, grid, dim3(256), 0, st, c, scales, n, chunks, padded, out, ld);
+  const bool many = n >= 1u << 20;
+  if (f32 && many) launch_dequantize_as<true, 4>(codes, scales, n, chunks, padded, out, ld, st);
+  else if (f32) launch_dequantize_as<true, 1>(codes, scales, n, chunks, padded, out, ld, st);
+  else if (many) launch_dequantize_as<false, 4>(codes, scales, n, chunks, padded, out, ld, st);
+  else launch_dequantize_as<false, 1>(codes, scales, n, chunks, padded, out, ld, st);
   return hipGetLastError();
 }
 

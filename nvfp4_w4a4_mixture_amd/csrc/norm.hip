@@ -79,7 +79,10 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uin
 // between the passes.  POST: the row is y, and the first norm, gate, residual
 // scale and residual give r'; otherwise the row is x itself.  Everything the
 // row needs is loaded before the first sum, so that one memory latency covers
-// it; the sums are FP32, in a fixed order.
+// it; the sums are FP32, in a fixed order, and results are rounded once, to
+// BF16.  Memory bound: norm_out of 8192 x 6144 with FP32 y moves 503 MB in 82 us
+// (6.1 TB/s; a copy with streaming stores reaches 6.05).  Loading the residual
+// and the weights after the first sum took 99 us, cached stores 90.
 template <int NW, int V, bool POST, bool YF32, bool VEC>
 __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
   __shared__ float lds[2][4];
