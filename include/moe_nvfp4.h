@@ -486,9 +486,7 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
  * and gate are BF16, y is BF16 or FP32 (y_dtype).  gate (NULL: 1) has element
  * (t, c) at gate[t * gate_row_stride + c * gate_col_stride], gate_col_stride 0
  * (one value a token) or 1.  Any H from 1 to 16384 and any row strides from H to
- * 2^31 - 1;
- * 16-byte accesses are used when H % 8 == 0 and every pointer and row stride is a
- * multiple of 16 bytes.  Pointers aligned to their element, codes to 4 bytes.
+ * 2^31 - 1.  Pointers aligned to their element, codes to 4 bytes.
  * r_out may be r, and n may be x (in place, same strides); other outputs must
  * not overlap inputs. */
 moe_status moe_norm_in(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, const uint16_t* w, float eps,

@@ -281,8 +281,6 @@ static moe_status check_norm(const char* fn, int64_t T, int64_t H, float eps, co
   return MOE_OK;
 }
 
-static bool vec16(const void* p, int64_t ld, int64_t size) { return aligned(p, 16) && (ld * size) % 16 == 0; }
-
 moe_status moe_norm_in(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, const uint16_t* w, float eps,
                        uint16_t* n, int64_t ldn, uint8_t* codes, uint8_t* scales, void* stream) {
   const char* fn = "moe_norm_in";
@@ -303,8 +301,7 @@ moe_status moe_norm_in(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, con
   a.H = (uint32_t)H;
   a.Hp = (uint32_t)(codes ? mx_padded(H) : H);
   a.eps = eps;
-  const bool vec = H % 8 == 0 && vec16(x, ldx, 2) && vec16(w, 0, 2) && vec16(n, ldn, 2);
-  return launched(moe::launch_norm(a, T, false, false, vec, (hipStream_t)stream), fn);
+  return launched(moe::launch_norm(a, T, false, false, (hipStream_t)stream), fn);
 }
 
 moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, int64_t ldy, const uint16_t* r,
@@ -346,10 +343,7 @@ moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, in
   a.gate_row = gate_col_stride == 0;
   a.scale = residual_scale;
   a.eps = eps;
-  const bool vec = H % 8 == 0 && vec16(y, ldy, y_dtype ? 4 : 2) && vec16(r, ldr, 2) && vec16(r_out, ldro, 2) &&
-                   vec16(w_post, 0, 2) && vec16(w_next, 0, 2) && vec16(n, ldn, 2) &&
-                   (gate_col_stride == 0 || vec16(gate, gate_row_stride, 2));
-  return launched(moe::launch_norm(a, T, true, y_dtype == 1, vec, (hipStream_t)stream), fn);
+  return launched(moe::launch_norm(a, T, true, y_dtype == 1, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

@@ -172,6 +172,6 @@ struct NormArgs {
 };
 static_assert(sizeof(NormArgs) <= 112, "see MxArgs");
 int64_t norm_max_cols();
-hipError_t launch_norm(const NormArgs& a, int64_t T, bool post, bool y_f32, bool vec, hipStream_t st);
+hipError_t launch_norm(const NormArgs& a, int64_t T, bool post, bool y_f32, hipStream_t st);
 
 }  // namespace moe

@@ -22,17 +22,22 @@ __device__ __forceinline__ float row_sum(float v, float* lds, int w) {
   return s;
 }
 
-// Eight BF16 (FP32) elements at column c of a row of H, as they lie in memory:
-// 16-byte accesses in the vector form, element by element (and only the ones
-// below H) in the other.  Elements past H are zero.
-template <bool VEC>
+// 16 bytes at an address aligned to an element only: one access on gfx950 all
+// the same, so rows of any length and stride move in 16-byte pieces.
+typedef uint32_t u32x4_any2_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef float float4_any4_t __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight BF16 (FP32) elements at column c of a row of H, as they lie in memory;
+// zero past H.  Only the row's last piece, if it is short, goes by elements.
 __device__ __forceinline__ uint4 load8_bf16(const uint16_t* p, int c, int H) {
   uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (VEC) {
-    if (c < H) return *reinterpret_cast<const uint4*>(p + c);
-  } else {
+  if (c + 8 <= H) {
+    const u32x4_any2_t v = *reinterpret_cast<const u32x4_any2_t*>(p + c);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  if (c < H) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
       if (c + i < H) w[i >> 1] |= (uint32_t)p[c + i] << (16 * (i & 1));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -45,30 +50,33 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
-template <bool VEC>
 __device__ __forceinline__ void load8_f32(const float* p, int c, int H, float* f) {
+  if (c + 8 <= H) {
+    const float4_any4_t u = *reinterpret_cast<const float4_any4_t*>(p + c), v = *reinterpret_cast<const float4_any4_t*>(p + c + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = u[i];
+      f[4 + i] = v[i];
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-  if (VEC) {
-    if (c < H) {
-      const float4 a = *reinterpret_cast<const float4*>(p + c), b = *reinterpret_cast<const float4*>(p + c + 4);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    }
-  } else {
+  if (c < H) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
       if (c + i < H) f[i] = p[c + i];
   }
 }
-template <bool VEC>
 __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uint32_t* b) {
-  if (VEC) {
-    if (c < H)
-      store16_streaming(p + c, b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16));
-  } else {
+  if (c + 8 <= H) {
+    const u32x4_any2_t v = {b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16)};
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any2_t*>(p + c));  // see store16_streaming
+    return;
+  }
+  if (c < H) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
       if (c + i < H) p[c + i] = (uint16_t)b[i];
   }
 }
@@ -83,7 +91,7 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uin
 // BF16.  Memory bound: norm_out of 8192 x 6144 with FP32 y moves 503 MB in 82 us
 // (6.1 TB/s; a copy with streaming stores reaches 6.05).  Loading the residual
 // and the weights after the first sum took 99 us, cached stores 90.
-template <int NW, int V, bool POST, bool YF32, bool VEC>
+template <int NW, int V, bool POST, bool YF32>
 __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
   __shared__ float lds[2][4];
   const int w = threadIdx.x >> 6, t = threadIdx.x;
@@ -95,23 +103,23 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * 64 * NW + t) * 8;
-    if constexpr (YF32) load8_f32<VEC>(static_cast<const float*>(a.x) + row * a.ldx, c, H, x[v]);
-    else unpack8(load8_bf16<VEC>(static_cast<const uint16_t*>(a.x) + row * a.ldx, c, H), x[v]);
-    if constexpr (POST) rr[v] = load8_bf16<VEC>(a.r + row * a.ldr, c, H);
+    if constexpr (YF32) load8_f32(static_cast<const float*>(a.x) + row * a.ldx, c, H, x[v]);
+    else unpack8(load8_bf16(static_cast<const uint16_t*>(a.x) + row * a.ldx, c, H), x[v]);
+    if constexpr (POST) rr[v] = load8_bf16(a.r + row * a.ldr, c, H);
   }
   if constexpr (POST) {
     if (a.gate && !a.gate_row) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) gg[v] = load8_bf16<VEC>(a.gate + row * a.gate_rs, (v * 64 * NW + t) * 8, H);
+      for (int v = 0; v < V; ++v) gg[v] = load8_bf16(a.gate + row * a.gate_rs, (v * 64 * NW + t) * 8, H);
     }
     if (a.w_post) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) wp[v] = load8_bf16<VEC>(a.w_post, (v * 64 * NW + t) * 8, H);
+      for (int v = 0; v < V; ++v) wp[v] = load8_bf16(a.w_post, (v * 64 * NW + t) * 8, H);
     }
   }
   if (follow) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) wn[v] = load8_bf16<VEC>(a.w, (v * 64 * NW + t) * 8, H);
+    for (int v = 0; v < V; ++v) wn[v] = load8_bf16(a.w, (v * 64 * NW + t) * 8, H);
   }
   if constexpr (POST) {
     const float g_row = a.gate && a.gate_row ? bf16_to_f32(a.gate[row * a.gate_rs]) : 1.0f;
@@ -139,7 +147,7 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
         o[i] = bf16_bits_rne(fmaf(a.scale, z, rv[i]));
         x[v][i] = bf16_to_f32(o[i]);  // the next norm reads the residual that is kept
       }
-      store8_bf16<VEC>(a.r_out + row * a.ldro, (v * 64 * NW + t) * 8, H, o);
+      store8_bf16(a.r_out + row * a.ldro, (v * 64 * NW + t) * 8, H, o);
     }
     if (!follow) return;
   }
@@ -161,7 +169,7 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
       o[i] = c + i < H ? bf16_bits_rne(x[v][i] * inv * wv[i]) : 0u;
       m = max(m, (o[i] & 0x7FFFu) << 16);
     }
-    if (a.n) store8_bf16<VEC>(a.n + row * a.ldn, c, H, o);
+    if (a.n) store8_bf16(a.n + row * a.ldn, c, H, o);
     if (a.codes) {  // H % 32 == 0: a quad of lanes holds one block
       m = max(m, (uint32_t)__shfl_xor((int)m, 1));
       m = max(m, (uint32_t)__shfl_xor((int)m, 2));
@@ -180,39 +188,42 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
 namespace {
 
 template <int NW, int V, bool POST>
-void launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, bool vec, hipStream_t st) {
+void launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const dim3 grid((unsigned)T), block(64 * NW);
   if constexpr (POST) {
     if (y_f32) {
-      if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, true>), grid, block, 0, st, a);
-      else hipLaunchKernelGGL((norm_kernel<NW, V, POST, true, false>), grid, block, 0, st, a);
+      hipLaunchKernelGGL((norm_kernel<NW, V, POST, true>), grid, block, 0, st, a);
       return;
     }
   }
-  if (vec) hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((norm_kernel<NW, V, POST, false, false>), grid, block, 0, st, a);
+  hipLaunchKernelGGL((norm_kernel<NW, V, POST, false>), grid, block, 0, st, a);
 }
 
-// The fewest lanes that hold a row in a few chunks each: a wave alone needs no barrier.
+// A wave alone needs no barrier and leaves fewer lanes idle, four waves finish a
+// row sooner.  8192 rows of 1032: 8.5 us by one wave each, 10.8 by four (norm_out
+// 24.5 and 28.2); 500 rows of 1999: 5.5 and 4.2 us.  From 2056 columns on four
+// are as fast or faster at any number of rows.
 template <bool POST>
-void launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, bool vec, hipStream_t st) {
+void launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const int cols = (int)a.Hp;
-  if (cols <= 512) launch_norm_as<1, 1, POST>(a, T, y_f32, vec, st);
-  else if (cols <= 1024) launch_norm_as<1, 2, POST>(a, T, y_f32, vec, st);
-  else if (cols <= 2048) launch_norm_as<4, 1, POST>(a, T, y_f32, vec, st);
-  else if (cols <= 4096) launch_norm_as<4, 2, POST>(a, T, y_f32, vec, st);
-  else if (cols <= 6144) launch_norm_as<4, 3, POST>(a, T, y_f32, vec, st);
-  else if (cols <= 8192) launch_norm_as<4, 4, POST>(a, T, y_f32, vec, st);
-  else launch_norm_as<4, 8, POST>(a, T, y_f32, vec, st);
+  if (cols <= 512) launch_norm_as<1, 1, POST>(a, T, y_f32, st);
+  else if (cols <= 1024) launch_norm_as<1, 2, POST>(a, T, y_f32, st);
+  else if (cols <= 1536 && T >= 2048) launch_norm_as<1, 3, POST>(a, T, y_f32, st);
+  else if (cols <= 2047 && T >= 2048) launch_norm_as<1, 4, POST>(a, T, y_f32, st);
+  else if (cols <= 2048) launch_norm_as<4, 1, POST>(a, T, y_f32, st);
+  else if (cols <= 4096) launch_norm_as<4, 2, POST>(a, T, y_f32, st);
+  else if (cols <= 6144) launch_norm_as<4, 3, POST>(a, T, y_f32, st);
+  else if (cols <= 8192) launch_norm_as<4, 4, POST>(a, T, y_f32, st);
+  else launch_norm_as<4, 8, POST>(a, T, y_f32, st);
 }
 
 }  // namespace
 
 int64_t norm_max_cols() { return 16384; }
 
-hipError_t launch_norm(const NormArgs& a, int64_t T, bool post, bool y_f32, bool vec, hipStream_t st) {
-  if (post) launch_norm_shape<true>(a, T, y_f32, vec, st);
-  else launch_norm_shape<false>(a, T, false, vec, st);
+hipError_t launch_norm(const NormArgs& a, int64_t T, bool post, bool y_f32, hipStream_t st) {
+  if (post) launch_norm_shape<true>(a, T, y_f32, st);
+  else launch_norm_shape<false>(a, T, false, st);
   return hipGetLastError();
 }
 

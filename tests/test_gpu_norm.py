@@ -45,7 +45,8 @@ def close(got, ref, extra, what):
 
 
 SHAPES = [(1, 1), (1, 64), (3, 7), (2, 512), (5, 520), (4, 1015), (3, 1024), (2, 1032), (3, 2048), (2, 2056), (1, 4096),
-          (1, 6144), (7, 6144), (2, 6152), (2, 8192), (2, 9999), (1, 16384)]
+          (1, 6144), (7, 6144), (2, 6152), (2, 8192), (2, 9999), (1, 16384),
+          (2050, 1049), (2049, 1999)]  # the last two: one wave a row for many rows
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
