@@ -58,12 +58,15 @@ def build_binding() -> str:
     import torch
     from torch.utils import cpp_extension
 
-    inc = [f"-I{d}" for d in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"])]
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    inc = [f"-I{d}" for d in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+                              os.path.join(rocm, "include"))]
     libs = cpp_extension.TORCH_LIB_PATH
     tmp = BINDING + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, os.path.join(CSRC, "py_binding.cpp"),
-           "-o", tmp, f"-L{libs}", "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libs}"]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+           os.path.join(CSRC, "py_binding.cpp"), "-o", tmp, f"-L{libs}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_python", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compiling the binding failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

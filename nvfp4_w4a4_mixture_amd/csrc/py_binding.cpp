@@ -11,6 +11,7 @@
 // names, defaults and documentation.  The library's entry points are passed in
 // by address (bind), so that both bindings call the same loaded library.
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -38,8 +39,7 @@ struct Entry {
   decltype(&moe_norm_out) norm_out;
   decltype(&moe_combine) combine;
 } g_entry;
-PyObject* g_check = nullptr;   // check(status, name): raises for a status other than MOE_OK
-PyObject* g_stream = nullptr;  // stream(stream or None): the stream's address
+PyObject* g_check = nullptr;  // check(status, name): raises for a status other than MOE_OK
 
 [[noreturn]] __attribute__((format(printf, 2, 3))) void raise(PyObject* type, const char* fmt, ...) {
   char buf[512];
@@ -168,9 +168,11 @@ void* address(PyObject* o) {
   if (!p && PyErr_Occurred()) throw python_error();
   return p;
 }
-// Asked for after the tensors are checked: without a GPU it raises.
+// A torch stream's address; None: the current device's current stream.  Asked
+// for after the tensors are checked: without a GPU it raises.
 void* stream_of(PyObject* o) {
-  PyObject* r = PyObject_CallOneArg(g_stream, o);
+  if (!given(o)) return c10::hip::getCurrentHIPStream().stream();
+  PyObject* r = PyObject_GetAttrString(o, "cuda_stream");
   if (!r) throw python_error();
   void* p = PyLong_AsVoidPtr(r);
   Py_DECREF(r);
@@ -359,18 +361,15 @@ PyObject* combine(PyObject* const* a) {
   return wrap(y);
 }
 
-// check, stream, then the addresses in Entry's order
+// check, then the addresses in Entry's order
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 2 + (Py_ssize_t)(sizeof(Entry) / sizeof(void*))) raise(PyExc_TypeError, "bind: wrong number of entry points");
+  if (n != 1 + (Py_ssize_t)(sizeof(Entry) / sizeof(void*))) raise(PyExc_TypeError, "bind: wrong number of entry points");
   void** to = reinterpret_cast<void**>(&g_entry);
-  for (Py_ssize_t i = 2; i < n; ++i) to[i - 2] = address(a[i]);
-  for (int i = 0; i < 2; ++i) {
-    PyObject*& held = i == 0 ? g_check : g_stream;
-    Py_INCREF(a[i]);
-    Py_XDECREF(held);
-    held = a[i];
-  }
+  for (Py_ssize_t i = 1; i < n; ++i) to[i - 1] = address(a[i]);
+  Py_INCREF(a[0]);
+  Py_XDECREF(g_check);
+  g_check = a[0];
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

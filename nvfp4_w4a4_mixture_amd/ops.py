@@ -510,7 +510,7 @@ def _bound():
         raise RuntimeError("the compiled binding is not built; run `python -m nvfp4_w4a4_mixture_amd.build`") from e
     names = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear_workspace_bytes", "mxfp4_linear",
              "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine")
-    _binding.bind(check, _stream, *(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names))
+    _binding.bind(check, *(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names))
     return _binding
 
 
