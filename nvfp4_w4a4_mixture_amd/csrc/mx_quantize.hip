@@ -187,32 +187,21 @@ hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t col
   const dim3 grid((unsigned)(((uint64_t)n + 255) / 256));
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   if (f32)
-    hipLaunchKernelGGL(mx_quantize_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), n, (uint32_t)cols,
-                       ld, chunks, c, scales);
-  else
-    hipLaunchKernelGGL(mx_quantize_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(x), n,
+    return launch_kernel(mx_quantize_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), n,
+                         (uint32_t)cols, ld, chunks, c, scales);
+  return launch_kernel(mx_quantize_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(x), n,
                        (uint32_t)cols, ld, chunks, c, scales);
-  return hipGetLastError();
 }
-
-namespace {
-template <bool F32, int V>
-void launch_dequantize_as(const uint8_t* codes, const uint8_t* scales, uint32_t n, uint32_t chunks, uint32_t padded,
-                          void* out, int64_t ld, hipStream_t st) {
-  hipLaunchKernelGGL((mx_dequantize_kernel<F32, V>), dim3((unsigned)(((uint64_t)n + 256 * V - 1) / (256 * V))), dim3(256),
-                     0, st, reinterpret_cast<const uint32_t*>(codes), scales, n, chunks, padded, out, ld);
-}
-}  // namespace
 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
                                 void* out, int64_t ld, hipStream_t st) {
   const uint32_t chunks = (uint32_t)(cols / 8), padded = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
   const bool many = n >= 1u << 20;
-  if (f32 && many) launch_dequantize_as<true, 4>(codes, scales, n, chunks, padded, out, ld, st);
-  else if (f32) launch_dequantize_as<true, 1>(codes, scales, n, chunks, padded, out, ld, st);
-  else if (many) launch_dequantize_as<false, 4>(codes, scales, n, chunks, padded, out, ld, st);
-  else launch_dequantize_as<false, 1>(codes, scales, n, chunks, padded, out, ld, st);
-  return hipGetLastError();
+  auto* k = f32 ? (many ? mx_dequantize_kernel<true, 4> : mx_dequantize_kernel<true, 1>)
+                : (many ? mx_dequantize_kernel<false, 4> : mx_dequantize_kernel<false, 1>);
+  const uint64_t per = many ? 1024 : 256;
+  return launch_kernel(k, dim3((unsigned)((n + per - 1) / per)), dim3(256), 0, st, reinterpret_cast<const uint32_t*>(codes),
+                       scales, n, chunks, padded, out, ld);
 }
 
 namespace {

@@ -188,15 +188,12 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
 namespace {
 
 template <int NW, int V, bool POST>
-void launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
+hipError_t launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const dim3 grid((unsigned)T), block(64 * NW);
   if constexpr (POST) {
-    if (y_f32) {
-      hipLaunchKernelGGL((norm_kernel<NW, V, POST, true>), grid, block, 0, st, a);
-      return;
-    }
+    if (y_f32) return launch_kernel(norm_kernel<NW, V, POST, true>, grid, block, 0, st, a);
   }
-  hipLaunchKernelGGL((norm_kernel<NW, V, POST, false>), grid, block, 0, st, a);
+  return launch_kernel(norm_kernel<NW, V, POST, false>, grid, block, 0, st, a);
 }
 
 // A wave alone needs no barrier and leaves fewer lanes idle, four waves finish a
@@ -204,17 +201,17 @@ void launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
 // 24.5 and 28.2); 500 rows of 1999: 5.5 and 4.2 us.  From 2056 columns on four
 // are as fast or faster at any number of rows.
 template <bool POST>
-void launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
+hipError_t launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const int cols = (int)a.Hp;
-  if (cols <= 512) launch_norm_as<1, 1, POST>(a, T, y_f32, st);
-  else if (cols <= 1024) launch_norm_as<1, 2, POST>(a, T, y_f32, st);
-  else if (cols <= 1536 && T >= 2048) launch_norm_as<1, 3, POST>(a, T, y_f32, st);
-  else if (cols <= 2047 && T >= 2048) launch_norm_as<1, 4, POST>(a, T, y_f32, st);
-  else if (cols <= 2048) launch_norm_as<4, 1, POST>(a, T, y_f32, st);
-  else if (cols <= 4096) launch_norm_as<4, 2, POST>(a, T, y_f32, st);
-  else if (cols <= 6144) launch_norm_as<4, 3, POST>(a, T, y_f32, st);
-  else if (cols <= 8192) launch_norm_as<4, 4, POST>(a, T, y_f32, st);
-  else launch_norm_as<4, 8, POST>(a, T, y_f32, st);
+  if (cols <= 512) return launch_norm_as<1, 1, POST>(a, T, y_f32, st);
+  if (cols <= 1024) return launch_norm_as<1, 2, POST>(a, T, y_f32, st);
+  if (cols <= 1536 && T >= 2048) return launch_norm_as<1, 3, POST>(a, T, y_f32, st);
+  if (cols <= 2047 && T >= 2048) return launch_norm_as<1, 4, POST>(a, T, y_f32, st);
+  if (cols <= 2048) return launch_norm_as<4, 1, POST>(a, T, y_f32, st);
+  if (cols <= 4096) return launch_norm_as<4, 2, POST>(a, T, y_f32, st);
+  if (cols <= 6144) return launch_norm_as<4, 3, POST>(a, T, y_f32, st);
+  if (cols <= 8192) return launch_norm_as<4, 4, POST>(a, T, y_f32, st);
+  return launch_norm_as<4, 8, POST>(a, T, y_f32, st);
 }
 
 }  // namespace
@@ -222,9 +219,7 @@ void launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st)
 int64_t norm_max_cols() { return 16384; }
 
 hipError_t launch_norm(const NormArgs& a, int64_t T, bool post, bool y_f32, hipStream_t st) {
-  if (post) launch_norm_shape<true>(a, T, y_f32, st);
-  else launch_norm_shape<false>(a, T, false, st);
-  return hipGetLastError();
+  return post ? launch_norm_shape<true>(a, T, y_f32, st) : launch_norm_shape<false>(a, T, false, st);
 }
 
 }  // namespace moe
