@@ -667,12 +667,15 @@ int64_t most_mtiles(int64_t pairs, int64_t E, int64_t tok) { return pairs / tok 
 // any size, but a lane's pieces of x come from as many rows as there are tokens:
 // at K = 6144 and 50,000 weight rows 1, 8, 16 and 32 tokens take 25, 26, 29 and
 // 43 us, where a 128 x 64 tile takes 26 for up to 64; at 6144 rows (192 groups)
-// they take 4.2 to 7.3 us and the tile, latency bound, 10.  Of the tiles the
+// they take 4.2 to 7.3 us and the tile, latency bound, 10.  They meet near tokens
+// times groups of 32 * 256, each CU having 32 rows of x a group to fetch: on the two
+// sides of it 32 tokens take 8.2 (streamed) and 9.6 us (tile), 16 take 11.0 and
+// 11.1, 9 take 16.9 and 15.8; at 32 x 10,240 13.2 and 9.9.  Of the tiles the
 // largest that still come to about one for each CU: fewer bytes a product.
 Shape linear_shape(int64_t T, int64_t G) {
   const int64_t cus = 256;
   auto tiles = [&](int64_t rows, int64_t tok) { return (G + rows / 32 - 1) / (rows / 32) * ((T + tok - 1) / tok); };
-  if (T <= 8 || (T <= 32 && T * G <= 40 * cus) || tiles(32, 32) <= cus) return kStream;
+  if (T <= 8 || (T <= 32 && T * G <= 32 * cus) || tiles(32, 32) <= cus) return kStream;
   if (tiles(256, 256) >= cus * 3 / 4) return k256x256;
   if (tiles(256, 128) >= cus * 3 / 4) return k256x128;
   if (tiles(128, 128) >= cus / 2) return k128x128;
