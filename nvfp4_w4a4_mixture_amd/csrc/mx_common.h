@@ -62,11 +62,26 @@ __device__ __forceinline__ uint32_t mx_encode8(const float* x, uint32_t byte) {
   return byte == 255u ? 0u : d;
 }
 
-// BF16 bits of a float, round to nearest even; NaN stays NaN
-__device__ __forceinline__ uint32_t bf16_bits_rne(float f) {
-  const uint32_t u = __float_as_uint(f);
-  const uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-  return (u & 0x7FFFFFFFu) > 0x7F800000u ? (u >> 16) | 0x40u : r;
+// Two values rounded to nearest even in BF16, the first in the low half; NaN stays NaN
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
+
+// The value of the lane that DPP control CTRL names: an ALU operand, where a
+// shuffle goes through LDS.  kLaneXor1, kLaneXor2: exchange inside quads;
+// kLaneHalfMirror, kLaneMirror: lane 7 - i of 8, 15 - i of 16.
+enum { kLaneXor1 = 0xB1, kLaneXor2 = 0x4E, kLaneHalfMirror = 0x141, kLaneMirror = 0x140 };
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+// Largest of v over aligned groups of four lanes, in every one of them
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, lane_dpp<kLaneXor1>(v));
+  return max(v, lane_dpp<kLaneXor2>(v));
 }
 
 // A 16-byte store that does not stay in L2: for results larger than it, whose

@@ -34,14 +34,9 @@ __device__ __forceinline__ int pair_exponent(float wp, uint32_t bh, int bw, int 
   return min(max(e, max(ew, 0) - 126), 113);
 }
 
-// Two values rounded to nearest even in 16 bits, the first in the low half
+// Two values rounded to nearest even in FP16, the first in the low half
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
-}
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
 __device__ __forceinline__ uint32_t max_byte(uint32_t d) {
@@ -152,9 +147,8 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
           h[q] = silu(v[0][q]) * v[1][q];
           m = max(m, abs_bits(h[q]));
         }
-        m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 4));
+        m = quad_max(m);
+        m = max(m, lane_dpp<kLaneHalfMirror>(m));
         const uint32_t byte = mx_scale_byte(m);
         const int64_t blk = blockIdx.x;
         reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + row * a.ldo)[blk * 8 + p] = (uint16_t)mx_encode8(h, byte);

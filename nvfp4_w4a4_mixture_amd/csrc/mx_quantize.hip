@@ -43,8 +43,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const X* __restrict__ 
   uint32_t m = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) m = max(m, abs_bits(f[k]));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+  m = quad_max(m);
   const uint32_t byte = mx_scale_byte(m);
   codes[i] = mx_encode8(f, byte);
   if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;

@@ -11,8 +11,15 @@ namespace {
 // Sum over the row's waves, in a fixed order; every thread gets it.
 template <int NW>
 __device__ __forceinline__ float row_sum(float v, float* lds, int w) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  v += __uint_as_float(lane_dpp<kLaneXor1>(__float_as_uint(v)));
+  v += __uint_as_float(lane_dpp<kLaneXor2>(__float_as_uint(v)));
+  v += __uint_as_float(lane_dpp<kLaneHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(lane_dpp<kLaneMirror>(__float_as_uint(v)));
+  // each result holds one of a pair of 16 (32) lanes in both
+  auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   if (NW == 1) return v;
   if ((threadIdx.x & 63) == 0) lds[w] = v;
   __syncthreads();
@@ -50,6 +57,9 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
 __device__ __forceinline__ void load8_f32(const float* p, int c, int H, float* f) {
   if (c + 8 <= H) {
     const float4_any4_t u = *reinterpret_cast<const float4_any4_t*>(p + c), v = *reinterpret_cast<const float4_any4_t*>(p + c + 4);
@@ -68,16 +78,17 @@ __device__ __forceinline__ void load8_f32(const float* p, int c, int H, float* f
       if (c + i < H) f[i] = p[c + i];
   }
 }
-__device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uint32_t* b) {
+__device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uint4& b) {
+  const uint32_t d[4] = {b.x, b.y, b.z, b.w};
   if (c + 8 <= H) {
-    const u32x4_any2_t v = {b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16)};
+    const u32x4_any2_t v = {b.x, b.y, b.z, b.w};
     __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any2_t*>(p + c));  // see store16_streaming
     return;
   }
   if (c < H) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-      if (c + i < H) p[c + i] = (uint16_t)b[i];
+      if (c + i < H) p[c + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
   }
 }
 
@@ -88,12 +99,15 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uin
 // scale and residual give r'; otherwise the row is x itself.  Everything the
 // row needs is loaded before the first sum, so that one memory latency covers
 // it; the sums are FP32, in a fixed order, and results are rounded once, to
-// BF16.  Memory bound: norm_out of 8192 x 6144 with FP32 y moves 503 MB in 82 us
-// (6.1 TB/s; a copy with streaming stores reaches 6.05).  Loading the residual
-// and the weights after the first sum took 99 us, cached stores 90.
+// BF16.  Memory bound: norm_out of 8192 x 6144 with FP32 y moves 503 MB in 78 us
+// (6.4 TB/s; a copy with streaming stores reaches 6.05).  Loading the residual
+// and the weights after the first sum took 99 us, cached stores 90.  Few rows
+// are bound by one latency of memory and by the two sums: 2.0 us (norm_in) and
+// 3.0 (norm_out) for one row of 6144, where sums through LDS shuffles and
+// rounding in integer steps took 3.0 and 4.7.
 template <int NW, int V, bool POST, bool YF32>
 __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
-  __shared__ float lds[2][4];
+  __shared__ float lds[2][NW];
   const int w = threadIdx.x >> 6, t = threadIdx.x;
   const int64_t row = blockIdx.x;
   const int H = (int)a.H;
@@ -135,7 +149,6 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float wv[8], rv[8], gv[8];
-      uint32_t o[8];
       unpack8(rr[v], rv);
       if (a.w_post) unpack8(wp[v], wv);
       if (a.gate && !a.gate_row) unpack8(gg[v], gv);
@@ -144,9 +157,10 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
         float z = x[v][i];
         if (a.w_post) z = z * inv * wv[i];
         if (a.gate) z *= a.gate_row ? g_row : gv[i];
-        o[i] = bf16_bits_rne(fmaf(a.scale, z, rv[i]));
-        x[v][i] = bf16_to_f32(o[i]);  // the next norm reads the residual that is kept
+        x[v][i] = fmaf(a.scale, z, rv[i]);
       }
+      const uint4 o = pack8(x[v]);
+      unpack8(o, x[v]);  // the next norm reads the residual that is kept
       store8_bf16(a.r_out + row * a.ldro, (v * 64 * NW + t) * 8, H, o);
     }
     if (!follow) return;
@@ -160,23 +174,21 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * 64 * NW + t) * 8;
-    float wv[8];
-    uint32_t o[8];
+    float wv[8], q[8];
     unpack8(wn[v], wv);
-    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      o[i] = c + i < H ? bf16_bits_rne(x[v][i] * inv * wv[i]) : 0u;
-      m = max(m, (o[i] & 0x7FFFu) << 16);
-    }
+    for (int i = 0; i < 8; ++i) q[i] = x[v][i] * inv * wv[i];
+    const uint4 o = pack8(q);
     if (a.n) store8_bf16(a.n + row * a.ldn, c, H, o);
     if (a.codes) {  // H % 32 == 0: a quad of lanes holds one block
-      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-      const uint32_t byte = mx_scale_byte(m);
-      float q[8];
+      uint32_t m = 0;
+      unpack8(o, q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = bf16_to_f32(o[i]);
+      for (int i = 0; i < 8; ++i) {
+        if (c >= H) q[i] = 0.0f;  // the padding is zero whatever the norm is
+        m = max(m, abs_bits(q[i]));
+      }
+      const uint32_t byte = mx_scale_byte(quad_max(m));
       if (c < (int)a.Hp) {
         reinterpret_cast<uint32_t*>(a.codes)[(row * (int)a.Hp + c) / 8] = mx_encode8(q, byte);
         if ((t & 3) == 0) a.scales[(row * (int)a.Hp + c) / 32] = (uint8_t)byte;
@@ -199,7 +211,8 @@ hipError_t launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, hipStream_t 
 // A wave alone needs no barrier and leaves fewer lanes idle, four waves finish a
 // row sooner.  8192 rows of 1032: 8.5 us by one wave each, 10.8 by four (norm_out
 // 24.5 and 28.2); 500 rows of 1999: 5.5 and 4.2 us.  From 2056 columns on four
-// are as fast or faster at any number of rows.
+// are as fast or faster at any number of rows; twelve take one row of 6144 in
+// 1.8 (2.8) us against 2.0 (3.0), but 1024 rows in 4.8 (8.3) against 4.3 (7.2).
 template <bool POST>
 hipError_t launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const int cols = (int)a.Hp;
