@@ -58,13 +58,13 @@ __device__ __forceinline__ void zero_h_pad(const MxArgs& a, int64_t row, int p, 
 // up group of the same h columns) and tiles of 32 tokens; its NW waves split
 // the columns and load their fragments straight from memory to registers (a
 // packed fragment is one contiguous kilobyte), and the partial sums meet in LDS
-// in a fixed order.  One token, 6144 x 6144: 5.2 us, of which a launch takes
-// about 2; 8 waves on 1 row group where 4 waves on 2 take 6.8 (too few
-// workgroups).  Token groups past the first would cost more here than in a
+// in a fixed order.  One token, 6144 x 6144: 4.6 us, of which a launch takes
+// about 2; 8 waves on 1 row group where 4 waves on 2 take 10.4 (too few
+// workgroups), 16 waves or loads two groups ahead 4.5 to 4.8.  Token groups past the first would cost more here than in a
 // tile: a lane's 16 bytes of x come from 32 different rows.
 template <int MODE, int R, int NW>
 __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
-  __shared__ float part[NW][R][16][64];
+  __shared__ float4 part[NW][R][4 * 68];  // strides 68 and 34: 16 lanes of a reader take 16 different slots
   __shared__ uint32_t hmax[NW][32];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, n = l & 31, f = l >> 5;
   const int e = MODE == kLinear ? 0 : blockIdx.y;
@@ -89,6 +89,16 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
     const int64_t arow = MODE == kGateUp ? a.sorted[pos] / a.aux : pos;
     const uint8_t* xc = a.a_codes + arow * (a.KK * 128) + f * 64;
     const uint8_t* xs = a.a_scales + arow * (a.KK * 8) + f * 4;
+    // thread (tok, p) of the epilogue: features 4 p .. 4 p + 3 of one token; what it needs of the pair
+    // is loaded here, under the products (two latencies less: down of a small layer 4.7 us, not 5.7)
+    const int tok = tid >> 3, p = tid & 7;
+    int pair = 0, wmax = 0;
+    float wp = 0.0f;
+    if constexpr (MODE == kDown) {
+      pair = a.sorted[t0 + min(tok, cnt - 1)];
+      wp = a.topk_w[pair];
+      wmax = a.w_max[e];
+    }
     float16_t acc[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -123,21 +133,27 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) part[w][i][r][l] = acc[i][r];
+      for (int q = 0; q < 4; ++q)
+        part[w][i][q * 68 + f * 34 + n] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
     __syncthreads();
-    // thread (tok, p): features 4 p .. 4 p + 3 of one token
-    const int tok = tid >> 3, p = tid & 7;
     if (tid < 256 && tok < cnt) {
       float v[R][4];
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+      for (int i = 0; i < R; ++i) {
+        float4 s = part[0][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float s = part[0][i][4 * (p & 3) + q][32 * (p >> 2) + tok];
-#pragma unroll
-          for (int k = 1; k < NW; ++k) s += part[k][i][4 * (p & 3) + q][32 * (p >> 2) + tok];
-          v[i][q] = s;
+        for (int k = 1; k < NW; ++k) {
+          const float4 u = part[k][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
+          s.x += u.x;
+          s.y += u.y;
+          s.z += u.z;
+          s.w += u.w;
         }
+        v[i][0] = s.x;
+        v[i][1] = s.y;
+        v[i][2] = s.z;
+        v[i][3] = s.w;
+      }
       const int64_t row = t0 + tok;
       if constexpr (MODE == kGateUp) {
         float h[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -158,12 +174,11 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
         float factor = 1.0f;
         int64_t out = row;
         if constexpr (MODE == kDown) {
-          out = a.sorted[row];
-          const float wp = a.topk_w[out];
+          out = pair;
           uint32_t b = hmax[0][tok];
 #pragma unroll
           for (int k = 1; k < NW; ++k) b = max(b, hmax[k][tok]);
-          const int E = pair_exponent(wp, b, a.w_max[e], a.aux);
+          const int E = pair_exponent(wp, b, wmax, a.aux);
           factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
           if (blockIdx.x == 0 && p == 0) static_cast<float*>(a.out_scales)[out] = __uint_as_float((uint32_t)(127 + E) << 23);
         }
@@ -661,9 +676,9 @@ int64_t most_mtiles(int64_t pairs, int64_t E, int64_t tok) { return pairs / tok 
 // any size, but a lane's pieces of x come from as many rows as there are tokens:
 // at K = 6144 and 50,000 weight rows 1, 8, 16 and 32 tokens take 25, 26, 29 and
 // 43 us, where a 128 x 64 tile takes 26 for up to 64; at 6144 rows (192 groups)
-// they take 4.2 to 7.3 us and the tile, latency bound, 10.  They meet near tokens
+// they take 4.0 to 6.6 us and the tile, latency bound, 10.  They meet near tokens
 // times groups of 32 * 256, each CU having 32 rows of x a group to fetch: on the two
-// sides of it 32 tokens take 8.2 (streamed) and 9.6 us (tile), 16 take 11.0 and
+// sides of it 32 tokens take 7.2 (streamed) and 9.6 us (tile), 16 take 10.4 and
 // 11.1, 9 take 16.9 and 15.8; at 32 x 10,240 13.2 and 9.9.  Of the tiles the
 // largest that still come to about one for each CU: fewer bytes a product.
 Shape linear_shape(int64_t T, int64_t G) {
