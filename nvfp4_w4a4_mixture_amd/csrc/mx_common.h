@@ -62,6 +62,15 @@ __device__ __forceinline__ uint32_t mx_encode8(const float* x, uint32_t byte) {
   return byte == 255u ? 0u : d;
 }
 
+// The elements of eight codes, unscaled
+__device__ __forceinline__ void mx_decode8(uint32_t d, float* f) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 1),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 3)};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = p[k >> 1][k & 1];
+}
+
 // Two values rounded to nearest even in BF16, the first in the low half; NaN stays NaN
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));

@@ -49,53 +49,36 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const X* __restrict__ 
   if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
-// The values that codes stand for.  A thread takes 8 elements, V times: from
-// some 2^20 chunks on four loads in flight are faster (8192 x 6144 BF16: 25 us
-// against 28), below that the workgroups are too few.  Streaming stores:
-// quantising 8192 x 6144 BF16 and reading it back takes 46 us with them and 54
-// us without.
-template <bool F32, int V>
+// The values that codes stand for, 8 elements a thread.  Memory bound: 8192 x
+// 6144 to BF16 in 20 us (6.3 TB/s); four times 8 a thread take the same, decoding
+// in integer steps took 23.  Streaming
+// stores: quantising 8192 x 6144 BF16 and reading it back took 46 us with them
+// and 54 us without.
+template <bool F32>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales, uint32_t n,
                                                             uint32_t chunks, uint32_t chunks_padded,
                                                             void* __restrict__ out, int64_t ld) {
-  const uint32_t i0 = blockIdx.x * (256u * V) + threadIdx.x;
-  uint32_t d[V], byte[V];
-  int64_t at[V];
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n) return;
+  const uint32_t r = i / chunks, c = i - r * chunks;
+  const int64_t src = (int64_t)r * chunks_padded + c, at = r * ld + (int64_t)c * 8;
+  const float s = mx_scale_value(scales[src >> 2]);
+  float f[8];
+  mx_decode8(codes[src], f);  // without the scale: the conversion has no byte 0 and no NaN
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const uint32_t i = i0 + 256u * v, r = i / chunks, c = i - r * chunks;
-    const int64_t src = (int64_t)r * chunks_padded + c;
-    at[v] = r * ld + (int64_t)c * 8;
-    if (i < n) {
-      d[v] = codes[src];
-      byte[v] = scales[src >> 2];
-    }
-  }
+  for (int k = 0; k < 8; ++k) f[k] *= s;
+  if (F32) {
+    float* p = static_cast<float*>(out) + at;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (i0 + 256u * v >= n) break;
-    const float s = mx_scale_value(byte[v]);
-    float f[8];
+    for (int k = 0; k < 8; k += 4)
+      store16_streaming(p + k, __float_as_uint(f[k]), __float_as_uint(f[k + 1]), __float_as_uint(f[k + 2]),
+                        __float_as_uint(f[k + 3]));
+  } else {  // exact: two significant bits, and BF16 has FP32's exponents (down to 2^-133)
+    uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t code = (d[v] >> (4 * k)) & 15u, m = code & 7u;
-      // 0, .5, 1, 1.5, 2, 3, 4, 6: exponent m / 2, mantissa bit m % 2
-      const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-      f[k] = ((code & 8u) ? -a : a) * s;
-    }
-    if (F32) {
-      float* p = static_cast<float*>(out) + at[v];
-#pragma unroll
-      for (int k = 0; k < 8; k += 4)
-        store16_streaming(p + k, __float_as_uint(f[k]), __float_as_uint(f[k + 1]), __float_as_uint(f[k + 2]),
-                          __float_as_uint(f[k + 3]));
-    } else {  // exact: two significant bits, and BF16 has FP32's exponents (down to 2^-133)
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = (__float_as_uint(f[2 * k]) >> 16) | (__float_as_uint(f[2 * k + 1]) & 0xFFFF0000u);
-      store16_streaming(static_cast<uint16_t*>(out) + at[v], w[0], w[1], w[2], w[3]);
-    }
+    for (int k = 0; k < 4; ++k) w[k] = (__float_as_uint(f[2 * k]) >> 16) | (__float_as_uint(f[2 * k + 1]) & 0xFFFF0000u);
+    store16_streaming(static_cast<uint16_t*>(out) + at, w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -195,12 +178,9 @@ hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t col
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
                                 void* out, int64_t ld, hipStream_t st) {
   const uint32_t chunks = (uint32_t)(cols / 8), padded = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
-  const bool many = n >= 1u << 20;
-  auto* k = f32 ? (many ? mx_dequantize_kernel<true, 4> : mx_dequantize_kernel<true, 1>)
-                : (many ? mx_dequantize_kernel<false, 4> : mx_dequantize_kernel<false, 1>);
-  const uint64_t per = many ? 1024 : 256;
-  return launch_kernel(k, dim3((unsigned)((n + per - 1) / per)), dim3(256), 0, st, reinterpret_cast<const uint32_t*>(codes),
-                       scales, n, chunks, padded, out, ld);
+  auto* k = f32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>;
+  return launch_kernel(k, dim3((n + 255) / 256), dim3(256), 0, st, reinterpret_cast<const uint32_t*>(codes), scales, n,
+                       chunks, padded, out, ld);
 }
 
 namespace {

@@ -99,8 +99,8 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uin
 // scale and residual give r'; otherwise the row is x itself.  Everything the
 // row needs is loaded before the first sum, so that one memory latency covers
 // it; the sums are FP32, in a fixed order, and results are rounded once, to
-// BF16.  Memory bound: norm_out of 8192 x 6144 with FP32 y moves 503 MB in 78 us
-// (6.4 TB/s; a copy with streaming stores reaches 6.05).  Loading the residual
+// BF16.  Memory bound: norm_out of 8192 x 6144 with FP32 y moves 503 MB in 82 us
+// (6.1 TB/s; a copy with streaming stores reaches 6.05).  Loading the residual
 // and the weights after the first sum took 99 us, cached stores 90.  Few rows
 // are bound by one latency of memory and by the two sums: 2.0 us (norm_in) and
 // 3.0 (norm_out) for one row of 6144, where sums through LDS shuffles and
