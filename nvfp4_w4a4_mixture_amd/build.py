@@ -65,7 +65,7 @@ def build_binding() -> str:
     tmp = BINDING + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
-           os.path.join(CSRC, "py_binding.cpp"), "-o", tmp, f"-L{libs}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+           os.path.join(CSRC, "py_binding.cpp"), "-o", tmp, f"-L{libs}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip",
            "-ltorch_python", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
