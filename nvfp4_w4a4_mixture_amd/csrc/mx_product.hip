@@ -637,9 +637,9 @@ namespace {
 // bound is the weight stream, and grids too small for the large ones: at 256 x
 // 6144 x 6144 128 x 64 takes 11.8 us, 128 x 128 13.7 and 256 x 256 30; at 512
 // tokens 22, 17 and 33.  256 x 128 (78 KB of LDS, two workgroups a CU) hides
-// its epilogue and suits short reductions: 60.7 us at 8192 x 2048 x 6144, where
-// 256 x 256 takes 67.  256 x 256 moves two thirds of its bytes per product: 164
-// against 180 us at 8192 x 6144 x 6144.  Its eight waves of 64 x 128 measured
+// its epilogue and suits short reductions: 62 us at 8192 x 2048 x 6144, where
+// 256 x 256 takes 65.  256 x 256 moves two thirds of its bytes per product: 154
+// against 161 us at 8192 x 6144 x 6144.  Its eight waves of 64 x 128 measured
 // the same as four of 128 x 128.
 using Mx128x64 = MxTile<4, 2, 2, 1, 4>;
 using Mx128x128 = MxTile<4, 2, 2, 2, 4>;
@@ -680,12 +680,16 @@ int64_t most_mtiles(int64_t pairs, int64_t E, int64_t tok) { return pairs / tok 
 // times groups of 32 * 256, each CU having 32 rows of x a group to fetch: on the two
 // sides of it 32 tokens take 7.2 (streamed) and 9.6 us (tile), 16 take 10.4 and
 // 11.1, 9 take 16.9 and 15.8; at 32 x 10,240 13.2 and 9.9.  Of the tiles the
-// largest that still come to about one for each CU: fewer bytes a product.
-Shape linear_shape(int64_t T, int64_t G) {
+// largest that still come to about one for each CU: fewer bytes a product; 256 x
+// 256, with one workgroup a CU, from 4096 columns on, where its epilogue weighs
+// less than what it saves: 4096 x K x 8192 takes 24.4 (K = 512), 47.6 (2048) and 69.0
+// us (3584), by 256 x 128 21.6, 45.1 and 68.5; 8192 x K x 6144 110 and 154 us (K
+// = 4096, 6144), by 256 x 128 111 and 161.
+Shape linear_shape(int64_t T, int64_t G, int64_t KK) {
   const int64_t cus = 256;
   auto tiles = [&](int64_t rows, int64_t tok) { return (G + rows / 32 - 1) / (rows / 32) * ((T + tok - 1) / tok); };
   if (T <= 8 || (T <= 32 && T * G <= 32 * cus) || tiles(32, 32) <= cus) return kStream;
-  if (tiles(256, 256) >= cus * 3 / 4) return k256x256;
+  if (KK >= 16 && tiles(256, 256) >= cus * 3 / 4) return k256x256;
   if (tiles(256, 128) >= cus * 3 / 4) return k256x128;
   if (tiles(128, 128) >= cus / 2) return k128x128;
   return k128x64;
@@ -732,7 +736,7 @@ int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E) { return most_mtiles(T * 
 
 hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
   const int64_t T = a.T;
-  switch (linear_shape(T, a.G)) {
+  switch (linear_shape(T, a.G, a.KK)) {
     case kStream: return launch_stream<kLinear>(a, 1, st);
     case k128x64: return launch_tiled<kLinear, Mx128x64>(a, (T + 63) / 64, st);
     case k128x128: return launch_tiled<kLinear, Mx128x128>(a, (T + 127) / 128, st);

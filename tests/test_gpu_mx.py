@@ -135,7 +135,8 @@ LINEAR = [(1, 32, 1), (1, 256, 33), (1, 2080, 1000), (2, 64, 31), (3, 6144, 96),
           (128, 256, 256), (129, 800, 260), (255, 288, 511), (256, 1024, 256), (257, 544, 513), (384, 4096, 320),
           (515, 352, 1030), (1031, 288, 289),
           # every tile shape, with ragged last tiles and short and long reductions
-          (20, 288, 16420), (400, 288, 4203), (390, 1568, 4200), (900, 320, 6203), (897, 1344, 6200), (1800, 288, 6507), (1797, 1888, 6504)]
+          (20, 288, 16420), (400, 288, 4203), (390, 1568, 4200), (900, 320, 6203), (897, 1344, 6200), (1800, 288, 6507),
+          (1797, 1888, 6504), (1797, 4128, 6504)]
 
 
 @pytest.mark.parametrize("T,K,N", LINEAR)
