@@ -52,18 +52,12 @@ moe_status check_weights(const char* fn, int64_t batch, int64_t N, int64_t K) {
 }
 
 struct MxFfnWs {
-  size_t tiles[2], h_codes, h_scales, total;
+  size_t h_codes, h_scales, total;
 };
 
-MxFfnWs mx_ffn_ws(int64_t T, int64_t k, int64_t E, int64_t I) {
+MxFfnWs mx_ffn_ws(int64_t T, int64_t k, int64_t I) {
   MxFfnWs w{};
-  size_t o = 0;
-  for (size_t& t : w.tiles) {
-    t = o;
-    o = round_up(o + (size_t)(moe::mx_max_mtiles(T, k, E) + 1) * 16, 256);
-  }
-  w.h_codes = o;
-  o = round_up(o + (size_t)(T * k) * (size_t)(mx_padded(I) / 2), 256);
+  size_t o = round_up((size_t)(T * k) * (size_t)(mx_padded(I) / 2), 256);
   w.h_scales = o;
   o = round_up(o + (size_t)(T * k) * (size_t)(mx_padded(I) / 32), 256);
   w.total = o;
@@ -189,7 +183,7 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
 
 size_t mxfp4_ffn_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   if (T < 0 || k < 1 || E < 1 || H < 1 || I < 1) return 0;
-  return mx_ffn_ws(T, k, E, I).total;
+  return mx_ffn_ws(T, k, I).total;
 }
 
 moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t H,
@@ -219,7 +213,7 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
       !aligned(x_scales, 4) || !aligned(w13_scales, 4) || !aligned(w2_scales, 4) || !aligned(pair_scale, 4) ||
       !aligned(w2_max_scale, 4) || !aligned(expert_offsets, 4) || !aligned(sorted_pair_ids, 4) || !aligned(topk_w, 4))
     return fail(MOE_ERR_ALIGN, "%s: code arrays and pair_out must be 16-byte, the other arrays 4-byte aligned", fn);
-  const MxFfnWs L = mx_ffn_ws(T, k, E, I);
+  const MxFfnWs L = mx_ffn_ws(T, k, I);
   if (!workspace || workspace_bytes < L.total) return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, L.total);
   if (!aligned(workspace, 256)) return fail(MOE_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
   if (moe_status s = check_device()) return s;
@@ -229,8 +223,6 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
   x.T = T;
   x.k = k;
   x.E = E;
-  x.offsets = expert_offsets;
-  for (int i = 0; i < 2; ++i) x.tiles[i] = reinterpret_cast<int32_t*>(ws + L.tiles[i]);
   moe::MxArgs& a = x.gate_up;
   a.a_codes = x_codes;
   a.a_scales = x_scales;
@@ -238,7 +230,9 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
   a.w_scales = w13_scales;
   a.out = ws + L.h_codes;
   a.out_scales = ws + L.h_scales;
+  a.offsets = expert_offsets;
   a.sorted = sorted_pair_ids;
+  a.E = (int32_t)E;
   a.KK = (int32_t)(mx_padded(H) / 256);
   a.N = (int32_t)(2 * I);
   a.G = (int32_t)(2 * I / 32);
@@ -251,7 +245,9 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
   d.w_scales = w2_scales;
   d.out = pair_out;
   d.out_scales = pair_scale;
+  d.offsets = expert_offsets;
   d.sorted = sorted_pair_ids;
+  d.E = (int32_t)E;
   d.topk_w = topk_w;
   d.w_max = w2_max_scale;
   d.KK = (int32_t)(mx_padded(I) / 256);

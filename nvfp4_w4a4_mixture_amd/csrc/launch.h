@@ -133,7 +133,7 @@ struct MxArgs {
   const uint8_t* w_scales;
   void* out;               // linear: BF16 or FP32 [T, ldo]; gate_up: h codes [T*k, ldo]; down: FP16 pair rows [T*k, ldo]
   void* out_scales;        // gate_up: h scale bytes [T*k, ldo / 16]; down: FP32 pair scales [T*k]
-  const int32_t* route;    // experts: the expert offsets (streaming) or the m-tile schedule (tiled)
+  const int32_t* offsets;  // experts: first pair of each, and their end [E + 1]
   const int32_t* sorted;   // experts: pairs by expert
   const float* topk_w;     // down: routing weights [T*k]
   const int32_t* w_max;    // down: largest weight scale byte per expert
@@ -141,7 +141,8 @@ struct MxArgs {
   int32_t N;               // weight rows (per expert)
   int32_t G;               // groups of 32 weight rows (per expert)
   int32_t ldo;             // elements (gate_up: bytes) of an output row
-  int32_t T;               // linear: tokens; experts, tiled: their number if each has one m-tile (route: offsets), or 0
+  int32_t T;               // linear: tokens; experts, tiled: 1 if each has one m-tile at most, or 0
+  int32_t E;               // experts: their number
   int32_t aux;             // gate_up: k; down: ceil(log2(36 I)); linear: bit 0 FP32 results, bit 1 rows on 16 bytes
 };
 static_assert(sizeof(MxArgs) <= 112, "see above");
@@ -149,10 +150,8 @@ constexpr int32_t kMxOutF32 = 1, kMxOutVec = 2;
 
 // Both stages of the experts' FFN.
 struct MxExperts {
-  MxArgs gate_up, down;  // route is set at the launch
+  MxArgs gate_up, down;  // their T is set at the launch
   int64_t T, k, E;
-  const int32_t* offsets;
-  int32_t* tiles[2];  // m-tile schedules of the two stages
 };
 
 hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
@@ -166,8 +165,6 @@ hipError_t launch_mx_relayout(uint8_t* codes, uint8_t* scales, int64_t batch, in
                               uint8_t* pscales, int32_t* max_scale, bool pack, hipStream_t st);
 hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st);
 hipError_t launch_mx_experts(MxExperts x, hipStream_t st);
-// an upper bound on the experts' m-tiles
-int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E);
 
 // Norms around a block; x is the row to norm (norm_in) or the block output y
 // (norm_out).  As short as MxArgs, for the same reason.

@@ -71,8 +71,8 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   const int KK = (int)a.KK;
   int64_t lo = 0, hi = a.T;
   if (MODE != kLinear) {
-    lo = a.route[e];
-    hi = a.route[e + 1];
+    lo = a.offsets[e];
+    hi = a.offsets[e + 1];
   }
   const uint8_t* wc[R];
   const uint8_t* ws[R];
@@ -241,6 +241,48 @@ struct MxTile {
 // group, both over 8 rows (128 bytes a cycle) and over 16.
 __device__ __forceinline__ int mx_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
+// The m-tiles of up to 256 experts, TOK pairs each, found by every wave for
+// itself: lane l counts those of experts 4 l .. 4 l + 3, and a scan gives each
+// lane's first.  It costs a tile 0.3 us (10 us of the 1.6 ms of
+// 8192 tokens, 80 experts, top-8) and saves a launch of 3 us before the first stage.
+template <int TOK>
+struct ExpertTiles {
+  int off[5], end;  // the lane's offsets; tiles up to the end of its experts
+  __device__ __forceinline__ int tiles(int i) const { return (off[i + 1] - off[i] + TOK - 1) / TOK; }
+  __device__ __forceinline__ void count(const int32_t* offsets, int E, int l) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) off[i] = offsets[min(4 * l + i, E)];
+    end = tiles(0) + tiles(1) + tiles(2) + tiles(3);
+    // within rows of 16 lanes, then the last lanes' sums on to the rows after them
+    end += __builtin_amdgcn_update_dpp(0, end, 0x111, 0xF, 0xF, false);  // from 1 lane before
+    end += __builtin_amdgcn_update_dpp(0, end, 0x112, 0xF, 0xF, false);  // 2
+    end += __builtin_amdgcn_update_dpp(0, end, 0x114, 0xF, 0xF, false);  // 4
+    end += __builtin_amdgcn_update_dpp(0, end, 0x118, 0xF, 0xF, false);  // 8
+    end += __builtin_amdgcn_update_dpp(0, end, 0x142, 0xA, 0xF, false);  // lane 15 of row 0 (2) to row 1 (3)
+    end += __builtin_amdgcn_update_dpp(0, end, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
+  }
+  __device__ __forceinline__ int total() const { return __builtin_amdgcn_readlane(end, 63); }
+  // {expert, its first m-tile, its first pair, its pairs} of m-tile m < total()
+  __device__ __forceinline__ int4 find(int m) const {
+    const int lane = __builtin_ctzll(__ballot(end > m));
+    int o[5], n[4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) o[i] = __builtin_amdgcn_readlane(off[i], lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = (o[i + 1] - o[i] + TOK - 1) / TOK;
+    int y = __builtin_amdgcn_readlane(end, lane) - n[0] - n[1] - n[2] - n[3], i = 0, lo = o[0], hi = o[1];
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+      if (m >= y + n[k - 1] && i == k - 1) {
+        y += n[k - 1];
+        i = k;
+        lo = o[k];
+        hi = o[k + 1];
+      }
+    return make_int4(4 * lane + i, y, lo, hi - lo);
+  }
+};
+
 template <int MODE, class S>
 __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   constexpr int NW = S::kWaves, WM = S::kWM, GW = S::GW, GX = S::GX, RING = S::kRing;
@@ -251,8 +293,10 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 
   // ---- which tile: each XCD takes one contiguous run of the tile order (under 2^23 tiles)
   const int nw = MODE == kGateUp ? (a.G / 2 + S::kSlots / 2 - 1) / (S::kSlots / 2) : (a.G + S::kSlots - 1) / S::kSlots;
-  const bool one = MODE != kLinear && a.T != 0;  // an m-tile for each of T experts: route is their offsets
-  const int mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : (one ? a.T : a.route[0]);
+  const bool one = MODE != kLinear && a.T != 0;  // an m-tile for each expert
+  ExpertTiles<S::kTok> experts;
+  if (MODE != kLinear && !one) experts.count(a.offsets, a.E, l);
+  const int mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : (one ? a.E : experts.total());
   const int total = mtiles * nw, chunk = (total + 7) / 8, slot = blockIdx.x >> 3;
   const int at = (int)(blockIdx.x & 7) * chunk + slot;
   if (slot >= chunk || at >= total) return;
@@ -260,19 +304,19 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   int64_t first = 0;
   if (one) {
     // weight tiles outermost: the experts without pairs, which end here, are spread over the XCDs
-    wt = at / a.T;
-    e = at - wt * a.T;
-    first = a.route[e];
-    cnt = a.route[e + 1] - (int)first;
+    wt = at / a.E;
+    e = at - wt * a.E;
+    first = a.offsets[e];
+    cnt = a.offsets[e + 1] - (int)first;
     if (cnt == 0) return;
   } else {
     int rows = a.T, span = mtiles, q = at;
     if (MODE != kLinear) {
-      const int4 t = reinterpret_cast<const int4*>(a.route)[1 + at / nw];
+      const int4 t = experts.find(at / nw);
       e = t.x;
       q = at - t.y * nw;
       first = t.z;
-      rows = t.w - t.z;
+      rows = t.w;
       span = (rows + S::kTok - 1) / S::kTok;
     }
     // blocks of up to four token tiles by all weight tiles, tokens fastest
@@ -593,44 +637,6 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   }
 }
 
-// The m-tiles of every expert, for the two stages (block 0: gate_up, 1: down),
-// whose tiles may differ in tokens: tiles[0] their number; from tiles[4] on,
-// four words each: {expert, the expert's first m-tile, its first pair, the end of
-// its pairs}.  Thread
-// e counts expert e's tiles, a scan gives the first ones, and then tiles are
-// dealt to the threads, which find a tile's expert by bisection.
-__global__ __launch_bounds__(256) void mx_schedule_kernel(const int32_t* __restrict__ offsets, int E, int tok0,
-                                                          int tok1, int32_t* tiles0, int32_t* tiles1) {
-  const int tok = blockIdx.x == 0 ? tok0 : tok1;
-  int32_t* tiles = blockIdx.x == 0 ? tiles0 : tiles1;
-  __shared__ int32_t start[257], wave_sum[4];
-  const int e = threadIdx.x, l = e & 63;
-  const int n = e < E ? (offsets[e + 1] - offsets[e] + tok - 1) / tok : 0;
-  int sum = n;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(sum, d);
-    if (l >= d) sum += v;
-  }
-  if (l == 63) wave_sum[e >> 6] = sum;
-  __syncthreads();
-  for (int w = 0; w < (e >> 6); ++w) sum += wave_sum[w];
-  start[e + 1] = sum;
-  if (e == 0) start[0] = 0;
-  __syncthreads();
-  const int total = start[256];
-  if (e == 0) tiles[0] = total;
-  for (int i = e; i < total; i += 256) {
-    int lo = 0, hi = 256;  // start[lo] <= i < start[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (start[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    *reinterpret_cast<int4*>(tiles + 4 + (int64_t)i * 4) = make_int4(lo, start[lo], offsets[lo], offsets[lo + 1]);
-  }
-}
-
 namespace {
 
 // Weight rows by tokens.  The small tiles serve few tokens per expert, whose
@@ -646,7 +652,7 @@ using Mx128x128 = MxTile<4, 2, 2, 2, 4>;
 using Mx256x128 = MxTile<4, 2, 4, 2, 3>;
 using Mx256x256 = MxTile<8, 4, 2, 4, 4>;
 
-// max_mtiles: an upper bound on the m-tiles (the experts' schedule knows their number)
+// max_mtiles: an upper bound on the m-tiles (for experts the kernel counts them)
 template <int MODE, class S>
 hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
   auto* k = &mx_tiled_kernel<MODE, S>;
@@ -702,8 +708,8 @@ Shape linear_shape(int64_t T, int64_t G, int64_t KK) {
 //   128 x 64              149 (76)   183 (103)  265 (121)  365 (179)
 //   256 x 128             157 (79)   179 (106)  193 (118)  275 (150)  386 (216)  959 (599)
 //   256 x 256             167 (91)   185 (117)  198 (130)  239 (156)  384 (240)  883 (599)
-// Small layers (16 experts of 1024 x 512) are latency bound: streaming, which
-// needs no schedule, takes 4.1 us at 2 pairs an expert where 128 x 64 takes 4.8,
+// Small layers (16 experts of 1024 x 512) are latency bound: streaming
+// takes 4.1 us at 2 pairs an expert where 128 x 64 takes 4.8,
 // and 128 x 64 stays ahead of 256 x 128 (6.4 against 8.9 us at 128) until the
 // larger tiles fill the chip.
 Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
@@ -713,14 +719,13 @@ Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   return pairs < 128 * E || KK < 16 ? k256x128 : k256x256;
 }
 
-// A token picks an expert once, so with this few tokens every expert's pairs fit one m-tile and no schedule is needed.
+// A token picks an expert once, so with this few tokens every expert's pairs fit one m-tile.
 bool one_mtile(Shape s, int64_t T) { return s != kStream && T <= shape_tokens(s); }
 
 template <int MODE>
-hipError_t launch_experts_stage(MxArgs a, Shape s, const MxExperts& x, const int32_t* tiles, hipStream_t st) {
+hipError_t launch_experts_stage(MxArgs a, Shape s, const MxExperts& x, hipStream_t st) {
   const bool one = one_mtile(s, x.T);
-  a.route = s == kStream || one ? x.offsets : tiles;
-  a.T = one ? (int32_t)x.E : 0;
+  a.T = one;
   const int64_t mtiles = one ? x.E : most_mtiles(x.T * x.k, x.E, shape_tokens(s));
   switch (s) {
     case kStream: return launch_stream<MODE>(a, x.E, st);
@@ -731,8 +736,6 @@ hipError_t launch_experts_stage(MxArgs a, Shape s, const MxExperts& x, const int
 }
 
 }  // namespace
-
-int64_t mx_max_mtiles(int64_t T, int64_t k, int64_t E) { return most_mtiles(T * k, E, Mx128x64::kTok); }
 
 hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
   const int64_t T = a.T;
@@ -748,14 +751,8 @@ hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
 hipError_t launch_mx_experts(MxExperts x, hipStream_t st) {
   const int64_t pairs = x.T * x.k;
   const Shape s0 = experts_shape(pairs, x.E, x.gate_up.N, x.gate_up.KK), s1 = experts_shape(pairs, x.E, x.down.N, x.down.KK);
-  auto scheduled = [&](Shape s) { return s != kStream && !one_mtile(s, x.T); };
-  if (scheduled(s0) || scheduled(s1)) {
-    if (hipError_t e = launch_kernel(mx_schedule_kernel, dim3(2), dim3(256), 0, st, x.offsets, (int)x.E,
-                                     shape_tokens(s0), shape_tokens(s1), x.tiles[0], x.tiles[1]))
-      return e;
-  }
-  if (hipError_t e = launch_experts_stage<kGateUp>(x.gate_up, s0, x, x.tiles[0], st)) return e;
-  return launch_experts_stage<kDown>(x.down, s1, x, x.tiles[1], st);
+  if (hipError_t e = launch_experts_stage<kGateUp>(x.gate_up, s0, x, st)) return e;
+  return launch_experts_stage<kDown>(x.down, s1, x, st);
 }
 
 }  // namespace moe
