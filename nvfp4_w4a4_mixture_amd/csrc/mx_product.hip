@@ -243,8 +243,8 @@ __device__ __forceinline__ int mx_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >
 
 // The m-tiles of up to 256 experts, TOK pairs each, found by every wave for
 // itself: lane l counts those of experts 4 l .. 4 l + 3, and a scan gives each
-// lane's first.  It costs a tile 0.3 us (10 us of the 1.6 ms of
-// 8192 tokens, 80 experts, top-8) and saves a launch of 3 us before the first stage.
+// lane's first.  It costs a tile 0.3 us (10 us of the 1.6 ms of 8192 tokens, 80
+// experts, top-8) and saves a launch of 3 us before the first stage.
 template <int TOK>
 struct ExpertTiles {
   int off[5], end;  // the lane's offsets; tiles up to the end of its experts
@@ -708,12 +708,13 @@ Shape linear_shape(int64_t T, int64_t G, int64_t KK) {
 //   128 x 64              149 (76)   183 (103)  265 (121)  365 (179)
 //   256 x 128             157 (79)   179 (106)  193 (118)  275 (150)  386 (216)  959 (599)
 //   256 x 256             167 (91)   185 (117)  198 (130)  239 (156)  384 (240)  883 (599)
-// Small layers (16 experts of 1024 x 512) are latency bound: streaming
-// takes 4.1 us at 2 pairs an expert where 128 x 64 takes 4.8,
-// and 128 x 64 stays ahead of 256 x 128 (6.4 against 8.9 us at 128) until the
-// larger tiles fill the chip.
+// Small layers (16 experts of 1024 x 512) are latency bound: streaming takes
+// 4.0 us at 16 pairs an expert where 128 x 64 takes 4.4; past that its second
+// token tile costs more (10 experts of 4992 x 896, 29 pairs each: 20.0 against
+// 11.5 us), and 128 x 64 stays ahead of 256 x 128 (6.4 against 8.9 us at 128)
+// until the larger tiles fill the chip.
 Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
-  if (pairs <= 32 * E && (pairs < E ? pairs : E) * (rows / 32) <= 2048) return kStream;
+  if (pairs <= 16 * E && (pairs < E ? pairs : E) * (rows / 32) <= 2048) return kStream;
   const int64_t tiles = (pairs / 128 + (pairs < E ? pairs : E) / 2) * ((rows + 255) / 256);
   if (pairs <= 32 * E || tiles < 256) return k128x64;
   return pairs < 128 * E || KK < 16 ? k256x128 : k256x256;
