@@ -459,7 +459,7 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
  * H % 32 == 0, I % 32 == 0, 1 <= k <= E <= 256, T * k < 2^31; x codes
  * (T*Hp/2 bytes) and h codes (T*k*Ip/2 bytes) under 4 GiB, and (T*k/128 + E) *
  * ceil(max(2I, H) / 256) < 2^22.  expert_offsets and sorted_pair_ids as moe_route
- * writes them (a token's k experts are distinct).  Code arrays and
+ * writes them; a token may name an expert more than once.  Code arrays and
  * pair_out 16-byte, scale arrays, pair_scale and w2_max_scale 4-byte aligned;
  * workspace mxfp4_ffn_workspace_bytes(...) bytes, 256-byte aligned.  Pairs not
  * listed in sorted_pair_ids are not written. */

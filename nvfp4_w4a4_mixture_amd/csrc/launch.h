@@ -141,7 +141,7 @@ struct MxArgs {
   int32_t N;               // weight rows (per expert)
   int32_t G;               // groups of 32 weight rows (per expert)
   int32_t ldo;             // elements (gate_up: bytes) of an output row
-  int32_t T;               // linear: tokens; experts, tiled: 1 if each has one m-tile at most, or 0
+  int32_t T;               // linear: tokens
   int32_t E;               // experts: their number
   int32_t aux;             // gate_up: k; down: ceil(log2(36 I)); linear: bit 0 FP32 results, bit 1 rows on 16 bytes
 };
@@ -150,7 +150,7 @@ constexpr int32_t kMxOutF32 = 1, kMxOutVec = 2;
 
 // Both stages of the experts' FFN.
 struct MxExperts {
-  MxArgs gate_up, down;  // their T is set at the launch
+  MxArgs gate_up, down;
   int64_t T, k, E;
 };
 
@@ -164,7 +164,7 @@ hipError_t launch_mx_quantize_weights(const uint16_t* w, int64_t batch, int64_t 
 hipError_t launch_mx_relayout(uint8_t* codes, uint8_t* scales, int64_t batch, int64_t N, int64_t K, uint8_t* pcodes,
                               uint8_t* pscales, int32_t* max_scale, bool pack, hipStream_t st);
 hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st);
-hipError_t launch_mx_experts(MxExperts x, hipStream_t st);
+hipError_t launch_mx_experts(const MxExperts& x, hipStream_t st);
 
 // Norms around a block; x is the row to norm (norm_in) or the block output y
 // (norm_out).  As short as MxArgs, for the same reason.

@@ -244,7 +244,10 @@ __device__ __forceinline__ int mx_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >
 // The m-tiles of up to 256 experts, TOK pairs each, found by every wave for
 // itself: lane l counts those of experts 4 l .. 4 l + 3, and a scan gives each
 // lane's first.  It costs a tile 0.3 us (10 us of the 1.6 ms of 8192 tokens, 80
-// experts, top-8) and saves a launch of 3 us before the first stage.
+// experts, top-8) and saves a launch of 3 us before the first stage.  One m-tile
+// an expert without the scan, for so few tokens that an expert's pairs fit one,
+// was no faster: 16 tokens of that layer took 185 us against 179, 2 took 52
+// against 50, 64 249 against 239, 8 the same.
 template <int TOK>
 struct ExpertTiles {
   int off[5], end;  // the lane's offsets; tiles up to the end of its experts
@@ -293,39 +296,26 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 
   // ---- which tile: each XCD takes one contiguous run of the tile order (under 2^23 tiles)
   const int nw = MODE == kGateUp ? (a.G / 2 + S::kSlots / 2 - 1) / (S::kSlots / 2) : (a.G + S::kSlots - 1) / S::kSlots;
-  const bool one = MODE != kLinear && a.T != 0;  // an m-tile for each expert
   ExpertTiles<S::kTok> experts;
-  if (MODE != kLinear && !one) experts.count(a.offsets, a.E, l);
-  const int mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : (one ? a.E : experts.total());
+  if (MODE != kLinear) experts.count(a.offsets, a.E, l);
+  const int mtiles = MODE == kLinear ? (a.T + S::kTok - 1) / S::kTok : experts.total();
   const int total = mtiles * nw, chunk = (total + 7) / 8, slot = blockIdx.x >> 3;
   const int at = (int)(blockIdx.x & 7) * chunk + slot;
   if (slot >= chunk || at >= total) return;
-  int e = 0, wt, cnt;
+  int e = 0, rows = a.T, span = mtiles, q = at;
   int64_t first = 0;
-  if (one) {
-    // weight tiles outermost: the experts without pairs, which end here, are spread over the XCDs
-    wt = at / a.E;
-    e = at - wt * a.E;
-    first = a.offsets[e];
-    cnt = a.offsets[e + 1] - (int)first;
-    if (cnt == 0) return;
-  } else {
-    int rows = a.T, span = mtiles, q = at;
-    if (MODE != kLinear) {
-      const int4 t = experts.find(at / nw);
-      e = t.x;
-      q = at - t.y * nw;
-      first = t.z;
-      rows = t.w;
-      span = (rows + S::kTok - 1) / S::kTok;
-    }
-    // blocks of up to four token tiles by all weight tiles, tokens fastest
-    const int blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min(4, span - 4 * blk);
-    wt = rem / tc;
-    const int t0 = (4 * blk + rem - wt * tc) * S::kTok;
-    cnt = min(S::kTok, rows - t0);
-    first += t0;
+  if (MODE != kLinear) {
+    const int4 t = experts.find(at / nw);
+    e = t.x;
+    q = at - t.y * nw;
+    first = t.z;
+    rows = t.w;
+    span = (rows + S::kTok - 1) / S::kTok;
   }
+  // blocks of up to four token tiles by all weight tiles, tokens fastest
+  const int blk = q / (4 * nw), rem = q - blk * 4 * nw, tc = min(4, span - 4 * blk), wt = rem / tc;
+  const int t0 = (4 * blk + rem - wt * tc) * S::kTok, cnt = min(S::kTok, rows - t0);
+  first += t0;
 
   // weight group of slot s (of kSlots)
   auto group = [&](int s) -> int {
@@ -720,14 +710,9 @@ Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   return pairs < 128 * E || KK < 16 ? k256x128 : k256x256;
 }
 
-// A token picks an expert once, so with this few tokens every expert's pairs fit one m-tile.
-bool one_mtile(Shape s, int64_t T) { return s != kStream && T <= shape_tokens(s); }
-
 template <int MODE>
-hipError_t launch_experts_stage(MxArgs a, Shape s, const MxExperts& x, hipStream_t st) {
-  const bool one = one_mtile(s, x.T);
-  a.T = one;
-  const int64_t mtiles = one ? x.E : most_mtiles(x.T * x.k, x.E, shape_tokens(s));
+hipError_t launch_experts_stage(const MxArgs& a, Shape s, const MxExperts& x, hipStream_t st) {
+  const int64_t mtiles = most_mtiles(x.T * x.k, x.E, shape_tokens(s));
   switch (s) {
     case kStream: return launch_stream<MODE>(a, x.E, st);
     case k128x64: return launch_tiled<MODE, Mx128x64>(a, mtiles, st);
@@ -749,7 +734,7 @@ hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
   }
 }
 
-hipError_t launch_mx_experts(MxExperts x, hipStream_t st) {
+hipError_t launch_mx_experts(const MxExperts& x, hipStream_t st) {
   const int64_t pairs = x.T * x.k;
   const Shape s0 = experts_shape(pairs, x.E, x.gate_up.N, x.gate_up.KK), s1 = experts_shape(pairs, x.E, x.down.N, x.down.KK);
   if (hipError_t e = launch_experts_stage<kGateUp>(x.gate_up, s0, x, st)) return e;
