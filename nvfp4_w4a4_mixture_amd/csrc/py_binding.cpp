@@ -22,6 +22,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "../../include/moe_nvfp4.h"
@@ -176,17 +177,36 @@ void* address(PyObject* o) {
   if (!p && PyErr_Occurred()) throw python_error();
   return p;
 }
-// A torch stream's address; None: the current device's current stream.  Asked
-// for after the tensors are checked: without a GPU it raises.
-void* stream_of(PyObject* o) {
-  if (!given(o)) return c10::hip::getCurrentHIPStream().stream();
-  PyObject* r = PyObject_GetAttrString(o, "cuda_stream");
-  if (!r) throw python_error();
-  void* p = PyLong_AsVoidPtr(r);
-  Py_DECREF(r);
-  if (!p && PyErr_Occurred()) throw python_error();
-  return p;
-}
+
+// The stream that a call is enqueued on: a given torch stream, or the current
+// one.  A given stream is the current one of the tensors' device while this
+// object lives, so that missing outputs and workspaces come from its pool: the
+// allocator hands a block on in the order of its own stream's work, and a
+// workspace is dropped here while the kernels that use it are still queued.
+// Constructed after the tensors are checked: without a GPU it raises.
+class OnStream {
+ public:
+  OnStream(PyObject* o, const Tensor& like) {
+    if (!given(o)) return;
+    PyObject* r = PyObject_GetAttrString(o, "cuda_stream");
+    if (!r) throw python_error();
+    hipStream_t s = static_cast<hipStream_t>(PyLong_AsVoidPtr(r));
+    Py_DECREF(r);
+    if (!s && PyErr_Occurred()) throw python_error();
+    given_ = s;
+    before_ = c10::hip::getCurrentHIPStream(like.get_device());
+    c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(s, like.get_device()));
+  }
+  OnStream(const OnStream&) = delete;
+  ~OnStream() {
+    if (before_) c10::hip::setCurrentHIPStream(*before_);
+  }
+  void* get() const { return before_ ? given_ : c10::hip::getCurrentHIPStream().stream(); }
+
+ private:
+  hipStream_t given_ = nullptr;
+  std::optional<c10::hip::HIPStream> before_;
+};
 
 int64_t padded(int64_t cols) { return (cols + 255) / 256 * 256; }
 
@@ -236,9 +256,10 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // x, codes, scales, stream
 PyObject* quantize(PyObject* const* a) {
   const Rows x = matrix(a[0], "x", true);
+  const OnStream st(a[3], x.t);
   const Codes q = mx_output(a[1], a[2], x.t, x.rows, x.cols);
   check(g_entry.quantize(x.t.data_ptr(), x.t.scalar_type() == ScalarType::Float, x.rows, x.cols, x.ld,
-                         ptr<uint8_t>(q.codes), ptr<uint8_t>(q.scales), stream_of(a[3])),
+                         ptr<uint8_t>(q.codes), ptr<uint8_t>(q.scales), st.get()),
         "mxfp4_quantize");
   return tuple_of({q.codes, q.scales});
 }
@@ -246,9 +267,10 @@ PyObject* quantize(PyObject* const* a) {
 // codes, scales, cols, dtype code, out, stream
 PyObject* dequantize(PyObject* const* a) {
   const int64_t cols = integer(a[2]), rows = mx_input(a[0], a[1], cols), type = integer(a[3]);
+  const OnStream st(a[5], tensor(a[0], "x_codes"));
   const Out y = output(a[4], "out", tensor(a[0], "x_codes"), float_type(type), rows, cols);
   check(g_entry.dequantize(ptr<uint8_t>(tensor(a[0], "")), ptr<uint8_t>(tensor(a[1], "")), rows, cols, (int32_t)type,
-                           y.t.data_ptr(), y.ld, stream_of(a[5])),
+                           y.t.data_ptr(), y.ld, st.get()),
         "mxfp4_dequantize");
   return wrap(y.t);
 }
@@ -262,11 +284,12 @@ PyObject* linear(PyObject* const* a) {
   need(a[2], "w_codes", ScalarType::Byte, {G, KK, 4, 64, 16});
   const Tensor& ws = need(a[3], "w_scales", ScalarType::Byte, {G, KK, 64, 4});
   const Tensor &xc = tensor(a[0], ""), &xs = tensor(a[1], "");
+  const OnStream st(a[8], xc);
   const Out y = output(a[6], "y", xc, float_type(type), T, N);
   const size_t bytes = g_entry.linear_ws(T, K, N);
   const Tensor w = bytes || given(a[7]) ? workspace(a[7], xc, bytes) : Tensor();
   check(g_entry.linear(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, K, ptr<uint8_t>(wc), ptr<uint8_t>(ws), N, (int32_t)type,
-                       y.t.data_ptr(), y.ld, ptr<void>(w), w.defined() ? (size_t)w.numel() : 0, stream_of(a[8])),
+                       y.t.data_ptr(), y.ld, ptr<void>(w), w.defined() ? (size_t)w.numel() : 0, st.get()),
         "mxfp4_linear");
   return wrap(y.t);
 }
@@ -286,12 +309,13 @@ PyObject* grouped_ffn(PyObject* const* a) {
   const Tensor& off = need(a[10], "expert_offsets", ScalarType::Int, {E + 1});
   const Tensor& srt = need(a[11], "sorted_pair_ids", ScalarType::Int, {T * k});
   const Tensor& tw = need(a[12], "topk_w", ScalarType::Float, {T, k});
+  const OnStream st(a[16], xc);
   const Tensor po = buffer(a[13], "pair_out", xc, ScalarType::Half, {T * k, H});
   const Tensor ps = buffer(a[14], "pair_scale", xc, ScalarType::Float, {T * k});
   const Tensor ws = workspace(a[15], xc, g_entry.ffn_ws(T, k, E, H, I));
   check(g_entry.ffn(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, H, ptr<uint8_t>(c13), ptr<uint8_t>(s13), ptr<uint8_t>(c2),
                     ptr<uint8_t>(s2), ptr<int32_t>(m2), E, I, k, ptr<int32_t>(off), ptr<int32_t>(srt), ptr<float>(tw),
-                    ptr<uint16_t>(po), ptr<float>(ps), ptr<void>(ws), (size_t)ws.numel(), stream_of(a[16])),
+                    ptr<uint16_t>(po), ptr<float>(ps), ptr<void>(ws), (size_t)ws.numel(), st.get()),
         "mxfp4_grouped_ffn");
   return tuple_of({po, ps});
 }
@@ -313,9 +337,10 @@ Normed norm_output(PyObject* n, PyObject* quantize, PyObject* codes, PyObject* s
 PyObject* norm_in(PyObject* const* a) {
   const Rows x = matrix(a[0], "x");
   const Tensor& w = need(a[1], "w", ScalarType::BFloat16, {x.cols});
+  const OnStream st(a[7], x.t);
   const Normed r = norm_output(a[3], a[4], a[5], a[6], x.t, x.rows, x.cols);
   check(g_entry.norm_in(ptr<uint16_t>(x.t), x.rows, x.cols, x.ld, ptr<uint16_t>(w), (float)real(a[2]), ptr<uint16_t>(r.n.t),
-                        r.n.ld, ptr<uint8_t>(r.q.codes), ptr<uint8_t>(r.q.scales), stream_of(a[7])),
+                        r.n.ld, ptr<uint8_t>(r.q.codes), ptr<uint8_t>(r.q.scales), st.get()),
         "moe_norm_in");
   return r.q.codes.defined() ? tuple_of({r.n.t, r.q.codes, r.q.scales}) : wrap(r.n.t);
 }
@@ -338,6 +363,7 @@ PyObject* norm_out(PyObject* const* a) {
     grs = g.size(0) == 1 ? 0 : g.stride(0);
     gcs = g.size(1) == 1 ? 0 : g.stride(1);
   }
+  const OnStream st(a[12], y.t);
   const Out ro = output(a[7], "out", y.t, ScalarType::BFloat16, T, H);
   Normed q{{Tensor(), H}, {}};
   if (wn.defined())
@@ -347,7 +373,7 @@ PyObject* norm_out(PyObject* const* a) {
   check(g_entry.norm_out(y.t.data_ptr(), y.t.scalar_type() == ScalarType::Float, T, H, y.ld, ptr<uint16_t>(r.t), r.ld,
                          ptr<uint16_t>(wp), ptr<uint16_t>(g), grs, gcs, (float)real(a[5]), ptr<uint16_t>(wn),
                          (float)real(a[6]), ptr<uint16_t>(ro.t), ro.ld, ptr<uint16_t>(q.n.t), q.n.ld,
-                         ptr<uint8_t>(q.q.codes), ptr<uint8_t>(q.q.scales), stream_of(a[12])),
+                         ptr<uint8_t>(q.q.codes), ptr<uint8_t>(q.q.scales), st.get()),
         "moe_norm_out");
   if (!wn.defined()) return wrap(ro.t);
   if (!q.q.codes.defined()) return tuple_of({ro.t, q.n.t});
@@ -363,8 +389,9 @@ PyObject* combine(PyObject* const* a) {
   if (ps.numel() < T * k)
     raise(PyExc_ValueError, "pair_scale must hold T*k = %lld scales, got %lld", (long long)(T * k), (long long)ps.numel());
   if (!po.is_contiguous() || !ps.is_contiguous()) raise(PyExc_ValueError, "pair_out and pair_scale must be contiguous");
+  const OnStream st(a[6], po);
   const Tensor y = given(a[5]) ? tensor(a[5], "y") : fresh(po, float_type(type), {T, po.size(1)});
-  check(g_entry.combine(ptr<uint16_t>(po), ptr<float>(ps), T, k, po.size(1), (int32_t)type, y.data_ptr(), stream_of(a[6])),
+  check(g_entry.combine(ptr<uint16_t>(po), ptr<float>(ps), T, k, po.size(1), (int32_t)type, y.data_ptr(), st.get()),
         "moe_combine");
   return wrap(y);
 }
