@@ -52,11 +52,20 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, contiguous
         raise ValueError(f"{name} must be contiguous")
 
 
-def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An uninitialized tensor from the pool of the stream that uses it: the allocator hands a freed block on in the
+    order of that stream's work, and a workspace is freed while its kernels are still queued."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> torch.Tensor:
     if ws is not None:
         return ws
     # torch's caching allocator returns 256-byte aligned blocks
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return _empty((max(nbytes, 1),), torch.uint8, device, stream)
 
 
 def moe_route_workspace_bytes(T: int, H: int, E: int, k: int) -> int:
@@ -79,6 +88,12 @@ class RouteOut(NamedTuple):
     sorted_pair_ids: torch.Tensor  # [T*k] int32
 
 
+def _route_out(T: int, k: int, E: int, dev, stream) -> RouteOut:
+    return RouteOut(_empty((T, k), torch.int32, dev, stream), _empty((T, k), torch.float32, dev, stream),
+                    _empty((E,), torch.int32, dev, stream), _empty((E + 1,), torch.int32, dev, stream),
+                    _empty((T * k,), torch.int32, dev, stream))
+
+
 def moe_route(x_bf16: torch.Tensor, w_router_bf16: torch.Tensor, bias: torch.Tensor, k: int,
               routed_scaling_factor: float, out: Optional[RouteOut] = None,
               workspace: Optional[torch.Tensor] = None, stream=None) -> RouteOut:
@@ -92,13 +107,9 @@ def moe_route(x_bf16: torch.Tensor, w_router_bf16: torch.Tensor, bias: torch.Ten
     _need(bias, "bias", torch.float32, (E,))
     dev = x_bf16.device
     if out is None:
-        out = RouteOut(torch.empty((T, k), dtype=torch.int32, device=dev),
-                       torch.empty((T, k), dtype=torch.float32, device=dev),
-                       torch.empty((E,), dtype=torch.int32, device=dev),
-                       torch.empty((E + 1,), dtype=torch.int32, device=dev),
-                       torch.empty((T * k,), dtype=torch.int32, device=dev))
+        out = _route_out(T, k, E, dev, stream)
     nbytes = moe_route_workspace_bytes(T, H, E, k)
-    ws = _workspace(nbytes, dev, workspace)
+    ws = _workspace(nbytes, dev, workspace, stream)
     st = lib().moe_route(_p(x_bf16), T, H, ldx, _p(w_router_bf16), _p(bias), E, k,
                          float(routed_scaling_factor), _p(out.topk_ids), _p(out.topk_w), _p(out.expert_counts),
                          _p(out.expert_offsets), _p(out.sorted_pair_ids), _p(ws), ws.numel(), _stream(stream))
@@ -122,19 +133,15 @@ def moe_route_quantize(x_bf16: torch.Tensor, w_router_bf16: torch.Tensor, bias: 
     _need(x_gs, "x_gs", torch.float32, (1,))
     dev = x_bf16.device
     if out is None:
-        out = RouteOut(torch.empty((T, k), dtype=torch.int32, device=dev),
-                       torch.empty((T, k), dtype=torch.float32, device=dev),
-                       torch.empty((E,), dtype=torch.int32, device=dev),
-                       torch.empty((E + 1,), dtype=torch.int32, device=dev),
-                       torch.empty((T * k,), dtype=torch.int32, device=dev))
+        out = _route_out(T, k, E, dev, stream)
     if x_codes is None:
-        x_codes = torch.empty((T, H // 2), dtype=torch.uint8, device=dev)
+        x_codes = _empty((T, H // 2), torch.uint8, dev, stream)
     if x_scales is None:
-        x_scales = torch.empty((T, H // 16), dtype=torch.uint8, device=dev)
+        x_scales = _empty((T, H // 16), torch.uint8, dev, stream)
     _need(x_codes, "x_codes", torch.uint8, (T, H // 2))
     _need(x_scales, "x_scales", torch.uint8, (T, H // 16))
     nbytes = moe_route_workspace_bytes(T, H, E, k)
-    ws = _workspace(nbytes, dev, workspace)
+    ws = _workspace(nbytes, dev, workspace, stream)
     st = lib().moe_route_quantize(_p(x_bf16), T, H, ldx, _p(w_router_bf16), _p(bias), E, k,
                                   float(routed_scaling_factor), _p(x_gs), _p(x_codes), _p(x_scales),
                                   _p(out.topk_ids), _p(out.topk_w), _p(out.expert_counts), _p(out.expert_offsets),
@@ -153,9 +160,9 @@ def nvfp4_quantize_act(x_bf16: torch.Tensor, global_scale: torch.Tensor, codes: 
     ld = x_bf16.stride(0) if rows > 0 else cols
     dev = x_bf16.device
     if codes is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+        codes = _empty((rows, cols // 2), torch.uint8, dev, stream)
     if scales is None:
-        scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev)
+        scales = _empty((rows, cols // 16), torch.uint8, dev, stream)
     st = lib().nvfp4_quantize_act(_p(x_bf16), rows, cols, ld, _p(global_scale), _p(codes),
                                   _p(scales), _stream(stream))
     check(st, "nvfp4_quantize_act")
@@ -172,11 +179,11 @@ def nvfp4_quantize_weights(w_bf16: torch.Tensor, stream=None):
         raise ValueError("w_bf16 must be [batch, rows, cols]")
     b, r, c = w_bf16.shape
     dev = w_bf16.device
-    codes = torch.empty((b, r, c // 2), dtype=torch.uint8, device=dev)
+    codes = _empty((b, r, c // 2), torch.uint8, dev, stream)
     if r % 16 or c % 128:
         raise ValueError("nvfp4_quantize_weights needs rows % 16 == 0 and cols % 128 == 0")
-    scales = torch.empty((b, r // 16, c // 128, 16, 8), dtype=torch.uint8, device=dev)
-    gs = torch.empty((b,), dtype=torch.float32, device=dev)
+    scales = _empty((b, r // 16, c // 128, 16, 8), torch.uint8, dev, stream)
+    gs = _empty((b,), torch.float32, dev, stream)
     st = lib().nvfp4_quantize_weights(_p(w_bf16), b, r, c, _p(codes), _p(scales), _p(gs), _stream(stream))
     check(st, "nvfp4_quantize_weights")
     return codes, scales, gs
@@ -188,16 +195,16 @@ def _ffn_dims(x_codes, w13_codes, w2_codes):
     return T, 2 * h_half, E, two_i // 2
 
 
-def _pair_outputs(npairs: int, H: int, dev, pair_out, pair_scale, pair_sqnorm):
+def _pair_outputs(npairs: int, H: int, dev, pair_out, pair_scale, pair_sqnorm, stream):
     """The pair-row outputs: given ones checked, missing ones allocated (pair_sqnorm True: allocate, None/False: skip)."""
     if pair_out is None:
-        pair_out = torch.empty((npairs, H), dtype=torch.float16, device=dev)
+        pair_out = _empty((npairs, H), torch.float16, dev, stream)
     if pair_scale is None:
-        pair_scale = torch.empty((npairs,), dtype=torch.float32, device=dev)
+        pair_scale = _empty((npairs,), torch.float32, dev, stream)
     _need(pair_out, "pair_out", torch.float16, (npairs, H))
     _need(pair_scale, "pair_scale", torch.float32, (npairs,))
     if pair_sqnorm is True:
-        pair_sqnorm = torch.empty((npairs,), dtype=torch.float32, device=dev)
+        pair_sqnorm = _empty((npairs,), torch.float32, dev, stream)
     elif pair_sqnorm is False:
         pair_sqnorm = None
     if pair_sqnorm is not None:
@@ -224,8 +231,8 @@ def moe_nvfp4_grouped_ffn(x_codes, x_scales, x_gs, w13_codes, w13_scales, w13_gs
     _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, (T * k,))
     _need(topk_w, "topk_w", torch.float32)
     dev = x_codes.device
-    pair_out, pair_scale, pair_sqnorm = _pair_outputs(T * k, H, dev, pair_out, pair_scale, pair_sqnorm)
-    ws = _workspace(moe_ffn_workspace_bytes(T, k, E, H, I), dev, workspace)
+    pair_out, pair_scale, pair_sqnorm = _pair_outputs(T * k, H, dev, pair_out, pair_scale, pair_sqnorm, stream)
+    ws = _workspace(moe_ffn_workspace_bytes(T, k, E, H, I), dev, workspace, stream)
     st = lib().moe_nvfp4_grouped_ffn(_p(x_codes), _p(x_scales), _p(x_gs), T, H, _p(w13_codes), _p(w13_scales),
                                      _p(w13_gs), _p(w2_codes), _p(w2_scales), _p(w2_gs), _p(h_gs), E, I, k,
                                      _p(expert_offsets), _p(sorted_pair_ids), _p(topk_w), _p(pair_out),
@@ -275,10 +282,10 @@ def moe_nvfp4_gate_up_swiglu(x_codes, x_scales, x_gs, w13_codes, w13_scales, w13
     _need(w13_scales, "w13_scales", torch.uint8, (E, 2 * I // 16, H // 128, 16, 8))
     dev = x_codes.device
     if h_codes is None:
-        h_codes = torch.empty((T * k, I // 2), dtype=torch.uint8, device=dev)
+        h_codes = _empty((T * k, I // 2), torch.uint8, dev, stream)
     if h_scales is None:
-        h_scales = torch.empty((T * k, I // 16), dtype=torch.uint8, device=dev)
-    ws = _workspace(moe_ffn_stage_workspace_bytes(T, k, E, H, I), dev, workspace)
+        h_scales = _empty((T * k, I // 16), torch.uint8, dev, stream)
+    ws = _workspace(moe_ffn_stage_workspace_bytes(T, k, E, H, I), dev, workspace, stream)
     st = lib().moe_nvfp4_gate_up_swiglu(_p(x_codes), _p(x_scales), _p(x_gs), T, H, _p(w13_codes), _p(w13_scales),
                                         _p(w13_gs), _p(h_gs), E, I, k, _p(expert_offsets), _p(sorted_pair_ids),
                                         _p(h_codes), _p(h_scales), _p(ws), ws.numel(), _stream(stream))
@@ -294,8 +301,8 @@ def moe_nvfp4_down_scatter(h_codes, h_scales, h_gs, T: int, w2_codes, w2_scales,
     I = 2 * i_half
     _need(h_codes, "h_codes", torch.uint8, (T * k, I // 2))
     dev = h_codes.device
-    pair_out, pair_scale, pair_sqnorm = _pair_outputs(T * k, H, dev, pair_out, pair_scale, pair_sqnorm)
-    ws = _workspace(moe_ffn_stage_workspace_bytes(T, k, E, H, I), dev, workspace)
+    pair_out, pair_scale, pair_sqnorm = _pair_outputs(T * k, H, dev, pair_out, pair_scale, pair_sqnorm, stream)
+    ws = _workspace(moe_ffn_stage_workspace_bytes(T, k, E, H, I), dev, workspace, stream)
     st = lib().moe_nvfp4_down_scatter(_p(h_codes), _p(h_scales), _p(h_gs), T, H, _p(w2_codes), _p(w2_scales),
                                       _p(w2_gs), E, I, k, _p(expert_offsets), _p(sorted_pair_ids), _p(topk_w),
                                       _p(pair_out), _p(pair_scale), _p(pair_sqnorm), _p(ws), ws.numel(),
@@ -326,9 +333,9 @@ def moe_combine_reap(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k
     H = _need_pairs(pair_out, pair_scale, T, k)
     code = {torch.bfloat16: 0, torch.float32: 1}[out_dtype]
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=pair_out.device)
+        y = _empty((T, H), out_dtype, pair_out.device, stream)
     if saliency is None:
-        saliency = torch.empty((E,), dtype=torch.float32, device=pair_out.device)
+        saliency = _empty((E,), torch.float32, pair_out.device, stream)
     st = lib().moe_combine_reap(_p(pair_out), _p(pair_scale), T, k, H, code, _p(y), _p(pair_sqnorm), _p(topk_w),
                                 _p(expert_offsets), _p(sorted_pair_ids), E, _p(saliency), _stream(stream))
     check(st, "moe_combine_reap")
@@ -338,7 +345,7 @@ def moe_combine_reap(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k
 def reap_saliency(pair_sqnorm, topk_w, expert_offsets, sorted_pair_ids, T: int, k: int, E: int, out=None,
                   stream=None) -> torch.Tensor:
     if out is None:
-        out = torch.empty((E,), dtype=torch.float32, device=pair_sqnorm.device)
+        out = _empty((E,), torch.float32, pair_sqnorm.device, stream)
     st = lib().reap_saliency(_p(pair_sqnorm), _p(topk_w), _p(expert_offsets), _p(sorted_pair_ids), T, k, E,
                              _p(out), _stream(stream))
     check(st, "reap_saliency")
@@ -350,7 +357,7 @@ def reap_prune_select(saliency: torch.Tensor, n_keep: int, out=None, stream=None
     _need(saliency, "saliency", torch.float32)
     E = saliency.shape[0]
     if out is None:
-        out = torch.empty((n_keep,), dtype=torch.int32, device=saliency.device)
+        out = _empty((n_keep,), torch.int32, saliency.device, stream)
     _need(out, "keep_ids", torch.int32, (n_keep,))
     st = lib().reap_prune_select(_p(saliency), E, n_keep, _p(out), _stream(stream))
     check(st, "reap_prune_select")
@@ -364,7 +371,7 @@ def moe_gather_experts(src: torch.Tensor, keep_ids: torch.Tensor, out=None, stre
     _need(keep_ids, "keep_ids", torch.int32)
     n = keep_ids.shape[0]
     if out is None:
-        out = torch.empty((n, *src.shape[1:]), dtype=src.dtype, device=src.device)
+        out = _empty((n, *src.shape[1:]), src.dtype, src.device, stream)
     _need(out, "out", src.dtype, (n, *src.shape[1:]))
     per = src[0].numel() * src.element_size() if src.shape[0] > 0 else 0
     st = lib().moe_gather_experts(_p(src), src.shape[0], per, _p(keep_ids), n, _p(out), _stream(stream))
@@ -392,10 +399,10 @@ def moe_shared_expert(x_bf16, w13_bf16, w2_bf16, out=None, workspace=None, strea
     _need(x_bf16, "x_bf16", torch.bfloat16, contiguous=False)
     T, H, I = _shared_dims(x_bf16, w13_bf16, w2_bf16)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x_bf16.device)
+        out = _empty((T, H), torch.float32, x_bf16.device, stream)
     _need(out, "shared_out", torch.float32, (T, H))
     nb = moe_shared_workspace_bytes(T, H, I)
-    ws = _workspace(nb, x_bf16.device, workspace)
+    ws = _workspace(nb, x_bf16.device, workspace, stream)
     st = lib().moe_shared_expert(_p(x_bf16), T, H, x_bf16.stride(0), _p(w13_bf16), _p(w2_bf16), I, _p(out), _p(ws),
                                  ws.numel(), _stream(stream))
     check(st, "moe_shared_expert")
@@ -411,9 +418,9 @@ def moe_shared_gate_up(x_bf16, w13_bf16, h=None, workspace=None, stream=None) ->
     I = w13_bf16.shape[0] // 2
     _need(w13_bf16, "w13_bf16", torch.bfloat16, (2 * I, H))
     if h is None:
-        h = torch.empty((T, I), dtype=torch.bfloat16, device=x_bf16.device)
+        h = _empty((T, I), torch.bfloat16, x_bf16.device, stream)
     _need(h, "h_bf16", torch.bfloat16, (T, I))
-    ws = _workspace(moe_shared_workspace_bytes(T, H, I), x_bf16.device, workspace)
+    ws = _workspace(moe_shared_workspace_bytes(T, H, I), x_bf16.device, workspace, stream)
     st = lib().moe_shared_gate_up(_p(x_bf16), T, H, x_bf16.stride(0), _p(w13_bf16), I, _p(h), _p(ws), ws.numel(),
                                   _stream(stream))
     check(st, "moe_shared_gate_up")
@@ -427,9 +434,9 @@ def moe_shared_down(h_bf16, w2_bf16, out=None, workspace=None, stream=None) -> t
     H = w2_bf16.shape[0]
     _need(w2_bf16, "w2_bf16", torch.bfloat16, (H, I))
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=h_bf16.device)
+        out = _empty((T, H), torch.float32, h_bf16.device, stream)
     _need(out, "shared_out", torch.float32, (T, H))
-    ws = _workspace(moe_shared_workspace_bytes(T, H, I), h_bf16.device, workspace)
+    ws = _workspace(moe_shared_workspace_bytes(T, H, I), h_bf16.device, workspace, stream)
     st = lib().moe_shared_down(_p(h_bf16), T, I, _p(w2_bf16), H, _p(out), _p(ws), ws.numel(), _stream(stream))
     check(st, "moe_shared_down")
     return out
@@ -442,7 +449,7 @@ def moe_combine_block(pair_out: torch.Tensor, pair_scale: torch.Tensor, shared_o
     _need(shared_out, "shared_out", torch.float32, (T, H))
     code = {torch.bfloat16: 0, torch.float32: 1}[out_dtype]
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=pair_out.device)
+        y = _empty((T, H), out_dtype, pair_out.device, stream)
     st = lib().moe_combine_block(_p(pair_out), _p(pair_scale), _p(shared_out), T, k, H, code, _p(y), _stream(stream))
     check(st, "moe_combine_block")
     return y
@@ -457,7 +464,7 @@ def hadamard_rotate_bf16(src: torch.Tensor, signs: Optional[torch.Tensor], block
     cols = src.shape[-1]
     s2 = src.reshape(-1, cols) if src.dim() != 2 else src
     if out is None:
-        out = torch.empty(src.shape, dtype=torch.bfloat16, device=src.device)
+        out = _empty(src.shape, torch.bfloat16, src.device, stream)
     _need(out, "out", torch.bfloat16, tuple(src.shape), contiguous=False)
     o2 = out.reshape(-1, cols) if out.dim() != 2 else out
     if o2.data_ptr() != out.data_ptr() or (out.dim() != 2 and not out.is_contiguous()):
@@ -477,11 +484,11 @@ def _relayout(fn: str, codes: torch.Tensor, scales: torch.Tensor, kind: int, to_
     K = 2 * kh
     if to_tiled:
         _need(scales, "scales", torch.uint8, (E, N, K // 16))
-        out_s = torch.empty((E, N // 16, K // 128, 16, 8), dtype=torch.uint8, device=codes.device)
+        out_s = _empty((E, N // 16, K // 128, 16, 8), torch.uint8, codes.device, stream)
     else:
         _need(scales, "scales", torch.uint8, (E, N // 16, K // 128, 16, 8))
-        out_s = torch.empty((E, N, K // 16), dtype=torch.uint8, device=codes.device)
-    out_c = torch.empty_like(codes)
+        out_s = _empty((E, N, K // 16), torch.uint8, codes.device, stream)
+    out_c = _empty(codes.shape, codes.dtype, codes.device, stream)
     st = getattr(lib(), fn)(_p(codes), _p(scales), E, N, K, kind, _p(out_c), _p(out_s), _stream(stream))
     check(st, fn)
     return out_c, out_s
@@ -550,9 +557,9 @@ def mxfp4_quantize_weights(w_bf16: torch.Tensor, stream=None):
     b, n, k = w_bf16.shape
     cs, ss = _mx_weight_shapes(n, k)
     dev = w_bf16.device
-    codes = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
-    scales = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
-    max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
+    codes = _empty((b, *cs), torch.uint8, dev, stream)
+    scales = _empty((b, *ss), torch.uint8, dev, stream)
+    max_scale = _empty((b,), torch.int32, dev, stream)
     st = lib().mxfp4_quantize_weights(_p(w_bf16), b, n, k, _p(codes), _p(scales), _p(max_scale), _stream(stream))
     check(st, "mxfp4_quantize_weights")
     return codes, scales, max_scale
@@ -569,9 +576,9 @@ def mxfp4_pack_weights(codes: torch.Tensor, scales: torch.Tensor, stream=None):
     _need(scales, "scales", torch.uint8, (b, n, kh // 16))
     cs, ss = _mx_weight_shapes(n, 2 * kh)
     dev = codes.device
-    pc = torch.empty((b, *cs), dtype=torch.uint8, device=dev)
-    ps = torch.empty((b, *ss), dtype=torch.uint8, device=dev)
-    max_scale = torch.empty((b,), dtype=torch.int32, device=dev)
+    pc = _empty((b, *cs), torch.uint8, dev, stream)
+    ps = _empty((b, *ss), torch.uint8, dev, stream)
+    max_scale = _empty((b,), torch.int32, dev, stream)
     st = lib().mxfp4_pack_weights(_p(codes), _p(scales), b, n, 2 * kh, _p(pc), _p(ps), _p(max_scale), _stream(stream))
     check(st, "mxfp4_pack_weights")
     return pc, ps, max_scale
@@ -585,8 +592,8 @@ def mxfp4_unpack_weights(codes: torch.Tensor, scales: torch.Tensor, N: int, K: i
     _need(scales, "scales", torch.uint8, (b, *ss))
     if K % 32:
         raise ValueError("K must be a multiple of 32")
-    oc = torch.empty((b, N, K // 2), dtype=torch.uint8, device=codes.device)
-    os_ = torch.empty((b, N, K // 32), dtype=torch.uint8, device=codes.device)
+    oc = _empty((b, N, K // 2), torch.uint8, codes.device, stream)
+    os_ = _empty((b, N, K // 32), torch.uint8, codes.device, stream)
     st = lib().mxfp4_unpack_weights(_p(codes), _p(scales), b, N, K, _p(oc), _p(os_), _stream(stream))
     check(st, "mxfp4_unpack_weights")
     return oc, os_

@@ -34,7 +34,9 @@ def allocations(call):
 
 
 def flat(out):
-    return [t for t in (out if isinstance(out, (tuple, list)) else (out,)) if t is not None]
+    if isinstance(out, (tuple, list)):
+        return [t for o in out for t in flat(o)]
+    return [] if out is None else [out]
 
 
 def bf16(*shape, seed=0):
@@ -96,3 +98,48 @@ def test_a_refusal_leaves_the_current_stream(ops):
     with pytest.raises(ValueError, match="codes must have shape"):
         ops.mxfp4_quantize(x, codes=torch.empty((T, 1), dtype=torch.uint8, device="cuda"), stream=side)
     assert torch.cuda.current_stream() == before
+
+
+def test_weight_packing(ops):
+    w = bf16(E, 96, H)
+    check(lambda st: ops.mxfp4_quantize_weights(w, stream=st), 3)
+    codes, scales, _ = ops.mxfp4_quantize_weights(w)
+    check(lambda st: ops.mxfp4_unpack_weights(codes, scales, 96, H, stream=st), 2)
+    c, s = ops.mxfp4_unpack_weights(codes, scales, 96, H)
+    check(lambda st: ops.mxfp4_pack_weights(c, s, stream=st), 3)
+
+
+def test_nvfp4_layer(ops):
+    x, wr, bias = bf16(T, H), bf16(E, H, seed=3), torch.zeros(E, device="cuda")
+    gs = torch.full((1,), 40.0, device="cuda")
+    check(lambda st: ops.moe_route(x, wr, bias, K, 2.5, stream=st), 6)
+    check(lambda st: ops.moe_route_quantize(x, wr, bias, K, 2.5, gs, stream=st), 8)
+    check(lambda st: ops.nvfp4_quantize_act(x, gs, stream=st), 2)
+    w = bf16(2 * E, I, H, seed=1)
+    check(lambda st: ops.nvfp4_quantize_weights(w, stream=st), 3)
+    c13, s13, g13 = ops.nvfp4_quantize_weights(w)
+    w13 = (c13.view(E, 2 * I, H // 2), s13.view(E, 2 * I // 16, H // 128, 16, 8), g13.view(E, 2))
+    w2 = ops.nvfp4_quantize_weights(bf16(E, H, I, seed=2))
+    h_gs = torch.full((E,), 40.0, device="cuda")
+    r, xc, xs = ops.moe_route_quantize(x, wr, bias, K, 2.5, gs)
+    pairs = (r.expert_offsets, r.sorted_pair_ids, r.topk_w)
+    check(lambda st: ops.moe_nvfp4_grouped_ffn(xc, xs, gs, *w13, *w2, h_gs, K, *pairs, pair_sqnorm=True, stream=st), 4)
+    check(lambda st: ops.moe_nvfp4_gate_up_swiglu(xc, xs, gs, *w13, h_gs, K, *pairs[:2], stream=st), 3)
+    hc, hs = ops.moe_nvfp4_gate_up_swiglu(xc, xs, gs, *w13, h_gs, K, *pairs[:2])
+    check(lambda st: ops.moe_nvfp4_down_scatter(hc, hs, h_gs, T, *w2, K, *pairs, pair_sqnorm=True, stream=st), 4)
+    po, ps, sq = ops.moe_nvfp4_down_scatter(hc, hs, h_gs, T, *w2, K, *pairs, pair_sqnorm=True)
+    check(lambda st: ops.moe_combine_reap(po, ps, T, K, sq, r.topk_w, *pairs[:2], E, stream=st), 2)
+    check(lambda st: ops.reap_saliency(sq, r.topk_w, *pairs[:2], T, K, E, stream=st), 1)
+    sal = ops.reap_saliency(sq, r.topk_w, *pairs[:2], T, K, E)
+    check(lambda st: ops.reap_prune_select(sal, 2, stream=st), 1)
+    keep = ops.reap_prune_select(sal, 2)
+    check(lambda st: ops.moe_gather_experts(wr, keep, stream=st), 1)
+    ws13, ws2 = bf16(2 * I, H, seed=4), bf16(H, I, seed=5)
+    check(lambda st: ops.moe_shared_expert(x, ws13, ws2, stream=st), 2)
+    check(lambda st: ops.moe_shared_gate_up(x, ws13, stream=st), 2)
+    h = ops.moe_shared_gate_up(x, ws13)
+    check(lambda st: ops.moe_shared_down(h, ws2, stream=st), 2)
+    shared = ops.moe_shared_down(h, ws2)
+    check(lambda st: ops.moe_combine_block(po, ps, shared, T, K, stream=st), 1)
+    check(lambda st: ops.hadamard_rotate_bf16(x, None, 128, stream=st), 1)
+    check(lambda st: ops.moe_nvfp4_unpack_weights(*w13[:2], 0, stream=st), 2)
