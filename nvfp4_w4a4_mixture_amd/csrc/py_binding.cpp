@@ -390,7 +390,15 @@ PyObject* combine(PyObject* const* a) {
     raise(PyExc_ValueError, "pair_scale must hold T*k = %lld scales, got %lld", (long long)(T * k), (long long)ps.numel());
   if (!po.is_contiguous() || !ps.is_contiguous()) raise(PyExc_ValueError, "pair_out and pair_scale must be contiguous");
   const OnStream st(a[6], po);
-  const Tensor y = given(a[5]) ? tensor(a[5], "y") : fresh(po, float_type(type), {T, po.size(1)});
+  Tensor y;
+  if (given(a[5])) {  // any shape: the result is the first T * H elements
+    y = typed(a[5], "y", float_type(type));
+    if (!y.is_contiguous()) raise(PyExc_ValueError, "y must be contiguous");
+    if (y.numel() < T * po.size(1))
+      raise(PyExc_ValueError, "y must hold T*H = %lld elements, got %lld", (long long)(T * po.size(1)), (long long)y.numel());
+  } else {
+    y = fresh(po, float_type(type), {T, po.size(1)});
+  }
   check(g_entry.combine(ptr<uint16_t>(po), ptr<float>(ps), T, k, po.size(1), (int32_t)type, y.data_ptr(), st.get()),
         "moe_combine");
   return wrap(y);

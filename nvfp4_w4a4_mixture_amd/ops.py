@@ -323,7 +323,8 @@ def _need_pairs(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k: int
 
 def moe_combine(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k: int,
                 out_dtype: torch.dtype = torch.bfloat16, y=None, stream=None) -> torch.Tensor:
-    return _b.moe_combine(pair_out, pair_scale, T, k, _DTYPE[out_dtype], y, stream)
+    """y [T, H], the sum of each token's k pair rows, in out_dtype (a given y's type)."""
+    return _b.moe_combine(pair_out, pair_scale, T, k, _code(out_dtype, y), y, stream)
 
 
 def moe_combine_reap(pair_out: torch.Tensor, pair_scale: torch.Tensor, T: int, k: int, pair_sqnorm, topk_w,
