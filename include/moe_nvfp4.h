@@ -454,7 +454,9 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
  * [T*k] are pair rows in the form of the header comment (moe_combine,
  * moe_combine_block read them), with E = floor(log2 |w_p|) + 1 +
  * ceil(log2(36 I)) + bh + bw - 269 clamped to [max(0, floor(log2 |w_p|)) - 126,
- * 113], bh the largest scale byte of the pair's h and bw = w2_max_scale[e]:
+ * 113], bh the largest scale byte of the pair's h and bw = w2_max_scale[e], or
+ * the expert's largest scale byte under 255 if that is 255 (NaN blocks: the
+ * features that they reach are NaN, the others keep their values):
  * |w_p f| < 2^(E + 15).
  * H % 32 == 0, I % 32 == 0, 1 <= k <= E <= 256, T * k < 2^31; x codes
  * (T*Hp/2 bytes) and h codes (T*k*Ip/2 bytes) under 4 GiB, and (T*k/128 + E) *

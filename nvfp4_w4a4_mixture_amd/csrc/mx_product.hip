@@ -34,6 +34,30 @@ __device__ __forceinline__ int pair_exponent(float wp, uint32_t bh, int bw, int 
   return min(max(e, max(ew, 0) - 126), 113);
 }
 
+// bw for an expert whose weights hold NaN blocks, so that its largest byte is
+// 255 and says nothing: the largest of its other scale bytes, which bounds the
+// features that those blocks do not reach.  N lanes (8 or 64, in a row) read
+// the expert's scales; weights without NaN never come here.
+template <int N>
+__device__ __forceinline__ int finite_scale_max(const MxArgs& a, int e, int lane) {
+  const int64_t bytes = (int64_t)a.G * a.KK * kMxFragScales;
+  const uint8_t* scales = a.w_scales + e * bytes;
+  uint32_t m = 0;
+  for (int64_t i = 4 * lane; i < bytes; i += 4 * N) {
+    const uint32_t d = *reinterpret_cast<const uint32_t*>(scales + i);
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {
+      const uint32_t b = (d >> k) & 255u;
+      m = b == 255u ? m : max(m, b);
+    }
+  }
+  m = quad_max(m);
+  m = max(m, lane_dpp<kLaneHalfMirror>(m));
+#pragma unroll
+  for (int x = 8; x < N; x *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, x));
+  return (int)m;
+}
+
 // Two values rounded to nearest even in FP16, the first in the low half
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
@@ -178,6 +202,7 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
           uint32_t b = hmax[0][tok];
 #pragma unroll
           for (int k = 1; k < NW; ++k) b = max(b, hmax[k][tok]);
+          if (wmax == 255) wmax = finite_scale_max<8>(a, e, p);  // by the whole wave under the products: 0.2 us more
           const int E = pair_exponent(wp, b, wmax, a.aux);
           factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
           if (blockIdx.x == 0 && p == 0) static_cast<float*>(a.out_scales)[out] = __uint_as_float((uint32_t)(127 + E) << 23);
@@ -537,6 +562,11 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   else all_cols(Const<0>());
 
   int* out_row = reinterpret_cast<int*>(smem + S::kTok * S::kOutRow);
+  int wmax = 0;
+  if constexpr (MODE == kDown) {
+    wmax = a.w_max[e];
+    if (wmax == 255) wmax = finite_scale_max<64>(a, e, l);
+  }
   // ---- epilogue: a lane holds 16 consecutive features (half f of a group) of token n
 #pragma unroll
   for (int j = 0; j < GX; ++j) {
@@ -587,7 +617,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
       if constexpr (MODE == kDown) {
         const uint32_t b = max(bh[j], (uint32_t)__shfl_xor((int)bh[j], 32));
         if (in) {
-          const int E = pair_exponent(pair_w[j], b, a.w_max[e], a.aux);
+          const int E = pair_exponent(pair_w[j], b, wmax, a.aux);
           factor = pair_w[j] * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
           if (wm == 0 && f == 0) {
             out_row[tok] = pair[j];

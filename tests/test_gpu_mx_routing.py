@@ -53,3 +53,33 @@ def test_repeated_experts(ops, monkeypatch, T, E, k, H, I):
 
     with_ids(monkeypatch, make)
     mxt.test_experts(ops, T, E, k, H, I, "repeated")
+
+
+# streaming; 128 x 64 tiles; 256 x 128 tiles
+@pytest.mark.parametrize("T,E,k,H,I", [(2, 4, 2, 288, 96), (200, 4, 2, 288, 96), (2048, 256, 8, 96, 64)])
+def test_nan_weights_leave_the_other_features(ops, T, E, k, H, I):
+    """NaN blocks in an expert's down weights make NaN of their own features; every other one is, bit for bit, what it
+    is with zeros in their place."""
+    rng = np.random.default_rng(T)
+    _, xb = mxt.bf16(mxt.draw(rng, T, H))
+    _, b13 = mxt.bf16(rng.standard_normal((E, 2 * I, H)) * H ** -0.5)
+    w2 = (rng.standard_normal((E, H, I)) * I ** -0.5).astype(np.float32)
+    bad = np.zeros((E, H), bool)
+    clean = w2.copy()
+    for e, row, block, value in ((0, 5, 1, np.nan), (0, H - 1, 0, -np.inf), (2, 33, I // 32 - 1, np.inf)):
+        w2[e, row, 32 * block + 7] = value
+        clean[e, row, 32 * block: 32 * block + 32] = 0
+        bad[e, row] = True
+    w2[3] = np.nan  # an expert with nothing else
+    clean[3] = 0
+    bad[3] = True
+    ids, w, offsets, order = mxt.routing(rng, T, E, k, "even")
+    w[0] = 3e4  # a row whose scale matters
+    args = (ids, w, offsets, order, E, k, H, I)
+    po, ps = mxt.run_experts(ops, xb, b13, mxt.bf16(w2)[1], *args)
+    want, want_scale = mxt.run_experts(ops, xb, b13, mxt.bf16(clean)[1], *args)
+    assert torch.equal(ps, want_scale)
+    mask = torch.from_numpy(bad[ids.reshape(-1)]).cuda()  # [T*k, H]: the pair's expert has NaN in this feature
+    assert bool(torch.isnan(po[mask]).all())
+    assert torch.equal(po[~mask].view(torch.int16), want[~mask].view(torch.int16))
+    assert bool((want[~mask] != 0).any())
