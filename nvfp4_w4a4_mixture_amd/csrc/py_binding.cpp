@@ -172,6 +172,11 @@ double real(PyObject* o) {
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
   return v;
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
 void* address(PyObject* o) {
   void* p = PyLong_AsVoidPtr(o);
   if (!p && PyErr_Occurred()) throw python_error();
@@ -329,7 +334,7 @@ Normed norm_output(PyObject* n, PyObject* quantize, PyObject* codes, PyObject* s
                    int64_t H) {
   Normed r{{Tensor(), H}, {}};
   if (n != Py_False) r.n = output(n, "n", like, ScalarType::BFloat16, T, H);
-  if (quantize == Py_True || given(codes) || given(scales)) r.q = mx_output(codes, scales, like, T, H);
+  if (truth(quantize) || given(codes) || given(scales)) r.q = mx_output(codes, scales, like, T, H);
   return r;
 }
 
@@ -368,7 +373,7 @@ PyObject* norm_out(PyObject* const* a) {
   Normed q{{Tensor(), H}, {}};
   if (wn.defined())
     q = norm_output(a[8], a[9], a[10], a[11], y.t, T, H);
-  else if (given(a[8]) || a[9] == Py_True || given(a[10]) || given(a[11]))
+  else if (given(a[8]) || truth(a[9]) || given(a[10]) || given(a[11]))
     raise(PyExc_ValueError, "n and its quantization need w_next");
   check(g_entry.norm_out(y.t.data_ptr(), y.t.scalar_type() == ScalarType::Float, T, H, y.ld, ptr<uint16_t>(r.t), r.ld,
                          ptr<uint16_t>(wp), ptr<uint16_t>(g), grs, gcs, (float)real(a[5]), ptr<uint16_t>(wn),

@@ -1,5 +1,6 @@
 """What the binding accepts and refuses of tensors on the device."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -40,3 +41,20 @@ def test_combine_into_a_given_y(ops):
     refused(ValueError, "GPU", torch.empty((T, H)))
     with pytest.raises(TypeError, match="output type"):
         ops.moe_combine(po, ps, T, k, torch.float16)
+
+
+@pytest.mark.parametrize("flag", [1, np.True_, True])
+def test_quantize_is_any_truth_value(ops, flag):
+    x = torch.randn(3, 64, device="cuda").to(torch.bfloat16)
+    want = ops.moe_norm_in(x, x[0], quantize=True)
+    got = ops.moe_norm_in(x, x[0], quantize=flag)
+    assert len(got) == 3 and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert len(ops.moe_norm_out(x, x, None, x[0], quantize=flag)) == 4
+    with pytest.raises(ValueError, match="need w_next"):
+        ops.moe_norm_out(x, x, quantize=flag)
+
+
+@pytest.mark.parametrize("flag", [0, np.False_, False, None])
+def test_quantize_is_any_false_value(ops, flag):
+    x = torch.randn(3, 64, device="cuda").to(torch.bfloat16)
+    assert torch.equal(ops.moe_norm_in(x, x[0], quantize=flag), ops.moe_norm_in(x, x[0]))
