@@ -8,9 +8,10 @@
     y          = moe_combine(pair rows)                                  (FP32)
     r2, n, c, s = moe_norm_out(y, r1, w_post_moe, w_next, gate, scale)    (residual, the next layer's first norm, quantized)
 
-``enter`` is the norm before a first layer.  All buffers for a token count are
-allocated once and reused, so a forward pass enqueues only kernels on the
-current stream and can be captured in a HIP graph.
+``enter`` is the norm before a first layer.  The buffers of the token counts
+used last are kept and reused (``buffers.Buffers``), so a forward pass of one of
+them enqueues only kernels on the current stream, and a pass can be captured in
+a HIP graph.
 
 ``python -m nvfp4_w4a4_mixture_amd.mx_block`` runs one block with random
 weights and prints its shapes and time.
@@ -24,6 +25,7 @@ from typing import Optional
 import torch
 
 from . import ops
+from .buffers import Buffers
 
 
 @dataclass
@@ -51,7 +53,7 @@ class MXFP4Block:
         self.norms = (w_post_attn, w_pre_moe, w_post_moe, w_next)
         self.gate, self.residual_scale, self.eps = gate, float(residual_scale), float(eps)
         self.device = w_router_bf16.device
-        self._bufs: dict = {}
+        self._bufs = Buffers(self.device)
 
     @classmethod
     def from_bf16(cls, w_o, w_router_bf16, bias, k, rsf, w13, w2, w_pre_moe, w_next, **kw) -> "MXFP4Block":
@@ -63,24 +65,20 @@ class MXFP4Block:
                    ops.mxfp4_quantize_weights(w2), w_pre_moe, w_next, **kw)
 
     def _buffers(self, T: int, K: int) -> dict:
-        b = self._bufs.get((T, K))
-        if b is None:
-            d, E, H, I, k = self.device, self.E, self.H, self.I, self.k
-            new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=d)  # noqa: E731
-            rows = lambda c: dict(codes=new((T, -(-c // 256) * 128), torch.uint8),  # noqa: E731
-                                  scales=new((T, -(-c // 256) * 8), torch.uint8))
-            b = dict(a=rows(K), o=new((T, H), torch.float32), r1=new((T, H), torch.bfloat16),
-                     n1=new((T, H), torch.bfloat16), x=rows(H),
-                     route=ops.RouteOut(new((T, k), torch.int32), new((T, k), torch.float32), new((E,), torch.int32),
-                                        new((E + 1,), torch.int32), new((T * k,), torch.int32)),
-                     route_ws=new((max(ops.moe_route_workspace_bytes(T, H, E, k), 1),), torch.uint8),
-                     linear_ws=new((max(ops.mxfp4_linear_workspace_bytes(T, K, H), 1),), torch.uint8),
-                     ffn_ws=new((max(ops.mxfp4_ffn_workspace_bytes(T, k, E, H, I), 1),), torch.uint8),
-                     pair_out=new((T * k, H), torch.float16), pair_scale=new((T * k,), torch.float32),
-                     y=new((T, H), torch.float32), r2=new((T, H), torch.bfloat16), n2=new((T, H), torch.bfloat16),
-                     out=rows(H))
-            self._bufs[(T, K)] = b
-        return b
+        d, E, H, I, k = self.device, self.E, self.H, self.I, self.k
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=d)  # noqa: E731
+        rows = lambda c: dict(codes=new((T, -(-c // 256) * 128), torch.uint8),  # noqa: E731
+                              scales=new((T, -(-c // 256) * 8), torch.uint8))
+        return dict(a=rows(K), o=new((T, H), torch.float32), r1=new((T, H), torch.bfloat16),
+                    n1=new((T, H), torch.bfloat16), x=rows(H),
+                    route=ops.RouteOut(new((T, k), torch.int32), new((T, k), torch.float32), new((E,), torch.int32),
+                                       new((E + 1,), torch.int32), new((T * k,), torch.int32)),
+                    route_ws=new((max(ops.moe_route_workspace_bytes(T, H, E, k), 1),), torch.uint8),
+                    linear_ws=new((max(ops.mxfp4_linear_workspace_bytes(T, K, H), 1),), torch.uint8),
+                    ffn_ws=new((max(ops.mxfp4_ffn_workspace_bytes(T, k, E, H, I), 1),), torch.uint8),
+                    pair_out=new((T * k, H), torch.float16), pair_scale=new((T * k,), torch.float32),
+                    y=new((T, H), torch.float32), r2=new((T, H), torch.bfloat16), n2=new((T, H), torch.bfloat16),
+                    out=rows(H))
 
     def enter(self, x: torch.Tensor, w: torch.Tensor):
         """The norm before a first layer: (n, codes, scales) of x [T, H]."""
@@ -91,7 +89,7 @@ class MXFP4Block:
 
         The returned tensors are the block's buffers for this T: the next call of the same T overwrites them."""
         T, K = attn.shape
-        b = self._buffers(T, K)
+        b = self._bufs.take((T, K), lambda: self._buffers(T, K))
         w_post_attn, w_pre, w_post_moe, w_next = self.norms
         ops.mxfp4_quantize(attn, **b["a"])
         ops.mxfp4_linear(b["a"]["codes"], b["a"]["scales"], *self.w_o, self.H, y=b["o"], workspace=b["linear_ws"])
