@@ -4,8 +4,9 @@ forward(x):  moe_route_quantize -> moe_nvfp4_gate_up_swiglu ->
              moe_nvfp4_down_scatter -> moe_combine (moe_combine_reap with REAP)
 block output: moe_shared_expert on a second stream, joined by moe_combine_block
 (the two FFN calls are the stages of moe_nvfp4_grouped_ffn)
-All buffers for a given token count are allocated once and reused, so a
-forward pass enqueues only kernels on the current stream.
+The buffers of the token counts used last are kept and reused
+(``buffers.Buffers``), so a forward pass of one of them enqueues only kernels on
+the current stream.
 """
 
 from __future__ import annotations
@@ -16,6 +17,7 @@ from typing import Optional
 import torch
 
 from . import ops
+from .buffers import Buffers
 
 
 @dataclass
@@ -47,7 +49,7 @@ class NVFP4MoELayer:
         self.E, two_i, h_half = w13_codes.shape
         self.H, self.I = 2 * h_half, two_i // 2
         self.device = w13_codes.device
-        self._bufs: dict = {}
+        self._bufs = Buffers(self.device)
         self.keep_ids = None  # set on a layer made by prune(): its experts' ids in the unpruned layer
         self.shared = None  # (w13 [2I_s, H], w2 [H, I_s]) BF16 of the shared expert, if attached
         self._side = None  # stream the shared expert runs on, beside the routed path
@@ -69,37 +71,33 @@ class NVFP4MoELayer:
                    s13.view(E, 2 * I // 16, H // 128, 16, 8), g13.view(E, 2), c2, s2, g2)
 
     def _buffers(self, T: int, reap: bool, out_dtype: torch.dtype, block: bool = False):
-        key = (T, reap, out_dtype, block)
-        b = self._bufs.get(key)
-        if b is None:
-            d, E, H, I, k = self.device, self.E, self.H, self.I, self.k
-            b = dict(
-                route=ops.RouteOut(torch.empty((T, k), dtype=torch.int32, device=d),
-                                   torch.empty((T, k), dtype=torch.float32, device=d),
-                                   torch.empty((E,), dtype=torch.int32, device=d),
-                                   torch.empty((E + 1,), dtype=torch.int32, device=d),
-                                   torch.empty((T * k,), dtype=torch.int32, device=d)),
-                route_ws=torch.empty((max(ops.moe_route_workspace_bytes(T, H, E, k), 1),), dtype=torch.uint8, device=d),
-                x_codes=torch.empty((T, H // 2), dtype=torch.uint8, device=d),
-                x_scales=torch.empty((T, H // 16), dtype=torch.uint8, device=d),
-                pair_out=torch.empty((T * k, H), dtype=torch.float16, device=d),
-                pair_scale=torch.empty((T * k,), dtype=torch.float32, device=d),
-                pair_sqnorm=torch.empty((T * k,), dtype=torch.float32, device=d) if reap else None,
-                h_codes=torch.empty((T * k, I // 2), dtype=torch.uint8, device=d),
-                h_scales=torch.empty((T * k, I // 16), dtype=torch.uint8, device=d),
-                ffn_ws=torch.empty((max(ops.moe_ffn_stage_workspace_bytes(T, k, E, H, I), 1),), dtype=torch.uint8,
-                                   device=d),
-                y=torch.empty((T, H), dtype=out_dtype, device=d),
-                saliency=torch.empty((E,), dtype=torch.float32, device=d) if reap else None,
-            )
-            if block:
-                Is = self.shared[1].shape[1]
-                b["shared_out"] = torch.empty((T, H), dtype=torch.float32, device=d)
-                b["shared_ws"] = torch.empty((max(ops.moe_shared_workspace_bytes(T, H, Is), 1),), dtype=torch.uint8,
-                                             device=d)
-                b["ev_in"] = torch.cuda.Event()
-                b["ev_shared"] = torch.cuda.Event()
-            self._bufs[key] = b
+        d, E, H, I, k = self.device, self.E, self.H, self.I, self.k
+        b = dict(
+            route=ops.RouteOut(torch.empty((T, k), dtype=torch.int32, device=d),
+                               torch.empty((T, k), dtype=torch.float32, device=d),
+                               torch.empty((E,), dtype=torch.int32, device=d),
+                               torch.empty((E + 1,), dtype=torch.int32, device=d),
+                               torch.empty((T * k,), dtype=torch.int32, device=d)),
+            route_ws=torch.empty((max(ops.moe_route_workspace_bytes(T, H, E, k), 1),), dtype=torch.uint8, device=d),
+            x_codes=torch.empty((T, H // 2), dtype=torch.uint8, device=d),
+            x_scales=torch.empty((T, H // 16), dtype=torch.uint8, device=d),
+            pair_out=torch.empty((T * k, H), dtype=torch.float16, device=d),
+            pair_scale=torch.empty((T * k,), dtype=torch.float32, device=d),
+            pair_sqnorm=torch.empty((T * k,), dtype=torch.float32, device=d) if reap else None,
+            h_codes=torch.empty((T * k, I // 2), dtype=torch.uint8, device=d),
+            h_scales=torch.empty((T * k, I // 16), dtype=torch.uint8, device=d),
+            ffn_ws=torch.empty((max(ops.moe_ffn_stage_workspace_bytes(T, k, E, H, I), 1),), dtype=torch.uint8,
+                               device=d),
+            y=torch.empty((T, H), dtype=out_dtype, device=d),
+            saliency=torch.empty((E,), dtype=torch.float32, device=d) if reap else None,
+        )
+        if block:
+            Is = self.shared[1].shape[1]
+            b["shared_out"] = torch.empty((T, H), dtype=torch.float32, device=d)
+            b["shared_ws"] = torch.empty((max(ops.moe_shared_workspace_bytes(T, H, Is), 1),), dtype=torch.uint8,
+                                         device=d)
+            b["ev_in"] = torch.cuda.Event()
+            b["ev_shared"] = torch.cuda.Event()
         return b
 
     def prune(self, saliency: torch.Tensor, n_keep: int) -> "NVFP4MoELayer":
@@ -133,7 +131,7 @@ class NVFP4MoELayer:
         T = x_bf16.shape[0]
         if block and self.shared is None:
             raise ValueError("block=True needs a shared expert (set_shared_expert)")
-        b = self._buffers(T, reap, out_dtype, block)
+        b = self._bufs.take((T, reap, out_dtype, block), lambda: self._buffers(T, reap, out_dtype, block))
         def mark(i):  # record event i if one was given for that position
             if events is not None and events[i] is not None:
                 events[i].record()

@@ -78,3 +78,20 @@ def test_block_on_two_streams(mx_block):
             torch.cuda.current_stream().wait_stream(side)
             assert torch.equal(got, want[T])
             assert torch.equal(blk(x[T], x[T]).y, want[T])
+
+
+def test_nvfp4_layer_of_many_token_counts(mx_block):
+    from nvfp4_w4a4_mixture_amd import workload_io
+    from workloads import by_name
+
+    cfg, dev = by_name("tiny"), torch.device("cuda:0")
+    plain, _ = workload_io.build_layer(cfg, dev)
+    tight, _ = workload_io.build_layer(cfg, dev)
+    tight._bufs.keep_bytes = 1 << 20
+    x = workload_io.tokens(cfg, dev)
+    for T in list(range(1, 65)) + [64, 3]:
+        for reap in (False, True):
+            a, b = plain(x[:T], reap=reap), tight(x[:T], reap=reap)
+            assert torch.equal(a.y, b.y) and (not reap or torch.equal(a.saliency, b.saliency))
+            assert held(tight) <= tight._bufs.keep_bytes
+    assert len(plain._bufs) == 128 > len(tight._bufs)
