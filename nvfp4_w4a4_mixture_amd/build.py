@@ -77,7 +77,8 @@ def build_binding() -> str:
 def build(verbose: bool = False, out_dir: str = OUT_DIR, build_dir: str = BUILD_DIR, defines=(),
           sanitize: bool = False) -> str:
     """Compile every source and link ``<out_dir>/libmoe_nvfp4.so``; returns its path.  The product
-    build (the default ``out_dir``) compiles the binding too.
+    build (the default ``out_dir``) compiles the binding too, and any other does if there is none: it is
+    given the library's entry points by address, so one serves every build.
 
     ``defines`` (NAME=VALUE strings) override compile-time tile parameters.  ``sanitize``
     instruments the host code with AddressSanitizer and UndefinedBehaviorSanitizer (the library
@@ -90,10 +91,8 @@ def build(verbose: bool = False, out_dir: str = OUT_DIR, build_dir: str = BUILD_
     os.makedirs(build_dir, exist_ok=True)
     os.makedirs(out_dir, exist_ok=True)
     with ThreadPoolExecutor(min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(build_binding) if out_dir == OUT_DIR else None
+        binding = ex.submit(build_binding) if out_dir == OUT_DIR or not os.path.exists(BINDING) else None
         objs = list(ex.map(lambda src: _compile(src, build_dir, defines, extra), SOURCES))
-        if binding is not None:
-            binding.result()
     tmp = os.path.join(out_dir, LIB_NAME + ".tmp")
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *extra, *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -101,6 +100,8 @@ def build(verbose: bool = False, out_dir: str = OUT_DIR, build_dir: str = BUILD_
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     out = os.path.join(out_dir, LIB_NAME)
     shutil.move(tmp, out)
+    if binding is not None:
+        binding.result()  # raises here if it failed: the library is there, and most of ops needs no more
     if verbose:
         print("built", out)
     return out

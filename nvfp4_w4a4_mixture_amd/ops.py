@@ -510,19 +510,27 @@ def moe_nvfp4_unpack_weights(codes: torch.Tensor, packed_scales: torch.Tensor, k
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
-def _bound():
-    """The compiled binding, with the loaded library's entry points."""
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError("the compiled binding is not built; run `python -m nvfp4_w4a4_mixture_amd.build`") from e
-    names = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear_workspace_bytes", "mxfp4_linear",
-             "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine")
-    _binding.bind(check, *(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names))
-    return _binding
+class _Binding:
+    """The compiled binding's functions.  It is imported, and given the loaded library's entry points, at the first use
+    of one: the functions that are marshalled here need only the library."""
+
+    _ENTRIES = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear_workspace_bytes", "mxfp4_linear",
+                "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine")
+
+    def __getattr__(self, name):  # only until the functions are this object's own attributes
+        if name not in self._ENTRIES:
+            raise AttributeError(name)
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"{name}: the compiled binding is not built; run "
+                               "`python -m nvfp4_w4a4_mixture_amd.build`") from e
+        _binding.bind(check, *(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in self._ENTRIES))
+        self.__dict__.update((n, f) for n, f in vars(_binding).items() if n in self._ENTRIES)
+        return self.__dict__[name]
 
 
-_b = _bound()
+_b = _Binding()
 
 
 def _code(out_dtype: torch.dtype, out) -> int:
