@@ -83,3 +83,35 @@ def test_nan_weights_leave_the_other_features(ops, T, E, k, H, I):
     assert bool(torch.isnan(po[mask]).all())
     assert torch.equal(po[~mask].view(torch.int16), want[~mask].view(torch.int16))
     assert bool((want[~mask] != 0).any())
+
+
+# 65 to 256 experts, whose tiles are found over all the lanes of a wave (four experts a lane): 128 x 64 and 256 x 128
+# tiles; pairs everywhere, only in the last half, only at every seventh expert
+@pytest.mark.parametrize("T,E,k,H,I", [(200, 70, 8, 320, 160), (300, 128, 8, 96, 64), (600, 256, 8, 96, 64),
+                                       (2048, 256, 8, 96, 64), (999, 130, 5, 64, 288), (700, 255, 6, 64, 32)])
+@pytest.mark.parametrize("where", ["all", "late", "sparse"])
+def test_many_experts(ops, monkeypatch, T, E, k, H, I, where):
+    def make(rng, T, E, k):
+        pool = {"all": np.arange(E), "late": np.arange(E // 2, E), "sparse": np.arange(E - 1, 0, -7)}[where]
+        return np.stack([rng.permutation(pool)[:k] for _ in range(T)])
+
+    with_ids(monkeypatch, make)
+    mxt.test_experts(ops, T, E, k, H, I, where)
+
+
+# rows on 16 bytes, written eight BF16 at a time: every tile shape (128 x 64, 128 x 128, 256 x 128, 256 x 256), ragged
+# last tiles in both directions, and rows of which the last piece goes by elements
+@pytest.mark.parametrize("T,K,N", [(1, 288, 64), (40, 288, 8200), (400, 288, 4208), (390, 1568, 4200), (900, 320, 6216),
+                                   (897, 1344, 6200), (1800, 288, 6512), (1797, 1888, 6504), (1797, 4128, 6504)])
+@pytest.mark.parametrize("extra", [0, 5])
+def test_linear_bf16_vector_stores(ops, T, K, N, extra):
+    mxt.say(f"linear BF16 T={T} K={K} N={N}+{extra}")
+    x, xb, w, wb = mxt.linear_case(T + K + N, T, K, N + extra)
+    wc, wsc, _ = ops.mxfp4_quantize_weights(mxt.dev_bf16(wb)[None])
+    codes, scales = ops.mxfp4_quantize(mxt.dev_bf16(xb))
+    n = N + extra
+    y = torch.full((T, -(-n // 8) * 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    ops.mxfp4_linear(codes, scales, wc[0], wsc[0], n, y=y[:, :n])
+    mxt.check_linear(mxt.to_np(y[:, :n].float()).astype(np.float64), mxt.mx.rounded(x), mxt.mx.rounded(w), True)
+    assert bool((y[:, n:] == 7.0).all())
+    assert torch.equal(ops.mxfp4_linear(codes, scales, wc[0], wsc[0], n), y[:, :n])
