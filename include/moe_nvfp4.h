@@ -433,8 +433,8 @@ moe_status mxfp4_unpack_weights(const uint8_t* packed_codes, const uint8_t* pack
  * form, w packed [N, K]; y [T, ldy] (ldy >= N) in out_dtype (BF16
  * round-to-nearest-even).  Code arrays 16-byte, scale arrays 4-byte, y 4-byte
  * (BF16: 2-byte) aligned.  T * Kp / 2 < 2^32 bytes (Kp = round_up(K, 256)) and
- * T <= 2097120, N <= 2^27, ldy < 2^31, and under 2^22 tiles of 256 x 256.  workspace: mxfp4_linear_workspace_bytes(T, K, N) bytes
- * (0 possible: workspace may then be NULL), 256-byte aligned. */
+ * T <= 2097120, N <= 2^27, ldy < 2^31, and under 2^22 tiles of 256 x 256.
+ * mxfp4_linear_workspace_bytes is 0: workspace is not read and may be NULL. */
 size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K, int64_t N);
 moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t K,
                         const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int32_t out_dtype, void* y,

@@ -141,16 +141,11 @@ static moe_status check_linear(int64_t T, int64_t K, int64_t N) {
   return MOE_OK;
 }
 
-size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K, int64_t N) {
-  (void)T;
-  (void)K;
-  (void)N;
-  return 0;
-}
+size_t mxfp4_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t K,
                         const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int32_t out_dtype, void* y,
-                        int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+                        int64_t ldy, void*, size_t, void* stream) {
   const char* fn = "mxfp4_linear";
   if (!dtype_ok(out_dtype)) return fail(MOE_ERR_SHAPE, "%s: out_dtype must be 0 (BF16) or 1 (FP32)", fn);
   if (moe_status s = check_linear(T, K, N)) return s;
@@ -160,10 +155,6 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
   if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
       !aligned(y, out_dtype ? 4 : 2))
     return fail(MOE_ERR_ALIGN, "%s: code arrays must be 16-byte, scale arrays 4-byte aligned, y to its element", fn);
-  const size_t need = mxfp4_linear_workspace_bytes(T, K, N);
-  if (need > 0 && (!workspace || workspace_bytes < need))
-    return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, need);
-  if (need > 0 && !aligned(workspace, 256)) return fail(MOE_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
   if (moe_status s = check_device()) return s;
   moe::MxArgs a{};
   a.a_codes = x_codes;

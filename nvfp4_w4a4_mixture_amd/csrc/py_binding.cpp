@@ -35,7 +35,6 @@ using at::Tensor;
 struct Entry {
   decltype(&mxfp4_quantize) quantize;
   decltype(&mxfp4_dequantize) dequantize;
-  decltype(&mxfp4_linear_workspace_bytes) linear_ws;
   decltype(&mxfp4_linear) linear;
   decltype(&mxfp4_ffn_workspace_bytes) ffn_ws;
   decltype(&mxfp4_grouped_ffn) ffn;
@@ -291,10 +290,9 @@ PyObject* linear(PyObject* const* a) {
   const Tensor &xc = tensor(a[0], ""), &xs = tensor(a[1], "");
   const OnStream st(a[8], xc);
   const Out y = output(a[6], "y", xc, float_type(type), T, N);
-  const size_t bytes = g_entry.linear_ws(T, K, N);
-  const Tensor w = bytes || given(a[7]) ? workspace(a[7], xc, bytes) : Tensor();
+  if (given(a[7])) workspace(a[7], xc, 0);  // of the right kind; the product uses none
   check(g_entry.linear(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, K, ptr<uint8_t>(wc), ptr<uint8_t>(ws), N, (int32_t)type,
-                       y.t.data_ptr(), y.ld, ptr<void>(w), w.defined() ? (size_t)w.numel() : 0, st.get()),
+                       y.t.data_ptr(), y.ld, nullptr, 0, st.get()),
         "mxfp4_linear");
   return wrap(y.t);
 }

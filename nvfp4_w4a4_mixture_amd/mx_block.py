@@ -74,7 +74,6 @@ class MXFP4Block:
                     route=ops.RouteOut(new((T, k), torch.int32), new((T, k), torch.float32), new((E,), torch.int32),
                                        new((E + 1,), torch.int32), new((T * k,), torch.int32)),
                     route_ws=new((max(ops.moe_route_workspace_bytes(T, H, E, k), 1),), torch.uint8),
-                    linear_ws=new((max(ops.mxfp4_linear_workspace_bytes(T, K, H), 1),), torch.uint8),
                     ffn_ws=new((max(ops.mxfp4_ffn_workspace_bytes(T, k, E, H, I), 1),), torch.uint8),
                     pair_out=new((T * k, H), torch.float16), pair_scale=new((T * k,), torch.float32),
                     y=new((T, H), torch.float32), r2=new((T, H), torch.bfloat16), n2=new((T, H), torch.bfloat16),
@@ -92,7 +91,7 @@ class MXFP4Block:
         b = self._bufs.take((T, K), lambda: self._buffers(T, K))
         w_post_attn, w_pre, w_post_moe, w_next = self.norms
         ops.mxfp4_quantize(attn, **b["a"])
-        ops.mxfp4_linear(b["a"]["codes"], b["a"]["scales"], *self.w_o, self.H, y=b["o"], workspace=b["linear_ws"])
+        ops.mxfp4_linear(b["a"]["codes"], b["a"]["scales"], *self.w_o, self.H, y=b["o"])
         ops.moe_norm_out(b["o"], residual, w_post_attn, w_pre, eps=self.eps, out=b["r1"], n=b["n1"], **b["x"])
         r = ops.moe_route(b["n1"], self.w_router, self.bias, self.k, self.rsf, out=b["route"], workspace=b["route_ws"])
         ops.mxfp4_grouped_ffn(b["x"]["codes"], b["x"]["scales"], *self.w13, *self.w2, self.H, self.I, self.k,

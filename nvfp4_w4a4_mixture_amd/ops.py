@@ -514,8 +514,8 @@ class _Binding:
     """The compiled binding's functions.  It is imported, and given the loaded library's entry points, at the first use
     of one: the functions that are marshalled here need only the library."""
 
-    _ENTRIES = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear_workspace_bytes", "mxfp4_linear",
-                "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine")
+    _ENTRIES = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_ffn_workspace_bytes",
+                "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine")
 
     def __getattr__(self, name):  # only until the functions are this object's own attributes
         if name not in self._ENTRIES:
@@ -609,6 +609,7 @@ def mxfp4_unpack_weights(codes: torch.Tensor, scales: torch.Tensor, N: int, K: i
 
 
 def mxfp4_linear_workspace_bytes(T: int, K: int, N: int) -> int:
+    """0: the dense product uses no workspace."""
     return int(lib().mxfp4_linear_workspace_bytes(T, K, N))
 
 
