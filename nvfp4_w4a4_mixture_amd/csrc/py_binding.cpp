@@ -387,18 +387,20 @@ PyObject* norm_out(PyObject* const* a) {
 PyObject* combine(PyObject* const* a) {
   const Tensor &po = typed(a[0], "pair_out", ScalarType::Half), &ps = typed(a[1], "pair_scale", ScalarType::Float);
   const int64_t T = integer(a[2]), k = integer(a[3]), type = integer(a[4]);
-  if (po.dim() != 2 || po.size(0) < T * k)
+  const __int128 pairs = (__int128)T * k;  // of the caller's numbers: in 64 bits they may wrap
+  if (po.dim() != 2 || po.size(0) < pairs)
     raise(PyExc_ValueError, "pair_out must be [>= T*k, H], got %s", shape_name(po.sizes()).c_str());
-  if (ps.numel() < T * k)
-    raise(PyExc_ValueError, "pair_scale must hold T*k = %lld scales, got %lld", (long long)(T * k), (long long)ps.numel());
+  if (ps.numel() < pairs)
+    raise(PyExc_ValueError, "pair_scale must hold T*k = %lld scales, got %lld", (long long)pairs, (long long)ps.numel());
   if (!po.is_contiguous() || !ps.is_contiguous()) raise(PyExc_ValueError, "pair_out and pair_scale must be contiguous");
   const OnStream st(a[6], po);
   Tensor y;
   if (given(a[5])) {  // any shape: the result is the first T * H elements
     y = typed(a[5], "y", float_type(type));
     if (!y.is_contiguous()) raise(PyExc_ValueError, "y must be contiguous");
-    if (y.numel() < T * po.size(1))
-      raise(PyExc_ValueError, "y must hold T*H = %lld elements, got %lld", (long long)(T * po.size(1)), (long long)y.numel());
+    if (y.numel() < (__int128)T * po.size(1))
+      raise(PyExc_ValueError, "y must hold T*H = %lld * %lld elements, got %lld", (long long)T, (long long)po.size(1),
+            (long long)y.numel());
   } else {
     y = fresh(po, float_type(type), {T, po.size(1)});
   }

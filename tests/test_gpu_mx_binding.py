@@ -58,3 +58,16 @@ def test_quantize_is_any_truth_value(ops, flag):
 def test_quantize_is_any_false_value(ops, flag):
     x = torch.randn(3, 64, device="cuda").to(torch.bfloat16)
     assert torch.equal(ops.moe_norm_in(x, x[0], quantize=flag), ops.moe_norm_in(x, x[0]))
+
+
+def test_combine_of_sizes_that_wrap(ops):
+    """T * k and T * H beyond 64 bits are not taken for small numbers (nothing may be enqueued)."""
+    po, ps = torch.zeros(8, 64, dtype=torch.float16, device="cuda"), torch.zeros(8, device="cuda")
+    y = torch.zeros(8, 64, device="cuda")
+    for T, k in ((1 << 62, 4), (1 << 62, 8), (1 << 58, 64)):
+        with pytest.raises(ValueError, match="pair_out must be"):
+            ops.moe_combine(po, ps, T, k, y=y)
+    with pytest.raises(ValueError, match="y must hold"):
+        ops.moe_combine(po, ps, 1 << 62, 0, y=y)
+    with pytest.raises(ops.MoEError, match="MOE_ERR_SHAPE"):
+        ops.moe_combine(po, ps, -1, 2, y=y)
