@@ -463,8 +463,8 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
  * ceil(max(2I, H) / 256) < 2^22.  expert_offsets and sorted_pair_ids as moe_route
  * writes them; a token may name an expert more than once.  Code arrays and
  * pair_out 16-byte, scale arrays, pair_scale and w2_max_scale 4-byte aligned;
- * workspace mxfp4_ffn_workspace_bytes(...) bytes, 256-byte aligned.  Pairs not
- * listed in sorted_pair_ids are not written. */
+ * workspace mxfp4_ffn_workspace_bytes(...) bytes (0 for sizes out of range),
+ * 256-byte aligned.  Pairs not listed in sorted_pair_ids are not written. */
 size_t mxfp4_ffn_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t H,
                              const uint8_t* w13_codes, const uint8_t* w13_scales, const uint8_t* w2_codes,

@@ -18,6 +18,7 @@ using moe::round_up;
 constexpr uint64_t kMaxThreads = (uint64_t)1 << 32;
 constexpr uint64_t kMaxOperand = (uint64_t)1 << 32;  // bytes that 32-bit offsets reach
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxInner = (int64_t)1 << 24;  // H and I of the experts
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // of one launch (the kernels count them in 32 bits)
 
 bool dtype_ok(int32_t d) { return d == 0 || d == 1; }
@@ -36,7 +37,7 @@ moe_status check_rows(const char* fn, int64_t rows, int64_t cols, int64_t ld, in
   if (!rows_fit(rows, cols)) return fail(MOE_ERR_SHAPE, "%s: too many elements for one call", fn);
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales) return fail(MOE_ERR_NULL, "%s: a required pointer is NULL", fn);
-  if ((ld * (dtype ? 4 : 2)) % 16 != 0 || !aligned(x, 16) || !aligned(codes, 16))
+  if (ld % (dtype ? 4 : 8) != 0 || !aligned(x, 16) || !aligned(codes, 16))
     return fail(MOE_ERR_ALIGN, "%s: rows must start on 16-byte boundaries and codes be 16-byte aligned", fn);
   return MOE_OK;
 }
@@ -173,7 +174,7 @@ moe_status mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
 }
 
 size_t mxfp4_ffn_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
-  if (T < 0 || k < 1 || E < 1 || H < 1 || I < 1) return 0;
+  if (T < 0 || k < 1 || E < 1 || H < 1 || I < 1 || T >= kMaxDim || k > 256 || I >= kMaxInner) return 0;
   return mx_ffn_ws(T, k, I).total;
 }
 
@@ -188,7 +189,7 @@ moe_status mxfp4_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
   if (H <= 0 || H % 32 != 0) return fail(MOE_ERR_SHAPE, "%s: H must be a positive multiple of 32", fn);
   if (I <= 0 || I % 32 != 0) return fail(MOE_ERR_SHAPE, "%s: I must be a positive multiple of 32", fn);
   if (k < 1 || E < k || E > 256) return fail(MOE_ERR_SHAPE, "%s: need 1 <= k <= E <= 256", fn);
-  if (H >= ((int64_t)1 << 24) || I >= ((int64_t)1 << 24)) return fail(MOE_ERR_SHAPE, "%s: H and I must be under 2^24", fn);
+  if (H >= kMaxInner || I >= kMaxInner) return fail(MOE_ERR_SHAPE, "%s: H and I must be under 2^24", fn);
   if (T >= kMaxDim || T * k >= kMaxDim) return fail(MOE_ERR_SHAPE, "%s: T*k must be < 2^31", fn);
   if ((uint64_t)T * (uint64_t)(mx_padded(H) / 2) >= kMaxOperand)
     return fail(MOE_ERR_SHAPE, "%s: x codes must be under 4 GiB", fn);
