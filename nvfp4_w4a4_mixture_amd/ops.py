@@ -15,6 +15,8 @@ import torch
 
 from ._lib import MoEError, check, lib  # noqa: F401
 
+lib()  # raises here if the library is not built
+
 __all__ = ["moe_route", "moe_route_quantize", "nvfp4_quantize_act", "nvfp4_quantize_weights", "moe_nvfp4_grouped_ffn",
            "moe_nvfp4_grouped_ffn_noalloc", "moe_nvfp4_gate_up_swiglu", "moe_nvfp4_down_scatter", "moe_combine", "reap_saliency",
            "moe_combine_reap", "reap_prune_select", "moe_gather_experts", "moe_shared_workspace_bytes", "moe_shared_expert",

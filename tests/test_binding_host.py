@@ -66,3 +66,10 @@ def test_a_failed_binding_leaves_the_library(monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="no compiler"):
         build.build(out_dir=str(tmp_path / "lib"), build_dir=str(tmp_path / "b"))
     assert made and os.path.exists(tmp_path / "lib" / build.LIB_NAME)
+
+
+def test_importing_ops_without_the_library_raises():
+    env = dict(os.environ, MOE_NVFP4_LIB=os.path.join(ROOT, "no", "such.so"))
+    r = subprocess.run([sys.executable, "-c", "import nvfp4_w4a4_mixture_amd.ops"], cwd=ROOT, env=env,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode != 0 and "is not built" in r.stderr
