@@ -3,11 +3,12 @@
 //
 // With few tokens the weights' bytes bound a product, with many the matrix
 // cores.  A register-only loop of the 32x32x64 FP4 MFMA takes 32 cycles an
-// instruction; on operands of random bits the card lowers its clock to 1.6 GHz
-// under it (6.5 PFLOP/s; 8.5 at 2.1 GHz on zeros).  The tiled kernel on 4096 x
-// 16384 x 4096 reaches 4.6 PFLOP/s, 5.2 without its DMA, and 6.2 on zeros: what
-// remains is mostly power, and a shape that moves fewer bytes per product wins
-// over one that hides latencies better.
+// instruction; on operands of random bits the card lowers its clock to some 1.6
+// GHz under it (6.4 to 6.6 PFLOP/s by card; 9.8 on zeros).  The tiled kernel on
+// 4096 x 16384 x 4096 reaches 4.6 PFLOP/s, 5.2 without its DMA, and 6.2 on zeros:
+// in such long reductions what remains is mostly power, and a shape that moves
+// fewer bytes per product wins over one that hides latencies better.  Short ones
+// (the down stage's eight column groups) fill their ring and empty it for little.
 #include "launch.h"
 #include "mx_common.h"
 
@@ -27,7 +28,10 @@ enum { kLinear = 0, kGateUp = 1, kDown = 2 };
 // byte bh of the h row and bw of the expert's down weights, 36 I <= 2^lg, and
 // |w_p| < 2^(ew + 1).  FP16's normal range reaches 29 binades below 2^15, so a
 // loose bound costs no precision.  Clamped so that 2^E, 2^-E and w_p 2^-E are
-// normal or zero (a row of zeros has a bound far below its weight).
+// normal or zero (a row of zeros has a bound far below its weight).  FP16 and not
+// FP32 because the rows are what the layer writes most of (805 MB for 8192 tokens
+// of 8 x 6144) and its combine reads again; it rounds a row by 2.1e-4 in the
+// 2-norm, which takes one BF16 result in some thirty to its neighbour.
 __device__ __forceinline__ int pair_exponent(float wp, uint32_t bh, int bw, int lg) {
   const int ew = (int)((__float_as_uint(wp) >> 23) & 255u) - 127;
   const int e = ew + 1 + lg + (int)bh + bw - 254 - 15;
@@ -82,10 +86,11 @@ __device__ __forceinline__ void zero_h_pad(const MxArgs& a, int64_t row, int p, 
 // up group of the same h columns) and tiles of 32 tokens; its NW waves split
 // the columns and load their fragments straight from memory to registers (a
 // packed fragment is one contiguous kilobyte), and the partial sums meet in LDS
-// in a fixed order.  One token, 6144 x 6144: 4.6 us, of which a launch takes
-// about 2; 8 waves on 1 row group where 4 waves on 2 take 10.4 (too few
-// workgroups), 16 waves or loads two groups ahead 4.5 to 4.8.  Token groups past the first would cost more here than in a
-// tile: a lane's 16 bytes of x come from 32 different rows.
+// in a fixed order.  One token, 6144 x 6144: 4.6 to 5.2 us, of which a launch
+// takes about 2; 8 waves on 1 row group where 4 waves on 2 take 10.4 (too few
+// workgroups), 16 waves or loads two groups ahead as many.  Token groups past
+// the first would cost more here than in a tile: a lane's 16 bytes of x come
+// from 32 different rows.
 template <int MODE, int R, int NW>
 __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
   __shared__ float4 part[NW][R][4 * 68];  // strides 68 and 34: 16 lanes of a reader take 16 different slots
@@ -724,10 +729,11 @@ Shape linear_shape(int64_t T, int64_t G, int64_t KK) {
 // The shape of a stage of the experts' FFN over weights of `rows` rows; both
 // sides measured on 80 experts of 6144 x 2048, top-8, us of gate_up (down):
 //   mean pairs an expert      1.6        32         64         128        256        819
-//   streaming             164 (87)   289 (150)
-//   128 x 64              149 (76)   183 (103)  265 (121)  365 (179)
-//   256 x 128             157 (79)   179 (106)  193 (118)  275 (150)  386 (216)  959 (599)
-//   256 x 256             167 (91)   185 (117)  198 (130)  239 (156)  384 (240)  883 (599)
+//   streaming             163 (87)   288 (144)  462 (222)
+//   128 x 64              148 (75)   183 (101)  268 (121)  366 (182)  610 (312)
+//   256 x 128             158 (79)   179 (101)  195 (109)  275 (146)  387 (218)  983 (597)
+//   256 x 256             169 (93)   188 (112)  200 (121)  242 (148)  402 (243)  920 (632)
+//   weights read          137 (69)   168 (84) from 32 on; operations 446 (223) at 819
 // Small layers (16 experts of 1024 x 512) are latency bound: streaming takes
 // 4.0 us at 16 pairs an expert where 128 x 64 takes 4.4; past that its second
 // token tile costs more (10 experts of 4992 x 896, 29 pairs each: 20.0 against
