@@ -499,6 +499,96 @@ moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, in
                         uint16_t* r_out, int64_t ldro, uint16_t* n, int64_t ldn, uint8_t* codes, uint8_t* scales,
                         void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* MXFP8 activations over MXFP4 weights (W4A8): the same operators with 8-bit
+ * activations, for the same packed weights.
+ *
+ *  Block      32 consecutive elements of a row: E4M3 elements (E4M3-FN bytes,
+ *             largest magnitude 448) under one E8M0 byte b; value = e4m3(element)
+ *             * 2^(b - 127).  Quantization of a block with largest magnitude
+ *             amax: b = floor(log2(amax)) - 8 + 127, clamped to [0, 254] (0 for a
+ *             zero block); element = E4M3 RNE-even of x * 2^(127 - b), saturating
+ *             at 448, sign bit = sign bit of x.  A block that holds a NaN or an
+ *             infinity gets b = 255 and zero elements: all of it stands for NaN.
+ *  Rows       [rows, cols], cols % 32 == 0, padded to Cp = round_up(cols, 256)
+ *             columns: codes [rows, Cp] and scales [rows, Cp/32]; the padding is
+ *             zero elements under scale 0.
+ *  Sums       FP32.  The matrix instruction aligns the products of one block to
+ *             the largest of them and drops what lies some 17 binades below it;
+ *             where a result is FP32, and where up to 32 tokens or columns of them
+ *             are streamed, activations are multiplied as two operands of half the
+ *             range, which leaves the FP32 rounding only.  Elsewhere results are
+ *             rounded to BF16, FP16 or MXFP8 anyway, and a sum may be off by 2^-11
+ *             of the largest sum of magnitudes of a block (some 1e-5 in the 2-norm
+ *             of usual activations). */
+
+/* As mxfp4_quantize and mxfp4_dequantize (the same limits and alignment).  BF16
+ * results are exact but under 2^-130, where BF16's own step may be larger. */
+moe_status mxfp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                          uint8_t* codes, uint8_t* scales, void* stream);
+moe_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                            int32_t out_dtype, void* out, int64_t ld_out, void* stream);
+
+/* y[t, n] = act(sum_k x[t, k] * w[n, k] + bias[n]) + residual[t, n], FP32, one
+ * rounding to out_dtype.  bias BF16 [N] or NULL; residual [T, ld_residual] in
+ * residual_dtype or NULL; activation 0 none, 1 ReLU, 2 SiLU z / (1 + e^-z), 3 GELU
+ * 0.5 z (1 + erf(z / sqrt 2)), 4 GELU by tanh, 0.5 z (1 + tanh(sqrt(2 / pi) (z +
+ * 0.044715 z^3))).  y may be residual (the same type and stride), and must not
+ * overlap anything else.  Limits as mxfp4_linear, x codes T * Kp < 2^32 bytes;
+ * code arrays 16-byte, scale arrays 4-byte, the others aligned to their element. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2
+#define MOE_ACT_GELU 3
+#define MOE_ACT_GELU_TANH 4
+moe_status mxfp8_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t K,
+                        const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint16_t* bias,
+                        int32_t activation, const void* residual, int32_t residual_dtype, int64_t ld_residual,
+                        int32_t out_dtype, void* y, int64_t ldy, void* stream);
+
+/* mxfp4_grouped_ffn with x and h in MXFP8: the same arguments, limits (x codes
+ * T*Hp and h codes T*k*Ip bytes under 4 GiB) and pair rows, with E =
+ * floor(log2 |w_p|) + 1 + ceil(log2(2688 I)) + bh + bw - 269 (2688 = 6 * 448). */
+size_t mxfp8_ffn_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
+moe_status mxfp8_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t H,
+                             const uint8_t* w13_codes, const uint8_t* w13_scales, const uint8_t* w2_codes,
+                             const uint8_t* w2_scales, const int32_t* w2_max_scale, int64_t E, int64_t I, int64_t k,
+                             const int32_t* expert_offsets, const int32_t* sorted_pair_ids, const float* topk_w,
+                             uint16_t* pair_out, float* pair_scale, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* The whole routed layer for up to 32 tokens: moe_route, mxfp8_quantize,
+ * mxfp8_grouped_ffn and moe_combine in three launches, with the sum over a
+ * token's experts in FP32 (no pair rows), in the order of the experts:
+ *
+ *   topk_ids, topk_w as moe_route;  y[t] = sum_j topk_w[t, j] * f(topk_ids[t, j], q(x[t]))
+ *
+ * x_bf16 [T, ldx] BF16 (any ldx >= H), w_router_bf16 [E, H], bias [E] FP32, w13
+ * packed [E][2I, H] (gate rows, then up rows), w2 packed [E][H, I]; y [T, H] in
+ * out_dtype, topk_ids [T, k] INT32, topk_w [T, k] FP32.  H % 32 == 0, I % 32 == 0
+ * (both under 2^24), 1 <= k <= E <= 256, routed_scaling_factor > 0.  Code arrays
+ * and y 16-byte, scale arrays, bias and the top-k arrays 4-byte aligned; workspace
+ * mxfp8_moe_layer_workspace_bytes(...) bytes (0 for sizes out of range), 256-byte
+ * aligned, of any content. */
+size_t mxfp8_moe_layer_workspace_bytes(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I);
+moe_status mxfp8_moe_layer(const uint16_t* x_bf16, int64_t T, int64_t H, int64_t ldx,
+                           const uint16_t* w_router_bf16, const float* bias, int64_t E, int64_t k,
+                           float routed_scaling_factor, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                           const uint8_t* w2_codes, const uint8_t* w2_scales, int64_t I, int32_t out_dtype, void* y,
+                           int32_t* topk_ids, float* topk_w, void* workspace, size_t workspace_bytes, void* stream);
+
+/* moe_norm_in and moe_norm_out with n quantized to MXFP8 instead of MXFP4
+ * (bit-identical to mxfp8_quantize of n): codes and scales are required, n (and
+ * for moe_norm_out_mxfp8 nothing else) may be NULL, w_next is required.  Codes
+ * 8-byte aligned. */
+moe_status moe_norm_in_mxfp8(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, const uint16_t* w, float eps,
+                             uint16_t* n, int64_t ldn, uint8_t* codes, uint8_t* scales, void* stream);
+moe_status moe_norm_out_mxfp8(const void* y, int32_t y_dtype, int64_t T, int64_t H, int64_t ldy, const uint16_t* r,
+                              int64_t ldr, const uint16_t* w_post, const uint16_t* gate, int64_t gate_row_stride,
+                              int64_t gate_col_stride, float residual_scale, const uint16_t* w_next, float eps,
+                              uint16_t* r_out, int64_t ldro, uint16_t* n, int64_t ldn, uint8_t* codes,
+                              uint8_t* scales, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

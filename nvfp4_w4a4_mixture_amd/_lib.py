@@ -71,9 +71,21 @@ SIGNATURES = {
     "mxfp4_ffn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "mxfp4_grouped_ffn": (_i32, [_p, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p,
                                  _sz, _p]),
+    "mxfp8_quantize": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _p]),
+    "mxfp8_dequantize": (_i32, [_p, _p, _i64, _i64, _i32, _p, _i64, _p]),
+    "mxfp8_linear": (_i32, [_p, _p, _i64, _i64, _p, _p, _i64, _p, _i32, _p, _i32, _i64, _i32, _p, _i64, _p]),
+    "mxfp8_ffn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "mxfp8_grouped_ffn": (_i32, [_p, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p,
+                                 _sz, _p]),
+    "mxfp8_moe_layer_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "mxfp8_moe_layer": (_i32, [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _f32, _p, _p, _p, _p, _i64, _i32, _p, _p, _p,
+                               _p, _sz, _p]),
     "moe_norm_in": (_i32, [_p, _i64, _i64, _i64, _p, _f32, _p, _i64, _p, _p, _p]),
     "moe_norm_out": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _f32, _p, _f32, _p, _i64, _p,
                             _i64, _p, _p, _p]),
+    "moe_norm_in_mxfp8": (_i32, [_p, _i64, _i64, _i64, _p, _f32, _p, _i64, _p, _p, _p]),
+    "moe_norm_out_mxfp8": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _f32, _p, _f32, _p, _i64,
+                                  _p, _i64, _p, _p, _p]),
 }
 
 

@@ -19,7 +19,7 @@ OUT_DIR = os.path.join(PKG, "lib")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libmoe_nvfp4.so"
 SOURCES = ["quantize.hip", "route.hip", "ffn.hip", "combine.hip", "prune.hip", "shared.hip", "rotate.hip", "mx_quantize.hip",
-           "mx_product.hip", "norm.hip", "api.cpp", "api_mx.cpp"]
+           "mx_product.hip", "mx8_product.hip", "mx_layer.hip", "norm.hip", "api.cpp", "api_mx.cpp"]
 
 BINDING = os.path.join(PKG, "_binding.so")
 

@@ -157,6 +157,19 @@ __host__ __device__ __forceinline__ int64_t tiled_scale_index(int64_t row, int64
   return (row >> 4) * K + (b >> 3) * 128 + (row & 15) * 8 + (b & 7);
 }
 
+// Selection key of an FP64 score: a signed 64-bit integer in the order of the
+// scores, with -0 equal to +0 and NaN below every number (below -inf).  Keys
+// are totally ordered, so with ties going to the lower expert index every rank
+// 0..E-1 is taken by exactly one expert, also when scores are NaN (a token
+// whose x holds a NaN or an infinity, or a NaN bias).  This is the order of a
+// stable sort of the scores, descending, with NaN last.
+__device__ __forceinline__ long long score_key(double v) {
+  if (v != v) return (long long)0x8000000000000000ull;  // NaN: the smallest key
+  long long b = __double_as_longlong(v);
+  if (b == (long long)0x8000000000000000ull) b = 0;  // -0 -> +0
+  return b < 0 ? (b ^ 0x7FFFFFFFFFFFFFFFll) : b;      // negatives: larger magnitude, smaller key
+}
+
 // global -> LDS DMA of 16 (4) bytes per lane: lane l's bytes land at lds + 16 l (4 l);
 // lds must be wave-uniform
 typedef __attribute__((address_space(3))) void lds_void_t;

@@ -127,14 +127,20 @@ constexpr int64_t mx_padded(int64_t cols) { return (cols + 255) / 256 * 256; }
 // arguments was measured 0.8 us shorter on the host (2.9 against 3.7 us) than
 // one with 128 or more, so the stages share fields and sizes are 32 bits.
 struct MxArgs {
-  const uint8_t* a_codes;   // activations [rows, KK * 128]
+  const uint8_t* a_codes;   // activations [rows, KK * 128] (8 bits: KK * 256)
   const uint8_t* a_scales;  // [rows, KK * 8]
   const uint8_t* w_codes;   // packed weights (experts one after another)
   const uint8_t* w_scales;
   void* out;               // linear: BF16 or FP32 [T, ldo]; gate_up: h codes [T*k, ldo]; down: FP16 pair rows [T*k, ldo]
   void* out_scales;        // gate_up: h scale bytes [T*k, ldo / 16]; down: FP32 pair scales [T*k]
-  const int32_t* offsets;  // experts: first pair of each, and their end [E + 1]
-  const int32_t* sorted;   // experts: pairs by expert
+  union {
+    const int32_t* offsets;  // experts: first pair of each, and their end [E + 1]
+    const uint16_t* bias;    // linear of 8-bit activations: BF16 [N], or null
+  };
+  union {
+    const int32_t* sorted;  // experts: pairs by expert
+    const void* residual;   // linear of 8-bit activations: [T, ldr], or null
+  };
   const float* topk_w;     // down: routing weights [T*k]
   const int32_t* w_max;    // down: largest weight scale byte per expert
   int32_t KK;              // column groups of 256 in the reduction
@@ -142,11 +148,16 @@ struct MxArgs {
   int32_t G;               // groups of 32 weight rows (per expert)
   int32_t ldo;             // elements (gate_up: bytes) of an output row
   int32_t T;               // linear: tokens
-  int32_t E;               // experts: their number
-  int32_t aux;             // gate_up: k; down: ceil(log2(36 I)); linear: bit 0 FP32 results, bit 1 rows on 16 bytes
+  union {
+    int32_t E;    // experts: their number
+    int32_t ldr;  // linear of 8-bit activations: elements of a residual row
+  };
+  int32_t aux;             // gate_up: k; down: ceil(log2(36 I)) (8 bits: 2688 I); linear: bits below
 };
 static_assert(sizeof(MxArgs) <= 112, "see above");
-constexpr int32_t kMxOutF32 = 1, kMxOutVec = 2;
+// linear: FP32 results, result rows on 16 bytes, FP32 residual; from bit kMxActShift on the activation
+constexpr int32_t kMxOutF32 = 1, kMxOutVec = 2, kMxResF32 = 4, kMxActShift = 3;
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActCount = 5 };
 
 // Both stages of the experts' FFN.
 struct MxExperts {
@@ -158,6 +169,10 @@ hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int64_t col
                               uint8_t* scales, hipStream_t st);
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
                                 void* out, int64_t ld, hipStream_t st);
+hipError_t launch_mx8_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                               uint8_t* scales, hipStream_t st);
+hipError_t launch_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
+                                 void* out, int64_t ld, hipStream_t st);
 hipError_t launch_mx_quantize_weights(const uint16_t* w, int64_t batch, int64_t N, int64_t K, uint8_t* codes,
                                       uint8_t* scales, int32_t* max_scale, hipStream_t st);
 // canonical -> packed (pack) or back; max_scale (pack only) may be null
@@ -165,6 +180,30 @@ hipError_t launch_mx_relayout(uint8_t* codes, uint8_t* scales, int64_t batch, in
                               uint8_t* pscales, int32_t* max_scale, bool pack, hipStream_t st);
 hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st);
 hipError_t launch_mx_experts(const MxExperts& x, hipStream_t st);
+// the same with MXFP8 activations (and h), the linear with its epilogue
+hipError_t launch_mx8_linear(const MxArgs& a, hipStream_t st);
+hipError_t launch_mx8_experts(const MxExperts& x, hipStream_t st);
+
+// The whole layer for a few tokens (MXFP8 activations): sizes in 32 bits, checked by the caller.
+struct MxLayerArgs {
+  const uint16_t* x;         // BF16 [T, ldx]
+  const uint16_t* w_router;  // BF16 [E, H]
+  const float* bias;         // [E]
+  const uint8_t* w13_codes;
+  const uint8_t* w13_scales;
+  const uint8_t* w2_codes;
+  const uint8_t* w2_scales;
+  void* y;                   // [T, H]
+  int32_t* topk_ids;         // [T, k]
+  float* topk_w;             // [T, k]
+  uint8_t* ws;               // mx_layer_workspace
+  int32_t ldx, T, E, k, H, I;
+  float rsf;
+  int32_t y_f32;
+};
+constexpr int64_t kLayerMaxTokens = 32;
+size_t mx_layer_workspace(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I);
+hipError_t launch_mx_layer(const MxLayerArgs& a, hipStream_t st);
 
 // Norms around a block; x is the row to norm (norm_in) or the block output y
 // (norm_out).  As short as MxArgs, for the same reason.
@@ -180,7 +219,7 @@ struct NormArgs {
   uint8_t* scales;
   int32_t ldx, ldr, ldro, ldn;
   int32_t gate_rs;
-  uint32_t H : 16, Hp : 15, gate_row : 1;  // Hp: columns the row's lanes cover (padded when it is quantised)
+  uint32_t H : 15, Hp : 15, gate_row : 1, a8 : 1;  // Hp: columns the row's lanes cover (padded when it is quantised); a8: MXFP8 codes
   float scale, eps;
 };
 static_assert(sizeof(NormArgs) <= 112, "see MxArgs");

@@ -13,6 +13,13 @@
 // block 4 f + s at step s.  A lane's four blocks of a column group are then 64
 // consecutive bytes of codes, and their scale bytes one dword.
 //
+// MXFP8 activations (E4M3 elements under the same kind of scale; the byte is
+// floor(log2(amax)) - 8 + 127, 8 = the exponent of 448) multiply the same packed
+// weights.  Of an 8-bit operand lane l takes two runs of 16 bytes a step:
+// elements 16 f .. 16 f + 15 of the step's first block (s) and of its second
+// (4 + s), where a 4-bit operand takes one whole block; scales go by lane as
+// above (layout checked on the device).
+//
 // Result rows.  Lane l holds column l % 32 of the result and, in register
 // 4 q + j, row 8 q + 4 (l / 32) + j.  Weights are the row operand, and packed
 // so that MFMA row 8 q + 4 h + j is weight row 16 h + 4 q + j of its group of
@@ -62,6 +69,35 @@ __device__ __forceinline__ uint32_t mx_encode8(const float* x, uint32_t byte) {
   return byte == 255u ? 0u : d;
 }
 
+// Scale byte of an MXFP8 block; as mx_scale_byte, with E4M3's exponent
+__device__ __forceinline__ uint32_t mx8_scale_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e == 255u ? 255u : (e > 8u ? e - 8u : 0u);
+}
+
+// Four E4M3 elements (one dword) of x[0..3] under a block's scale byte: round to
+// nearest even, saturating (the convert alone gives NaN past 448; checked on the
+// device against the definition for every BF16 value).  A NaN block is zero.
+__device__ __forceinline__ uint32_t mx8_encode4(const float* x, uint32_t byte) {
+  const float inv = mx_inverse_scale(byte);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_fmed3f(x[i] * inv, -kE4M3Max, kE4M3Max);
+  int d = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  d = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], d, true);
+  return byte == 255u ? 0u : (uint32_t)d;
+}
+
+// The elements of four bytes, unscaled
+__device__ __forceinline__ void mx8_decode4(uint32_t d, float* f) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)d, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)d, true);
+  f[0] = lo[0];
+  f[1] = lo[1];
+  f[2] = hi[0];
+  f[3] = hi[1];
+}
+
 // The elements of eight codes, unscaled
 __device__ __forceinline__ void mx_decode8(uint32_t d, float* f) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -108,6 +144,28 @@ __device__ __forceinline__ float16_t mx_mfma(i32x4_t a, i32x4_t b, float16_t c, 
   const i32x8_t a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
   const i32x8_t b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, S, sa, S, sb);
+}
+
+// The same step with 8-bit activations.  The instruction aligns the products of
+// a block to the largest of them and drops what lies some 17 binades below: of
+// normal data a product of 6144 columns is off by 4e-6 in the 2-norm, with
+// outliers of 300 times the rest by 7e-5.  EXACT: x is multiplied as two operands
+// whose elements each span 9 binades (the exponent's upper bit tells which), and
+// all that is left is the rounding of the FP32 accumulator (3e-8 and 1e-7), for
+// twice the matrix instructions.
+__device__ __forceinline__ i32x8_t mx8_large(i32x8_t b) {
+  i32x8_t r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = (uint32_t)b[i] & 0x40404040u, h = m << 1;
+    r[i] = b[i] & (int)(h | (h - (m >> 6)));  // bytes with that bit, whole
+  }
+  return r;
+}
+template <int S>
+__device__ __forceinline__ float16_t mx8_mfma(i32x4_t a, i32x8_t b, float16_t c, int sa, int sb) {
+  const i32x8_t a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b, c, 4, 0, S, sa, S, sb);
 }
 
 // Lane (of 64) and byte of the packed layout for weight row `row` and block `blk` (of 32 columns):

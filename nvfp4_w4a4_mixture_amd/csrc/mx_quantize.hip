@@ -82,6 +82,54 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
   }
 }
 
+// MXFP8 of activations: as mx_quantize_kernel, but a chunk of 8 elements is 8
+// bytes of codes.
+template <typename X>
+__global__ __launch_bounds__(256) void mx8_quantize_kernel(const X* __restrict__ x, uint32_t n, uint32_t cols,
+                                                           int64_t ld, uint32_t chunks, uint2* __restrict__ codes,
+                                                           uint8_t* __restrict__ scales) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n) return;
+  const uint32_t r = i / chunks, c = (i - r * chunks) * 8;
+  float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < cols) load8(x + r * ld + c, f);
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, abs_bits(f[k]));
+  m = quad_max(m);
+  const uint32_t byte = mx8_scale_byte(m);
+  codes[i] = make_uint2(mx8_encode4(f, byte), mx8_encode4(f + 4, byte));
+  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void mx8_dequantize_kernel(const uint2* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, uint32_t n,
+                                                             uint32_t chunks, uint32_t chunks_padded,
+                                                             void* __restrict__ out, int64_t ld) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n) return;
+  const uint32_t r = i / chunks, c = i - r * chunks;
+  const int64_t src = (int64_t)r * chunks_padded + c, at = r * ld + (int64_t)c * 8;
+  const float s = mx_scale_value(scales[src >> 2]);
+  const uint2 d = codes[src];
+  float f[8];
+  mx8_decode4(d.x, f);
+  mx8_decode4(d.y, f + 4);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] *= s;
+  if (F32) {
+    float* p = static_cast<float*>(out) + at;
+#pragma unroll
+    for (int k = 0; k < 8; k += 4)
+      store16_streaming(p + k, __float_as_uint(f[k]), __float_as_uint(f[k + 1]), __float_as_uint(f[k + 2]),
+                        __float_as_uint(f[k + 3]));
+  } else {  // four significant bits: exact, but below 2^-130, whose values BF16's subnormals (steps of 2^-133) may round
+    store16_streaming(static_cast<uint16_t*>(out) + at, bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                      bf16_pair(f[6], f[7]));
+  }
+}
+
 // ---- weights: one thread per (row, block of 32) of the padded matrix, once per
 // weight set.  The atomics bound the two kernels that give a largest byte, one a
 // block on one word a matrix: 8 matrices of 4096 x 6144 take 71 ms, and 0.1 on the
@@ -184,6 +232,27 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
   auto* k = f32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>;
   return launch_kernel(k, dim3((n + 255) / 256), dim3(256), 0, st, reinterpret_cast<const uint32_t*>(codes), scales, n,
                        chunks, padded, out, ld);
+}
+
+// rows * padded columns / 8 < 2^32 (checked by the caller)
+hipError_t launch_mx8_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                               uint8_t* scales, hipStream_t st) {
+  const uint32_t chunks = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
+  const dim3 grid((unsigned)(((uint64_t)n + 255) / 256));
+  uint2* c = reinterpret_cast<uint2*>(codes);
+  if (f32)
+    return launch_kernel(mx8_quantize_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), n,
+                         (uint32_t)cols, ld, chunks, c, scales);
+  return launch_kernel(mx8_quantize_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(x), n,
+                       (uint32_t)cols, ld, chunks, c, scales);
+}
+
+hipError_t launch_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
+                                 void* out, int64_t ld, hipStream_t st) {
+  const uint32_t chunks = (uint32_t)(cols / 8), padded = (uint32_t)(mx_padded(cols) / 8), n = (uint32_t)(rows * chunks);
+  auto* k = f32 ? mx8_dequantize_kernel<true> : mx8_dequantize_kernel<false>;
+  return launch_kernel(k, dim3((unsigned)(((uint64_t)n + 255) / 256)), dim3(256), 0, st, reinterpret_cast<const uint2*>(codes),
+                       scales, n, chunks, padded, out, ld);
 }
 
 namespace {

@@ -1,6 +1,6 @@
 // RMS norms before and after a block, fused with the block's gate, residual
-// scale and residual, and with the MXFP4 quantisation of what the next product
-// reads.
+// scale and residual, and with the MXFP4 or MXFP8 quantisation of what the next
+// product reads.
 #include "launch.h"
 #include "mx_common.h"
 
@@ -188,10 +188,12 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
         if (c >= H) q[i] = 0.0f;  // the padding is zero whatever the norm is
         m = max(m, abs_bits(q[i]));
       }
-      const uint32_t byte = mx_scale_byte(quad_max(m));
+      const uint32_t amax = quad_max(m), byte = a.a8 ? mx8_scale_byte(amax) : mx_scale_byte(amax);
       if (c < (int)a.Hp) {
-        reinterpret_cast<uint32_t*>(a.codes)[(row * (int)a.Hp + c) / 8] = mx_encode8(q, byte);
-        if ((t & 3) == 0) a.scales[(row * (int)a.Hp + c) / 32] = (uint8_t)byte;
+        const int64_t at = (row * (int)a.Hp + c) / 8;
+        if (a.a8) reinterpret_cast<uint2*>(a.codes)[at] = make_uint2(mx8_encode4(q, byte), mx8_encode4(q + 4, byte));
+        else reinterpret_cast<uint32_t*>(a.codes)[at] = mx_encode8(q, byte);
+        if ((t & 3) == 0) a.scales[at / 4] = (uint8_t)byte;
       }
     }
   }

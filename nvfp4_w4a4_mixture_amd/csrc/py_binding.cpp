@@ -1,4 +1,4 @@
-// Argument marshalling of the MXFP4 operators, the block norms and the combine
+// Argument marshalling of the MXFP4 and MXFP8 operators, the block norms and the combine
 // for Python, compiled: checks of the tensors, allocation of missing outputs,
 // the C-ABI call.
 //
@@ -41,6 +41,15 @@ struct Entry {
   decltype(&moe_norm_in) norm_in;
   decltype(&moe_norm_out) norm_out;
   decltype(&moe_combine) combine;
+  decltype(&mxfp8_quantize) quantize8;
+  decltype(&mxfp8_dequantize) dequantize8;
+  decltype(&mxfp8_linear) linear8;
+  decltype(&mxfp8_ffn_workspace_bytes) ffn8_ws;
+  decltype(&mxfp8_grouped_ffn) ffn8;
+  decltype(&moe_norm_in_mxfp8) norm_in8;
+  decltype(&moe_norm_out_mxfp8) norm_out8;
+  decltype(&mxfp8_moe_layer_workspace_bytes) layer_ws;
+  decltype(&mxfp8_moe_layer) layer;
 } g_entry;
 PyObject* g_check = nullptr;  // check(status, name): raises for a status other than MOE_OK
 
@@ -218,17 +227,18 @@ int64_t padded(int64_t cols) { return (cols + 255) / 256 * 256; }
 struct Codes {
   Tensor codes, scales;
 };
-Codes mx_output(PyObject* codes, PyObject* scales, const Tensor& like, int64_t rows, int64_t cols) {
+// `bits` of an element: 4 (MXFP4) or 8 (MXFP8).
+Codes mx_output(PyObject* codes, PyObject* scales, const Tensor& like, int64_t rows, int64_t cols, int bits) {
   const int64_t c = padded(cols);
-  return {buffer(codes, "codes", like, ScalarType::Byte, {rows, c / 2}),
+  return {buffer(codes, "codes", like, ScalarType::Byte, {rows, c * bits / 8}),
           buffer(scales, "scales", like, ScalarType::Byte, {rows, c / 32})};
 }
 // Given ones of `cols` columns; returns the rows.
-int64_t mx_input(PyObject* codes, PyObject* scales, int64_t cols) {
+int64_t mx_input(PyObject* codes, PyObject* scales, int64_t cols, int bits) {
   const int64_t c = padded(cols);
   const Tensor& t = tensor(codes, "x_codes");
   const int64_t rows = t.dim() == 2 ? t.size(0) : 0;
-  need(codes, "x_codes", ScalarType::Byte, {rows, c / 2});
+  need(codes, "x_codes", ScalarType::Byte, {rows, c * bits / 8});
   need(scales, "x_scales", ScalarType::Byte, {rows, c / 32});
   return rows;
 }
@@ -258,24 +268,26 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // x, codes, scales, stream
+template <int BITS>
 PyObject* quantize(PyObject* const* a) {
   const Rows x = matrix(a[0], "x", true);
   const OnStream st(a[3], x.t);
-  const Codes q = mx_output(a[1], a[2], x.t, x.rows, x.cols);
-  check(g_entry.quantize(x.t.data_ptr(), x.t.scalar_type() == ScalarType::Float, x.rows, x.cols, x.ld,
+  const Codes q = mx_output(a[1], a[2], x.t, x.rows, x.cols, BITS);
+  check((BITS == 4 ? g_entry.quantize : g_entry.quantize8)(x.t.data_ptr(), x.t.scalar_type() == ScalarType::Float, x.rows, x.cols, x.ld,
                          ptr<uint8_t>(q.codes), ptr<uint8_t>(q.scales), st.get()),
-        "mxfp4_quantize");
+        BITS == 4 ? "mxfp4_quantize" : "mxfp8_quantize");
   return tuple_of({q.codes, q.scales});
 }
 
 // codes, scales, cols, dtype code, out, stream
+template <int BITS>
 PyObject* dequantize(PyObject* const* a) {
-  const int64_t cols = integer(a[2]), rows = mx_input(a[0], a[1], cols), type = integer(a[3]);
+  const int64_t cols = integer(a[2]), rows = mx_input(a[0], a[1], cols, BITS), type = integer(a[3]);
   const OnStream st(a[5], tensor(a[0], "x_codes"));
   const Out y = output(a[4], "out", tensor(a[0], "x_codes"), float_type(type), rows, cols);
-  check(g_entry.dequantize(ptr<uint8_t>(tensor(a[0], "")), ptr<uint8_t>(tensor(a[1], "")), rows, cols, (int32_t)type,
+  check((BITS == 4 ? g_entry.dequantize : g_entry.dequantize8)(ptr<uint8_t>(tensor(a[0], "")), ptr<uint8_t>(tensor(a[1], "")), rows, cols, (int32_t)type,
                            y.t.data_ptr(), y.ld, st.get()),
-        "mxfp4_dequantize");
+        BITS == 4 ? "mxfp4_dequantize" : "mxfp8_dequantize");
   return wrap(y.t);
 }
 
@@ -284,7 +296,7 @@ PyObject* linear(PyObject* const* a) {
   const Tensor& wc = tensor(a[2], "w_codes");
   if (wc.dim() != 5) raise(PyExc_ValueError, "w_codes must be [G, KK, 4, 64, 16]");
   const int64_t N = integer(a[4]), type = integer(a[5]), KK = wc.size(1), K = 256 * KK, G = (N + 31) / 32;
-  const int64_t T = mx_input(a[0], a[1], K);  // K is the padded width: the padding is zero on both sides
+  const int64_t T = mx_input(a[0], a[1], K, 4);  // K is the padded width: the padding is zero on both sides
   need(a[2], "w_codes", ScalarType::Byte, {G, KK, 4, 64, 16});
   const Tensor& ws = need(a[3], "w_scales", ScalarType::Byte, {G, KK, 64, 4});
   const Tensor &xc = tensor(a[0], ""), &xs = tensor(a[1], "");
@@ -297,11 +309,42 @@ PyObject* linear(PyObject* const* a) {
   return wrap(y.t);
 }
 
+// x_codes, x_scales, w_codes, w_scales, N, dtype code, bias, activation code, residual, y, stream
+PyObject* linear8(PyObject* const* a) {
+  const Tensor& wc = tensor(a[2], "w_codes");
+  if (wc.dim() != 5) raise(PyExc_ValueError, "w_codes must be [G, KK, 4, 64, 16]");
+  const int64_t N = integer(a[4]), type = integer(a[5]), KK = wc.size(1), K = 256 * KK, G = (N + 31) / 32;
+  const int64_t T = mx_input(a[0], a[1], K, 8);
+  need(a[2], "w_codes", ScalarType::Byte, {G, KK, 4, 64, 16});
+  const Tensor& ws = need(a[3], "w_scales", ScalarType::Byte, {G, KK, 64, 4});
+  const Tensor &xc = tensor(a[0], ""), &xs = tensor(a[1], "");
+  const Tensor bias = given(a[6]) ? need(a[6], "bias", ScalarType::BFloat16, {N}) : Tensor();
+  Tensor r;
+  int64_t ldr = N, rtype = 0;
+  if (given(a[8])) {
+    const Rows m = matrix(a[8], "residual", true);
+    if (m.rows != T || m.cols != N)
+      raise(PyExc_ValueError, "residual must have shape %s, got %s", shape_name({T, N}).c_str(),
+                              shape_name(m.t.sizes()).c_str());
+    r = m.t;
+    ldr = m.ld;
+    rtype = m.t.scalar_type() == ScalarType::Float;
+  }
+  const OnStream st(a[10], xc);
+  const Out y = output(a[9], "y", xc, float_type(type), T, N);
+  check(g_entry.linear8(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, K, ptr<uint8_t>(wc), ptr<uint8_t>(ws), N,
+                        ptr<uint16_t>(bias), (int32_t)integer(a[7]), r.defined() ? r.data_ptr() : nullptr,
+                        (int32_t)rtype, ldr, (int32_t)type, y.t.data_ptr(), y.ld, st.get()),
+        "mxfp8_linear");
+  return wrap(y.t);
+}
+
 // x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_scales, w2_max_scale, H, I, k, expert_offsets,
 // sorted_pair_ids, topk_w, pair_out, pair_scale, workspace, stream
+template <int BITS>
 PyObject* grouped_ffn(PyObject* const* a) {
   const int64_t H = integer(a[7]), I = integer(a[8]), k = integer(a[9]);
-  const int64_t T = mx_input(a[0], a[1], H), E = tensor(a[2], "w13_codes").dim() ? tensor(a[2], "").size(0) : 0;
+  const int64_t T = mx_input(a[0], a[1], H, BITS), E = tensor(a[2], "w13_codes").dim() ? tensor(a[2], "").size(0) : 0;
   const Tensor &xc = tensor(a[0], ""), &xs = tensor(a[1], "");
   const int64_t G13 = (2 * I + 31) / 32, K13 = padded(H) / 256, G2 = (H + 31) / 32, K2 = padded(I) / 256;
   const Tensor& c13 = need(a[2], "w13_codes", ScalarType::Byte, {E, G13, K13, 4, 64, 16});
@@ -315,12 +358,40 @@ PyObject* grouped_ffn(PyObject* const* a) {
   const OnStream st(a[16], xc);
   const Tensor po = buffer(a[13], "pair_out", xc, ScalarType::Half, {T * k, H});
   const Tensor ps = buffer(a[14], "pair_scale", xc, ScalarType::Float, {T * k});
-  const Tensor ws = workspace(a[15], xc, g_entry.ffn_ws(T, k, E, H, I));
-  check(g_entry.ffn(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, H, ptr<uint8_t>(c13), ptr<uint8_t>(s13), ptr<uint8_t>(c2),
+  const Tensor ws = workspace(a[15], xc, (BITS == 4 ? g_entry.ffn_ws : g_entry.ffn8_ws)(T, k, E, H, I));
+  check((BITS == 4 ? g_entry.ffn : g_entry.ffn8)(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, H, ptr<uint8_t>(c13), ptr<uint8_t>(s13), ptr<uint8_t>(c2),
                     ptr<uint8_t>(s2), ptr<int32_t>(m2), E, I, k, ptr<int32_t>(off), ptr<int32_t>(srt), ptr<float>(tw),
                     ptr<uint16_t>(po), ptr<float>(ps), ptr<void>(ws), (size_t)ws.numel(), st.get()),
-        "mxfp4_grouped_ffn");
+        BITS == 4 ? "mxfp4_grouped_ffn" : "mxfp8_grouped_ffn");
   return tuple_of({po, ps});
+}
+
+// x, w_router, bias, k, rsf, w13_codes, w13_scales, w2_codes, w2_scales, dtype code, y, topk_ids, topk_w, workspace,
+// stream
+PyObject* layer(PyObject* const* a) {
+  const Rows x = matrix(a[0], "x_bf16");
+  const int64_t T = x.rows, H = x.cols, k = integer(a[3]), type = integer(a[9]);
+  const int64_t E = tensor(a[1], "w_router_bf16").dim() ? tensor(a[1], "").size(0) : 0;
+  const Tensor& wr = need(a[1], "w_router_bf16", ScalarType::BFloat16, {E, H});
+  const Tensor& bias = need(a[2], "bias", ScalarType::Float, {E});
+  const Tensor& w13 = tensor(a[5], "w13_codes");
+  const int64_t G13 = w13.dim() == 6 ? w13.size(1) : 0, I = 16 * G13;  // gate and up rows in groups of 32
+  const int64_t K13 = padded(H) / 256, G2 = (H + 31) / 32, K2 = padded(I) / 256;
+  const Tensor& c13 = need(a[5], "w13_codes", ScalarType::Byte, {E, G13, K13, 4, 64, 16});
+  const Tensor& s13 = need(a[6], "w13_scales", ScalarType::Byte, {E, G13, K13, 64, 4});
+  const Tensor& c2 = need(a[7], "w2_codes", ScalarType::Byte, {E, G2, K2, 4, 64, 16});
+  const Tensor& s2 = need(a[8], "w2_scales", ScalarType::Byte, {E, G2, K2, 64, 4});
+  if (k < 1 || k > E) raise(PyExc_ValueError, "need 1 <= k <= E, got k = %lld, E = %lld", (long long)k, (long long)E);
+  const OnStream st(a[14], x.t);
+  const Tensor y = buffer(a[10], "y", x.t, float_type(type), {T, H});
+  const Tensor ids = buffer(a[11], "topk_ids", x.t, ScalarType::Int, {T, k});
+  const Tensor tw = buffer(a[12], "topk_w", x.t, ScalarType::Float, {T, k});
+  const Tensor ws = workspace(a[13], x.t, g_entry.layer_ws(T, H, E, k, I));
+  check(g_entry.layer(ptr<uint16_t>(x.t), T, H, x.ld, ptr<uint16_t>(wr), ptr<float>(bias), E, k, (float)real(a[4]),
+                      ptr<uint8_t>(c13), ptr<uint8_t>(s13), ptr<uint8_t>(c2), ptr<uint8_t>(s2), I, (int32_t)type,
+                      y.data_ptr(), ptr<int32_t>(ids), ptr<float>(tw), ptr<void>(ws), (size_t)ws.numel(), st.get()),
+        "mxfp8_moe_layer");
+  return tuple_of({y, ids, tw});
 }
 
 // n of [T, H] (False: none) and, if asked for, its codes and scales
@@ -328,27 +399,29 @@ struct Normed {
   Out n;
   Codes q;
 };
-Normed norm_output(PyObject* n, PyObject* quantize, PyObject* codes, PyObject* scales, const Tensor& like, int64_t T,
-                   int64_t H) {
+Normed norm_output(PyObject* n, bool quantize, PyObject* codes, PyObject* scales, const Tensor& like, int64_t T,
+                   int64_t H, int bits) {
   Normed r{{Tensor(), H}, {}};
   if (n != Py_False) r.n = output(n, "n", like, ScalarType::BFloat16, T, H);
-  if (truth(quantize) || given(codes) || given(scales)) r.q = mx_output(codes, scales, like, T, H);
+  if (quantize || given(codes) || given(scales)) r.q = mx_output(codes, scales, like, T, H, bits);
   return r;
 }
 
-// x, w, eps, n, quantize, codes, scales, stream
+// x, w, eps, n, quantize, codes, scales, stream (quantize: of the MXFP8 form always true)
+template <int BITS>
 PyObject* norm_in(PyObject* const* a) {
   const Rows x = matrix(a[0], "x");
   const Tensor& w = need(a[1], "w", ScalarType::BFloat16, {x.cols});
   const OnStream st(a[7], x.t);
-  const Normed r = norm_output(a[3], a[4], a[5], a[6], x.t, x.rows, x.cols);
-  check(g_entry.norm_in(ptr<uint16_t>(x.t), x.rows, x.cols, x.ld, ptr<uint16_t>(w), (float)real(a[2]), ptr<uint16_t>(r.n.t),
+  const Normed r = norm_output(a[3], truth(a[4]), a[5], a[6], x.t, x.rows, x.cols, BITS);
+  check((BITS == 4 ? g_entry.norm_in : g_entry.norm_in8)(ptr<uint16_t>(x.t), x.rows, x.cols, x.ld, ptr<uint16_t>(w), (float)real(a[2]), ptr<uint16_t>(r.n.t),
                         r.n.ld, ptr<uint8_t>(r.q.codes), ptr<uint8_t>(r.q.scales), st.get()),
-        "moe_norm_in");
+        BITS == 4 ? "moe_norm_in" : "moe_norm_in_mxfp8");
   return r.q.codes.defined() ? tuple_of({r.n.t, r.q.codes, r.q.scales}) : wrap(r.n.t);
 }
 
 // y, residual, w_post, w_next, gate, residual_scale, eps, out, n, quantize, codes, scales, stream
+template <int BITS>
 PyObject* norm_out(PyObject* const* a) {
   const Rows y = matrix(a[0], "y", true), r = matrix(a[1], "residual");
   const int64_t T = y.rows, H = y.cols;
@@ -370,14 +443,14 @@ PyObject* norm_out(PyObject* const* a) {
   const Out ro = output(a[7], "out", y.t, ScalarType::BFloat16, T, H);
   Normed q{{Tensor(), H}, {}};
   if (wn.defined())
-    q = norm_output(a[8], a[9], a[10], a[11], y.t, T, H);
+    q = norm_output(a[8], truth(a[9]), a[10], a[11], y.t, T, H, BITS);
   else if (given(a[8]) || truth(a[9]) || given(a[10]) || given(a[11]))
     raise(PyExc_ValueError, "n and its quantization need w_next");
-  check(g_entry.norm_out(y.t.data_ptr(), y.t.scalar_type() == ScalarType::Float, T, H, y.ld, ptr<uint16_t>(r.t), r.ld,
+  check((BITS == 4 ? g_entry.norm_out : g_entry.norm_out8)(y.t.data_ptr(), y.t.scalar_type() == ScalarType::Float, T, H, y.ld, ptr<uint16_t>(r.t), r.ld,
                          ptr<uint16_t>(wp), ptr<uint16_t>(g), grs, gcs, (float)real(a[5]), ptr<uint16_t>(wn),
                          (float)real(a[6]), ptr<uint16_t>(ro.t), ro.ld, ptr<uint16_t>(q.n.t), q.n.ld,
                          ptr<uint8_t>(q.q.codes), ptr<uint8_t>(q.q.scales), st.get()),
-        "moe_norm_out");
+        BITS == 4 ? "moe_norm_out" : "moe_norm_out_mxfp8");
   if (!wn.defined()) return wrap(ro.t);
   if (!q.q.codes.defined()) return tuple_of({ro.t, q.n.t});
   return tuple_of({ro.t, q.n.t, q.q.codes, q.q.scales});
@@ -429,13 +502,20 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&bind)), METH_FASTCALL, nullptr},
-    method<4, quantize>("mxfp4_quantize"),
-    method<6, dequantize>("mxfp4_dequantize"),
+    method<4, quantize<4>>("mxfp4_quantize"),
+    method<6, dequantize<4>>("mxfp4_dequantize"),
     method<9, linear>("mxfp4_linear"),
-    method<17, grouped_ffn>("mxfp4_grouped_ffn"),
-    method<8, norm_in>("moe_norm_in"),
-    method<13, norm_out>("moe_norm_out"),
+    method<17, grouped_ffn<4>>("mxfp4_grouped_ffn"),
+    method<8, norm_in<4>>("moe_norm_in"),
+    method<13, norm_out<4>>("moe_norm_out"),
     method<7, combine>("moe_combine"),
+    method<4, quantize<8>>("mxfp8_quantize"),
+    method<6, dequantize<8>>("mxfp8_dequantize"),
+    method<11, linear8>("mxfp8_linear"),
+    method<17, grouped_ffn<8>>("mxfp8_grouped_ffn"),
+    method<8, norm_in<8>>("moe_norm_in_mxfp8"),
+    method<13, norm_out<8>>("moe_norm_out_mxfp8"),
+    method<15, layer>("mxfp8_moe_layer"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

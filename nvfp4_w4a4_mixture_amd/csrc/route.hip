@@ -119,19 +119,6 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Selection key of an FP64 score: a signed 64-bit integer in the order of the
-// scores, with -0 equal to +0 and NaN below every number (below -inf).  Keys
-// are totally ordered, so with ties going to the lower expert index every rank
-// 0..E-1 is taken by exactly one expert, also when scores are NaN (a token
-// whose x holds a NaN or an infinity, or a NaN bias).  This is the order of a
-// stable sort of the scores, descending, with NaN last.
-__device__ __forceinline__ long long score_key(double v) {
-  if (v != v) return (long long)0x8000000000000000ull;  // NaN: the smallest key
-  long long b = __double_as_longlong(v);
-  if (b == (long long)0x8000000000000000ull) b = 0;  // -0 -> +0
-  return b < 0 ? (b ^ 0x7FFFFFFFFFFFFFFFll) : b;      // negatives: larger magnitude, smaller key
-}
-
 // Top-k of one token by one wave from its scores.  Lane holds, for the
 // experts e = lane + 64 i (i < NG, e < E), sg = sigmoid(logit) and
 // sc = sg + bias.  The top-k are the experts whose rank under the total order

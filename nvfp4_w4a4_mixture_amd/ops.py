@@ -25,7 +25,9 @@ __all__ = ["moe_route", "moe_route_quantize", "nvfp4_quantize_act", "nvfp4_quant
            "moe_route_workspace_bytes", "moe_ffn_workspace_bytes", "moe_ffn_stage_workspace_bytes", "RouteOut",
            "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_quantize_weights", "mxfp4_pack_weights", "mxfp4_unpack_weights",
            "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_ffn_workspace_bytes", "mxfp4_grouped_ffn",
-           "moe_norm_in", "moe_norm_out"]
+           "moe_norm_in", "moe_norm_out",
+           "mxfp8_quantize", "mxfp8_dequantize", "mxfp8_linear", "mxfp8_ffn_workspace_bytes", "mxfp8_grouped_ffn",
+           "mxfp8_moe_layer_workspace_bytes", "mxfp8_moe_layer", "moe_norm_in_mxfp8", "moe_norm_out_mxfp8"]
 
 
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -507,7 +509,7 @@ def moe_nvfp4_unpack_weights(codes: torch.Tensor, packed_scales: torch.Tensor, k
     return _relayout("moe_nvfp4_unpack_weights", codes, packed_scales, kind, False, stream)
 
 
-# ---- MXFP4 operators and block norms: checks, allocation and the call are compiled (csrc/py_binding.cpp)
+# ---- MXFP4 and MXFP8 operators and block norms: checks, allocation and the call are compiled (csrc/py_binding.cpp)
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
@@ -517,7 +519,9 @@ class _Binding:
     of one: the functions that are marshalled here need only the library."""
 
     _ENTRIES = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_ffn_workspace_bytes",
-                "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine")
+                "mxfp4_grouped_ffn", "moe_norm_in", "moe_norm_out", "moe_combine", "mxfp8_quantize",
+                "mxfp8_dequantize", "mxfp8_linear", "mxfp8_ffn_workspace_bytes", "mxfp8_grouped_ffn",
+                "moe_norm_in_mxfp8", "moe_norm_out_mxfp8", "mxfp8_moe_layer_workspace_bytes", "mxfp8_moe_layer")
 
     def __getattr__(self, name):  # only until the functions are this object's own attributes
         if name not in self._ENTRIES:
@@ -652,3 +656,78 @@ def moe_norm_out(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch
     (r', n, codes, scales) when n is quantized to MXFP4 as well (n=False then skips the BF16 n)."""
     return _b.moe_norm_out(y, residual, w_post, w_next, gate, residual_scale, eps, out, n, quantize, codes, scales,
                            stream)
+
+
+# ---- MXFP8 activations (E4M3 elements, one power of two per 32) over the same packed MXFP4 weights
+
+ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def mxfp8_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """x [rows, cols] BF16 or FP32 -> (codes [rows, Cp], scales [rows, Cp/32]), Cp = cols rounded up to 256."""
+    return _b.mxfp8_quantize(x, codes, scales, stream)
+
+
+def mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out_dtype: torch.dtype = torch.bfloat16,
+                     out=None, stream=None) -> torch.Tensor:
+    """The values that the codes stand for, [rows, cols] in BF16 or FP32 (exact; BF16 from 2^-130 up)."""
+    return _b.mxfp8_dequantize(codes, scales, cols, _code(out_dtype, out), out, stream)
+
+
+def mxfp8_linear(x_codes, x_scales, w_codes, w_scales, N: int, out_dtype: torch.dtype = torch.bfloat16,
+                 bias: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+                 residual: Optional[torch.Tensor] = None, y=None, stream=None) -> torch.Tensor:
+    """y [T, N] = act(x W^T + bias) + residual for quantized x (mxfp8_quantize) and packed weights (as mxfp4_linear).
+
+    bias: BF16 [N]; activation: None, "relu", "silu", "gelu" (by erf) or "gelu_tanh"; residual: [T, N] BF16 or FP32 of
+    any row stride.  y may be the residual (in place, then in its type)."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    return _b.mxfp8_linear(x_codes, x_scales, w_codes, w_scales, N, _code(out_dtype, y), bias, ACTIVATIONS[activation],
+                           residual, y, stream)
+
+
+def mxfp8_ffn_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
+    return int(lib().mxfp8_ffn_workspace_bytes(T, k, E, H, I))
+
+
+def mxfp8_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_scales, w2_max_scale, H: int, I: int,
+                      k: int, expert_offsets, sorted_pair_ids, topk_w, pair_out=None, pair_scale=None, workspace=None,
+                      stream=None):
+    """mxfp4_grouped_ffn with x and what is between the two products in MXFP8: (pair_out, pair_scale)."""
+    return _b.mxfp8_grouped_ffn(x_codes, x_scales, w13_codes, w13_scales, w2_codes, w2_scales, w2_max_scale, H, I, k,
+                                expert_offsets, sorted_pair_ids, topk_w, pair_out, pair_scale, workspace, stream)
+
+
+MOE_LAYER_MAX_TOKENS = 32  # of one mxfp8_moe_layer call
+
+
+def mxfp8_moe_layer_workspace_bytes(T: int, H: int, E: int, k: int, I: int) -> int:
+    return int(lib().mxfp8_moe_layer_workspace_bytes(T, H, E, k, I))
+
+
+def mxfp8_moe_layer(x_bf16: torch.Tensor, w_router_bf16: torch.Tensor, bias: torch.Tensor, k: int,
+                    routed_scaling_factor: float, w13_codes, w13_scales, w2_codes, w2_scales,
+                    out_dtype: torch.dtype = torch.bfloat16, y=None, topk_ids=None, topk_w=None, workspace=None,
+                    stream=None):
+    """The whole routed layer for up to 32 tokens in three launches: (y [T, H], topk_ids [T, k], topk_w [T, k]).
+
+    Routing as moe_route, the experts as mxfp8_grouped_ffn on mxfp8_quantize(x), summed in FP32 without pair rows."""
+    return _b.mxfp8_moe_layer(x_bf16, w_router_bf16, bias, k, routed_scaling_factor, w13_codes, w13_scales, w2_codes,
+                              w2_scales, _code(out_dtype, y), y, topk_ids, topk_w, workspace, stream)
+
+
+def moe_norm_in_mxfp8(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, n=None, codes=None, scales=None,
+                      stream=None):
+    """(n, codes, scales): n = bf16(x / rms(x) * w) and its MXFP8 form; n=False skips the BF16 result (None)."""
+    return _b.moe_norm_in_mxfp8(x, w, eps, n, True, codes, scales, stream)
+
+
+def moe_norm_out_mxfp8(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch.Tensor], w_next: torch.Tensor,
+                       gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, eps: float = 1e-6, out=None,
+                       n=None, codes=None, scales=None, stream=None):
+    """(r', n, codes, scales): moe_norm_out with n quantized to MXFP8; n=False skips the BF16 n (None)."""
+    if w_next is None:
+        raise TypeError("w_next must be a torch.Tensor")
+    return _b.moe_norm_out_mxfp8(y, residual, w_post, w_next, gate, residual_scale, eps, out, n, True, codes, scales,
+                                 stream)
