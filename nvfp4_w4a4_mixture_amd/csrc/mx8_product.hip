@@ -11,7 +11,7 @@ namespace {
 using Mx8_128x64 = MxTile<4, 2, 2, 1, 4, true>;
 using Mx8_128x128 = MxTile<4, 2, 2, 2, 3, true>;
 using Mx8_256x128 = MxTile<8, 4, 2, 2, 4, true>;
-using Mx8_256x256 = MxTile<8, 4, 2, 4, 3, true>;
+using Mx8_256x256 = MxTile<8, 2, 4, 2, 3, true>;
 
 Shape linear_shape(int64_t T, int64_t G, int64_t KK) {
   const int64_t cus = 256;
@@ -45,7 +45,8 @@ template <bool EXACT>
 hipError_t launch_linear(const MxArgs& a, hipStream_t st) {
   const int64_t T = a.T;
   switch (linear_shape(T, a.G, a.KK)) {
-    case kStream: return launch_stream<kLinear, true>(a, 1, st);
+    case kStream:
+      return T <= 16 ? launch_stream<kLinear, true, true>(a, 1, st) : launch_stream<kLinear, true>(a, 1, st);
     case k128x64: return launch_tiled<kLinear, Mx8_128x64, EXACT>(a, (T + 63) / 64, st);
     case k128x128: return launch_tiled<kLinear, Mx8_128x128, EXACT>(a, (T + 127) / 128, st);
     case k256x128: return launch_tiled<kLinear, Mx8_256x128, EXACT>(a, (T + 127) / 128, st);

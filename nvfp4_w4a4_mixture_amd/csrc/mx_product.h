@@ -106,7 +106,7 @@ __device__ __forceinline__ float16_t act_mfma(i32x4_t w, const i32x4_t& x, float
 template <int S, bool EXACT>
 __device__ __forceinline__ float16_t act_mfma(i32x4_t w, const i32x8_t& x, float16_t c, int sw, int sx) {
   if constexpr (!EXACT) return mx8_mfma<S>(w, x, c, sw, sx);
-  const i32x8_t large = mx8_large(x);
+  const i32x8_t large = mx8_part(x, false);
   return mx8_mfma<S>(w, x ^ large, mx8_mfma<S>(w, large, c, sw, sx), sw, sx);
 }
 __device__ __forceinline__ i32x8_t join_halves(i32x4_t a, i32x4_t b) {
@@ -143,44 +143,57 @@ __device__ __forceinline__ float epilogue1(const MxArgs& a, float z, int64_t row
 typedef uint32_t mx_u32x4_any2_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef float mx_float4_any4_t __attribute__((ext_vector_type(4), aligned(4)));
 
-// acc[r] of column col + r, r < 16
-__device__ __forceinline__ void epilogue16(const MxArgs& a, float16_t& acc, int64_t row, int col) {
-  const int act = a.aux >> kMxActShift;
-  if (!a.bias && !a.residual && act == kActNone) return;
-  if (col + 16 > a.N) {
+// v[0..7] are columns col .. col + 7 of row `row`: the epilogue, and their store.
+// y may be the residual: a thread writes what it alone has read.
+__device__ __forceinline__ void epilogue8(const MxArgs& a, float* v, int64_t row, int col) {
+  if (col + 8 > a.N) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (col + r < a.N) acc[r] = epilogue1(a, acc[r], row, col + r);
+    for (int r = 0; r < 8; ++r) {
+      if (col + r >= a.N) break;
+      const float z = epilogue1(a, v[r], row, col + r);
+      if (a.aux & kMxOutF32) static_cast<float*>(a.out)[row * a.ldo + col + r] = z;
+      else static_cast<uint16_t*>(a.out)[row * a.ldo + col + r] = (uint16_t)bf16_pair(z, 0.0f);
+    }
     return;
   }
   auto add_bf16 = [&](const uint16_t* p) {
+    const mx_u32x4_any2_t u = *reinterpret_cast<const mx_u32x4_any2_t*>(p);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const mx_u32x4_any2_t v = *reinterpret_cast<const mx_u32x4_any2_t*>(p + 8 * q);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        acc[8 * q + 2 * r] += bf16_to_f32(v[r] & 0xFFFFu);
-        acc[8 * q + 2 * r + 1] += __uint_as_float(v[r] & 0xFFFF0000u);
-      }
+    for (int r = 0; r < 4; ++r) {
+      v[2 * r] += bf16_to_f32(u[r] & 0xFFFFu);
+      v[2 * r + 1] += __uint_as_float(u[r] & 0xFFFF0000u);
     }
   };
   if (a.bias) add_bf16(a.bias + col);
+  const int act = a.aux >> kMxActShift;
   if (act != kActNone) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = activate(act, acc[r]);
+    for (int r = 0; r < 8; ++r) v[r] = activate(act, v[r]);
   }
-  if (!a.residual) return;
-  const int64_t at = row * a.ldr + col;
-  if (a.aux & kMxResF32) {
-    const float* p = static_cast<const float*>(a.residual) + at;
+  if (a.residual) {
+    const int64_t at = row * a.ldr + col;
+    if (a.aux & kMxResF32) {
+      const float* p = static_cast<const float*>(a.residual) + at;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const mx_float4_any4_t v = *reinterpret_cast<const mx_float4_any4_t*>(p + 4 * q);
+      for (int q = 0; q < 2; ++q) {
+        const mx_float4_any4_t u = *reinterpret_cast<const mx_float4_any4_t*>(p + 4 * q);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[4 * q + r] += v[r];
+        for (int r = 0; r < 4; ++r) v[4 * q + r] += u[r];
+      }
+    } else {
+      add_bf16(static_cast<const uint16_t*>(a.residual) + at);
+    }
+  }
+  if (a.aux & kMxOutF32) {
+    float* p = static_cast<float*>(a.out) + row * a.ldo + col;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const mx_float4_any4_t u = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      __builtin_nontemporal_store(u, reinterpret_cast<mx_float4_any4_t*>(p + 4 * q));  // see store16_streaming
     }
   } else {
-    add_bf16(static_cast<const uint16_t*>(a.residual) + at);
+    const mx_u32x4_any2_t u = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    __builtin_nontemporal_store(u, reinterpret_cast<mx_u32x4_any2_t*>(static_cast<uint16_t*>(a.out) + row * a.ldo + col));
   }
 }
 
@@ -196,8 +209,14 @@ __device__ __forceinline__ void epilogue16(const MxArgs& a, float16_t& acc, int6
 // workgroups), 16 waves or loads two groups ahead as many.  Token groups past
 // the first would cost more here than in a tile: a lane's 16 bytes of x come
 // from 32 different rows.
-template <int MODE, int R, int NW, bool A8>
+//
+// 8-bit activations go in as two operands (see mx8_mfma).  HALF: at most 16
+// tokens, so both fit the 32 columns of one: column n takes the large elements of
+// token n % 16 if n < 16 and the rest if not, and the two columns' sums are added
+// at the end.
+template <int MODE, int R, int NW, bool A8, bool HALF = false>
 __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
+  static_assert(!HALF || (A8 && MODE == kLinear), "of the dense product");
   constexpr int kGroup = A8 ? 256 : 128;  // bytes of a column group of an activation row
   __shared__ float4 part[NW][R][4 * 68];  // strides 68 and 34: 16 lanes of a reader take 16 different slots
   __shared__ uint32_t hmax[NW][32];
@@ -220,7 +239,7 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
 
   for (int64_t t0 = lo + (MODE == kLinear ? (int64_t)blockIdx.y * 32 : 0); t0 < hi; t0 += 32) {
     const int cnt = (int)min((int64_t)32, hi - t0);
-    const int64_t pos = t0 + min(n, cnt - 1);  // lanes past the last token repeat it
+    const int64_t pos = t0 + min(HALF ? n & 15 : n, cnt - 1);  // lanes past the last token repeat it
     const int64_t arow = MODE == kGateUp ? a.sorted[pos] / a.aux : pos;
     const uint8_t* xc = a.a_codes + arow * (a.KK * kGroup) + f * (A8 ? 16 : 64);
     const uint8_t* xs = a.a_scales + arow * (a.KK * 8) + f * 4;
@@ -241,15 +260,8 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
       for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
     uint32_t bh = 0;
     for (int64_t c = w; c < KK; c += NW) {
-      i32x4_t wf[R][4];
+      // the activations first: they come from a cache, and their operands are made while the weights arrive
       typename ActFrag<A8>::type xf[4];
-      int sw[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) wf[i][s] = reinterpret_cast<const i32x4_t*>(wc[i] + c * kMxFragCodes)[s * 64 + l];
-        sw[i] = reinterpret_cast<const int*>(ws[i] + c * kMxFragScales)[l];
-      }
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if constexpr (A8)
@@ -258,13 +270,25 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
         else xf[s] = reinterpret_cast<const i32x4_t*>(xc + c * kGroup)[s];
       }
       const int sx = *reinterpret_cast<const int*>(xs + c * 8);
+      i32x4_t wf[R][4];
+      int sw[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) wf[i][s] = reinterpret_cast<const i32x4_t*>(wc[i] + c * kMxFragCodes)[s * 64 + l];
+        sw[i] = reinterpret_cast<const int*>(ws[i] + c * kMxFragScales)[l];
+      }
+      if constexpr (HALF) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) xf[s] = mx8_part(xf[s], n >= 16);
+      }
       if (MODE == kDown) bh = max(bh, max_byte((uint32_t)sx));
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        acc[i] = act_mfma<0, true>(wf[i][0], xf[0], acc[i], sw[i], sx);
-        acc[i] = act_mfma<1, true>(wf[i][1], xf[1], acc[i], sw[i], sx);
-        acc[i] = act_mfma<2, true>(wf[i][2], xf[2], acc[i], sw[i], sx);
-        acc[i] = act_mfma<3, true>(wf[i][3], xf[3], acc[i], sw[i], sx);
+        acc[i] = act_mfma<0, !HALF>(wf[i][0], xf[0], acc[i], sw[i], sx);
+        acc[i] = act_mfma<1, !HALF>(wf[i][1], xf[1], acc[i], sw[i], sx);
+        acc[i] = act_mfma<2, !HALF>(wf[i][2], xf[2], acc[i], sw[i], sx);
+        acc[i] = act_mfma<3, !HALF>(wf[i][3], xf[3], acc[i], sw[i], sx);
       }
     }
     if (MODE == kDown) {
@@ -283,8 +307,8 @@ __global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
       for (int i = 0; i < R; ++i) {
         float4 s = part[0][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
 #pragma unroll
-        for (int k = 1; k < NW; ++k) {
-          const float4 u = part[k][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
+        for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
+          const float4 u = part[k % NW][i][(p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
           s.x += u.x;
           s.y += u.y;
           s.z += u.z;
@@ -698,6 +722,42 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   else if (GX > 1 && groups == 1) all_cols(Const<(GX > 1 ? 1 : 0)>());
   else all_cols(Const<0>());
 
+  // ---- epilogue of the dense product of 8-bit activations: FP32 results go through LDS (the ring is no longer needed),
+  // as many token groups at a time as it holds, so that bias, residual and result move in runs of whole rows
+  if constexpr (MODE == kLinear && A8) {
+    constexpr int kCols = S::kSlots * 32, kRow = kCols + 4;  // floats; 16 bytes more against bank conflicts
+    constexpr int JP = S::kWX * GX * 32 * kRow * 4 <= S::kLds ? GX : GX / 2;
+    static_assert(S::kWX * JP * 32 * kRow * 4 <= S::kLds && GX % JP == 0, "a pass fits the ring");
+    constexpr int kLanes = kCols / 8, kRows = NW * 64 / kLanes;
+    const int c8 = tid % kLanes * 8, col = wt * kCols + c8;
+    float* tile = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int j0 = 0; j0 < GX; j0 += JP) {
+      if (j0 > 0) barrier_after_lds();
+#pragma unroll
+      for (int j = 0; j < JP; ++j)
+#pragma unroll
+        for (int i = 0; i < GW; ++i) {
+          float4* p = reinterpret_cast<float4*>(tile + ((wx * JP + j) * 32 + n) * kRow + (wm * GW + i) * 32 + f * 16);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            p[q] = make_float4(acc[i][j0 + j][4 * q], acc[i][j0 + j][4 * q + 1], acc[i][j0 + j][4 * q + 2], acc[i][j0 + j][4 * q + 3]);
+        }
+      barrier_after_lds();
+      if (col < a.N) {
+#pragma unroll 1
+        for (int r = tid / kLanes; r < S::kWX * JP * 32; r += kRows) {
+          const int tok = (r / (32 * JP) * GX + j0) * 32 + r % (32 * JP);
+          if (tok >= cnt) continue;
+          const float4 u = *reinterpret_cast<const float4*>(tile + r * kRow + c8), w4 = *reinterpret_cast<const float4*>(tile + r * kRow + c8 + 4);
+          float v[8] = {u.x, u.y, u.z, u.w, w4.x, w4.y, w4.z, w4.w};
+          epilogue8(a, v, first + tok, col);
+        }
+      }
+    }
+    return;
+  }
+
   int* out_row = reinterpret_cast<int*>(smem + S::kTok * S::kOutRow);
   int wmax = 0;
   if constexpr (MODE == kDown) {
@@ -710,12 +770,6 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     const int tok = (wx * GX + j) * 32 + n;
     const int64_t row = first + tok;
     const bool in = tok < cnt;
-    if constexpr (MODE == kLinear && A8) {
-      if (in) {
-#pragma unroll
-        for (int i = 0; i < GW; ++i) epilogue16(a, acc[i][j], row, (wt * S::kSlots + wm * GW + i) * 32 + f * 16);
-      }
-    }
     if constexpr (MODE == kGateUp) {
 #pragma unroll
       for (int i = 0; i < GW / 2; ++i) {
@@ -815,11 +869,11 @@ hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
   return launch_kernel(k, dim3((unsigned)grid), dim3(64 * S::kWaves), S::kLds, st, a);
 }
 
-template <int MODE, bool A8>
+template <int MODE, bool A8, bool HALF = false>
 hipError_t launch_stream(const MxArgs& a, int64_t E, hipStream_t st) {
   if constexpr (MODE == kLinear)
-    return launch_kernel(mx_stream_kernel<MODE, 1, 8, A8>, dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512), 0,
-                         st, a);
+    return launch_kernel(mx_stream_kernel<MODE, 1, 8, A8, HALF>, dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512),
+                         0, st, a);
   else
     return launch_kernel(mx_stream_kernel<MODE, 2, 4, A8>, dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st,
                          a);
