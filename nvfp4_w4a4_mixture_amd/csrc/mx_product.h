@@ -879,7 +879,7 @@ hipError_t launch_stream(const MxArgs& a, int64_t E, hipStream_t st) {
                          a);
 }
 
-enum Shape { kStream, k128x64, k128x128, k256x128, k256x256 };
+enum Shape { kStream, k128x64, k128x128, k256x64, k256x128, k256x256 };
 
 // m-tiles of `tok` pairs that E experts can have at most
 inline int64_t most_mtiles(int64_t pairs, int64_t E, int64_t tok) { return pairs / tok + (pairs < E ? pairs : E); }

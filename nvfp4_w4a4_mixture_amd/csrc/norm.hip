@@ -1,6 +1,8 @@
 // RMS norms before and after a block, fused with the block's gate, residual
 // scale and residual, and with the MXFP4 or MXFP8 quantisation of what the next
 // product reads.
+#include <type_traits>
+
 #include "launch.h"
 #include "mx_common.h"
 
@@ -28,6 +30,41 @@ __device__ __forceinline__ float row_sum(float v, float* lds, int w) {
   for (int i = 1; i < NW; ++i) s += lds[i];
   return s;
 }
+
+// The same in FP64
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)lane_dpp<CTRL>((uint32_t)(b >> 32)) << 32 | lane_dpp<CTRL>((uint32_t)b));
+}
+template <int NW>
+__device__ __forceinline__ double row_sum(double v, double* lds, int w) {
+  v += dpp_f64<kLaneXor1>(v);
+  v += dpp_f64<kLaneXor2>(v);
+  v += dpp_f64<kLaneHalfMirror>(v);
+  v += dpp_f64<kLaneMirror>(v);
+  uint64_t b = __builtin_bit_cast(uint64_t, v);
+  auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+  auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+  v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  b = __builtin_bit_cast(uint64_t, v);
+  hi = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+  lo = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
+  v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  if (NW == 1) return v;
+  if ((threadIdx.x & 63) == 0) lds[w] = v;
+  __syncthreads();
+  double s = lds[0];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) s += lds[i];
+  return s;
+}
+
+// Whether a value within `off` of f may round to another BF16 value than f does
+__device__ __forceinline__ bool near_bf16_tie(float f, float off) {
+  return fabsf(f - __uint_as_float((__float_as_uint(f) & 0xFFFF0000u) | 0x8000u)) <= off;
+}
+constexpr float kNormNoise = 0x1p-21f;  // relative, of the products of a result formed in FP32 (at most four roundings)
 
 // 16 bytes at an address aligned to an element only: one access on gfx950 all
 // the same, so rows of any length and stride move in 16-byte pieces.
@@ -105,13 +142,39 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, int c, int H, const uin
 // are bound by one latency of memory and by the two sums: 2.0 us (norm_in) and
 // 3.0 (norm_out) for one row of 6144, where sums through LDS shuffles and
 // rounding in integer steps took 3.0 and 4.7.
-template <int NW, int V, bool POST, bool YF32>
+//
+// A8 (the MXFP8 forms): results are all but always the exact ones, rounded to FP32
+// and to BF16.  E4M3 has steps
+// of up to an eighth of a value, so that the FP32 noise that moves one BF16 result
+// in some 10^5 to its neighbour moves one element in 10^6 by such a step.  So the
+// sums are FP64 (of FP32 sums of four squares: 10^-9 of a row's), and the eight results of a lane are formed again in FP64 if one of
+// them lies within FP32's noise of a border: one group in some 500.
+template <int NW, int V, bool POST, bool YF32, bool A8>
 __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
-  __shared__ float lds[2][NW];
+  using Sum = typename std::conditional<A8, double, float>::type;
+  __shared__ Sum lds[2][NW];
   const int w = threadIdx.x >> 6, t = threadIdx.x;
   const int64_t row = blockIdx.x;
   const int H = (int)a.H;
   const bool follow = !POST || a.w != nullptr;
+  auto square_sum = [](const float* v, Sum s) {  // of eight
+    if constexpr (A8) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float g = fmaf(v[i], v[i], fmaf(v[i + 1], v[i + 1], fmaf(v[i + 2], v[i + 2], v[i + 3] * v[i + 3])));
+        if (g > 1e-30f && g < 1e38f) {
+          s += (double)g;
+        } else {  // squares that leave FP32's range, NaN, or zeros
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s = fma((double)v[i + j], (double)v[i + j], s);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+    }
+    return s;
+  };
   float x[V][8];
   uint4 rr[V], wp[V], wn[V], gg[V];
 #pragma unroll
@@ -138,60 +201,91 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
   if constexpr (POST) {
     const float g_row = a.gate && a.gate_row ? bf16_to_f32(a.gate[row * a.gate_rs]) : 1.0f;
     float inv = 1.0f;
+    double inv64 = 1.0;
     if (a.w_post) {
-      float sq = 0.0f;
+      Sum sq = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(x[v][i], x[v][i], sq);
-      inv = rsqrtf(row_sum<NW>(sq, lds[0], w) / (float)H + a.eps);
+      for (int v = 0; v < V; ++v) sq = square_sum(x[v], sq);
+      if constexpr (A8) {
+        inv64 = rsqrt(row_sum<NW>(sq, lds[0], w) * (1.0 / (double)H) + (double)a.eps);
+        inv = (float)inv64;
+      } else {
+        inv = rsqrtf(row_sum<NW>(sq, lds[0], w) / (float)H + a.eps);
+      }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float wv[8], rv[8], gv[8];
+      float wv[8], rv[8], gv[8], f[8];
       unpack8(rr[v], rv);
       if (a.w_post) unpack8(wp[v], wv);
       if (a.gate && !a.gate_row) unpack8(gg[v], gv);
+      bool close = false;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float z = x[v][i];
         if (a.w_post) z = z * inv * wv[i];
         if (a.gate) z *= a.gate_row ? g_row : gv[i];
-        x[v][i] = fmaf(a.scale, z, rv[i]);
+        f[i] = fmaf(a.scale, z, rv[i]);
+        if constexpr (A8) close |= near_bf16_tie(f[i], kNormNoise * fabsf(a.scale * z) + kNormNoise * fabsf(f[i]));
       }
+      if (A8 && close) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          double z = (double)x[v][i] * inv64;
+          if (a.w_post) z *= (double)wv[i];
+          if (a.gate) z *= (double)(a.gate_row ? g_row : gv[i]);
+          f[i] = (float)fma(z, (double)a.scale, (double)rv[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[v][i] = f[i];
       const uint4 o = pack8(x[v]);
       unpack8(o, x[v]);  // the next norm reads the residual that is kept
       store8_bf16(a.r_out + row * a.ldro, (v * 64 * NW + t) * 8, H, o);
     }
     if (!follow) return;
   }
-  float sq = 0.0f;
+  Sum sq = 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(x[v][i], x[v][i], sq);
-  const float inv = rsqrtf(row_sum<NW>(sq, lds[1], w) / (float)H + a.eps);
+  for (int v = 0; v < V; ++v) sq = square_sum(x[v], sq);
+  float inv;
+  double inv64 = 0.0;
+  if constexpr (A8) {
+    inv64 = rsqrt(row_sum<NW>(sq, lds[1], w) * (1.0 / (double)H) + (double)a.eps);
+    inv = (float)inv64;
+  } else {
+    inv = rsqrtf(row_sum<NW>(sq, lds[1], w) / (float)H + a.eps);
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * 64 * NW + t) * 8;
     float wv[8], q[8];
     unpack8(wn[v], wv);
+    bool close = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = x[v][i] * inv * wv[i];
+    for (int i = 0; i < 8; ++i) {
+      q[i] = x[v][i] * inv * wv[i];
+      if constexpr (A8) close |= ((__float_as_uint(q[i]) + 8u) & 0xFFF0u) == 0x8000u;  // 2^-20 to 2^-21 of it
+    }
+    if (A8 && close) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = (float)((double)x[v][i] * inv64 * (double)wv[i]);
+    }
     const uint4 o = pack8(q);
     if (a.n) store8_bf16(a.n + row * a.ldn, c, H, o);
     if (a.codes) {  // H % 32 == 0: a quad of lanes holds one block
       uint32_t m = 0;
       unpack8(o, q);
+      if (c >= H) {  // the padding is zero whatever the norm is
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (c >= H) q[i] = 0.0f;  // the padding is zero whatever the norm is
-        m = max(m, abs_bits(q[i]));
+        for (int i = 0; i < 8; ++i) q[i] = 0.0f;
       }
-      const uint32_t amax = quad_max(m), byte = a.a8 ? mx8_scale_byte(amax) : mx_scale_byte(amax);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(q[i]));
+      const uint32_t amax = quad_max(m), byte = A8 ? mx8_scale_byte(amax) : mx_scale_byte(amax);
       if (c < (int)a.Hp) {
         const int64_t at = (row * (int)a.Hp + c) / 8;
-        if (a.a8) reinterpret_cast<uint2*>(a.codes)[at] = make_uint2(mx8_encode4(q, byte), mx8_encode4(q + 4, byte));
+        if constexpr (A8) reinterpret_cast<uint2*>(a.codes)[at] = make_uint2(mx8_encode4(q, byte), mx8_encode4(q + 4, byte));
         else reinterpret_cast<uint32_t*>(a.codes)[at] = mx_encode8(q, byte);
         if ((t & 3) == 0) a.scales[at / 4] = (uint8_t)byte;
       }
@@ -201,13 +295,13 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
 
 namespace {
 
-template <int NW, int V, bool POST>
+template <int NW, int V, bool POST, bool A8>
 hipError_t launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const dim3 grid((unsigned)T), block(64 * NW);
   if constexpr (POST) {
-    if (y_f32) return launch_kernel(norm_kernel<NW, V, POST, true>, grid, block, 0, st, a);
+    if (y_f32) return launch_kernel(norm_kernel<NW, V, POST, true, A8>, grid, block, 0, st, a);
   }
-  return launch_kernel(norm_kernel<NW, V, POST, false>, grid, block, 0, st, a);
+  return launch_kernel(norm_kernel<NW, V, POST, false, A8>, grid, block, 0, st, a);
 }
 
 // A wave alone needs no barrier and leaves fewer lanes idle, four waves finish a
@@ -215,18 +309,30 @@ hipError_t launch_norm_as(const NormArgs& a, int64_t T, bool y_f32, hipStream_t 
 // 24.5 and 28.2); 500 rows of 1999: 5.5 and 4.2 us.  From 2056 columns on four
 // are as fast or faster at any number of rows; twelve take one row of 6144 in
 // 1.8 (2.8) us against 2.0 (3.0), but 1024 rows in 4.8 (8.3) against 4.3 (7.2).
-template <bool POST>
+template <bool POST, bool A8>
 hipError_t launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const int cols = (int)a.Hp;
-  if (cols <= 512) return launch_norm_as<1, 1, POST>(a, T, y_f32, st);
-  if (cols <= 1024) return launch_norm_as<1, 2, POST>(a, T, y_f32, st);
-  if (cols <= 1536 && T >= 2048) return launch_norm_as<1, 3, POST>(a, T, y_f32, st);
-  if (cols <= 2047 && T >= 2048) return launch_norm_as<1, 4, POST>(a, T, y_f32, st);
-  if (cols <= 2048) return launch_norm_as<4, 1, POST>(a, T, y_f32, st);
-  if (cols <= 4096) return launch_norm_as<4, 2, POST>(a, T, y_f32, st);
-  if (cols <= 6144) return launch_norm_as<4, 3, POST>(a, T, y_f32, st);
-  if (cols <= 8192) return launch_norm_as<4, 4, POST>(a, T, y_f32, st);
-  return launch_norm_as<4, 8, POST>(a, T, y_f32, st);
+  if (cols <= 512) return launch_norm_as<1, 1, POST, A8>(a, T, y_f32, st);
+  if (cols <= 1024) return launch_norm_as<1, 2, POST, A8>(a, T, y_f32, st);
+  if (cols <= 1536 && T >= 2048) return launch_norm_as<1, 3, POST, A8>(a, T, y_f32, st);
+  if (cols <= 2047 && T >= 2048) return launch_norm_as<1, 4, POST, A8>(a, T, y_f32, st);
+  if (cols <= 2048) return launch_norm_as<4, 1, POST, A8>(a, T, y_f32, st);
+  if (cols <= 4096) return launch_norm_as<4, 2, POST, A8>(a, T, y_f32, st);
+  if (cols <= 6144) return launch_norm_as<4, 3, POST, A8>(a, T, y_f32, st);
+  if (cols <= 8192) return launch_norm_as<4, 4, POST, A8>(a, T, y_f32, st);
+  return launch_norm_as<4, 8, POST, A8>(a, T, y_f32, st);
+}
+
+// The MXFP8 forms do more arithmetic a row, so a row's waves share it further where
+// they leave few lanes idle (2080 columns: 1999 rows 9.4 us by four waves of two
+// chunks, 8.7 by five of one) or there are few rows (one of 6144: 5.3 us by four
+// waves, 4.7 by twelve; but 8192 of them 83 by four, 105 by twelve, 98 by six).
+template <bool POST>
+hipError_t launch_norm8_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
+  const int cols = (int)a.Hp;
+  if (cols > 2048 && cols <= 2560) return launch_norm_as<5, 1, POST, true>(a, T, y_f32, st);
+  if (cols > 2560 && cols <= 6144 && T <= 256) return launch_norm_as<12, 1, POST, true>(a, T, y_f32, st);
+  return launch_norm_shape<POST, true>(a, T, y_f32, st);
 }
 
 }  // namespace
@@ -234,7 +340,8 @@ hipError_t launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream
 int64_t norm_max_cols() { return 16384; }
 
 hipError_t launch_norm(const NormArgs& a, int64_t T, bool post, bool y_f32, hipStream_t st) {
-  return post ? launch_norm_shape<true>(a, T, y_f32, st) : launch_norm_shape<false>(a, T, false, st);
+  if (a.a8) return post ? launch_norm8_shape<true>(a, T, y_f32, st) : launch_norm8_shape<false>(a, T, false, st);
+  return post ? launch_norm_shape<true, false>(a, T, y_f32, st) : launch_norm_shape<false, false>(a, T, false, st);
 }
 
 }  // namespace moe

@@ -1,6 +1,6 @@
 """GPU parity of the MXFP8 operators against oracle/mx8.py (float64).
 
-Bitwise: codes, scale bytes, read-back values, the norms' MXFP8 forms.
+Bitwise: codes, scale bytes, read-back values, the norms and their MXFP8 forms.
 
 Products are checked element by element, u = 2^-24 (FP32):
 * an FP32 sum of K exact products, in any order: (K + 8) u * sum |x||w|;
@@ -22,6 +22,7 @@ import torch
 
 from gpu_cases import dev_bf16, pair_rows, say, to_np
 from oracle import mx, mx8
+from oracle import norm as onorm
 from test_gpu_mx import bf16, draw, routing, special
 
 pytestmark = pytest.mark.gpu
@@ -118,32 +119,70 @@ def test_quantize_no_rows(ops):
 
 
 @pytest.mark.parametrize("T,H,pad", [(1, 32, 0), (3, 288, 8), (5, 992, 3), (2, 2048, 0), (3, 4128, 0), (4, 6144, 0),
-                                     (2, 16384, 8), (2050, 1056, 0)])
+                                     (2, 16384, 8), (2050, 1056, 0), (2049, 1984, 0)])
 def test_norms(ops, T, H, pad):
-    """n and r' are those of the MXFP4 norms; the MXFP8 form is mxfp8_quantize of n, bit for bit, with and without n."""
+    """n and r' are the float64 results, rounded to FP32 and to BF16; the MXFP8 form is mxfp8_quantize of n, bit for bit, with and
+    without n.
+
+    Sums are FP64 over FP32 sums of four squares: one rounding of the innermost product (of FP32 y; a BF16 value's square
+    is exact) and three of the sums, 4 u of a row's mean square at most, so 1 / rms is good to 2 u and a product with it
+    to 2^-23, beside u for the FP32 value and half a BF16 step.  The roundings of a row's groups are independent, and their mean is 100 times
+    smaller: less than one result in 10^5 may lie that close to a border."""
     say(f"norms {T}x{H}+{pad}")
     rng = np.random.default_rng(H)
-    x = dev_bf16(bf16(rng.standard_normal((T, H + pad)))[1])[:, :H]
-    y = dev_bf16(bf16(rng.standard_normal((T, H + pad)))[1])[:, :H]
-    w = dev_bf16(bf16(1 + 0.3 * rng.standard_normal(H))[1])
+    (xv, xb), (yv, yb) = (bf16(rng.standard_normal((T, H + pad)) * np.exp(rng.standard_normal((T, 1)))) for _ in range(2))
+    xv, yv, x, y = xv[:, :H], yv[:, :H], dev_bf16(xb)[:, :H], dev_bf16(yb)[:, :H]
+    wv, wb = bf16(1 + 0.3 * rng.standard_normal(H))
+    w = dev_bf16(wb)
+    y32 = (yv * (1 + 1e-4 * rng.standard_normal((T, H)))).astype(np.float32)
+
+    def check_codes(n, codes, scales):
+        qc, qs = ops.mxfp8_quantize(n)
+        assert torch.equal(codes, qc) and torch.equal(scales, qs)
+
+    def close(got, ref, z):
+        g = f64(got)
+        half = np.ldexp(1.0, np.maximum(np.frexp(np.maximum(np.abs(g), np.abs(ref)))[1], -125) - 9)
+        assert (np.abs(g - ref) <= half + U * np.abs(ref) + 2.0 ** -23 * np.abs(z)).all()
+        differ = int((g != bf16(ref)[0]).sum())
+        print(f"  {differ} of {ref.size} not correctly rounded", flush=True)
+        assert differ <= 1 + ref.size // 100000
+
     n, codes, scales = ops.moe_norm_in_mxfp8(x, w, 1e-6)
-    assert torch.equal(n, ops.moe_norm_in(x, w, 1e-6))
-    qc, qs = ops.mxfp8_quantize(n)
-    assert torch.equal(codes, qc) and torch.equal(scales, qs)
+    ref = onorm.norm(xv, wv, np.float32(1e-6))
+    close(n, ref, ref)
+    check_codes(n, codes, scales)
     skipped = ops.moe_norm_in_mxfp8(x, w, 1e-6, n=False)
-    assert skipped[0] is None and torch.equal(skipped[1], qc) and torch.equal(skipped[2], qs)
-    for yt in (y, y.float()):
-        for gate in (None, w[None], x[:, :1]):
+    assert skipped[0] is None and torch.equal(skipped[1], codes) and torch.equal(skipped[2], scales)
+    for yt, ym in ((y, yv), (torch.from_numpy(y32).cuda(), y32.astype(np.float64))):
+        for gate, gm in ((None, None), (w[None], wv[None]), (x[:, :1], xv[:, :1]), (x, xv)):
             r, n, codes, scales = ops.moe_norm_out_mxfp8(yt, x, w, w, gate=gate, residual_scale=0.5)
-            want = ops.moe_norm_out(yt, x, w, w, gate=gate, residual_scale=0.5)
-            assert torch.equal(r, want[0]) and torch.equal(n, want[1])
-            qc, qs = ops.mxfp8_quantize(n)
-            assert torch.equal(codes, qc) and torch.equal(scales, qs)
-    r, n, codes, scales = ops.moe_norm_out_mxfp8(y, x, None, w, n=False, codes=torch.full_like(qc, 99),
-                                                 scales=torch.full_like(qs, 99))
-    want = ops.moe_norm_out(y, x, None, w)
-    qc, qs = ops.mxfp8_quantize(want[1])
-    assert n is None and torch.equal(r, want[0]) and torch.equal(codes, qc) and torch.equal(scales, qs)
+            ref = onorm.residual(ym, xv, wv, gm, 0.5, np.float32(1e-6))
+            close(r, ref, ref - xv)
+            ref = onorm.norm(f64(r), wv, np.float32(1e-6))  # of the residual that is kept
+            close(n, ref, ref)
+            check_codes(n, codes, scales)
+    r, n, codes, scales = ops.moe_norm_out_mxfp8(y, x, None, w, n=False, codes=torch.full_like(codes, 99),
+                                                 scales=torch.full_like(scales, 99))
+    rm = bf16(xv + yv)[0]
+    assert n is None and np.array_equal(f64(r), rm)  # a sum of two BF16 values
+    check_codes(ops.moe_norm_in_mxfp8(r, w)[0], codes, scales)
+    inplace = x.clone()
+    ops.moe_norm_out_mxfp8(y, inplace, None, w, out=inplace)
+    assert torch.equal(inplace, r)
+
+
+def test_norms_extremes(ops):
+    """NaN and infinities stay in their rows; zero rows give zeros; huge and tiny rows do not overflow the sums."""
+    H = 288
+    x = torch.randn(6, H, device="cuda").to(torch.bfloat16)
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    x[0, 7], x[1, 9], x[2], x[3], x[4] = float("nan"), float("inf"), 0.0, 1e30, 1e-30
+    n, codes, scales = ops.moe_norm_in_mxfp8(x, w, 1e-6)
+    v = ops.mxfp8_dequantize(codes, scales, H)
+    assert bool(n[0].isnan().all()) and bool(v[0].isnan().all()) and bool(n[1, 9].isnan())
+    assert bool((n[2] == 0).all()) and bool((v[2] == 0).all()) and bool((n[3] == 1).all()) and bool((v[3] == 1).all())
+    assert not bool(n[2:].isnan().any()) and torch.equal(n[5], ops.moe_norm_in_mxfp8(x[5:], w, 1e-6)[0][0])
 
 
 # ---------------------------------------------------------------------------------------------
