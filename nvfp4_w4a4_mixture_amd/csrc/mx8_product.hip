@@ -1,7 +1,110 @@
-// Products of MXFP8 activations: their shapes, by sizes.
+// Products of MXFP8 activations: the streaming kernel, and the shapes by sizes.
 #include "mx_product.h"
 
 namespace moe {
+
+// Streaming product of 8-bit activations: few tokens per weight row, as
+// mx_stream_kernel.  A workgroup takes 32 weight rows and up to 32 tokens; its
+// eight waves split the columns and load their weight fragments straight from
+// memory.  Their tokens' columns come as whole runs of 256 bytes and through LDS
+// into fragments, one column group ahead: fetched as fragments, 32 rows of 16 bytes
+// a load, they kept the memory pipes four times as long as the weights (16 x 6144 x
+// 6144 10.2 us, so 7.0; 32 tokens 10.4 and 8.7; one token 6.5 either way, where the
+// 4-bit product takes 4.6: twice the matrix instructions, and their operands to
+// make).
+//
+// Activations go in as two operands (see mx8_mfma).  HALF: at most 16 tokens, so
+// both fit the 32 columns of one: column n takes the large elements of token n %
+// 16 if n < 16 and the rest if not, and the two columns' sums are added at the end.
+template <bool HALF>
+__global__ __launch_bounds__(512) void mx8_stream_kernel(MxArgs a) {
+  constexpr int NW = 8, kRows = HALF ? 16 : 32, kParts = kRows / 4;  // tokens of a tile; loads of four rows
+  constexpr int kPart = NW * 4 * 68 * 16, kStaged = NW * kRows * 256;
+  __shared__ __align__(16) unsigned char smem[kPart > kStaged ? kPart : kStaged];
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, n = l & 31, f = l >> 5;
+  const int KK = (int)a.KK, tok_n = HALF ? n & 15 : n;
+  const int t0 = (int)blockIdx.y * kRows, cnt = min(kRows, a.T - t0);
+  const uint8_t* wc = a.w_codes + (int64_t)blockIdx.x * KK * kMxFragCodes;
+  const uint8_t* ws = a.w_scales + (int64_t)blockIdx.x * KK * kMxFragScales;
+  auto act_row = [&](int t) { return (uint32_t)(t0 + min(t, cnt - 1)); };  // rows past the last token repeat it
+  uint32_t xoff[kParts];
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) xoff[i] = act_row(4 * i + (l >> 4)) * (uint32_t)(KK * 256) + (uint32_t)(l & 15) * 16u;
+  const uint8_t* xs = a.a_scales + (int64_t)act_row(tok_n) * (KK * 8) + f * 4;
+  unsigned char* staged = smem + w * kRows * 256;  // the wave's own: 16-byte chunk c of row r at r * 256 + (c ^ (r & 15)) * 16
+  struct Cols {
+    i32x4_t x[kParts], w[4];
+    int sw, sx;
+  };
+  auto load = [&](int64_t c, Cols& d) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      if (4 * i < cnt) d.x[i] = *reinterpret_cast<const i32x4_t*>(a.a_codes + c * 256 + xoff[i]);
+    d.sx = *reinterpret_cast<const int*>(xs + c * 8);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) d.w[s] = reinterpret_cast<const i32x4_t*>(wc + c * kMxFragCodes)[s * 64 + l];
+    d.sw = reinterpret_cast<const int*>(ws + c * kMxFragScales)[l];
+  };
+  float16_t acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+  auto multiply = [&](Cols& d) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      const int r = 4 * i + (l >> 4);
+      if (4 * i < cnt) *reinterpret_cast<i32x4_t*>(staged + r * 256 + (((l & 15) ^ r) & 15) * 16) = d.x[i];
+    }
+    wave_lds_order();
+    i32x8_t xf[4];  // of columns past the last token: whatever was there, and their sums are not written
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      xf[s] = join_halves(*reinterpret_cast<const i32x4_t*>(staged + tok_n * 256 + (((2 * s + f) ^ tok_n) & 15) * 16),
+                          *reinterpret_cast<const i32x4_t*>(staged + tok_n * 256 + (((8 + 2 * s + f) ^ tok_n) & 15) * 16));
+      if constexpr (HALF) xf[s] = mx8_part(xf[s], n >= 16);
+    }
+    wave_lds_order();
+    acc = act_mfma<0, !HALF>(d.w[0], xf[0], acc, d.sw, d.sx);
+    acc = act_mfma<1, !HALF>(d.w[1], xf[1], acc, d.sw, d.sx);
+    acc = act_mfma<2, !HALF>(d.w[2], xf[2], acc, d.sw, d.sx);
+    acc = act_mfma<3, !HALF>(d.w[3], xf[3], acc, d.sw, d.sx);
+  };
+  Cols d0, d1;
+  if (w < KK) load(w, d0);
+  for (int c = w; c < KK; c += 2 * NW) {
+    if (c + NW < KK) load(c + NW, d1);
+    multiply(d0);
+    if (c + NW < KK) {
+      if (c + 2 * NW < KK) load(c + 2 * NW, d0);
+      multiply(d1);
+    }
+  }
+  __syncthreads();  // the waves' sums take the place of their columns
+  float4* part = reinterpret_cast<float4*>(smem);  // [NW][4 * 68]
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    part[w * 272 + q * 68 + f * 34 + n] = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+  __syncthreads();
+  const int tok = tid >> 3, p = tid & 7, col = (int)blockIdx.x * 32 + 4 * p;  // features 4 p .. 4 p + 3 of one token
+  if (tok >= cnt) return;
+  float4 s = part[(p & 3) * 68 + (p >> 2) * 34 + tok];
+#pragma unroll
+  for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
+    const float4 u = part[k % NW * 272 + (p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
+    s.x += u.x;
+    s.y += u.y;
+    s.z += u.z;
+    s.w += u.w;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  const int64_t row = t0 + tok;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (col + q >= a.N) break;
+    const float z = epilogue1(a, v[q], row, col + q);
+    if (a.aux & kMxOutF32) static_cast<float*>(a.out)[row * a.ldo + col + q] = z;
+    else static_cast<uint16_t*>(a.out)[row * a.ldo + col + q] = (uint16_t)bf16_pair(z, 0.0f);
+  }
+}
 
 namespace {
 
@@ -22,16 +125,17 @@ int64_t tiles(int64_t T, int64_t G, int64_t rows, int64_t tok) { return (G + row
 
 // The shape of a dense product with 16-bit results, both sides in us:
 //   T x K x N            stream  128x64  256x64  256x128  256x256
-//   16 x 6144 x 6144       10.2    11.8    15.2     20.5     32.4
-//   64 x 6144 x 6144       17.9    14.5    20.2     21.9     34.5
-//   77 x 2080 x 1000        5.7     7.3    10.8     11.6     16.9
-//   509 x 6144 x 2048      33.8    15.4    21.0     30.8     53.9
-//   512 x 6144 x 6144      99.3    32.4    24.8     33.9     56.6
-//   1024 x 6144 x 6144             51.7    43.0     37.2     66.0
-//   2048 x 2048 x 6144             33.8    28.1     38.8     35.7
-//   8192 x 512 x 4096              31.6    26.0     29.3     29.2
-//   8192 x 2048 x 6144            146.8    99.0    103.0     94.8
-//   8192 x 6144 x 6144            394.2   279.3    245.4    230.0
+//   16 x 6144 x 6144        7.2    11.9    15.8     21.4     33.1
+//   32 x 6144 x 10240      16.2    13.4    20.4     22.4     34.6
+//   64 x 6144 x 6144       15.8    14.8    20.4     22.4     35.0
+//   128 x 6144 x 1024       8.4    14.3    20.0     28.9     36.6
+//   509 x 6144 x 2048      32.0    15.8    21.1     31.5     55.2
+//   512 x 6144 x 6144      88.2    32.6    26.4     34.5     58.2
+//   1024 x 6144 x 6144             47.7    47.6     43.9     69.5
+//   2048 x 2048 x 6144             34.2    29.1     35.6     33.3
+//   8192 x 512 x 4096              34.7    29.0     32.3     30.5
+//   8192 x 2048 x 6144            144.4   111.1    108.8     93.0
+//   8192 x 6144 x 6144            390.7   284.2    246.8    225.6
 // Streaming while its tiles of 32 x 32 fit the chip once, or each CU fetches at
 // most 32 rows of x a weight group; the largest tile that still fills the chip;
 // 256 x 128 where its tiles fill it just once.
@@ -59,19 +163,19 @@ Shape linear_shape_exact(int64_t T, int64_t G) {
 }
 
 // The shape of a stage of the experts' FFN; both stages in one shape, us:
-//   E k H I, tokens          stream  128x64  256x64  256x128  256x256
-//   16 4 1024 512, 16           8.5     9.6    11.3     13.3     17.8
-//   16 4 1024 512, 128         20.3    10.7    13.3     17.0     19.8
-//   16 4 1024 512, 1024                20.3    19.1     19.4     28.0
-//   16 4 1024 512, 8192                93.7    72.2     90.0     87.8
-//   80 8 6144 2048, 16        168.3   165.1   157.7    171.6    199.4
-//   80 8 6144 2048, 256       498.7   320.1   291.8    308.0    348.8
-//   80 8 6144 2048, 1024              569.0   469.5    481.0    486.1
-//   80 8 6144 2048, 2048              985.9   762.9    747.7    709.4
-//   80 8 6144 2048, 8192               3227    2465     2358     2101
+//   E k H I, tokens         128x64  256x64  256x128  256x256
+//   16 4 1024 512, 16         10.0    11.5     13.3     17.9
+//   16 4 1024 512, 256        10.8    13.6     18.1     22.1
+//   16 4 1024 512, 1024       20.4    19.2     19.4     28.0
+//   16 4 1024 512, 8192      104.0    81.4     90.0     94.1
+//   80 8 6144 2048, 16       164.1   159.9    171.6    202.8
+//   80 8 6144 2048, 256      323.1   292.0    308.0    349.4
+//   80 8 6144 2048, 1024     578.1   474.5    481.0    506.2
+//   80 8 6144 2048, 2048     990.9   777.6    747.7    729.8
+//   80 8 6144 2048, 8192      3275    2529     2358     2156
+// (Few tokens through a small layer are streamed by mx_layer.hip's kernels.)
 Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
   const int64_t some = pairs < E ? pairs : E;
-  if (pairs <= 16 * E && some * (rows / 32) <= 2048) return kStream;
   if ((pairs / 64 + some / 2) * ((rows + 255) / 256) < 256) return k128x64;
   return pairs >= 160 * E && KK >= 8 ? k256x256 : k256x64;
 }
@@ -80,7 +184,6 @@ template <int MODE>
 hipError_t launch_experts_stage(const MxArgs& a, const MxExperts& x, hipStream_t st) {
   const int64_t pairs = x.T * x.k;
   switch (experts_shape(pairs, x.E, a.N, a.KK)) {
-    case kStream: return launch_stream<MODE, true>(a, x.E, st);
     case k128x64: return launch_tiled<MODE, Mx8_128x64>(a, most_mtiles(pairs, x.E, 64), st);
     case k256x64: return launch_tiled<MODE, Mx8_256x64>(a, most_mtiles(pairs, x.E, 64), st);
     default: return launch_tiled<MODE, Mx8_256x256>(a, most_mtiles(pairs, x.E, 256), st);
@@ -88,7 +191,8 @@ hipError_t launch_experts_stage(const MxArgs& a, const MxExperts& x, hipStream_t
 }
 
 hipError_t launch_linear_stream(const MxArgs& a, hipStream_t st) {
-  return a.T <= 16 ? launch_stream<kLinear, true, true>(a, 1, st) : launch_stream<kLinear, true>(a, 1, st);
+  const dim3 grid((unsigned)a.G, (unsigned)((a.T + 31) / 32));
+  return launch_kernel(a.T <= 16 ? &mx8_stream_kernel<true> : &mx8_stream_kernel<false>, grid, dim3(512), 0, st, a);
 }
 
 }  // namespace

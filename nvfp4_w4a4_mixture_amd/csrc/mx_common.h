@@ -138,6 +138,13 @@ __device__ __forceinline__ void store16_streaming(void* p, uint32_t a, uint32_t 
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// Orders this wave's LDS accesses before its later ones (lanes read what other lanes of the same wave wrote)
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // One scaled FP4 MFMA step: c += A . B over 64 columns; S = step = scale byte.
 template <int S>
 __device__ __forceinline__ float16_t mx_mfma(i32x4_t a, i32x4_t b, float16_t c, int sa, int sb) {

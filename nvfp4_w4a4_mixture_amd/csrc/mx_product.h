@@ -143,236 +143,68 @@ __device__ __forceinline__ float epilogue1(const MxArgs& a, float z, int64_t row
 typedef uint32_t mx_u32x4_any2_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef float mx_float4_any4_t __attribute__((ext_vector_type(4), aligned(4)));
 
-// v[0..7] are columns col .. col + 7 of row `row`: the epilogue, and their store.
-// y may be the residual: a thread writes what it alone has read.
-__device__ __forceinline__ void epilogue8(const MxArgs& a, float* v, int64_t row, int col) {
-  if (col + 8 > a.N) {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if (col + r >= a.N) break;
-      const float z = epilogue1(a, v[r], row, col + r);
-      if (a.aux & kMxOutF32) static_cast<float*>(a.out)[row * a.ldo + col + r] = z;
-      else static_cast<uint16_t*>(a.out)[row * a.ldo + col + r] = (uint16_t)bf16_pair(z, 0.0f);
-    }
-    return;
-  }
-  auto add_bf16 = [&](const uint16_t* p) {
+// Eight values of BF16 (FP32) elements from p on, of which n are there
+__device__ __forceinline__ void epilogue_load8(const uint16_t* p, int n, float* v) {
+  if (n >= 8) {
     const mx_u32x4_any2_t u = *reinterpret_cast<const mx_u32x4_any2_t*>(p);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      v[2 * r] += bf16_to_f32(u[r] & 0xFFFFu);
-      v[2 * r + 1] += __uint_as_float(u[r] & 0xFFFF0000u);
-    }
-  };
-  if (a.bias) add_bf16(a.bias + col);
-  const int act = a.aux >> kMxActShift;
-  if (act != kActNone) {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] = activate(act, v[r]);
-  }
-  if (a.residual) {
-    const int64_t at = row * a.ldr + col;
-    if (a.aux & kMxResF32) {
-      const float* p = static_cast<const float*>(a.residual) + at;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const mx_float4_any4_t u = *reinterpret_cast<const mx_float4_any4_t*>(p + 4 * q);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[4 * q + r] += u[r];
-      }
-    } else {
-      add_bf16(static_cast<const uint16_t*>(a.residual) + at);
-    }
-  }
-  if (a.aux & kMxOutF32) {
-    float* p = static_cast<float*>(a.out) + row * a.ldo + col;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const mx_float4_any4_t u = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-      __builtin_nontemporal_store(u, reinterpret_cast<mx_float4_any4_t*>(p + 4 * q));  // see store16_streaming
+      v[2 * r] = bf16_to_f32(u[r] & 0xFFFFu);
+      v[2 * r + 1] = __uint_as_float(u[r] & 0xFFFF0000u);
     }
   } else {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] = r < n ? bf16_to_f32(p[r]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void epilogue_load8(const float* p, int n, float* v) {
+  if (n >= 8) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const mx_float4_any4_t u = *reinterpret_cast<const mx_float4_any4_t*>(p + 4 * q);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[4 * q + r] = u[r];
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] = r < n ? p[r] : 0.0f;
+  }
+}
+__device__ __forceinline__ void epilogue_residual8(const MxArgs& a, int64_t row, int col, float* v) {
+  const int64_t at = row * a.ldr + col;
+  if (a.aux & kMxResF32) epilogue_load8(static_cast<const float*>(a.residual) + at, a.N - col, v);
+  else epilogue_load8(static_cast<const uint16_t*>(a.residual) + at, a.N - col, v);
+}
+// Columns col .. col + 7 of row `row`, those that there are
+__device__ __forceinline__ void epilogue_store8(const MxArgs& a, int64_t row, int col, const float* v) {
+  const int64_t at = row * a.ldo + col;
+  if (a.aux & kMxOutF32) {
+    float* p = static_cast<float*>(a.out) + at;
+    if (col + 8 <= a.N) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const mx_float4_any4_t u = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        __builtin_nontemporal_store(u, reinterpret_cast<mx_float4_any4_t*>(p + 4 * q));  // see store16_streaming
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (col + r < a.N) p[r] = v[r];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(a.out) + at;
     const mx_u32x4_any2_t u = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
-    __builtin_nontemporal_store(u, reinterpret_cast<mx_u32x4_any2_t*>(static_cast<uint16_t*>(a.out) + row * a.ldo + col));
+    if (col + 8 <= a.N) {
+      __builtin_nontemporal_store(u, reinterpret_cast<mx_u32x4_any2_t*>(p));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (col + r < a.N) p[r] = (uint16_t)(u[r >> 1] >> (16 * (r & 1)));
+    }
   }
 }
 
 }  // namespace
-
-// Streaming product: few tokens per weight row, so the weights' bytes bound it.
-// A workgroup takes R groups of 32 weight rows (gate_up: a gate group and the
-// up group of the same h columns) and tiles of 32 tokens; its NW waves split
-// the columns and load their fragments straight from memory to registers (a
-// packed fragment is one contiguous kilobyte), and the partial sums meet in LDS
-// in a fixed order.  One token, 6144 x 6144: 4.6 to 5.2 us, of which a launch
-// takes about 2; 8 waves on 1 row group where 4 waves on 2 take 10.4 (too few
-// workgroups), 16 waves or loads two groups ahead as many.  Token groups past
-// the first would cost more here than in a tile: a lane's 16 bytes of x come
-// from 32 different rows.
-//
-// 8-bit activations go in as two operands (see mx8_mfma).  HALF: at most 16
-// tokens, so both fit the 32 columns of one: column n takes the large elements of
-// token n % 16 if n < 16 and the rest if not, and the two columns' sums are added
-// at the end.
-template <int MODE, int R, int NW, bool A8, bool HALF = false>
-__global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
-  static_assert(!HALF || (A8 && MODE == kLinear), "of the dense product");
-  constexpr int kGroup = A8 ? 256 : 128;  // bytes of a column group of an activation row
-  __shared__ float4 part[NW][R][4 * 68];  // strides 68 and 34: 16 lanes of a reader take 16 different slots
-  __shared__ uint32_t hmax[NW][32];
-  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, n = l & 31, f = l >> 5;
-  const int e = MODE == kLinear ? 0 : blockIdx.y;
-  const int KK = (int)a.KK;
-  int64_t lo = 0, hi = a.T;
-  if (MODE != kLinear) {
-    lo = a.offsets[e];
-    hi = a.offsets[e + 1];
-  }
-  const uint8_t* wc[R];
-  const uint8_t* ws[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int g = MODE == kGateUp ? (int)blockIdx.x + i * (a.G / 2) : min((int)blockIdx.x * R + i, a.G - 1);
-    wc[i] = a.w_codes + ((int64_t)e * a.G + g) * a.KK * kMxFragCodes;
-    ws[i] = a.w_scales + ((int64_t)e * a.G + g) * a.KK * kMxFragScales;
-  }
-
-  for (int64_t t0 = lo + (MODE == kLinear ? (int64_t)blockIdx.y * 32 : 0); t0 < hi; t0 += 32) {
-    const int cnt = (int)min((int64_t)32, hi - t0);
-    const int64_t pos = t0 + min(HALF ? n & 15 : n, cnt - 1);  // lanes past the last token repeat it
-    const int64_t arow = MODE == kGateUp ? a.sorted[pos] / a.aux : pos;
-    const uint8_t* xc = a.a_codes + arow * (a.KK * kGroup) + f * (A8 ? 16 : 64);
-    const uint8_t* xs = a.a_scales + arow * (a.KK * 8) + f * 4;
-    // thread (tok, p) of the epilogue: features 4 p .. 4 p + 3 of one token; what it needs of the pair
-    // is loaded here, under the products (two latencies less: down of a small layer 4.7 us, not 5.7)
-    const int tok = tid >> 3, p = tid & 7;
-    int pair = 0, wmax = 0;
-    float wp = 0.0f;
-    if constexpr (MODE == kDown) {
-      pair = a.sorted[t0 + min(tok, cnt - 1)];
-      wp = a.topk_w[pair];
-      wmax = a.w_max[e];
-    }
-    float16_t acc[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
-    uint32_t bh = 0;
-    for (int64_t c = w; c < KK; c += NW) {
-      // the activations first: they come from a cache, and their operands are made while the weights arrive
-      typename ActFrag<A8>::type xf[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if constexpr (A8)
-          xf[s] = join_halves(*reinterpret_cast<const i32x4_t*>(xc + c * kGroup + 32 * s),
-                              *reinterpret_cast<const i32x4_t*>(xc + c * kGroup + 128 + 32 * s));
-        else xf[s] = reinterpret_cast<const i32x4_t*>(xc + c * kGroup)[s];
-      }
-      const int sx = *reinterpret_cast<const int*>(xs + c * 8);
-      i32x4_t wf[R][4];
-      int sw[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) wf[i][s] = reinterpret_cast<const i32x4_t*>(wc[i] + c * kMxFragCodes)[s * 64 + l];
-        sw[i] = reinterpret_cast<const int*>(ws[i] + c * kMxFragScales)[l];
-      }
-      if constexpr (HALF) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) xf[s] = mx8_part(xf[s], n >= 16);
-      }
-      if (MODE == kDown) bh = max(bh, max_byte((uint32_t)sx));
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        acc[i] = act_mfma<0, !HALF>(wf[i][0], xf[0], acc[i], sw[i], sx);
-        acc[i] = act_mfma<1, !HALF>(wf[i][1], xf[1], acc[i], sw[i], sx);
-        acc[i] = act_mfma<2, !HALF>(wf[i][2], xf[2], acc[i], sw[i], sx);
-        acc[i] = act_mfma<3, !HALF>(wf[i][3], xf[3], acc[i], sw[i], sx);
-      }
-    }
-    if (MODE == kDown) {
-      bh = max(bh, (uint32_t)__shfl_xor((int)bh, 32));
-      if (f == 0) hmax[w][n] = bh;
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        part[w][i][q * 68 + f * 34 + n] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
-    __syncthreads();
-    if (tid < 256 && tok < cnt) {
-      float v[R][4];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float4 s = part[0][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
-#pragma unroll
-        for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
-          const float4 u = part[k % NW][i][(p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
-          s.x += u.x;
-          s.y += u.y;
-          s.z += u.z;
-          s.w += u.w;
-        }
-        v[i][0] = s.x;
-        v[i][1] = s.y;
-        v[i][2] = s.z;
-        v[i][3] = s.w;
-      }
-      const int64_t row = t0 + tok;
-      if constexpr (MODE == kGateUp) {
-        float h[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          h[q] = silu(v[0][q]) * v[1][q];
-          m = max(m, abs_bits(h[q]));
-        }
-        m = quad_max(m);
-        m = max(m, lane_dpp<kLaneHalfMirror>(m));
-        const uint32_t byte = A8 ? mx8_scale_byte(m) : mx_scale_byte(m);
-        const int64_t blk = blockIdx.x;
-        uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.ldo;
-        if constexpr (A8) reinterpret_cast<uint32_t*>(out)[blk * 8 + p] = mx8_encode4(h, byte);
-        else reinterpret_cast<uint16_t*>(out)[blk * 8 + p] = (uint16_t)mx_encode8(h, byte);
-        if (p == 0) static_cast<uint8_t*>(a.out_scales)[row * (a.ldo / (A8 ? 32 : 16)) + blk] = (uint8_t)byte;
-        if (blk == 0) zero_h_pad<A8>(a, row, p, 8);
-      } else {
-        float factor = 1.0f;
-        int64_t out = row;
-        if constexpr (MODE == kDown) {
-          out = pair;
-          uint32_t b = hmax[0][tok];
-#pragma unroll
-          for (int k = 1; k < NW; ++k) b = max(b, hmax[k][tok]);
-          if (wmax == 255) wmax = finite_scale_max<8>(a, e, p);  // by the whole wave under the products: 0.2 us more
-          const int E = pair_exponent(wp, b, wmax, a.aux);
-          factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
-          if (blockIdx.x == 0 && p == 0) static_cast<float*>(a.out_scales)[out] = __uint_as_float((uint32_t)(127 + E) << 23);
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const int col = ((int)blockIdx.x * R + i) * 32 + 4 * p;
-          if (MODE == kDown) {  // N % 32 == 0 and the rows are aligned
-            if (col < a.N)
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out * a.ldo + col) =
-                  make_uint2(f16_pair(factor * v[i][0], factor * v[i][1]), f16_pair(factor * v[i][2], factor * v[i][3]));
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (col + q >= a.N) break;
-              if constexpr (A8) v[i][q] = epilogue1(a, v[i][q], out, col + q);
-              if (a.aux & kMxOutF32) static_cast<float*>(a.out)[out * a.ldo + col + q] = v[i][q];
-              else static_cast<uint16_t*>(a.out)[out * a.ldo + col + q] = (uint16_t)bf16_pair(v[i][q], 0.0f);
-            }
-          }
-        }
-      }
-    }
-    if (MODE == kLinear) break;
-    __syncthreads();
-  }
-}
 
 // Tiled product: four waves share a tile of kSlots * 32 weight rows by kTok
 // tokens through LDS.  A stage is half a column group (128 columns, two MFMA
@@ -729,11 +561,23 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     constexpr int JP = S::kWX * GX * 32 * kRow * 4 <= S::kLds ? GX : GX / 2;
     static_assert(S::kWX * JP * 32 * kRow * 4 <= S::kLds && GX % JP == 0, "a pass fits the ring");
     constexpr int kLanes = kCols / 8, kRows = NW * 64 / kLanes;
-    const int c8 = tid % kLanes * 8, col = wt * kCols + c8;
+    constexpr int kAll = S::kWX * JP * 32, kAhead = kAll / kRows < 4 ? kAll / kRows : 4;  // rows of a pass; rows a thread takes at a time
+    static_assert(kAll % (kRows * kAhead) == 0, "whole steps");
+    const int c8 = tid % kLanes * 8, col = wt * kCols + c8, act = a.aux >> kMxActShift;
     float* tile = reinterpret_cast<float*>(smem);
+    float bias[8];
+    if (a.bias && col < a.N) epilogue_load8(a.bias + col, a.N - col, bias);
 #pragma unroll
     for (int j0 = 0; j0 < GX; j0 += JP) {
+      auto token = [&](int r) { return (r / (32 * JP) * GX + j0) * 32 + r % (32 * JP); };
+      float res[kAhead][8];
+      auto load = [&](int r0) {  // residuals of rows r0, r0 + kRows, ...
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (a.residual && col < a.N && token(r0 + k * kRows) < cnt) epilogue_residual8(a, first + token(r0 + k * kRows), col, res[k]);
+      };
       if (j0 > 0) barrier_after_lds();
+      load(tid / kLanes);  // the first ones under the way through LDS
 #pragma unroll
       for (int j = 0; j < JP; ++j)
 #pragma unroll
@@ -746,12 +590,28 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
       barrier_after_lds();
       if (col < a.N) {
 #pragma unroll 1
-        for (int r = tid / kLanes; r < S::kWX * JP * 32; r += kRows) {
-          const int tok = (r / (32 * JP) * GX + j0) * 32 + r % (32 * JP);
-          if (tok >= cnt) continue;
-          const float4 u = *reinterpret_cast<const float4*>(tile + r * kRow + c8), w4 = *reinterpret_cast<const float4*>(tile + r * kRow + c8 + 4);
-          float v[8] = {u.x, u.y, u.z, u.w, w4.x, w4.y, w4.z, w4.w};
-          epilogue8(a, v, first + tok, col);
+        for (int r0 = tid / kLanes; r0 < kAll; r0 += kRows * kAhead) {
+          if (r0 >= kRows) load(r0);
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int r = r0 + k * kRows, tok = token(r);
+            if (tok >= cnt) continue;
+            const float4 u = *reinterpret_cast<const float4*>(tile + r * kRow + c8), w4 = *reinterpret_cast<const float4*>(tile + r * kRow + c8 + 4);
+            float v[8] = {u.x, u.y, u.z, u.w, w4.x, w4.y, w4.z, w4.w};
+            if (a.bias) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[q] += bias[q];
+            }
+            if (act != kActNone) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[q] = activate(act, v[q]);
+            }
+            if (a.residual) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[q] += res[k][q];
+            }
+            epilogue_store8(a, first + tok, col, v);
+          }
         }
       }
     }
@@ -867,16 +727,6 @@ hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
   const int64_t rows = MODE == kGateUp ? a.G / 2 : a.G, per = MODE == kGateUp ? S::kSlots / 2 : S::kSlots;
   const int64_t grid = (max_mtiles * ((rows + per - 1) / per) + 7) / 8 * 8;
   return launch_kernel(k, dim3((unsigned)grid), dim3(64 * S::kWaves), S::kLds, st, a);
-}
-
-template <int MODE, bool A8, bool HALF = false>
-hipError_t launch_stream(const MxArgs& a, int64_t E, hipStream_t st) {
-  if constexpr (MODE == kLinear)
-    return launch_kernel(mx_stream_kernel<MODE, 1, 8, A8, HALF>, dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512),
-                         0, st, a);
-  else
-    return launch_kernel(mx_stream_kernel<MODE, 2, 4, A8>, dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st,
-                         a);
 }
 
 enum Shape { kStream, k128x64, k128x128, k256x64, k256x128, k256x256 };

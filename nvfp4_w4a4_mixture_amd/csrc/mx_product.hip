@@ -1,9 +1,172 @@
-// Products of MXFP4 activations: their shapes, by sizes.
+// Products of MXFP4 activations: the streaming kernel, and the shapes by sizes.
 #include "mx_product.h"
 
 namespace moe {
 
+// Streaming product: few tokens per weight row, so the weights' bytes bound it.
+// A workgroup takes R groups of 32 weight rows (gate_up: a gate group and the
+// up group of the same h columns) and tiles of 32 tokens; its NW waves split
+// the columns and load their fragments straight from memory to registers (a
+// packed fragment is one contiguous kilobyte), and the partial sums meet in LDS
+// in a fixed order.  One token, 6144 x 6144: 4.6 to 5.2 us, of which a launch
+// takes about 2; 8 waves on 1 row group where 4 waves on 2 take 10.4 (too few
+// workgroups), 16 waves or loads two groups ahead as many.  Token groups past
+// the first would cost more here than in a tile: a lane's 16 bytes of x come
+// from 32 different rows.
+template <int MODE, int R, int NW>
+__global__ __launch_bounds__(NW * 64) void mx_stream_kernel(MxArgs a) {
+  __shared__ float4 part[NW][R][4 * 68];  // strides 68 and 34: 16 lanes of a reader take 16 different slots
+  __shared__ uint32_t hmax[NW][32];
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, n = l & 31, f = l >> 5;
+  const int e = MODE == kLinear ? 0 : blockIdx.y;
+  const int KK = (int)a.KK;
+  int64_t lo = 0, hi = a.T;
+  if (MODE != kLinear) {
+    lo = a.offsets[e];
+    hi = a.offsets[e + 1];
+  }
+  const uint8_t* wc[R];
+  const uint8_t* ws[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int g = MODE == kGateUp ? (int)blockIdx.x + i * (a.G / 2) : min((int)blockIdx.x * R + i, a.G - 1);
+    wc[i] = a.w_codes + ((int64_t)e * a.G + g) * a.KK * kMxFragCodes;
+    ws[i] = a.w_scales + ((int64_t)e * a.G + g) * a.KK * kMxFragScales;
+  }
+
+  for (int64_t t0 = lo + (MODE == kLinear ? (int64_t)blockIdx.y * 32 : 0); t0 < hi; t0 += 32) {
+    const int cnt = (int)min((int64_t)32, hi - t0);
+    const int64_t pos = t0 + min(n, cnt - 1);  // lanes past the last token repeat it
+    const int64_t arow = MODE == kGateUp ? a.sorted[pos] / a.aux : pos;
+    const uint8_t* xc = a.a_codes + arow * (a.KK * 128) + f * 64;
+    const uint8_t* xs = a.a_scales + arow * (a.KK * 8) + f * 4;
+    // thread (tok, p) of the epilogue: features 4 p .. 4 p + 3 of one token; what it needs of the pair
+    // is loaded here, under the products (two latencies less: down of a small layer 4.7 us, not 5.7)
+    const int tok = tid >> 3, p = tid & 7;
+    int pair = 0, wmax = 0;
+    float wp = 0.0f;
+    if constexpr (MODE == kDown) {
+      pair = a.sorted[t0 + min(tok, cnt - 1)];
+      wp = a.topk_w[pair];
+      wmax = a.w_max[e];
+    }
+    float16_t acc[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+    uint32_t bh = 0;
+    for (int64_t c = w; c < KK; c += NW) {
+      i32x4_t wf[R][4], xf[4];
+      int sw[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) wf[i][s] = reinterpret_cast<const i32x4_t*>(wc[i] + c * kMxFragCodes)[s * 64 + l];
+        sw[i] = reinterpret_cast<const int*>(ws[i] + c * kMxFragScales)[l];
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) xf[s] = reinterpret_cast<const i32x4_t*>(xc + c * 128)[s];
+      const int sx = *reinterpret_cast<const int*>(xs + c * 8);
+      if (MODE == kDown) bh = max(bh, max_byte((uint32_t)sx));
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        acc[i] = mx_mfma<0>(wf[i][0], xf[0], acc[i], sw[i], sx);
+        acc[i] = mx_mfma<1>(wf[i][1], xf[1], acc[i], sw[i], sx);
+        acc[i] = mx_mfma<2>(wf[i][2], xf[2], acc[i], sw[i], sx);
+        acc[i] = mx_mfma<3>(wf[i][3], xf[3], acc[i], sw[i], sx);
+      }
+    }
+    if (MODE == kDown) {
+      bh = max(bh, (uint32_t)__shfl_xor((int)bh, 32));
+      if (f == 0) hmax[w][n] = bh;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        part[w][i][q * 68 + f * 34 + n] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
+    __syncthreads();
+    if (tid < 256 && tok < cnt) {
+      float v[R][4];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float4 s = part[0][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) {
+          const float4 u = part[k][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
+          s.x += u.x;
+          s.y += u.y;
+          s.z += u.z;
+          s.w += u.w;
+        }
+        v[i][0] = s.x;
+        v[i][1] = s.y;
+        v[i][2] = s.z;
+        v[i][3] = s.w;
+      }
+      const int64_t row = t0 + tok;
+      if constexpr (MODE == kGateUp) {
+        float h[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h[q] = silu(v[0][q]) * v[1][q];
+          m = max(m, abs_bits(h[q]));
+        }
+        m = quad_max(m);
+        m = max(m, lane_dpp<kLaneHalfMirror>(m));
+        const uint32_t byte = mx_scale_byte(m);
+        const int64_t blk = blockIdx.x;
+        reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + row * a.ldo)[blk * 8 + p] = (uint16_t)mx_encode8(h, byte);
+        if (p == 0) static_cast<uint8_t*>(a.out_scales)[row * (a.ldo / 16) + blk] = (uint8_t)byte;
+        if (blk == 0) zero_h_pad<false>(a, row, p, 8);
+      } else {
+        float factor = 1.0f;
+        int64_t out = row;
+        if constexpr (MODE == kDown) {
+          out = pair;
+          uint32_t b = hmax[0][tok];
+#pragma unroll
+          for (int k = 1; k < NW; ++k) b = max(b, hmax[k][tok]);
+          if (wmax == 255) wmax = finite_scale_max<8>(a, e, p);  // by the whole wave under the products: 0.2 us more
+          const int E = pair_exponent(wp, b, wmax, a.aux);
+          factor = wp * __uint_as_float((uint32_t)(127 - E) << 23);  // exact
+          if (blockIdx.x == 0 && p == 0) static_cast<float*>(a.out_scales)[out] = __uint_as_float((uint32_t)(127 + E) << 23);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int col = ((int)blockIdx.x * R + i) * 32 + 4 * p;
+          if (MODE == kDown) {  // N % 32 == 0 and the rows are aligned
+            if (col < a.N)
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out * a.ldo + col) =
+                  make_uint2(f16_pair(factor * v[i][0], factor * v[i][1]), f16_pair(factor * v[i][2], factor * v[i][3]));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (col + q >= a.N) break;
+              if (a.aux & kMxOutF32) static_cast<float*>(a.out)[out * a.ldo + col + q] = v[i][q];
+              else static_cast<uint16_t*>(a.out)[out * a.ldo + col + q] = (uint16_t)bf16_pair(v[i][q], 0.0f);
+            }
+          }
+        }
+      }
+    }
+    if (MODE == kLinear) break;
+    __syncthreads();
+  }
+}
+
 namespace {
+
+template <int MODE>
+hipError_t launch_stream(const MxArgs& a, int64_t E, hipStream_t st) {
+  if constexpr (MODE == kLinear)
+    return launch_kernel(mx_stream_kernel<MODE, 1, 8>, dim3((unsigned)a.G, (unsigned)((a.T + 31) / 32)), dim3(512), 0, st,
+                         a);
+  else
+    return launch_kernel(mx_stream_kernel<MODE, 2, 4>, dim3((unsigned)((a.G + 1) / 2), (unsigned)E), dim3(256), 0, st, a);
+}
 
 // Weight rows by tokens.  The small tiles serve few tokens per expert, whose
 // bound is the weight stream, and grids too small for the large ones: at 256 x
@@ -67,7 +230,7 @@ template <int MODE>
 hipError_t launch_experts_stage(const MxArgs& a, Shape s, const MxExperts& x, hipStream_t st) {
   const int64_t mtiles = most_mtiles(x.T * x.k, x.E, shape_tokens(s));
   switch (s) {
-    case kStream: return launch_stream<MODE, false>(a, x.E, st);
+    case kStream: return launch_stream<MODE>(a, x.E, st);
     case k128x64: return launch_tiled<MODE, Mx128x64>(a, mtiles, st);
     case k256x256: return launch_tiled<MODE, Mx256x256>(a, mtiles, st);
     default: return launch_tiled<MODE, Mx256x128>(a, mtiles, st);
@@ -79,7 +242,7 @@ hipError_t launch_experts_stage(const MxArgs& a, Shape s, const MxExperts& x, hi
 hipError_t launch_mx_linear(const MxArgs& a, hipStream_t st) {
   const int64_t T = a.T;
   switch (linear_shape(T, a.G, a.KK)) {
-    case kStream: return launch_stream<kLinear, false>(a, 1, st);
+    case kStream: return launch_stream<kLinear>(a, 1, st);
     case k128x64: return launch_tiled<kLinear, Mx128x64>(a, (T + 63) / 64, st);
     case k128x128: return launch_tiled<kLinear, Mx128x128>(a, (T + 127) / 128, st);
     case k256x128: return launch_tiled<kLinear, Mx256x128>(a, (T + 127) / 128, st);

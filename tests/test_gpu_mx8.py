@@ -11,7 +11,10 @@ Products are checked element by element, u = 2^-24 (FP32):
   from the hardware's exponential and reciprocal on a rounded argument, are (8 + 4 |z| + 4 |z|^3) 2 u |act(z)| (the cube for
   the tanh form's argument) or, by erf, 4 u |z|;
 * h = silu(g) u known to delta (as for MXFP4) may move by mx8.grid_reach(h, delta);
-* a pair row is FP16 under a power of two: 2^-11 of the value, or half a subnormal step, 2^(E - 25).
+* a pair row is FP16 under a power of two: 2^-11 of the value, or half a subnormal step, 2^(E - 25).  In the 2-norm:
+  g and u are off by some d = 1e-5 of their size (the dropped products), h by sqrt(2) d; an element of h then rounds to
+  the other side with probability 0.8 sqrt(2) d / s for E4M3's spacing s (2^-3 to 2^-4 of the value), by s, so q(h) and f
+  are off by sqrt(0.8 sqrt(2) d s) = 1e-3, beside 2.1e-4 for FP16; twice that is allowed;
 BF16 results add half an ulp, 2^-8 of the value; in the 2-norm that is at most 2^-8 / sqrt(3) = 2.3e-3."""
 
 import math
@@ -401,7 +404,7 @@ def test_experts(ops, T, E, k, H, I, kind):
         worst = max(worst, float(np.max(np.abs(got[p] - ref) / bound)))
         off, norm = off + float(((got[p] - ref) ** 2).sum()), norm + float((ref ** 2).sum())
     print(f"  error / bound {worst:.3f}, rel-L2 {(off / norm) ** 0.5:.2e}", flush=True)
-    assert worst <= 1.0 and (off / norm) ** 0.5 <= 1e-3
+    assert worst <= 1.0 and (off / norm) ** 0.5 <= 2e-3
 
 
 @pytest.mark.parametrize("T", [2, 200])

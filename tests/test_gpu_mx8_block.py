@@ -59,7 +59,7 @@ def test_block_steps(mods, T, post):
             z = xq[t] @ matrix(blk.w13, e, 2 * I, H).T
             f = mx8.rounded(mx.silu(z[:, :I]) * z[:, I:]) @ matrix(blk.w2, e, H, I).T
             np.add.at(y, t, f * w[t, j][:, None])
-    assert rel_l2(values(out.y), y) < 1e-3  # FP16 pair rows, and the odd h that rounds the other way
+    assert rel_l2(values(out.y), y) < 2e-3  # FP16 pair rows, and the odd h that rounds the other way (see test_gpu_mx8.py)
     r2 = onorm.residual(values(out.y), values(b["r1"]), values(blk.norms[2]), values(blk.gate), blk.residual_scale, blk.eps)
     assert half(values(out.residual), r2)
     c, s = ops.mxfp8_quantize(out.n)

@@ -102,7 +102,8 @@ def test_layer_is_its_operators(ops, T, E, k, H, I):
     po, ps = ops.mxfp8_grouped_ffn(*ops.mxfp8_quantize(d["x"]), *d["w13"], *d["w2"], H, I, k, r.expert_offsets,
                                    r.sorted_pair_ids, r.topk_w)
     want = f64(ops.moe_combine(po, ps, T, k, torch.float32))
-    assert np.linalg.norm(f64(y) - want) <= 5e-4 * np.linalg.norm(want)
+    # q(h) of the tiled product is off by 1e-3 at most twice over (tests/test_gpu_mx8.py), that of the layer by far less
+    assert np.linalg.norm(f64(y) - want) <= 2e-3 * np.linalg.norm(want)
 
 
 def test_layer_strided_and_unaligned_rows(ops):
