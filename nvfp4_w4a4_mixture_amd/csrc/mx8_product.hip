@@ -36,10 +36,11 @@ __global__ __launch_bounds__(512) void mx8_stream_kernel(MxArgs a) {
     i32x4_t x[kParts], w[4];
     int sw, sx;
   };
+  // No branch stands before a load, so that the compiler can count those in flight (with one it waits for all of them)
   auto load = [&](int64_t c, Cols& d) {
+    c = min(c, (int64_t)KK - 1);
 #pragma unroll
-    for (int i = 0; i < kParts; ++i)
-      if (4 * i < cnt) d.x[i] = *reinterpret_cast<const i32x4_t*>(a.a_codes + c * 256 + xoff[i]);
+    for (int i = 0; i < kParts; ++i) d.x[i] = *reinterpret_cast<const i32x4_t*>(a.a_codes + c * 256 + xoff[i]);
     d.sx = *reinterpret_cast<const int*>(xs + c * 8);
 #pragma unroll
     for (int s = 0; s < 4; ++s) d.w[s] = reinterpret_cast<const i32x4_t*>(wc + c * kMxFragCodes)[s * 64 + l];
@@ -52,10 +53,10 @@ __global__ __launch_bounds__(512) void mx8_stream_kernel(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
       const int r = 4 * i + (l >> 4);
-      if (4 * i < cnt) *reinterpret_cast<i32x4_t*>(staged + r * 256 + (((l & 15) ^ r) & 15) * 16) = d.x[i];
+      *reinterpret_cast<i32x4_t*>(staged + r * 256 + (((l & 15) ^ r) & 15) * 16) = d.x[i];
     }
     wave_lds_order();
-    i32x8_t xf[4];  // of columns past the last token: whatever was there, and their sums are not written
+    i32x8_t xf[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       xf[s] = join_halves(*reinterpret_cast<const i32x4_t*>(staged + tok_n * 256 + (((2 * s + f) ^ tok_n) & 15) * 16),
@@ -69,14 +70,13 @@ __global__ __launch_bounds__(512) void mx8_stream_kernel(MxArgs a) {
     acc = act_mfma<3, !HALF>(d.w[3], xf[3], acc, d.sw, d.sx);
   };
   Cols d0, d1;
-  if (w < KK) load(w, d0);
+  load(w, d0);
   for (int c = w; c < KK; c += 2 * NW) {
-    if (c + NW < KK) load(c + NW, d1);
+    load(c + NW, d1);
     multiply(d0);
-    if (c + NW < KK) {
-      if (c + 2 * NW < KK) load(c + 2 * NW, d0);
-      multiply(d1);
-    }
+    if (c + NW >= KK) break;
+    load(c + 2 * NW, d0);
+    multiply(d1);
   }
   __syncthreads();  // the waves' sums take the place of their columns
   float4* part = reinterpret_cast<float4*>(smem);  // [NW][4 * 68]

@@ -160,15 +160,16 @@ __device__ __forceinline__ float16_t mx_mfma(i32x4_t a, i32x4_t b, float16_t c, 
 // whose elements each span 9 binades (the exponent's upper bit tells which), and
 // all that is left is the rounding of the FP32 accumulator (3e-8 and 1e-7), for
 // twice the matrix instructions.
+__device__ __forceinline__ uint32_t mx8_large_mask(uint32_t d) {  // bytes with that bit, whole
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  const u16x2_t bit = __builtin_bit_cast(u16x2_t, (d >> 6) & 0x01010101u);
+  return __builtin_bit_cast(uint32_t, bit * u16x2_t{255, 255});
+}
 __device__ __forceinline__ i32x8_t mx8_part(i32x8_t b, bool rest) {
-  const int flip = rest ? -1 : 0;
+  const uint32_t flip = rest ? ~0u : 0u;
   i32x8_t r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-    const u16x2_t bit = __builtin_bit_cast(u16x2_t, ((uint32_t)b[i] >> 6) & 0x01010101u);
-    r[i] = b[i] & (__builtin_bit_cast(int, bit * u16x2_t{255, 255}) ^ flip);  // bytes with that bit, whole, or those without
-  }
+  for (int i = 0; i < 8; ++i) r[i] = (int)((uint32_t)b[i] & (mx8_large_mask((uint32_t)b[i]) ^ flip));
   return r;
 }
 template <int S>

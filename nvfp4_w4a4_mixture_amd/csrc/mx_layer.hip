@@ -1,6 +1,6 @@
 // The whole routed-expert layer for up to 32 tokens, in three kernels: the
 // router's scores with the quantisation of x; gate_up with the selection; down
-// with the combine.
+// with the combine.  With many scores a fourth, before gate_up, ranks them.
 //
 //   z[t, e] = x[t] . W_r[e] in FP64, s = sigmoid(z)
 //   the k experts of a token: largest s + bias first, ties to the lower index
@@ -9,10 +9,9 @@
 //
 // With so few tokens the touched experts' weights bound it (and launches, where
 // the layer is small), so the tokens are the 32 columns of one MFMA tile whatever
-// they chose: no permutation of pairs is needed, columns that did not choose an
-// expert are multiplied as zeros and left out of the sums, and the sum over the
-// experts stays in FP32 accumulators, in the order of the experts.  A kernel's
-// end is the only synchronisation; no atomics decide an order.
+// they chose: no permutation of pairs is needed, columns of tokens that did not
+// choose an expert are left out of its results, and the sum over the experts stays
+// in FP32 accumulators, in a fixed order.  No atomic decides an order.
 #include "launch.h"
 #include "mx_common.h"
 #include "mx_product.h"
@@ -23,12 +22,33 @@ namespace {
 
 constexpr int kScoreThreads = 256;
 constexpr int kMaxTok = (int)kLayerMaxTokens;
-constexpr int kSparse = 512;  // scores that a workgroup of the sparse gate_up ranks
+constexpr int kMaxParts = 4;
+constexpr int64_t kRankWork = 1 << 16;  // comparisons past which the ranking is a kernel of its own
+constexpr int kRankScores = 1448;       // the most scores of no more: T * E <= sqrt(32 * kRankWork)
+
+// Workgroups that share 32 features of y: as many as leave each a CU, and each of
+// its waves four column groups of products.  With one workgroup H = 2048 used 64 of
+// 256 CUs: 32 tokens of 64 experts, I = 1408: 52.5 us in one, 40.3 in four; 16 of
+// 256, H = 4096, I = 1024: 60.8 and 55.4 in two; with two column groups a wave it
+// loses (1 of 256: 24.7 and 25.3).
+__host__ __device__ inline int64_t down_parts(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
+  const int64_t items = (T * k < E ? T * k : E) * ((I + 255) / 256), cus = 256 / (H / 32), n = items / 32 < cus ? items / 32 : cus;
+  return n < 1 ? 1 : n > kMaxParts ? kMaxParts : n;
+}
 
 // Everything between the kernels: keys (the order of the scores) and sigmoids of
-// all experts, the chosen sigmoids by slot, x and h in MXFP8.
+// all experts, the chosen sigmoids by slot, all experts' ranks, x and h in MXFP8,
+// the parts' sums and their counts.  Up to 16 tokens x and h are kept as the two
+// operands that they are multiplied as (see mx8_part), the large elements and the
+// rest, which are the halves of one operand's 32 columns: one instruction
+// multiplies both.  Past 16 they are kept whole and parted at the product (kept as
+// two, 32 tokens of 80 experts took 205 us instead of 170: twice the bytes of x
+// through the L1, which every tile reads anew).
+// x lies in the order of the fragments, [operand, KK, step, block of two, half,
+// column, 16] and scale bytes [KK, half, column, 4], so that a load of a wave is a
+// whole run; h in rows, of which a wave reads the few that chose its expert.
 struct LayerWs {
-  size_t key, sig, chosen, x_codes, x_scales, h_codes, h_scales, total;
+  size_t key, sig, chosen, slot, x_codes, x_scales, h_codes, h_scales, parts, arrived, total;
   __host__ __device__ LayerWs(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
     const size_t Hp = (size_t)((H + 255) / 256 * 256), Ip = (size_t)((I + 255) / 256 * 256), t = (size_t)T, p = t * (size_t)k;
     size_t o = 0;
@@ -40,10 +60,14 @@ struct LayerWs {
     key = take(t * (size_t)E * 8);
     sig = take(t * (size_t)E * 8);
     chosen = take(p * 8);
-    x_codes = take(t * Hp);
-    x_scales = take(t * Hp / 32);
-    h_codes = take(p * Ip);
+    slot = take(t * (size_t)E * 2);
+    x_codes = take(Hp * 32);
+    x_scales = take(Hp);
+    h_codes = take(p * Ip * (T <= 16 ? 2 : 1));
     h_scales = take(p * Ip / 32);
+    const size_t n = (size_t)down_parts(T, E, k, H, I), groups = (size_t)(H / 32);
+    parts = take(n > 1 ? n * groups * kMaxTok * 32 * 4 : 0);
+    arrived = take(n > 1 ? groups * 4 : 0);
     total = o;
   }
 };
@@ -53,6 +77,18 @@ typedef uint32_t u32x4_any2_t __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ u32x4_any2_t load8(const uint16_t* p) { return *reinterpret_cast<const u32x4_any2_t*>(p); }
 __device__ __forceinline__ float element(const u32x4_any2_t& v, int i) {
   return __uint_as_float((i & 1) ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+}
+
+// One step's products.  HALF: the columns hold the large elements and the rest;
+// else the operand is parted here.
+template <int S, bool HALF>
+__device__ __forceinline__ void layer_mfma(const i32x4_t& w, const i32x8_t& x, float16_t& acc, int sw, int sx) {
+  if constexpr (HALF) {
+    acc = mx8_mfma<S>(w, x, acc, sw, sx);
+  } else {
+    acc = mx8_mfma<S>(w, mx8_part(x, false), acc, sw, sx);
+    acc = mx8_mfma<S>(w, mx8_part(x, true), acc, sw, sx);
+  }
 }
 
 }  // namespace
@@ -66,6 +102,9 @@ template <int TT>
 __global__ __launch_bounds__(kScoreThreads) void mx_layer_score_kernel(MxLayerArgs a) {
   const LayerWs ws(a.T, a.E, a.k, a.H, a.I);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  if (down_parts(a.T, a.E, a.k, a.H, a.I) > 1 && blockIdx.y == 0)  // zero before the down kernel counts
+    for (int i = (int)blockIdx.x * kScoreThreads + tid; i < a.H / 32; i += (int)gridDim.x * kScoreThreads)
+      reinterpret_cast<uint32_t*>(a.ws + ws.arrived)[i] = 0;
   if ((int)blockIdx.x >= a.E) {
     const int chunks = (a.H + 255) / 256 * 32;  // of 8 columns, of a padded row
     const int i = (((int)blockIdx.x - a.E) * (int)gridDim.y + (int)blockIdx.y) * kScoreThreads + tid;
@@ -82,8 +121,19 @@ __global__ __launch_bounds__(kScoreThreads) void mx_layer_score_kernel(MxLayerAr
       }
     }
     const uint32_t byte = mx8_scale_byte(quad_max(m));
-    reinterpret_cast<uint2*>(a.ws + ws.x_codes)[i] = make_uint2(mx8_encode4(f, byte), mx8_encode4(f + 4, byte));
-    if ((tid & 3) == 0) (a.ws + ws.x_scales)[i >> 2] = (uint8_t)byte;
+    const int cg = c >> 8, u = (c >> 7) & 1, st = (c >> 5) & 3, half = (c >> 4) & 1;
+    const uint32_t d[2] = {mx8_encode4(f, byte), mx8_encode4(f + 4, byte)};
+    uint8_t* xc = a.ws + ws.x_codes + (int64_t)(((cg * 4 + st) * 2 + u) * 2 + half) * 512 + t * 16 + (c & 15);
+    uint8_t* xs = a.ws + ws.x_scales + ((int64_t)(cg * 2 + u) * 32 + t) * 4 + st;
+    if ((tid & 3) == 0) xs[0] = (uint8_t)byte;
+    if (a.T > 16) {
+      *reinterpret_cast<uint2*>(xc) = make_uint2(d[0], d[1]);
+      return;
+    }
+    const uint32_t large[2] = {d[0] & mx8_large_mask(d[0]), d[1] & mx8_large_mask(d[1])};
+    *reinterpret_cast<uint2*>(xc) = make_uint2(large[0], large[1]);
+    *reinterpret_cast<uint2*>(xc + 256) = make_uint2(d[0] ^ large[0], d[1] ^ large[1]);
+    if ((tid & 3) == 0) xs[64] = (uint8_t)byte;
     return;
   }
   __shared__ double red[kScoreThreads / 64][TT];
@@ -129,182 +179,216 @@ __global__ __launch_bounds__(kScoreThreads) void mx_layer_score_kernel(MxLayerAr
   reinterpret_cast<long long*>(a.ws + ws.key)[at] = score_key(s + (double)a.bias[e]);
 }
 
-// Workgroup (g, i): the 32 h columns of group g of one expert for the tokens that
-// chose it, as mx_stream_kernel's gate_up.  A token chose an expert if fewer than k
-// rank before it, and that number is its slot: found here from the token's keys,
-// so that no kernel stands between the scores and the weights.  SPARSE (few pairs
-// beside the experts): i counts the touched experts, which every workgroup finds
-// from all ranks; else i is the expert, and those that nobody chose end at once.
-// HALF: up to 16 tokens, both operands of a token in one (see mx_stream_kernel).
-template <bool SPARSE, bool HALF>
-__global__ __launch_bounds__(256) void mx_layer_gate_up_kernel(MxLayerArgs a) {
+// The number of experts that come before expert o of a token: of larger key, or of
+// the same and lower index.  The keys' upper halves decide unless two are alike.
+// Lane i of the NL that share an expert takes every NL-th comparison.
+template <int NL>
+__device__ __forceinline__ int rank_of(const int* high, const long long* key, int E, int o, int i) {
+  const int mine = high[o];
+  int r = 0, same = 0;
+#pragma unroll 8
+  for (int q = i; q < E; q += NL) {
+    r += (int)(high[q] > mine);
+    same += (int)(high[q] == mine);
+  }
+#pragma unroll
+  for (int m = 1; m < NL; m *= 2) {
+    r += __shfl_xor(r, m);
+    same += __shfl_xor(same, m);
+  }
+  if (same > 1) {
+    const long long whole = key[o];
+    r = 0;
+    for (int q = 0; q < E; ++q) r += (int)(key[q] > whole) | ((int)(key[q] == whole) & (int)(q < o));
+  }
+  return r;
+}
+
+// Workgroup t ranks token t's experts.
+__global__ __launch_bounds__(1024) void mx_layer_rank_kernel(MxLayerArgs a) {
+  __shared__ int high[256];
+  const LayerWs ws(a.T, a.E, a.k, a.H, a.I);
+  const int tid = threadIdx.x, o = tid >> 2, at = (int)blockIdx.x * a.E;
+  const long long* key = reinterpret_cast<const long long*>(a.ws + ws.key) + at;
+  if (tid < a.E) high[tid] = (int)(key[tid] >> 32);
+  __syncthreads();
+  if (o >= a.E) return;  // whole groups of four lanes
+  const int r = rank_of<4>(high, key, a.E, o, tid & 3);
+  if ((tid & 3) == 0) reinterpret_cast<uint16_t*>(a.ws + ws.slot)[at + o] = (uint16_t)r;
+}
+
+// The 32 h columns of one group of one expert (a tile) for the tokens that chose
+// it, as mx8_stream_kernel.  A token chose an expert if fewer than k rank before
+// it, and that number is its slot: found here from the token's keys, so that no
+// kernel stands between the scores and the weights.
+//
+// Every workgroup lists the touched experts and takes every gridDim.x-th of their
+// tiles, a column group ahead across tiles too.  RANK: it ranks all scores itself,
+// T * E * E comparisons; with many (kRankWork) a kernel before it does: 1 token of
+// 256 experts 24.5 us with the ranking here, 25.8 with the kernel; 16 of 64 49.3
+// and 47.6; 16 of 256 124 (by expert) and 63.
+//
+// Bounds: the weights' bytes.  16 tokens of 80 experts, H = 6144, I = 2048, 28
+// touched: 374 MB in 70 us (5.4 TB/s), after 5 of the ranking (ranked here 76).
+// One token, 8 touched: 20 us (5.4 TB/s).
+template <bool RANK, bool HALF>
+__global__ __launch_bounds__(256, 2) void mx_layer_gate_up_kernel(MxLayerArgs a) {
   constexpr int NW = 4;
   __shared__ float4 part[NW][2][4 * 68];
-  __shared__ int rank[kMaxTok];
+  __shared__ int high[RANK ? kRankScores : 1];
+  __shared__ uint16_t slot[RANK ? kRankScores : kMaxTok * 256], listed[256];
+  __shared__ uint32_t mask[8];
   const LayerWs ws(a.T, a.E, a.k, a.H, a.I);
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, n = l & 31, f = l >> 5;
-  const int blk = blockIdx.x, col_tok = HALF ? n & 15 : n;
+  const int col_tok = HALF ? n & 15 : n, groups = a.I / 32, KK = (a.H + 255) / 256, G = a.I / 16, all = a.T * a.E;
   const long long* key = reinterpret_cast<const long long*>(a.ws + ws.key);
-  if (tid < kMaxTok) rank[tid] = tid < a.T ? 0 : a.E;
-  int e = blockIdx.y;
-  if constexpr (SPARSE) {  // T * E <= kSparse scores
-    __shared__ long long keys[kSparse];
-    __shared__ uint16_t slot[kSparse];
-    __shared__ uint32_t mask[8];
-    if (tid < 8) mask[tid] = 0;
-    for (int i = tid; i < a.T * a.E; i += 256) keys[i] = key[i];
-    __syncthreads();
-    for (int i = tid; i < a.T * a.E; i += 256) {
-      const int t = i / a.E, o = i - t * a.E;
-      const long long mine = keys[i], *row = keys + t * a.E;
-      int r = 0;
-#pragma unroll 8
-      for (int q = 0; q < a.E; ++q) r += (int)(row[q] > mine) | ((int)(row[q] == mine) & (int)(q < o));
-      slot[i] = (uint16_t)r;
-      if (r < a.k) atomicOr(&mask[o >> 5], 1u << (o & 31));
-    }
-    __syncthreads();
-    int left = blockIdx.y;  // of the touched experts below the one sought
-    e = -1;
+  if (tid < 8) mask[tid] = 0;
+  if constexpr (RANK)
+    for (int i = tid; i < all; i += 256) high[i] = (int)(key[i] >> 32);
+  __syncthreads();
+  for (int i = tid; i < all; i += 256) {
+    const int t = i / a.E, o = i - t * a.E;
+    const int r = RANK ? rank_of<1>(high + t * a.E, key + t * a.E, a.E, o, 0) : reinterpret_cast<const uint16_t*>(a.ws + ws.slot)[i];
+    slot[i] = (uint16_t)r;
+    if (r < a.k) atomicOr(&mask[o >> 5], 1u << (o & 31));
+  }
+  __syncthreads();
+  int before = 0, touched = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = mask[i];
-      const int c = __popc(m);
-      if (e < 0 && left < c) {
-        for (; left > 0; --left) m &= m - 1;
-        e = 32 * i + __builtin_ctz(m);
-      }
-      left -= c;
-    }
-    if (e < 0) return;
-    if (tid < a.T) rank[tid] = slot[tid * a.E + e];
-    __syncthreads();
-  } else {
-    __syncthreads();
-    for (int i = tid; i < a.T * a.E; i += 256) {
-      const int t = i / a.E, o = i - t * a.E;
-      const long long mine = key[t * a.E + e], other = key[i];
-      if (other > mine || (other == mine && o < e)) atomicAdd(&rank[t], 1);  // a count: the order does not matter
-    }
-    __syncthreads();
+  for (int i = 0; i < 8; ++i) {
+    if (i < (tid >> 5)) before += __popc(mask[i]);
+    touched += __popc(mask[i]);
   }
-  const bool chosen = rank[col_tok] < a.k;
-  if (__ballot(chosen) == 0) return;  // the same in every wave
-  if (blk == 0 && tid < a.T && rank[tid] < a.k) {
-    const int p = tid * a.k + rank[tid];
-    a.topk_ids[p] = e;
-    reinterpret_cast<double*>(a.ws + ws.chosen)[p] = reinterpret_cast<const double*>(a.ws + ws.sig)[tid * a.E + e];
-  }
-
-  const int KK = (a.H + 255) / 256, G = a.I / 16;
-  const uint8_t* wc[2];
-  const uint8_t* wsc[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t g = (int64_t)e * G + blk + i * (G / 2);
-    wc[i] = a.w13_codes + g * KK * kMxFragCodes;
-    wsc[i] = a.w13_scales + g * KK * kMxFragScales;
-  }
-  const uint8_t* xc = a.ws + ws.x_codes + (int64_t)col_tok * KK * 256 + f * 16;
-  const uint8_t* xs = a.ws + ws.x_scales + (int64_t)col_tok * KK * 8 + f * 4;
+  if ((mask[tid >> 5] >> (tid & 31)) & 1) listed[before + __popc(mask[tid >> 5] & ((1u << (tid & 31)) - 1u))] = (uint16_t)tid;
+  const int tiles = touched * groups;
+  __syncthreads();
   struct Cols {
     i32x8_t x[4];
     i32x4_t w[2][4];
     int sw[2], sx;
   };
-  auto load = [&](int c, Cols& d) {
-    d.sx = 0;
+  // No branch stands before a load, so that the compiler can count those in
+  // flight: past the end they repeat what is there, and columns of tokens that did
+  // not choose the expert, whose sums nobody reads, all take the first one's place.
+  auto load = [&](int t, int c, Cols& d) {
+    t = min(t, tiles - 1);
+    c = min(c, KK - 1);
+    const int i = t / groups, e = listed[i], g = t - i * groups;
+    const bool chosen = col_tok < a.T && slot[min(col_tok, a.T - 1) * a.E + e] < a.k;
+    const int place = f * 32 + (chosen ? n : 0);
+    const uint8_t* xc = a.ws + ws.x_codes + (int64_t)c * 8192 + place * 16;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) d.x[s] = i32x8_t{0, 0, 0, 0, 0, 0, 0, 0};
-    if (chosen) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        d.x[s] = join_halves(*reinterpret_cast<const i32x4_t*>(xc + c * 256 + 32 * s),
-                             *reinterpret_cast<const i32x4_t*>(xc + c * 256 + 128 + 32 * s));
-      d.sx = *reinterpret_cast<const int*>(xs + c * 8);
+    for (int s = 0; s < 4; ++s) {
+      const uint8_t* p = xc + s * 2048;
+      d.x[s] = join_halves(*reinterpret_cast<const i32x4_t*>(p), *reinterpret_cast<const i32x4_t*>(p + 1024));
     }
+    d.sx = *reinterpret_cast<const int*>(a.ws + ws.x_scales + (int64_t)c * 256 + place * 4);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const int64_t at = ((int64_t)e * G + g + i * (G / 2)) * KK + c;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) d.w[i][s] = reinterpret_cast<const i32x4_t*>(wc[i] + (int64_t)c * kMxFragCodes)[s * 64 + l];
-      d.sw[i] = reinterpret_cast<const int*>(wsc[i] + (int64_t)c * kMxFragScales)[l];
+      for (int s = 0; s < 4; ++s) d.w[i][s] = reinterpret_cast<const i32x4_t*>(a.w13_codes + at * kMxFragCodes)[s * 64 + l];
+      d.sw[i] = reinterpret_cast<const int*>(a.w13_scales + at * kMxFragScales)[l];
     }
   };
   float16_t acc[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
-  auto multiply = [&](Cols& d) {
-    if constexpr (HALF) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) d.x[s] = mx8_part(d.x[s], n >= 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      acc[i] = act_mfma<0, !HALF>(d.w[i][0], d.x[0], acc[i], d.sw[i], d.sx);
-      acc[i] = act_mfma<1, !HALF>(d.w[i][1], d.x[1], acc[i], d.sw[i], d.sx);
-      acc[i] = act_mfma<2, !HALF>(d.w[i][2], d.x[2], acc[i], d.sw[i], d.sx);
-      acc[i] = act_mfma<3, !HALF>(d.w[i][3], d.x[3], acc[i], d.sw[i], d.sx);
-    }
+  auto multiply = [&](int c, const Cols& d) {
+    if (c >= KK) return;
+    layer_mfma<0, HALF>(d.w[0][0], d.x[0], acc[0], d.sw[0], d.sx);
+    layer_mfma<0, HALF>(d.w[1][0], d.x[0], acc[1], d.sw[1], d.sx);
+    layer_mfma<1, HALF>(d.w[0][1], d.x[1], acc[0], d.sw[0], d.sx);
+    layer_mfma<1, HALF>(d.w[1][1], d.x[1], acc[1], d.sw[1], d.sx);
+    layer_mfma<2, HALF>(d.w[0][2], d.x[2], acc[0], d.sw[0], d.sx);
+    layer_mfma<2, HALF>(d.w[1][2], d.x[2], acc[1], d.sw[1], d.sx);
+    layer_mfma<3, HALF>(d.w[0][3], d.x[3], acc[0], d.sw[0], d.sx);
+    layer_mfma<3, HALF>(d.w[1][3], d.x[3], acc[1], d.sw[1], d.sx);
   };
-  Cols d0, d1;  // one column group ahead
-  if (w < KK) load(w, d0);
-  for (int c = w; c < KK; c += 2 * NW) {
-    if (c + NW < KK) load(c + NW, d1);
-    multiply(d0);
-    if (c + NW < KK) {
-      if (c + 2 * NW < KK) load(c + 2 * NW, d0);
-      multiply(d1);
+  // The tile's sums, h and its quantisation
+  auto finish = [&](int t) {
+    const int e = listed[t / groups], blk = t % groups;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        part[w][i][q * 68 + f * 34 + n] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
+    __syncthreads();
+    const int tok = tid >> 3, p = tid & 7;  // features 4 p .. 4 p + 3 of one token
+    const int r = tok < a.T ? slot[tok * a.E + e] : a.E;
+    if (blk == 0 && p == 0 && r < a.k) {
+      a.topk_ids[tok * a.k + r] = e;
+      reinterpret_cast<double*>(a.ws + ws.chosen)[tok * a.k + r] = reinterpret_cast<const double*>(a.ws + ws.sig)[tok * a.E + e];
     }
-  }
+    if (r < a.k) {  // eight lanes together
+      float v[2][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        float4 s = part[0][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      part[w][i][q * 68 + f * 34 + n] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
-  __syncthreads();
-  const int tok = tid >> 3, p = tid & 7;  // features 4 p .. 4 p + 3 of one token
-  if (rank[tok] >= a.k) return;           // eight lanes together
-  float v[2][4];
+        for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
+          const float4 u = part[k % NW][i][(p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
+          s.x += u.x;
+          s.y += u.y;
+          s.z += u.z;
+          s.w += u.w;
+        }
+        v[i][0] = s.x;
+        v[i][1] = s.y;
+        v[i][2] = s.z;
+        v[i][3] = s.w;
+      }
+      float h[4];
+      uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float4 s = part[0][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
+      for (int q = 0; q < 4; ++q) {
+        h[q] = silu(v[0][q]) * v[1][q];
+        m = max(m, abs_bits(h[q]));
+      }
+      m = quad_max(m);
+      m = max(m, lane_dpp<kLaneHalfMirror>(m));
+      const uint32_t byte = mx8_scale_byte(m), d = mx8_encode4(h, byte), large = HALF ? d & mx8_large_mask(d) : d;
+      const int Ip = (a.I + 255) / 256 * 256;
+      const int64_t row = tok * a.k + r, rest = (int64_t)a.T * a.k * Ip;  // from a large element to what is left of it
+      uint8_t* hc = a.ws + ws.h_codes + row * Ip;
+      uint8_t* hs = a.ws + ws.h_scales + row * (Ip / 32);
+      reinterpret_cast<uint32_t*>(hc)[blk * 8 + p] = large;
+      if (HALF) reinterpret_cast<uint32_t*>(hc + rest)[blk * 8 + p] = d ^ large;
+      if (p == 0) hs[blk] = (uint8_t)byte;
+      if (blk == 0) {  // the padding past I is zero
+        for (int b = a.I / 32 + p; b < Ip / 32; b += 8) {
 #pragma unroll
-    for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
-      const float4 u = part[k % NW][i][(p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
-      s.x += u.x;
-      s.y += u.y;
-      s.z += u.z;
-      s.w += u.w;
+          for (int q = 0; q < (HALF ? 4 : 2); ++q) reinterpret_cast<uint4*>(hc + (q >> 1) * rest)[2 * b + (q & 1)] = make_uint4(0, 0, 0, 0);
+          hs[b] = 0;
+        }
+      }
     }
-    v[i][0] = s.x;
-    v[i][1] = s.y;
-    v[i][2] = s.z;
-    v[i][3] = s.w;
-  }
-  float h[4];
-  uint32_t m = 0;
+    __syncthreads();  // part is free
+  };
+  auto clear = [&] {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    h[q] = silu(v[0][q]) * v[1][q];
-    m = max(m, abs_bits(h[q]));
-  }
-  m = quad_max(m);
-  m = max(m, lane_dpp<kLaneHalfMirror>(m));
-  const uint32_t byte = mx8_scale_byte(m);
-  const int Ip = (a.I + 255) / 256 * 256;
-  const int64_t row = tok * a.k + rank[tok];
-  uint8_t* hc = a.ws + ws.h_codes + row * Ip;
-  uint8_t* hs = a.ws + ws.h_scales + row * (Ip / 32);
-  reinterpret_cast<uint32_t*>(hc)[blk * 8 + p] = mx8_encode4(h, byte);
-  if (p == 0) hs[blk] = (uint8_t)byte;
-  if (blk == 0) {  // the padding past I is zero
-    for (int b = a.I / 32 + p; b < Ip / 32; b += 8) {
-      reinterpret_cast<uint4*>(hc)[2 * b] = make_uint4(0, 0, 0, 0);
-      reinterpret_cast<uint4*>(hc)[2 * b + 1] = make_uint4(0, 0, 0, 0);
-      hs[b] = 0;
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+  };
+  // every wave takes as many steps a tile (the last of some past KK: nothing), so that all meet in finish
+  int t = blockIdx.x, c = w;
+  if (t >= tiles) return;
+  Cols d0, d1;
+  load(t, c, d0);
+  clear();
+  auto step = [&](Cols& now, Cols& next) {  // false: the last tile is done
+    const bool last = c - w + NW >= KK;
+    const int nt = last ? t + (int)gridDim.x : t, nc = last ? w : c + NW;
+    load(nt, nc, next);
+    multiply(c, now);
+    if (last) {
+      finish(t);
+      clear();
     }
+    t = nt;
+    c = nc;
+    return nt < tiles;
+  };
+  while (step(d0, d1) && step(d1, d0)) {
   }
 }
 
@@ -328,7 +412,13 @@ struct DownLds {
 
 // Workgroup g: 32 features of y for all tokens.  Its waves take the column groups
 // of the touched experts in turn, each product's FP32 result is added to the
-// wave's sum under the token's weight, and the waves' sums meet in LDS.
+// wave's sum under the token's weight, and the waves' sums meet in LDS.  Where H
+// gives few workgroups, gridDim.y share the products.
+//
+// 16 tokens of 80 experts, H = 6144, I = 2048, 28 touched: 187 MB in 49 us (3.8
+// TB/s).  A row of h is read by all H / 32 groups, and with both operands that is
+// twice the weights' bytes through the L1; four workgroups a group took 47, two
+// column groups ahead 52.
 template <bool F32, bool HALF>
 __global__ __launch_bounds__(512) void mx_layer_down_kernel(MxLayerArgs a) {
   constexpr int NW = 8;
@@ -357,7 +447,7 @@ __global__ __launch_bounds__(512) void mx_layer_down_kernel(MxLayerArgs a) {
     double sum = 0.0;
     for (int j = 0; j < a.k; ++j) sum += chosen[t * a.k + j];
     weight[p] = (float)((double)a.rsf * chosen[p] / sum);
-    if (blockIdx.x == 0) a.topk_w[p] = weight[p];
+    if (blockIdx.x == 0 && blockIdx.y == 0) a.topk_w[p] = weight[p];
   }
   __syncthreads();
   int before[8], touched = 0;  // touched experts below each word of the mask
@@ -376,26 +466,27 @@ __global__ __launch_bounds__(512) void mx_layer_down_kernel(MxLayerArgs a) {
   }
   __syncthreads();
 
-  const int KK = (a.I + 255) / 256, G = a.H / 32, g = blockIdx.x, items = touched * KK;
+  const int KK = (a.I + 255) / 256, G = a.H / 32, g = blockIdx.x, all = touched * KK;
+  const int parts = gridDim.y, each = (all + parts - 1) / parts, first = (int)blockIdx.y * each, items = min(all, first + each);
+  const int64_t rest = (int64_t)pairs * KK * 256;  // from a large element of h to what is left of it
   struct Item {
     i32x4_t w[4];
     i32x8_t h[4];
     int sw, sh, p;
   };
-  auto load = [&](int it, Item& d) {
+  auto load = [&](int it, Item& d) {  // no branch before a load, as in gate_up
+    it = min(it, all - 1);
     const int i = it / KK, c = it - i * KK;
     const int64_t at = ((int64_t)expert[i] * G + g) * KK + c;
     d.p = pair_of[i * kMaxTok + col_tok];
-    d.sh = 0;
+    const int64_t row = ((int64_t)max(d.p, 0) * KK + c) * 256;
+    const uint8_t* hc = a.ws + ws.h_codes + row + f * 16 + (HALF && n >= 16 ? rest : 0);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) d.h[s] = i32x8_t{0, 0, 0, 0, 0, 0, 0, 0};
-    if (d.p >= 0) {
-      const uint8_t* hc = a.ws + ws.h_codes + ((int64_t)d.p * KK + c) * 256 + f * 16;
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        d.h[s] = join_halves(*reinterpret_cast<const i32x4_t*>(hc + 32 * s), *reinterpret_cast<const i32x4_t*>(hc + 128 + 32 * s));
-      d.sh = *reinterpret_cast<const int*>(a.ws + ws.h_scales + ((int64_t)d.p * KK + c) * 8 + f * 4);
+    for (int s = 0; s < 4; ++s) {
+      const uint8_t* q = hc + s * 32;
+      d.h[s] = join_halves(*reinterpret_cast<const i32x4_t*>(q), *reinterpret_cast<const i32x4_t*>(q + 128));
     }
+    d.sh = *reinterpret_cast<const int*>(a.ws + ws.h_scales + row / 32 + f * 4);
 #pragma unroll
     for (int s = 0; s < 4; ++s) d.w[s] = reinterpret_cast<const i32x4_t*>(a.w2_codes + at * kMxFragCodes)[s * 64 + l];
     d.sw = reinterpret_cast<const int*>(a.w2_scales + at * kMxFragScales)[l];
@@ -403,48 +494,71 @@ __global__ __launch_bounds__(512) void mx_layer_down_kernel(MxLayerArgs a) {
   float16_t sum;
 #pragma unroll
   for (int r = 0; r < 16; ++r) sum[r] = 0.0f;
-  auto multiply = [&](Item& d) {
-    if constexpr (HALF) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) d.h[s] = mx8_part(d.h[s], n >= 16);
-    }
+  auto multiply = [&](const Item& d) {
     float16_t v;
 #pragma unroll
     for (int r = 0; r < 16; ++r) v[r] = 0.0f;
-    v = act_mfma<0, !HALF>(d.w[0], d.h[0], v, d.sw, d.sh);
-    v = act_mfma<1, !HALF>(d.w[1], d.h[1], v, d.sw, d.sh);
-    v = act_mfma<2, !HALF>(d.w[2], d.h[2], v, d.sw, d.sh);
-    v = act_mfma<3, !HALF>(d.w[3], d.h[3], v, d.sw, d.sh);
-    if (d.p >= 0) {
-      const float wp = weight[d.p];
+    layer_mfma<0, HALF>(d.w[0], d.h[0], v, d.sw, d.sh);
+    layer_mfma<1, HALF>(d.w[1], d.h[1], v, d.sw, d.sh);
+    layer_mfma<2, HALF>(d.w[2], d.h[2], v, d.sw, d.sh);
+    layer_mfma<3, HALF>(d.w[3], d.h[3], v, d.sw, d.sh);
+    const float wp = weight[max(d.p, 0)];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) sum[r] = fmaf(wp, v[r], sum[r]);
+    for (int r = 0; r < 16; ++r) {
+      const float with = fmaf(wp, v[r], sum[r]);
+      sum[r] = d.p >= 0 ? with : sum[r];
     }
   };
   Item d0, d1;  // one ahead
-  if (w < items) load(w, d0);
-  for (int it = w; it < items; it += 2 * NW) {
-    if (it + NW < items) load(it + NW, d1);
+  load(first + w, d0);
+  for (int it = first + w; it < items; it += 2 * NW) {
+    load(it + NW, d1);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
     multiply(d0);
-    if (it + NW < items) {
-      if (it + 2 * NW < items) load(it + 2 * NW, d0);
-      multiply(d1);
-    }
+    if (it + NW >= items) break;
+    load(it + 2 * NW, d0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(d1);
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     part[w * 272 + q * 68 + f * 34 + n] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
   __syncthreads();
   const int tok = tid >> 3, p = tid & 7;
-  if (tok >= a.T) return;
-  float4 s = part[(p & 3) * 68 + (p >> 2) * 34 + tok];
+  if (parts == 1 && tok >= a.T) return;
+  const float4* own = part + (p & 3) * 68 + (p >> 2) * 34 + (tok & 31);
+  float4 s = own[0];
 #pragma unroll
   for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
-    const float4 u = part[(k % NW) * 272 + (p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
+    const float4 u = own[(k % NW) * 272 + (k < NW ? 0 : 16)];
     s.x += u.x;
     s.y += u.y;
     s.z += u.z;
     s.w += u.w;
+  }
+  if (parts > 1) {
+    // The parts' sums meet in the workspace, and who comes last adds them, in the
+    // parts' order.  They are written through the caches and waited for before the
+    // count, so that nothing else has to be written back (a fence at the agent's
+    // scope for it took 80 us).
+    float* sums = reinterpret_cast<float*>(a.ws + ws.parts) + ((int64_t)g * parts * kMaxTok + tok) * 32 + 4 * p;
+    if (tok < a.T) {
+      const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __hip_atomic_store(sums + (int64_t)blockIdx.y * kMaxTok * 32 + q, v[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) mask[0] = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ws + ws.arrived) + g, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (mask[0] != (uint32_t)parts - 1 || tok >= a.T) return;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < parts; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] += __hip_atomic_load(sums + (int64_t)i * kMaxTok * 32 + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s = make_float4(v[0], v[1], v[2], v[3]);
   }
   const int64_t out = (int64_t)tok * a.H + g * 32 + 4 * p;
   if (F32) *reinterpret_cast<float4*>(static_cast<float*>(a.y) + out) = s;
@@ -460,17 +574,18 @@ hipError_t launch_mx_layer(const MxLayerArgs& a, hipStream_t st) {
   auto* score = TT == 1 ? &mx_layer_score_kernel<1> : TT == 2 ? &mx_layer_score_kernel<2> : &mx_layer_score_kernel<4>;
   if (hipError_t e = launch_kernel(score, grid, block, 0, st, a)) return e;
 
-  const bool half = a.T <= 16, sparse = a.T * a.k * 4 <= a.E && a.T * a.E <= kSparse;
-  auto* gate_up = half ? (sparse ? &mx_layer_gate_up_kernel<true, true> : &mx_layer_gate_up_kernel<false, true>)
-                       : (sparse ? &mx_layer_gate_up_kernel<true, false> : &mx_layer_gate_up_kernel<false, false>);
-  const dim3 tiles((unsigned)(a.I / 32), (unsigned)(sparse ? a.T * a.k : a.E));
-  if (hipError_t e = launch_kernel(gate_up, tiles, dim3(256), 0, st, a)) return e;
+  const bool half = a.T <= 16, rank = (int64_t)a.T * a.E * a.E <= kRankWork;
+  if (!rank)
+    if (hipError_t e = launch_kernel(&mx_layer_rank_kernel, dim3((unsigned)a.T), dim3(1024), 0, st, a)) return e;
+  auto* gate_up = half ? (rank ? &mx_layer_gate_up_kernel<true, true> : &mx_layer_gate_up_kernel<false, true>)
+                       : (rank ? &mx_layer_gate_up_kernel<true, false> : &mx_layer_gate_up_kernel<false, false>);
+  const int64_t most = (int64_t)(a.T * a.k < a.E ? a.T * a.k : a.E) * (a.I / 32);
+  if (hipError_t e = launch_kernel(gate_up, dim3((unsigned)(most < 512 ? most : 512)), dim3(256), 0, st, a)) return e;
 
   auto* down = half ? (a.y_f32 ? &mx_layer_down_kernel<true, true> : &mx_layer_down_kernel<false, true>)
                     : (a.y_f32 ? &mx_layer_down_kernel<true, false> : &mx_layer_down_kernel<false, false>);
-  const int most = DownLds(kMaxTok, 256, 256).total;
-  if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(down), most)) return e;
-  return launch_kernel(down, dim3((unsigned)(a.H / 32)), dim3(512), (size_t)DownLds(a.T, a.E, a.k).total, st, a);
+  if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(down), DownLds(kMaxTok, 256, 256).total)) return e;
+  return launch_kernel(down, dim3((unsigned)(a.H / 32), (unsigned)down_parts(a.T, a.E, a.k, a.H, a.I)), dim3(512), (size_t)DownLds(a.T, a.E, a.k).total, st, a);
 }
 
 }  // namespace moe

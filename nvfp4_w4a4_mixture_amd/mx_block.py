@@ -12,7 +12,7 @@ With ``act_bits=8`` the same over MXFP8 activations (the weights stay MXFP4):
 
     o          = mxfp8_linear(c, s, W_o, bias)                           (BF16; without a post norm the residual is added here)
     r1, n, c, s = moe_norm_out_mxfp8(o, residual, ...)                    (without a post norm: moe_norm_in_mxfp8(r1))
-    y          = mxfp8_moe_layer(n)                                      (up to 32 tokens: three launches), or
+    y          = mxfp8_moe_layer(n)                                      (up to 32 tokens: three or four launches), or
                  moe_route(n), mxfp8_grouped_ffn(c, s, route), moe_combine
     r2, n, c, s = moe_norm_out_mxfp8(y, r1, ...)
 

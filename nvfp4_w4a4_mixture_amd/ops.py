@@ -710,7 +710,7 @@ def mxfp8_moe_layer(x_bf16: torch.Tensor, w_router_bf16: torch.Tensor, bias: tor
                     routed_scaling_factor: float, w13_codes, w13_scales, w2_codes, w2_scales,
                     out_dtype: torch.dtype = torch.bfloat16, y=None, topk_ids=None, topk_w=None, workspace=None,
                     stream=None):
-    """The whole routed layer for up to 32 tokens in three launches: (y [T, H], topk_ids [T, k], topk_w [T, k]).
+    """The whole routed layer for up to 32 tokens in three or four launches: (y [T, H], topk_ids [T, k], topk_w [T, k]).
 
     Routing as moe_route, the experts as mxfp8_grouped_ffn on mxfp8_quantize(x), summed in FP32 without pair rows."""
     return _b.mxfp8_moe_layer(x_bf16, w_router_bf16, bias, k, routed_scaling_factor, w13_codes, w13_scales, w2_codes,

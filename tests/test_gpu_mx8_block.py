@@ -1,5 +1,5 @@
 """MXFP4Block with MXFP8 activations: its operators run together as a decoder layer would use them, for few tokens (the
-layer in three launches) and many, with and without the norm after attention."""
+layer in few launches) and many, with and without the norm after attention."""
 
 import numpy as np
 import pytest

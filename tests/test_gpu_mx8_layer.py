@@ -203,3 +203,45 @@ def test_layer_on_streams_and_in_graphs(ops):
             g.replay()
             assert all(torch.equal(u, v) for u, v in zip(out, want))
             assert all(torch.equal(u, v) for u, v in zip(a.call(ops, da), want_a))
+
+
+def test_layer_many_ties(ops):
+    """Ties and near ties among many experts, which a kernel of its own ranks: by the whole score, then the lower index."""
+    c = Case(24, 200, 6, 64, 32)
+    c.wrb[:] = c.wrb[2]
+    c.bias[:] = 0.25
+    c.bias[9] = np.nan
+    c.bias[150] = np.nextafter(np.float32(0.25), np.float32(1))  # the next FP32 value: an upper half of its FP64 key differs
+    c.bias[77] = 0.5
+    c.bias[30] = 0.125
+    _, ids, w = c.call(ops, c.device(ops), workspace=c.garbage(ops))
+    assert to_np(ids).tolist() == [[77, 150, 0, 1, 2, 3]] * c.T
+    assert np.allclose(to_np(w), c.rsf / c.k)
+    x32 = c.x.astype(np.float32)
+    x32[:] = 0  # scores of 1/2 and a bias that only a key's lower half shows
+    c.bias[:] = 0
+    c.bias[[180, 4]] = 2.0 ** -40
+    c.bias[11] = 2.0 ** -39
+    d = dict(c.device(ops), x=dev_bf16(bf16(x32)[1]))
+    assert to_np(c.call(ops, d)[1]).tolist() == [[11, 4, 180, 0, 1, 2]] * c.T
+
+
+def test_layer_of_shared_products_repeats(ops):
+    """Workgroups that share a feature group's products join them in one order: calls and replays are alike bit for bit."""
+    c = Case(16, 80, 8, 512, 512)
+    d = c.device(ops)
+    ws = c.garbage(ops)
+    want = c.call(ops, d, workspace=ws)
+    out = tuple(torch.empty_like(t) for t in want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(ops, d, workspace=ws, y=out[0], topk_ids=out[1], topk_w=out[2])
+    for i in range(20):
+        for t in out:
+            t.fill_(0)
+        if i % 2:
+            ws.fill_(0xFF)
+        g.replay()
+        assert all(torch.equal(u, v) for u, v in zip(out, want))
+        assert all(torch.equal(u, v) for u, v in zip(c.call(ops, d), want))
