@@ -559,7 +559,7 @@ moe_status mxfp8_grouped_ffn(const uint8_t* x_codes, const uint8_t* x_scales, in
 
 /* The whole routed layer for up to 32 tokens: moe_route, mxfp8_quantize,
  * mxfp8_grouped_ffn and moe_combine in three or four launches, with the sum over a
- * token's experts in FP32 (no pair rows), in the order of the experts:
+ * token's experts in FP32 (no pair rows), in a fixed order:
  *
  *   topk_ids, topk_w as moe_route;  y[t] = sum_j topk_w[t, j] * f(topk_ids[t, j], q(x[t]))
  *

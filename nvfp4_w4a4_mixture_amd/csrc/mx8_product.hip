@@ -13,7 +13,7 @@ namespace moe {
 // 4-bit product takes 4.6: twice the matrix instructions, and their operands to
 // make).
 //
-// Activations go in as two operands (see mx8_mfma).  HALF: at most 16 tokens, so
+// Activations go in as two operands (see mx8_part).  HALF: at most 16 tokens, so
 // both fit the 32 columns of one: column n takes the large elements of token n %
 // 16 if n < 16 and the rest if not, and the two columns' sums are added at the end.
 template <bool HALF>
@@ -116,6 +116,7 @@ namespace {
 // twice as long, ran at 2.3, for their 32-byte runs of a token.  Waves of 128 x 64
 // read two thirds of the LDS bytes of 64 x 128 and leave registers to spare, where
 // those spilled.  Rings of eight stages for the small tile were no faster.
+using Mx8_64x64 = MxTile<4, 2, 1, 1, 4, true>;
 using Mx8_128x64 = MxTile<4, 2, 2, 1, 4, true>;
 using Mx8_256x64 = MxTile<4, 4, 2, 2, 3, true>;
 using Mx8_256x128 = MxTile<8, 4, 2, 2, 4, true>;
@@ -124,41 +125,52 @@ using Mx8_256x256 = MxTile<8, 2, 4, 2, 3, true>;
 int64_t tiles(int64_t T, int64_t G, int64_t rows, int64_t tok) { return (G + rows / 32 - 1) / (rows / 32) * ((T + tok - 1) / tok); }
 
 // The shape of a dense product with 16-bit results, both sides in us:
-//   T x K x N            stream  128x64  256x64  256x128  256x256
-//   16 x 6144 x 6144        7.2    11.9    15.8     21.4     33.1
-//   32 x 6144 x 10240      16.2    13.4    20.4     22.4     34.6
-//   64 x 6144 x 6144       15.8    14.8    20.4     22.4     35.0
-//   128 x 6144 x 1024       8.4    14.3    20.0     28.9     36.6
-//   509 x 6144 x 2048      32.0    15.8    21.1     31.5     55.2
-//   512 x 6144 x 6144      88.2    32.6    26.4     34.5     58.2
-//   1024 x 6144 x 6144             47.7    47.6     43.9     69.5
-//   2048 x 2048 x 6144             34.2    29.1     35.6     33.3
-//   8192 x 512 x 4096              34.7    29.0     32.3     30.5
-//   8192 x 2048 x 6144            144.4   111.1    108.8     93.0
-//   8192 x 6144 x 6144            390.7   284.2    246.8    225.6
-// Streaming while its tiles of 32 x 32 fit the chip once, or each CU fetches at
-// most 32 rows of x a weight group; the largest tile that still fills the chip;
-// 256 x 128 where its tiles fill it just once.
+//   T x K x N            stream   64x64  128x64  256x64  256x128  256x256
+//   1 x 6144 x 10240       10.0    10.5    12.0    18.9
+//   1 x 6144 x 16384       12.7    11.4    12.3    19.7
+//   1 x 4096 x 32768       17.3    13.2    12.8    15.7
+//   32 x 6144 x 6144        8.1    10.6    12.4    16.4
+//   32 x 6144 x 10240      16.1    11.3    13.3    20.4     22.4     34.6
+//   64 x 6144 x 6144       14.7    11.8    14.6    20.2     22.4     35.0
+//   64 x 6144 x 24576      48.5    27.0    20.9    26.4
+//   128 x 6144 x 1024       7.9    11.3    14.7    20.2     28.9     36.6
+//   509 x 6144 x 2048      30.7    12.8    16.1    21.6     31.5     55.2
+//   512 x 6144 x 4096      59.7    25.3    19.0    25.8
+//   512 x 6144 x 6144      88.2    36.7    32.6    26.4     34.5     58.2
+//   1024 x 6144 x 6144             71.2    47.7    47.6     43.9     69.5
+//   2048 x 2048 x 6144             50.4    34.2    29.1     35.6     33.3
+//   8192 x 512 x 4096              38.2    34.7    29.0     32.3     30.5
+//   8192 x 2048 x 6144            165.7   144.4   111.1    108.8     93.0
+//   8192 x 6144 x 6144            467.5   390.7   284.2    246.8    225.6
+// Streaming while its tiles of 32 x 32 fit the chip once; the smallest tile while
+// its tiles do; the largest that still fills the chip; 256 x 128 where its tiles
+// fill it just once.
 Shape linear_shape(int64_t T, int64_t G, int64_t KK) {
   const int64_t cus = 256;
-  if (T <= 8 || (T <= 32 && T * G <= 32 * cus) || tiles(T, G, 32, 32) <= cus) return kStream;
+  if (tiles(T, G, 32, 32) <= cus) return kStream;
+  if (tiles(T, G, 64, 64) <= cus) return k64x64;
   if (KK >= 8 && tiles(T, G, 256, 256) >= cus * 3 / 4) return k256x256;
   const int64_t n = tiles(T, G, 256, 128);
   if (n >= cus * 3 / 4 && n <= cus) return k256x128;
   return tiles(T, G, 256, 64) >= cus * 3 / 4 ? k256x64 : k128x64;
 }
 
-// FP32 results take two operands (see mx8_mfma), so the matrix cores bound them earlier:
-//   T x K x N            stream  128x64  256x64  256x128  256x256
-//   32 x 6144 x 10240      18.5    21.4    25.4     23.0     37.0
-//   64 x 6144 x 6144       17.2    21.4    40.3     38.3     62.2
-//   256 x 6144 x 6144      48.3    24.6    41.6     60.0    105.2
-//   1024 x 6144 x 6144             63.8    69.9     74.1    115.6
-//   2048 x 6144 x 6144            122.9   117.3    148.0    133.0
-//   8192 x 2048 x 6144            185.1   169.5    198.4    191.6
-//   8192 x 6144 x 6144            484.3   441.6    453.9    411.0
+// FP32 results take two operands (see mx8_part), so the matrix cores bound them earlier:
+//   T x K x N            stream   64x64  128x64  256x64  256x128  256x256
+//   1 x 4096 x 32768       17.2    19.9    17.0    19.5
+//   32 x 6144 x 10240      16.1    19.2    22.4    26.7     23.0     37.0
+//   64 x 6144 x 6144       14.7    20.1    22.8    40.5     38.3     62.2
+//   64 x 6144 x 10240      23.0    21.2    22.9    41.7
+//   256 x 6144 x 6144      48.3            24.6    41.6     60.0    105.2
+//   509 x 6144 x 2048      30.3    22.7    23.8    41.9
+//   512 x 6144 x 4096      59.3    32.9    26.9    45.6
+//   1024 x 6144 x 6144                     63.8    69.9     74.1    115.6
+//   2048 x 6144 x 6144                    122.9   117.3    148.0    133.0
+//   8192 x 2048 x 6144                    185.1   169.5    198.4    191.6
+//   8192 x 6144 x 6144                    484.3   441.6    453.9    411.0
 Shape linear_shape_exact(int64_t T, int64_t G) {
   if (T <= 32 || tiles(T, G, 32, 32) <= 512) return kStream;
+  if (tiles(T, G, 64, 64) <= 256) return k64x64;
   return tiles(T, G, 256, 64) >= 512 ? k256x64 : k128x64;
 }
 
@@ -202,12 +214,14 @@ hipError_t launch_mx8_linear(const MxArgs& a, hipStream_t st) {
   if (a.aux & kMxOutF32) {
     switch (linear_shape_exact(T, a.G)) {
       case kStream: return launch_linear_stream(a, st);
+      case k64x64: return launch_tiled<kLinear, Mx8_64x64, true>(a, (T + 63) / 64, st);
       case k128x64: return launch_tiled<kLinear, Mx8_128x64, true>(a, (T + 63) / 64, st);
       default: return launch_tiled<kLinear, Mx8_256x64, true>(a, (T + 63) / 64, st);
     }
   }
   switch (linear_shape(T, a.G, a.KK)) {
     case kStream: return launch_linear_stream(a, st);
+    case k64x64: return launch_tiled<kLinear, Mx8_64x64>(a, (T + 63) / 64, st);
     case k128x64: return launch_tiled<kLinear, Mx8_128x64>(a, (T + 63) / 64, st);
     case k256x64: return launch_tiled<kLinear, Mx8_256x64>(a, (T + 63) / 64, st);
     case k256x128: return launch_tiled<kLinear, Mx8_256x128>(a, (T + 127) / 128, st);

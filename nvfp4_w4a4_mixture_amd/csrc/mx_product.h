@@ -729,7 +729,7 @@ hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
   return launch_kernel(k, dim3((unsigned)grid), dim3(64 * S::kWaves), S::kLds, st, a);
 }
 
-enum Shape { kStream, k128x64, k128x128, k256x64, k256x128, k256x256 };
+enum Shape { kStream, k64x64, k128x64, k128x128, k256x64, k256x128, k256x256 };
 
 // m-tiles of `tok` pairs that E experts can have at most
 inline int64_t most_mtiles(int64_t pairs, int64_t E, int64_t tok) { return pairs / tok + (pairs < E ? pairs : E); }
