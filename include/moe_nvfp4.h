@@ -515,9 +515,9 @@ moe_status moe_norm_out(const void* y, int32_t y_dtype, int64_t T, int64_t H, in
  *             zero elements under scale 0.
  *  Sums       FP32.  The matrix instruction aligns the products of one block to
  *             the largest of them and drops what lies some 17 binades below it;
- *             where a result is FP32, and where up to 32 tokens or columns of them
- *             are streamed, activations are multiplied as two operands of half the
- *             range, which leaves the FP32 rounding only.  Elsewhere results are
+ *             where a result of mxfp8_linear is FP32, in its small products and in
+ *             mxfp8_moe_layer, activations are multiplied as two operands of half
+ *             the range, which leaves the FP32 rounding only.  Elsewhere results are
  *             rounded to BF16, FP16 or MXFP8 anyway, and a sum may be off by 2^-11
  *             of the largest sum of magnitudes of a block (some 1e-5 in the 2-norm
  *             of usual activations). */

@@ -3,8 +3,8 @@
 The computation lives in the HIP library ``lib/libmoe_nvfp4.so`` (C ABI in
 ``include/moe_nvfp4.h``); ``ops`` binds each entry point under its own name,
 ``layer.NVFP4MoELayer`` composes them into one layer forward, and
-``mx_block.MXFP4Block`` the MXFP4 operators into the part of a decoder layer
-that follows attention.  Build with ``python -m nvfp4_w4a4_mixture_amd.build``.
+``mx_block.MXFP4Block`` the MXFP4 operators, or those with MXFP8 activations,
+into the part of a decoder layer that follows attention.  Build with ``python -m nvfp4_w4a4_mixture_amd.build``.
 
 Importing ``ops``/``layer`` loads the library and fails loudly if it is not
 built; there is no CPU path.
