@@ -13,7 +13,7 @@ namespace moe {
 // 4-bit product takes 4.6: twice the matrix instructions, and their operands to
 // make).
 //
-// Activations go in as two operands (see mx8_part).  HALF: at most 16 tokens, so
+// Activations go in as two operands (see mx8_mfma).  HALF: at most 16 tokens, so
 // both fit the 32 columns of one: column n takes the large elements of token n %
 // 16 if n < 16 and the rest if not, and the two columns' sums are added at the end.
 template <bool HALF>
@@ -64,10 +64,10 @@ __global__ __launch_bounds__(512) void mx8_stream_kernel(MxArgs a) {
       if constexpr (HALF) xf[s] = mx8_part(xf[s], n >= 16);
     }
     wave_lds_order();
-    acc = act_mfma<0, !HALF>(d.w[0], xf[0], acc, d.sw, d.sx);
-    acc = act_mfma<1, !HALF>(d.w[1], xf[1], acc, d.sw, d.sx);
-    acc = act_mfma<2, !HALF>(d.w[2], xf[2], acc, d.sw, d.sx);
-    acc = act_mfma<3, !HALF>(d.w[3], xf[3], acc, d.sw, d.sx);
+    acc = mx8_mfma<0, HALF>(d.w[0], xf[0], acc, d.sw, d.sx);
+    acc = mx8_mfma<1, HALF>(d.w[1], xf[1], acc, d.sw, d.sx);
+    acc = mx8_mfma<2, HALF>(d.w[2], xf[2], acc, d.sw, d.sx);
+    acc = mx8_mfma<3, HALF>(d.w[3], xf[3], acc, d.sw, d.sx);
   };
   Cols d0, d1;
   load(w, d0);
@@ -109,13 +109,13 @@ __global__ __launch_bounds__(512) void mx8_stream_kernel(MxArgs a) {
 namespace {
 
 // An 8-bit operand takes the matrix cores twice as long as a 4-bit one (a
-// register-only loop of these products: 3.9 PFLOP/s on data, 4.8 on zeros), and a
-// token's stage twice the LDS, so tiles are taller: weight rows are the cheaper
-// side.  256 x 256 runs at 2.9 PFLOP/s of its loop (90% of the zeros' rate on
-// zeros: the rest is power); stages of one MFMA step instead of two, with a ring
-// twice as long, ran at 2.3, for their 32-byte runs of a token.  Waves of 128 x 64
-// read two thirds of the LDS bytes of 64 x 128 and leave registers to spare, where
-// those spilled.  Rings of eight stages for the small tile were no faster.
+// register-only loop of these products: 3.9 PFLOP/s on data, 4.8 on zeros), it is
+// multiplied twice (see mx8_mfma), and a token's stage takes twice the LDS, so
+// tiles are taller: weight rows are the cheaper side, and a token's operand is
+// parted once for all weight groups of a wave.  Waves of 128 x 64 read two thirds of
+// the LDS bytes of 64 x 128 and leave registers to spare, where those spilled.  Rings
+// of eight stages for the small tile were no faster, and neither were the reads of
+// the next step before a step's products.
 using Mx8_64x64 = MxTile<4, 2, 1, 1, 4, true>;
 using Mx8_128x64 = MxTile<4, 2, 2, 1, 4, true>;
 using Mx8_256x64 = MxTile<4, 4, 2, 2, 3, true>;
@@ -124,82 +124,87 @@ using Mx8_256x256 = MxTile<8, 2, 4, 2, 3, true>;
 
 int64_t tiles(int64_t T, int64_t G, int64_t rows, int64_t tok) { return (G + rows / 32 - 1) / (rows / 32) * ((T + tok - 1) / tok); }
 
-// The shape of a dense product with 16-bit results, both sides in us:
-//   T x K x N            stream   64x64  128x64  256x64  256x128  256x256
-//   1 x 6144 x 10240       10.0    10.5    12.0    18.9
-//   1 x 6144 x 16384       12.7    11.4    12.3    19.7
-//   1 x 4096 x 32768       17.3    13.2    12.8    15.7
-//   32 x 6144 x 6144        8.1    10.6    12.4    16.4
-//   32 x 6144 x 10240      16.1    11.3    13.3    20.4     22.4     34.6
-//   64 x 6144 x 6144       14.7    11.8    14.6    20.2     22.4     35.0
-//   64 x 6144 x 24576      48.5    27.0    20.9    26.4
-//   128 x 6144 x 1024       7.9    11.3    14.7    20.2     28.9     36.6
-//   509 x 6144 x 2048      30.7    12.8    16.1    21.6     31.5     55.2
-//   512 x 6144 x 4096      59.7    25.3    19.0    25.8
-//   512 x 6144 x 6144      88.2    36.7    32.6    26.4     34.5     58.2
-//   1024 x 6144 x 6144             71.2    47.7    47.6     43.9     69.5
-//   2048 x 2048 x 6144             50.4    34.2    29.1     35.6     33.3
-//   8192 x 512 x 4096              38.2    34.7    29.0     32.3     30.5
-//   8192 x 2048 x 6144            165.7   144.4   111.1    108.8     93.0
-//   8192 x 6144 x 6144            467.5   390.7   284.2    246.8    225.6
-// Streaming while its tiles of 32 x 32 fit the chip once; the smallest tile while
-// its tiles do; the largest that still fills the chip; 256 x 128 where its tiles
-// fill it just once.
-Shape linear_shape(int64_t T, int64_t G, int64_t KK) {
-  const int64_t cus = 256;
-  if (tiles(T, G, 32, 32) <= cus) return kStream;
-  if (tiles(T, G, 64, 64) <= cus) return k64x64;
-  if (KK >= 8 && tiles(T, G, 256, 256) >= cus * 3 / 4) return k256x256;
-  const int64_t n = tiles(T, G, 256, 128);
-  if (n >= cus * 3 / 4 && n <= cus) return k256x128;
-  return tiles(T, G, 256, 64) >= cus * 3 / 4 ? k256x64 : k128x64;
+// Percentage of the products that are results, where tiles run one a CU in rounds of 256
+int64_t useful(int64_t T, int64_t G, int64_t rows, int64_t tok) {
+  return 100 * T * G * 32 / ((tiles(T, G, rows, tok) + 255) / 256 * 256 * rows * tok);
 }
 
-// FP32 results take two operands (see mx8_part), so the matrix cores bound them earlier:
-//   T x K x N            stream   64x64  128x64  256x64  256x128  256x256
-//   1 x 4096 x 32768       17.2    19.9    17.0    19.5
-//   32 x 6144 x 10240      16.1    19.2    22.4    26.7     23.0     37.0
-//   64 x 6144 x 6144       14.7    20.1    22.8    40.5     38.3     62.2
-//   64 x 6144 x 10240      23.0    21.2    22.9    41.7
-//   256 x 6144 x 6144      48.3            24.6    41.6     60.0    105.2
-//   509 x 6144 x 2048      30.3    22.7    23.8    41.9
-//   512 x 6144 x 4096      59.3    32.9    26.9    45.6
-//   1024 x 6144 x 6144                     63.8    69.9     74.1    115.6
-//   2048 x 6144 x 6144                    122.9   117.3    148.0    133.0
-//   8192 x 2048 x 6144                    185.1   169.5    198.4    191.6
-//   8192 x 6144 x 6144                    484.3   441.6    453.9    411.0
-Shape linear_shape_exact(int64_t T, int64_t G) {
-  if (T <= 32 || tiles(T, G, 32, 32) <= 512) return kStream;
+// The shape of a dense product, us (BF16 results; FP32 ones where they differ):
+//   T x K x N             stream   64x64  128x64  256x64  256x128  256x256
+//   1 x 6144 x 16384        12.8    17.7    20.8    23.6             35.4
+//   1 x 6144 x 20480        16.4    24.5    21.1    23.6             35.4
+//   8 x 6144 x 24576        18.4    24.9    21.5    24.0             36.0
+//   1 x 4096 x 32768        17.1    18.7    16.3    18.1             26.9
+//   1 x 6144 x 65536        40.6    45.0    35.5    32.9             39.2
+//   1 x 6144 x 131072       92.9    97.6    80.1    76.6             85.8
+//   16 x 6144 x 65536       43.7    45.6    38.1    32.9             40.6
+//   16 x 6144 x 131072       122     104    83.4    78.0             86.2
+//   32 x 6144 x 6144         8.3    17.0    20.4    23.5     22.0    35.4
+//   32 x 6144 x 16384       16.9    18.6    22.0    24.2     23.4    35.6
+//   24 x 6144 x 20480       22.2    25.0    21.5    24.2     22.7    35.8
+//   64 x 6144 x 6144        14.1    18.5    21.0    38.0     36.1    60.2
+//   64 x 6144 x 10240       22.5    19.5    21.6    38.7     36.8    60.8
+//   64 x 6144 x 65536        120    64.1    46.5    51.8     45.8    68.3
+//   64 x 6144 x 131072               169     118     102      105     138
+//   128 x 6144 x 65536               129    87.8    80.9     74.6    76.3
+//   256 x 6144 x 2048       14.8    18.9    21.4    38.3     56.3     103
+//   256 x 6144 x 6144       42.4    28.9    23.5    39.7     56.6     104
+//   509 x 6144 x 2048       29.6    20.7    22.6    39.2     56.4     104
+//   512 x 6144 x 6144       83.2    43.5    41.3    44.6     61.3     105
+//   1024 x 6144 x 6144       163    83.7    63.9    72.2     66.9     109
+//   2048 x 2048 x 6144              56.5    49.6    46.3     53.6    47.8 (FP32 57.0)
+//   2048 x 6144 x 6144               176     127     114      130     114 (FP32 123)
+//   4096 x 6144 x 2048               125    86.4    79.5     73.1     114 (FP32 78.5 in 256x64 and 256x128)
+//   4096 x 6144 x 6144               336     232     214      208     226 (FP32 218, 223, 243)
+//   8192 x 512 x 4096                       40.2    37.5     40.4    37.0 (FP32 48.8, 63.8, 78.8)
+//   8192 x 2048 x 6144                       187     164      162     142 (FP32 161, 182, 179)
+//   8192 x 6144 x 6144                       485     417      403     362 (FP32 423, 425, 394)
+// Streaming while its tiles of 32 x 32 fit the chip three times (up to 16 tokens,
+// which take half the instructions) or twice; the smallest tile while its tiles fit
+// it once.  Large tiles stand one a CU, so they need rounds that are nearly full of
+// tiles, and tiles nearly full of tokens; short reductions and FP32 results (twice
+// the epilogue, with nothing beside it) need two smaller tiles a CU instead.  Of
+// those the taller one where they fit the chip twice over, or once if they hold at
+// most 32 tokens: a wave then multiplies one group of two.
+Shape linear_shape(int64_t T, int64_t G, int64_t KK, bool f32) {
+  if (tiles(T, G, 32, 32) <= (T <= 16 ? 768 : 512)) return kStream;
   if (tiles(T, G, 64, 64) <= 256) return k64x64;
-  return tiles(T, G, 256, 64) >= 512 ? k256x64 : k128x64;
+  const int64_t large = KK >= (f32 ? 16 : 4) ? useful(T, G, 256, 256) : 0, wide = KK >= 4 && !f32 ? useful(T, G, 256, 128) : 0;
+  if (large >= (f32 ? 90 : 72) && 10 * large >= 9 * wide) return k256x256;
+  if (wide >= 72) return k256x128;
+  return tiles(T, G, 256, 64) >= (T <= 32 ? 256 : 512) ? k256x64 : k128x64;
 }
 
-// The shape of a stage of the experts' FFN; both stages in one shape, us:
-//   E k H I, tokens         128x64  256x64  256x128  256x256
-//   16 4 1024 512, 16         10.0    11.5     13.3     17.9
-//   16 4 1024 512, 256        10.8    13.6     18.1     22.1
-//   16 4 1024 512, 1024       20.4    19.2     19.4     28.0
-//   16 4 1024 512, 8192      104.0    81.4     90.0     94.1
-//   80 8 6144 2048, 16       164.1   159.9    171.6    202.8
-//   80 8 6144 2048, 256      323.1   292.0    308.0    349.4
-//   80 8 6144 2048, 1024     578.1   474.5    481.0    506.2
-//   80 8 6144 2048, 2048     990.9   777.6    747.7    729.8
-//   80 8 6144 2048, 8192      3275    2529     2358     2156
-// (Few tokens through a small layer are streamed by mx_layer.hip's kernels.)
-Shape experts_shape(int64_t pairs, int64_t E, int64_t rows, int64_t KK) {
-  const int64_t some = pairs < E ? pairs : E;
-  if ((pairs / 64 + some / 2) * ((rows + 255) / 256) < 256) return k128x64;
-  return pairs >= 160 * E && KK >= 8 ? k256x256 : k256x64;
+// The shape of a stage of the experts' FFN, us of both stages with the other in 256x64:
+//                             gate_up                      down
+//   E k H I, tokens      128x64  256x64  256x256     128x64  256x64  256x256
+//   80 8 6144 2048, 4       127     103      120       98.4     101      111
+//   80 8 6144 2048, 16      191     188      223        191     187      209
+//   80 8 6144 2048, 256     344     318      379        328     315      356
+//   80 8 6144 2048, 2048   1148    1075     1147       1116    1078     1114
+//   80 8 6144 2048, 8192   3988    3735     3653       3891    3741     3741
+//   16 4 6144 2048, 64     73.0    83.7     91.1       69.5    70.1     85.5
+//   16 4 6144 2048, 512     166     163      227        172     164      191
+//   8 2 4096 1024, 512     41.4    44.2     86.4       43.4    44.6     52.4
+//   8 2 4096 1024, 2048     105     112      113        112     108      124
+//   8 2 4096 1024, 8192     346     333      357        346     331      354
+//   16 4 1024 512, 256     15.0    18.3     27.4       16.2    18.0     23.1
+//   16 4 1024 512, 8192     107     109      120        109     103      114
+//   64 8 2048 768, 32      33.8    33.1     45.8       35.2    32.7     40.6
+//   64 8 2048 768, 4096     289     263      277        283     260      275
+// As above, by the number of tiles: the taller tile from some two and a half a CU on,
+// or one a CU while experts have few pairs.  256x256 gains 2 to 3% in gate_up of the
+// largest and loses elsewhere.
+Shape experts_shape(int64_t pairs, int64_t E, int64_t rows) {
+  const int64_t some = pairs < E ? pairs : E, n = (pairs / 64 + some / 2) * ((rows + 255) / 256);
+  return n < (pairs <= 32 * E ? 256 : 600) ? k128x64 : k256x64;
 }
 
 template <int MODE>
 hipError_t launch_experts_stage(const MxArgs& a, const MxExperts& x, hipStream_t st) {
-  const int64_t pairs = x.T * x.k;
-  switch (experts_shape(pairs, x.E, a.N, a.KK)) {
-    case k128x64: return launch_tiled<MODE, Mx8_128x64>(a, most_mtiles(pairs, x.E, 64), st);
-    case k256x64: return launch_tiled<MODE, Mx8_256x64>(a, most_mtiles(pairs, x.E, 64), st);
-    default: return launch_tiled<MODE, Mx8_256x256>(a, most_mtiles(pairs, x.E, 256), st);
-  }
+  const int64_t pairs = x.T * x.k, most = most_mtiles(pairs, x.E, 64);
+  if (experts_shape(pairs, x.E, a.N) == k128x64) return launch_tiled<MODE, Mx8_128x64>(a, most, st);
+  return launch_tiled<MODE, Mx8_256x64>(a, most, st);
 }
 
 hipError_t launch_linear_stream(const MxArgs& a, hipStream_t st) {
@@ -211,15 +216,7 @@ hipError_t launch_linear_stream(const MxArgs& a, hipStream_t st) {
 
 hipError_t launch_mx8_linear(const MxArgs& a, hipStream_t st) {
   const int64_t T = a.T;
-  if (a.aux & kMxOutF32) {
-    switch (linear_shape_exact(T, a.G)) {
-      case kStream: return launch_linear_stream(a, st);
-      case k64x64: return launch_tiled<kLinear, Mx8_64x64, true>(a, (T + 63) / 64, st);
-      case k128x64: return launch_tiled<kLinear, Mx8_128x64, true>(a, (T + 63) / 64, st);
-      default: return launch_tiled<kLinear, Mx8_256x64, true>(a, (T + 63) / 64, st);
-    }
-  }
-  switch (linear_shape(T, a.G, a.KK)) {
+  switch (linear_shape(T, a.G, a.KK, a.aux & kMxOutF32)) {
     case kStream: return launch_linear_stream(a, st);
     case k64x64: return launch_tiled<kLinear, Mx8_64x64>(a, (T + 63) / 64, st);
     case k128x64: return launch_tiled<kLinear, Mx8_128x64>(a, (T + 63) / 64, st);

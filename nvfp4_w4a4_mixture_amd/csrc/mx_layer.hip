@@ -39,7 +39,7 @@ __host__ __device__ inline int64_t down_parts(int64_t T, int64_t E, int64_t k, i
 // Everything between the kernels: keys (the order of the scores) and sigmoids of
 // all experts, the chosen sigmoids by slot, all experts' ranks, x and h in MXFP8,
 // the parts' sums and their counts.  Up to 16 tokens x and h are kept as the two
-// operands that they are multiplied as (see mx8_part), the large elements and the
+// operands that they are multiplied as (see mx8_mfma), the large elements and the
 // rest, which are the halves of one operand's 32 columns: one instruction
 // multiplies both.  Past 16 they are kept whole and parted at the product (kept as
 // two, 32 tokens of 80 experts took 205 us instead of 170: twice the bytes of x
@@ -77,18 +77,6 @@ typedef uint32_t u32x4_any2_t __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ u32x4_any2_t load8(const uint16_t* p) { return *reinterpret_cast<const u32x4_any2_t*>(p); }
 __device__ __forceinline__ float element(const u32x4_any2_t& v, int i) {
   return __uint_as_float((i & 1) ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
-}
-
-// One step's products.  HALF: the columns hold the large elements and the rest;
-// else the operand is parted here.
-template <int S, bool HALF>
-__device__ __forceinline__ void layer_mfma(const i32x4_t& w, const i32x8_t& x, float16_t& acc, int sw, int sx) {
-  if constexpr (HALF) {
-    acc = mx8_mfma<S>(w, x, acc, sw, sx);
-  } else {
-    acc = mx8_mfma<S>(w, mx8_part(x, false), acc, sw, sx);
-    acc = mx8_mfma<S>(w, mx8_part(x, true), acc, sw, sx);
-  }
 }
 
 }  // namespace
@@ -130,7 +118,7 @@ __global__ __launch_bounds__(kScoreThreads) void mx_layer_score_kernel(MxLayerAr
       *reinterpret_cast<uint2*>(xc) = make_uint2(d[0], d[1]);
       return;
     }
-    const uint32_t large[2] = {d[0] & mx8_large_mask(d[0]), d[1] & mx8_large_mask(d[1])};
+    const uint32_t large[2] = {mx8_large(d[0]), mx8_large(d[1])};
     *reinterpret_cast<uint2*>(xc) = make_uint2(large[0], large[1]);
     *reinterpret_cast<uint2*>(xc + 256) = make_uint2(d[0] ^ large[0], d[1] ^ large[1]);
     if ((tid & 3) == 0) xs[64] = (uint8_t)byte;
@@ -294,14 +282,14 @@ __global__ __launch_bounds__(256, 2) void mx_layer_gate_up_kernel(MxLayerArgs a)
   float16_t acc[2];
   auto multiply = [&](int c, const Cols& d) {
     if (c >= KK) return;
-    layer_mfma<0, HALF>(d.w[0][0], d.x[0], acc[0], d.sw[0], d.sx);
-    layer_mfma<0, HALF>(d.w[1][0], d.x[0], acc[1], d.sw[1], d.sx);
-    layer_mfma<1, HALF>(d.w[0][1], d.x[1], acc[0], d.sw[0], d.sx);
-    layer_mfma<1, HALF>(d.w[1][1], d.x[1], acc[1], d.sw[1], d.sx);
-    layer_mfma<2, HALF>(d.w[0][2], d.x[2], acc[0], d.sw[0], d.sx);
-    layer_mfma<2, HALF>(d.w[1][2], d.x[2], acc[1], d.sw[1], d.sx);
-    layer_mfma<3, HALF>(d.w[0][3], d.x[3], acc[0], d.sw[0], d.sx);
-    layer_mfma<3, HALF>(d.w[1][3], d.x[3], acc[1], d.sw[1], d.sx);
+    acc[0] = mx8_mfma<0, HALF>(d.w[0][0], d.x[0], acc[0], d.sw[0], d.sx);
+    acc[1] = mx8_mfma<0, HALF>(d.w[1][0], d.x[0], acc[1], d.sw[1], d.sx);
+    acc[0] = mx8_mfma<1, HALF>(d.w[0][1], d.x[1], acc[0], d.sw[0], d.sx);
+    acc[1] = mx8_mfma<1, HALF>(d.w[1][1], d.x[1], acc[1], d.sw[1], d.sx);
+    acc[0] = mx8_mfma<2, HALF>(d.w[0][2], d.x[2], acc[0], d.sw[0], d.sx);
+    acc[1] = mx8_mfma<2, HALF>(d.w[1][2], d.x[2], acc[1], d.sw[1], d.sx);
+    acc[0] = mx8_mfma<3, HALF>(d.w[0][3], d.x[3], acc[0], d.sw[0], d.sx);
+    acc[1] = mx8_mfma<3, HALF>(d.w[1][3], d.x[3], acc[1], d.sw[1], d.sx);
   };
   // The tile's sums, h and its quantisation
   auto finish = [&](int t) {
@@ -345,7 +333,7 @@ __global__ __launch_bounds__(256, 2) void mx_layer_gate_up_kernel(MxLayerArgs a)
       }
       m = quad_max(m);
       m = max(m, lane_dpp<kLaneHalfMirror>(m));
-      const uint32_t byte = mx8_scale_byte(m), d = mx8_encode4(h, byte), large = HALF ? d & mx8_large_mask(d) : d;
+      const uint32_t byte = mx8_scale_byte(m), d = mx8_encode4(h, byte), large = HALF ? mx8_large(d) : d;
       const int Ip = (a.I + 255) / 256 * 256;
       const int64_t row = tok * a.k + r, rest = (int64_t)a.T * a.k * Ip;  // from a large element to what is left of it
       uint8_t* hc = a.ws + ws.h_codes + row * Ip;
@@ -498,10 +486,10 @@ __global__ __launch_bounds__(512) void mx_layer_down_kernel(MxLayerArgs a) {
     float16_t v;
 #pragma unroll
     for (int r = 0; r < 16; ++r) v[r] = 0.0f;
-    layer_mfma<0, HALF>(d.w[0], d.h[0], v, d.sw, d.sh);
-    layer_mfma<1, HALF>(d.w[1], d.h[1], v, d.sw, d.sh);
-    layer_mfma<2, HALF>(d.w[2], d.h[2], v, d.sw, d.sh);
-    layer_mfma<3, HALF>(d.w[3], d.h[3], v, d.sw, d.sh);
+    v = mx8_mfma<0, HALF>(d.w[0], d.h[0], v, d.sw, d.sh);
+    v = mx8_mfma<1, HALF>(d.w[1], d.h[1], v, d.sw, d.sh);
+    v = mx8_mfma<2, HALF>(d.w[2], d.h[2], v, d.sw, d.sh);
+    v = mx8_mfma<3, HALF>(d.w[3], d.h[3], v, d.sw, d.sh);
     const float wp = weight[max(d.p, 0)];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {

@@ -99,15 +99,13 @@ template <>
 struct ActFrag<true> {
   typedef i32x8_t type;
 };
-template <int S, bool EXACT>
+template <int S>
 __device__ __forceinline__ float16_t act_mfma(i32x4_t w, const i32x4_t& x, float16_t c, int sw, int sx) {
   return mx_mfma<S>(w, x, c, sw, sx);
 }
-template <int S, bool EXACT>
+template <int S>
 __device__ __forceinline__ float16_t act_mfma(i32x4_t w, const i32x8_t& x, float16_t c, int sw, int sx) {
-  if constexpr (!EXACT) return mx8_mfma<S>(w, x, c, sw, sx);
-  const i32x8_t large = mx8_part(x, false);
-  return mx8_mfma<S>(w, x ^ large, mx8_mfma<S>(w, large, c, sw, sx), sw, sx);
+  return mx8_mfma<S, false>(w, x, c, sw, sx);
 }
 __device__ __forceinline__ i32x8_t join_halves(i32x4_t a, i32x4_t b) {
   return i32x8_t{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
@@ -292,7 +290,7 @@ struct ExpertTiles {
   }
 };
 
-template <int MODE, class S, bool EXACT = false>
+template <int MODE, class S>
 __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   constexpr bool A8 = S::kA8;
   constexpr int kGroup = A8 ? 256 : 128;  // bytes of a column group of an activation row
@@ -473,7 +471,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
     for (int i = 0; i < GW; ++i) {
 #pragma unroll
       for (int j = 0; j < LX; ++j) {
-        acc[i][j] = act_mfma<decltype(sel)::value, EXACT>(fr.w[i], fr.x[j], acc[i][j], sc.w[i], sc.x[j]);
+        acc[i][j] = act_mfma<decltype(sel)::value>(fr.w[i], fr.x[j], acc[i][j], sc.w[i], sc.x[j]);
 #pragma unroll
         for (int k = 0; k < kReads; ++k)
           if (k * kSpan / kReads == i * LX + j) read(nst, np, k, LX, nx);
@@ -720,9 +718,9 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
 namespace {
 
 // max_mtiles: an upper bound on the m-tiles (for experts the kernel counts them)
-template <int MODE, class S, bool EXACT = false>
+template <int MODE, class S>
 hipError_t launch_tiled(const MxArgs& a, int64_t max_mtiles, hipStream_t st) {
-  auto* k = &mx_tiled_kernel<MODE, S, EXACT>;
+  auto* k = &mx_tiled_kernel<MODE, S>;
   if (hipError_t e = set_max_dynamic_lds(reinterpret_cast<const void*>(k), S::kLds)) return e;
   const int64_t rows = MODE == kGateUp ? a.G / 2 : a.G, per = MODE == kGateUp ? S::kSlots / 2 : S::kSlots;
   const int64_t grid = (max_mtiles * ((rows + per - 1) / per) + 7) / 8 * 8;
