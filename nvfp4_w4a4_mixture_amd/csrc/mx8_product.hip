@@ -86,15 +86,7 @@ __global__ __launch_bounds__(512) void mx8_stream_kernel(MxArgs a) {
   __syncthreads();
   const int tok = tid >> 3, p = tid & 7, col = (int)blockIdx.x * 32 + 4 * p;  // features 4 p .. 4 p + 3 of one token
   if (tok >= cnt) return;
-  float4 s = part[(p & 3) * 68 + (p >> 2) * 34 + tok];
-#pragma unroll
-  for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
-    const float4 u = part[k % NW * 272 + (p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
-    s.x += u.x;
-    s.y += u.y;
-    s.z += u.z;
-    s.w += u.w;
-  }
+  const float4 s = add_waves<NW, HALF>(part, p, tok);
   const float v[4] = {s.x, s.y, s.z, s.w};
   const int64_t row = t0 + tok;
 #pragma unroll

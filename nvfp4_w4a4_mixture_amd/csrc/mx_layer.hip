@@ -310,15 +310,7 @@ __global__ __launch_bounds__(256, 2) void mx_layer_gate_up_kernel(MxLayerArgs a)
       float v[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float4 s = part[0][i][(p & 3) * 68 + (p >> 2) * 34 + tok];
-#pragma unroll
-        for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
-          const float4 u = part[k % NW][i][(p & 3) * 68 + (p >> 2) * 34 + tok + (k < NW ? 0 : 16)];
-          s.x += u.x;
-          s.y += u.y;
-          s.z += u.z;
-          s.w += u.w;
-        }
+        const float4 s = add_waves<NW, HALF, 2 * kWaveSums>(part[0][i], p, tok);
         v[i][0] = s.x;
         v[i][1] = s.y;
         v[i][2] = s.z;
@@ -513,17 +505,9 @@ __global__ __launch_bounds__(512) void mx_layer_down_kernel(MxLayerArgs a) {
     part[w * 272 + q * 68 + f * 34 + n] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
   __syncthreads();
   const int tok = tid >> 3, p = tid & 7;
-  if (parts == 1 && tok >= a.T) return;
-  const float4* own = part + (p & 3) * 68 + (p >> 2) * 34 + (tok & 31);
-  float4 s = own[0];
-#pragma unroll
-  for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
-    const float4 u = own[(k % NW) * 272 + (k < NW ? 0 : 16)];
-    s.x += u.x;
-    s.y += u.y;
-    s.z += u.z;
-    s.w += u.w;
-  }
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (tok < a.T) s = add_waves<NW, HALF>(part, p, tok);
+  else if (parts == 1) return;
   if (parts > 1) {
     // The parts' sums meet in the workspace, and who comes last adds them, in the
     // parts' order.  They are written through the caches and waited for before the

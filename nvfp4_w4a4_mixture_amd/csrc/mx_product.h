@@ -107,6 +107,25 @@ template <int S>
 __device__ __forceinline__ float16_t act_mfma(i32x4_t w, const i32x8_t& x, float16_t c, int sw, int sx) {
   return mx8_mfma<S, false>(w, x, c, sw, sx);
 }
+// Sums that a tile's waves exchange through LDS: wave w's of features 4 p .. 4 p + 3 of
+// column n are the float4 at w * STRIDE + (p & 3) * 68 + (p >> 2) * 34 + n.  Adds them over
+// NW waves in order; HALF: and over the columns tok and tok + 16.  tok < 32, or 16.
+constexpr int kWaveSums = 4 * 68;
+template <int NW, bool HALF, int STRIDE = kWaveSums>
+__device__ __forceinline__ float4 add_waves(const float4* part, int p, int tok) {
+  static_assert(3 * 68 + 34 + 31 < kWaveSums, "the last column of the last features is the wave's own");
+  const float4* own = part + (p & 3) * 68 + (p >> 2) * 34 + tok;
+  float4 s = own[0];
+#pragma unroll
+  for (int k = 1; k < (HALF ? 2 : 1) * NW; ++k) {
+    const float4 u = own[k % NW * STRIDE + (k < NW ? 0 : 16)];
+    s.x += u.x;
+    s.y += u.y;
+    s.z += u.z;
+    s.w += u.w;
+  }
+  return s;
+}
 __device__ __forceinline__ i32x8_t join_halves(i32x4_t a, i32x4_t b) {
   return i32x8_t{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
