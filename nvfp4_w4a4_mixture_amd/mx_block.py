@@ -10,7 +10,7 @@
 
 With ``act_bits=8`` the same over MXFP8 activations (the weights stay MXFP4):
 
-    o          = mxfp8_linear(c, s, W_o, bias)                           (BF16; without a post norm the residual is added here)
+    o          = mxfp8_linear(c, s, W_o, bias)                           (FP32; without a post norm r1, the residual added here)
     r1, n, c, s = moe_norm_out_mxfp8(o, residual, ...)                    (without a post norm: moe_norm_in_mxfp8(r1))
     y          = mxfp8_moe_layer(n)                                      (up to 32 tokens: three or four launches), or
                  moe_route(n), mxfp8_grouped_ffn(c, s, route), moe_combine
@@ -86,10 +86,12 @@ class MXFP4Block:
                               scales=new((T, -(-c // 256) * 8), torch.uint8))
         if self.act_bits == 8:
             few = T <= ops.MOE_LAYER_MAX_TOKENS
-            b = dict(a=rows(K), o=new((T, H), torch.bfloat16), r1=new((T, H), torch.bfloat16),
+            b = dict(a=rows(K), r1=new((T, H), torch.bfloat16),
                      n1=new((T, H), torch.bfloat16), x=rows(H), topk_ids=new((T, k), torch.int32),
                      topk_w=new((T, k), torch.float32), y=new((T, H), torch.float32), r2=new((T, H), torch.bfloat16),
                      n2=new((T, H), torch.bfloat16), out=rows(H))
+            if self.norms[0] is not None:  # the norm after attention reads the projection in FP32
+                b["o"] = new((T, H), torch.float32)
             if few:
                 return dict(b, ws=new((max(ops.mxfp8_moe_layer_workspace_bytes(T, H, E, k, I), 1),), torch.uint8))
             route = ops.RouteOut(b["topk_ids"], b["topk_w"], new((E,), torch.int32), new((E + 1,), torch.int32),
