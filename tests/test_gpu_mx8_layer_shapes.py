@@ -21,3 +21,10 @@ def ops():
 def test_layer_of_few_pairs_in_shared_products(ops, T, E, k, H, I):
     """Up to three pairs whose products several workgroups share: the smallest LDS, all of it the waves' sums."""
     check_layer(ops, T, E, k, H, I)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(16, 16, 4, 288, 1504), (16, 80, 8, 512, 512), (1, 40, 20, 64, 1056), (32, 30, 6, 96, 800)])
+def test_layer_of_many_tiles(ops, T, E, k, H, I):
+    """More than 512 tiles of h: a workgroup walks several, and loads ahead from one expert's into the next one's; ranked by
+    gate_up and by a kernel of its own, in one operand and in two."""
+    check_layer(ops, T, E, k, H, I)
