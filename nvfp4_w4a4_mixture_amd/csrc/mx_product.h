@@ -131,11 +131,35 @@ __device__ __forceinline__ i32x8_t join_halves(i32x4_t a, i32x4_t b) {
 }
 
 // ---- the dense product's epilogue: act(z + bias) + residual, in FP32
+
+// GELU by erf, z Phi(z), from the normal distribution's tail Phi(-a), a = |z|, so that
+// nothing cancels: -a Phi(-a) for negative z, z - a Phi(-a) else.  Hastings' form (1955)
+// of the tail, e^(-a^2/2) t P(t) with t = 1 / (1 + q a); P of degree 8 and q fitted for
+// the least relative error on 0 <= a <= 16, 2.7e-8.  The exponent is formed in two
+// parts, as its rounding alone would be 1e-5 of the result at a = 12.  At most 16 * 2^-24 of
+// the result, 5 over all BF16 arguments.  By the library's erfc 8192 x 512 x 4096 took 78 us, so
+// 61, by 0.5 z (1 + erf), which loses a result of -5 to 4%, 60.
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fminf(fabsf(z), 16.0f), t = __builtin_amdgcn_rcpf(fmaf(a, 0.3479999899864197f, 1.0f));
+  float p = -0.028869353234767914f;
+  p = fmaf(p, t, 0.1446346640586853f);
+  p = fmaf(p, t, -0.2620934247970581f);
+  p = fmaf(p, t, 0.1703842133283615f);
+  p = fmaf(p, t, -0.028765540570020676f);
+  p = fmaf(p, t, 0.10794074088335037f);
+  p = fmaf(p, t, 0.11882702261209488f);
+  p = fmaf(p, t, 0.13912083208560944f);
+  p = fmaf(p, t, 0.1388208419084549f);
+  constexpr float kHigh = -0.7213475108146667f, kLow = -9.629815167500055e-09f;  // -log2(e) / 2
+  const float s = a * a, e = s * kHigh, rest = fmaf(fmaf(a, a, -s), kHigh, fmaf(s, kLow, fmaf(s, kHigh, -e)));
+  const float x = __builtin_amdgcn_exp2f(e), tail = t * p * fmaf(x * 0.69314718055994531f, rest, x);
+  return fmaf(-a, tail, z < 0.0f ? 0.0f : z);  // past 16 the tail is 0; NaN stays
+}
 __device__ __forceinline__ float activate(int act, float z) {
   switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;  // NaN stays
     case kActSilu: return silu(z);
-    case kActGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case kActGelu: return gelu(z);
     case kActGeluTanh: {  // 0.5 (1 + tanh(u)) = 1 / (1 + e^-2u)
       const float u = 0.79788456080286536f * fmaf(0.044715f * z * z, z, z);
       return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-2.88539008177792681f * u));
