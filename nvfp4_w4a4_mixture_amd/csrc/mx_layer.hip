@@ -23,8 +23,8 @@ namespace {
 constexpr int kScoreThreads = 256;
 constexpr int kMaxTok = (int)kLayerMaxTokens;
 constexpr int kMaxParts = 4;
-constexpr int64_t kRankWork = 1 << 16;  // comparisons past which the ranking is a kernel of its own
-constexpr int kRankScores = 1448;       // the most scores of no more: T * E <= sqrt(32 * kRankWork)
+constexpr int64_t kRankWork = 1 << 15;  // comparisons past which the ranking is a kernel of its own
+constexpr int kRankScores = 1024;       // the most scores of no more: T * E <= sqrt(32 * kRankWork)
 
 // Workgroups that share 32 features of y: as many as leave each a CU, and each of
 // its waves four column groups of products.  With one workgroup H = 2048 used 64 of
@@ -212,9 +212,12 @@ __global__ __launch_bounds__(1024) void mx_layer_rank_kernel(MxLayerArgs a) {
 //
 // Every workgroup lists the touched experts and takes every gridDim.x-th of their
 // tiles, a column group ahead across tiles too.  RANK: it ranks all scores itself,
-// T * E * E comparisons; with many (kRankWork) a kernel before it does: 1 token of
-// 256 experts 24.5 us with the ranking here, 25.8 with the kernel; 16 of 64 49.3
-// and 47.6; 16 of 256 124 (by expert) and 63.
+// T * E * E comparisons; with many (kRankWork) a kernel before it does.  The layer in
+// us with the ranking here, and with the kernel (H = 2048, I = 768, top-8):
+//   T x E   1 x 128 16.5 K  2 x 128 33 K  8 x 64 33 K  32 x 32 33 K  16 x 48 37 K  12 x 64 49 K  4 x 128 66 K  16 x 64 66 K
+//   here         18.2          23.2         32.0          34.8          34.8          34.5          29.1          36.4
+//   kernel       18.3          23.9         32.6          34.3          35.0          34.4          27.8          35.0
+// (1 x 256, 66 K: H = 1024 17.2 and 17.1, H = 256 15.8 and 16.3.)  16 x 256: 124 and 63.
 //
 // Bounds: the weights' bytes.  16 tokens of 80 experts, H = 6144, I = 2048, 28
 // touched: 374 MB in 70 us (5.4 TB/s), after 5 of the ranking (ranked here 76).

@@ -28,3 +28,10 @@ def test_layer_of_many_tiles(ops, T, E, k, H, I):
     """More than 512 tiles of h: a workgroup walks several, and loads ahead from one expert's into the next one's; ranked by
     gate_up and by a kernel of its own, in one operand and in two."""
     check_layer(ops, T, E, k, H, I)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(32, 32, 4, 64, 32), (8, 64, 8, 96, 64), (2, 128, 8, 64, 32), (16, 48, 4, 64, 32),
+                                       (16, 64, 8, 96, 64), (1, 256, 8, 64, 32)])
+def test_layer_where_the_ranking_changes(ops, T, E, k, H, I):
+    """The most scores that gate_up ranks itself, and the fewest that a kernel before it does."""
+    check_layer(ops, T, E, k, H, I)
