@@ -328,14 +328,15 @@ hipError_t launch_norm_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream
 // and 2528 columns: 8.1 / 14.6, 8.1 / 15.0 and 8.3 / 15.6 us by four waves of two
 // chunks, 7.4 / 13.7, 7.4 / 14.1 and 7.5 / 14.6 by five of one; 8192 rows of 2304 23.9 /
 // 47.6 and 21.6 / 42.7, 16 rows 3.3 / 5.2 and 3.5 / 4.5), or where there are few long
-// rows (16 of 6144: 3.9 / 5.9 by four waves of three, 3.4 / 5.2 by twelve; 256 4.3 / 6.6
-// and 3.9 / 6.1; but 600 6.5 / 10.7 and 7.0 / 11.7, 8192 40 / 95 and 50 / 105).
+// rows (16 of 5120: 3.9 / 6.0 by four waves of three, 3.5 / 5.2 by twelve; 256 of 6144
+// 4.3 / 6.6 and 3.9 / 6.1; but 600 6.5 / 10.7 and 7.0 / 11.7, 8192 40 / 95 and 50 / 105,
+// and 16 of 4096 3.9 / 4.8 by four waves of two and 3.5 / 5.0).
 // A launch has less than 2^32 work-items, which the caller has checked for four waves a row.
 template <bool POST>
 hipError_t launch_norm8_shape(const NormArgs& a, int64_t T, bool y_f32, hipStream_t st) {
   const int cols = (int)a.Hp;
   if (cols > 2048 && cols <= 2560 && T * 320 < (int64_t)1 << 32) return launch_norm_as<5, 1, POST, true>(a, T, y_f32, st);
-  if (cols > 2560 && cols <= 6144 && T <= 256) return launch_norm_as<12, 1, POST, true>(a, T, y_f32, st);
+  if (cols > 4096 && cols <= 6144 && T <= 256) return launch_norm_as<12, 1, POST, true>(a, T, y_f32, st);
   return launch_norm_shape<POST, true>(a, T, y_f32, st);
 }
 
