@@ -213,13 +213,14 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
         inv = rsqrtf(row_sum<NW>(sq, lds[0], w) / (float)H + a.eps);
       }
     }
+    const bool far = A8 && isinf(inv);  // rows under 2^-128 without an eps: FP32 cannot hold it
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float wv[8], rv[8], gv[8], f[8];
       unpack8(rr[v], rv);
       if (a.w_post) unpack8(wp[v], wv);
       if (a.gate && !a.gate_row) unpack8(gg[v], gv);
-      bool close = false;
+      bool close = far;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float z = x[v][i];
@@ -261,7 +262,7 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
     const int c = (v * 64 * NW + t) * 8;
     float wv[8], q[8];
     unpack8(wn[v], wv);
-    bool close = false;
+    bool close = A8 && isinf(inv);  // as above
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       q[i] = x[v][i] * inv * wv[i];
