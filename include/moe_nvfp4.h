@@ -531,8 +531,9 @@ moe_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t
  * residual_dtype or NULL; activation 0 none, 1 ReLU, 2 SiLU z / (1 + e^-z), 3 GELU
  * 0.5 z (1 + erf(z / sqrt 2)), 4 GELU by tanh, 0.5 z (1 + tanh(sqrt(2 / pi) (z +
  * 0.044715 z^3))).  y may be residual (the same type and stride), and must not
- * overlap anything else.  Limits as mxfp4_linear, x codes T * Kp < 2^32 bytes;
- * code arrays 16-byte, scale arrays 4-byte, the others aligned to their element. */
+ * overlap anything else.  Limits as mxfp4_linear, x codes T * Kp < 2^32 bytes, and
+ * at most 2^24 - 8 tiles of 256 features x 64 tokens; code arrays 16-byte, scale
+ * arrays 4-byte, the others aligned to their element. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1
 #define MOE_ACT_SILU 2

@@ -201,6 +201,9 @@ moe_status mxfp8_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
   if (!dtype_ok(out_dtype)) return fail(MOE_ERR_SHAPE, "%s: out_dtype must be 0 (BF16) or 1 (FP32)", fn);
   if (activation < 0 || activation >= moe::kActCount) return fail(MOE_ERR_SHAPE, "%s: unknown activation", fn);
   if (moe_status s = check_linear(fn, T, K, N, 256)) return s;
+  // four waves a tile of 256 x 64, and a grid of whole eights
+  if (((uint64_t)T + 63) / 64 * (((uint64_t)N + 255) / 256) * 256 > kMaxThreads - 8 * 256)
+    return fail(MOE_ERR_SHAPE, "%s: the result is too large for one call", fn);
   if (ldy < N || ldy >= kMaxDim) return fail(MOE_ERR_SHAPE, "%s: ldy must be >= N and < 2^31", fn);
   if (residual) {
     if (!dtype_ok(residual_dtype)) return fail(MOE_ERR_SHAPE, "%s: residual_dtype must be 0 (BF16) or 1 (FP32)", fn);

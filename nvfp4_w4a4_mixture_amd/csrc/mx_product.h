@@ -343,7 +343,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void mx_tiled_kernel(MxArgs a) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w % WM, wx = w / WM;
 
-  // ---- which tile: each XCD takes one contiguous run of the tile order (under 2^23 tiles)
+  // ---- which tile: each XCD takes one contiguous run of the tile order (under 2^24 tiles)
   const int nw = MODE == kGateUp ? (a.G / 2 + S::kSlots / 2 - 1) / (S::kSlots / 2) : (a.G + S::kSlots - 1) / S::kSlots;
   ExpertTiles<S::kTok> experts;
   if (MODE != kLinear) experts.count(a.offsets, a.E, l);
