@@ -233,7 +233,6 @@ moe_status mxfp8_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t
   a.ldr = (int32_t)ld_residual;
   a.T = (int32_t)T;
   a.aux = (out_dtype ? moe::kMxOutF32 : 0) | (residual && residual_dtype ? moe::kMxResF32 : 0) |
-          (aligned(y, 16) && (ldy * (out_dtype ? 4 : 2)) % 16 == 0 ? moe::kMxOutVec : 0) |
           activation << moe::kMxActShift;
   return launched(moe::launch_mx8_linear(a, (hipStream_t)stream), fn);
 }

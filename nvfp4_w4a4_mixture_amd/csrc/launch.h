@@ -155,7 +155,8 @@ struct MxArgs {
   int32_t aux;             // gate_up: k; down: ceil(log2(36 I)) (8 bits: 2688 I); linear: bits below
 };
 static_assert(sizeof(MxArgs) <= 112, "see above");
-// linear: FP32 results, result rows on 16 bytes, FP32 residual; from bit kMxActShift on the activation
+// linear: FP32 results; of 4-bit activations result rows on 16 bytes; of 8-bit ones an FP32 residual, and from bit
+// kMxActShift on the activation
 constexpr int32_t kMxOutF32 = 1, kMxOutVec = 2, kMxResF32 = 4, kMxActShift = 3;
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActCount = 5 };
 
