@@ -94,11 +94,22 @@ const Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
+// The device of this call's tensors: that of the first one checked (-1: none yet)
+thread_local c10::DeviceIndex t_device = -1;
+
+void on_device(const Tensor& t, const char* name) {
+  if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be on a GPU device", name);
+  const c10::DeviceIndex d = t.get_device();
+  if (t_device < 0) t_device = d;
+  if (d != t_device)
+    raise(PyExc_ValueError, "%s must be on cuda:%d with the other tensors, got cuda:%d", name, (int)t_device, (int)d);
+}
+
 const Tensor& typed(PyObject* o, const char* name, ScalarType type) {
   const Tensor& t = tensor(o, name);
   if (t.scalar_type() != type)
     raise(PyExc_TypeError, "%s must be %s, got %s", name, type_name(type).c_str(), type_name(t.scalar_type()).c_str());
-  if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be on a GPU device", name);
+  on_device(t, name);
   return t;
 }
 
@@ -121,18 +132,16 @@ Rows matrix(PyObject* o, const char* name, bool f32 = false) {
   if (t.scalar_type() != ScalarType::BFloat16 && !(f32 && t.scalar_type() == ScalarType::Float))
     raise(PyExc_TypeError, "%s must be a tensor of torch.bfloat16%s, got %s", name, f32 ? " or torch.float32" : "",
                            type_name(t.scalar_type()).c_str());
-  if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be on a GPU device", name);
+  on_device(t, name);
   if (t.dim() != 2 || (t.size(1) > 1 && t.size(0) > 0 && t.stride(1) != 1))
     raise(PyExc_ValueError, "%s must be [rows, cols] with unit column stride", name);
   const int64_t rows = t.size(0), cols = t.size(1);
   return {t, rows, cols, rows > 1 ? t.stride(0) : (cols > 1 ? cols : 1)};
 }
 
-// An uninitialized tensor on `like`'s device.  On the current device straight
+// An uninitialized tensor on the call's device, the current one (see OnStream), straight
 // from its allocator: without the dispatcher an output costs 0.3 us, not 0.6.
-Tensor fresh(const Tensor& like, ScalarType type, at::IntArrayRef shape) {
-  if (like.get_device() != c10::hip::current_device())
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+Tensor fresh(ScalarType type, at::IntArrayRef shape) {
   return at::detail::empty_generic(shape, at::cuda::getCUDADeviceAllocator(), c10::DispatchKeySet(c10::DispatchKey::CUDA),
                                    type, std::nullopt);
 }
@@ -142,8 +151,8 @@ struct Out {
   Tensor t;
   int64_t ld;
 };
-Out output(PyObject* o, const char* name, const Tensor& like, ScalarType type, int64_t rows, int64_t cols) {
-  if (!given(o)) return {fresh(like, type, {rows, cols}), cols};
+Out output(PyObject* o, const char* name, ScalarType type, int64_t rows, int64_t cols) {
+  if (!given(o)) return {fresh(type, {rows, cols}), cols};
   const Rows m = matrix(o, name, true);
   if (m.t.scalar_type() != type)
     raise(PyExc_TypeError, "%s must be %s, got %s", name, type_name(type).c_str(), type_name(m.t.scalar_type()).c_str());
@@ -153,13 +162,13 @@ Out output(PyObject* o, const char* name, const Tensor& like, ScalarType type, i
   return {m.t, m.ld};
 }
 
-Tensor buffer(PyObject* o, const char* name, const Tensor& like, ScalarType type, at::IntArrayRef shape) {
-  return given(o) ? need(o, name, type, shape) : fresh(like, type, shape);
+Tensor buffer(PyObject* o, const char* name, ScalarType type, at::IntArrayRef shape) {
+  return given(o) ? need(o, name, type, shape) : fresh(type, shape);
 }
 
 // A workspace of at least one byte; the library checks a given one's size.
-Tensor workspace(PyObject* o, const Tensor& like, size_t bytes) {
-  if (!given(o)) return fresh(like, ScalarType::Byte, {(int64_t)(bytes ? bytes : 1)});
+Tensor workspace(PyObject* o, size_t bytes) {
+  if (!given(o)) return fresh(ScalarType::Byte, {(int64_t)(bytes ? bytes : 1)});
   const Tensor& t = typed(o, "workspace", ScalarType::Byte);
   if (!t.is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
   return t;
@@ -191,15 +200,33 @@ void* address(PyObject* o) {
   return p;
 }
 
+// The device of the call's tensors made the current one, if it is not.
+class OnDevice {
+ public:
+  explicit OnDevice(c10::DeviceIndex d) : before_(c10::hip::current_device()), other_(before_ != d) {
+    if (other_) c10::hip::set_device(d);
+  }
+  OnDevice(const OnDevice&) = delete;
+  ~OnDevice() {
+    if (other_) c10::hip::set_device(before_);
+  }
+
+ private:
+  c10::DeviceIndex before_;
+  bool other_;
+};
+
 // The stream that a call is enqueued on: a given torch stream, or the current
-// one.  A given stream is the current one of the tensors' device while this
+// one of the tensors' device, which is the current device while this object lives (a
+// kernel launched on another one would reach for memory that may not be mapped
+// there).  A given stream is the current one of the tensors' device while this
 // object lives, so that missing outputs and workspaces come from its pool: the
 // allocator hands a block on in the order of its own stream's work, and a
 // workspace is dropped here while the kernels that use it are still queued.
 // Constructed after the tensors are checked: without a GPU it raises.
 class OnStream {
  public:
-  OnStream(PyObject* o, const Tensor& like) {
+  OnStream(PyObject* o, const Tensor& like) : device_(like.get_device()) {
     if (!given(o)) return;
     PyObject* r = PyObject_GetAttrString(o, "cuda_stream");
     if (!r) throw python_error();
@@ -217,6 +244,7 @@ class OnStream {
   void* get() const { return before_ ? given_ : c10::hip::getCurrentHIPStream().stream(); }
 
  private:
+  OnDevice device_;
   hipStream_t given_ = nullptr;
   std::optional<c10::hip::HIPStream> before_;
 };
@@ -228,10 +256,10 @@ struct Codes {
   Tensor codes, scales;
 };
 // `bits` of an element: 4 (MXFP4) or 8 (MXFP8).
-Codes mx_output(PyObject* codes, PyObject* scales, const Tensor& like, int64_t rows, int64_t cols, int bits) {
+Codes mx_output(PyObject* codes, PyObject* scales, int64_t rows, int64_t cols, int bits) {
   const int64_t c = padded(cols);
-  return {buffer(codes, "codes", like, ScalarType::Byte, {rows, c * bits / 8}),
-          buffer(scales, "scales", like, ScalarType::Byte, {rows, c / 32})};
+  return {buffer(codes, "codes", ScalarType::Byte, {rows, c * bits / 8}),
+          buffer(scales, "scales", ScalarType::Byte, {rows, c / 32})};
 }
 // Given ones of `cols` columns; returns the rows.
 int64_t mx_input(PyObject* codes, PyObject* scales, int64_t cols, int bits) {
@@ -263,6 +291,7 @@ template <int N, PyObject* (*F)(PyObject* const*)>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != N) raise(PyExc_TypeError, "expected %d arguments, got %d", N, (int)n);
+  t_device = -1;
   return F(a);
   END_HANDLE_TH_ERRORS
 }
@@ -272,7 +301,7 @@ template <int BITS>
 PyObject* quantize(PyObject* const* a) {
   const Rows x = matrix(a[0], "x", true);
   const OnStream st(a[3], x.t);
-  const Codes q = mx_output(a[1], a[2], x.t, x.rows, x.cols, BITS);
+  const Codes q = mx_output(a[1], a[2], x.rows, x.cols, BITS);
   check((BITS == 4 ? g_entry.quantize : g_entry.quantize8)(x.t.data_ptr(), x.t.scalar_type() == ScalarType::Float, x.rows, x.cols, x.ld,
                          ptr<uint8_t>(q.codes), ptr<uint8_t>(q.scales), st.get()),
         BITS == 4 ? "mxfp4_quantize" : "mxfp8_quantize");
@@ -284,7 +313,7 @@ template <int BITS>
 PyObject* dequantize(PyObject* const* a) {
   const int64_t cols = integer(a[2]), rows = mx_input(a[0], a[1], cols, BITS), type = integer(a[3]);
   const OnStream st(a[5], tensor(a[0], "x_codes"));
-  const Out y = output(a[4], "out", tensor(a[0], "x_codes"), float_type(type), rows, cols);
+  const Out y = output(a[4], "out", float_type(type), rows, cols);
   check((BITS == 4 ? g_entry.dequantize : g_entry.dequantize8)(ptr<uint8_t>(tensor(a[0], "")), ptr<uint8_t>(tensor(a[1], "")), rows, cols, (int32_t)type,
                            y.t.data_ptr(), y.ld, st.get()),
         BITS == 4 ? "mxfp4_dequantize" : "mxfp8_dequantize");
@@ -301,8 +330,8 @@ PyObject* linear(PyObject* const* a) {
   const Tensor& ws = need(a[3], "w_scales", ScalarType::Byte, {G, KK, 64, 4});
   const Tensor &xc = tensor(a[0], ""), &xs = tensor(a[1], "");
   const OnStream st(a[8], xc);
-  const Out y = output(a[6], "y", xc, float_type(type), T, N);
-  if (given(a[7])) workspace(a[7], xc, 0);  // of the right kind; the product uses none
+  const Out y = output(a[6], "y", float_type(type), T, N);
+  if (given(a[7])) workspace(a[7], 0);  // of the right kind; the product uses none
   check(g_entry.linear(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, K, ptr<uint8_t>(wc), ptr<uint8_t>(ws), N, (int32_t)type,
                        y.t.data_ptr(), y.ld, nullptr, 0, st.get()),
         "mxfp4_linear");
@@ -331,7 +360,7 @@ PyObject* linear8(PyObject* const* a) {
     rtype = m.t.scalar_type() == ScalarType::Float;
   }
   const OnStream st(a[10], xc);
-  const Out y = output(a[9], "y", xc, float_type(type), T, N);
+  const Out y = output(a[9], "y", float_type(type), T, N);
   check(g_entry.linear8(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, K, ptr<uint8_t>(wc), ptr<uint8_t>(ws), N,
                         ptr<uint16_t>(bias), (int32_t)integer(a[7]), r.defined() ? r.data_ptr() : nullptr,
                         (int32_t)rtype, ldr, (int32_t)type, y.t.data_ptr(), y.ld, st.get()),
@@ -356,9 +385,9 @@ PyObject* grouped_ffn(PyObject* const* a) {
   const Tensor& srt = need(a[11], "sorted_pair_ids", ScalarType::Int, {T * k});
   const Tensor& tw = need(a[12], "topk_w", ScalarType::Float, {T, k});
   const OnStream st(a[16], xc);
-  const Tensor po = buffer(a[13], "pair_out", xc, ScalarType::Half, {T * k, H});
-  const Tensor ps = buffer(a[14], "pair_scale", xc, ScalarType::Float, {T * k});
-  const Tensor ws = workspace(a[15], xc, (BITS == 4 ? g_entry.ffn_ws : g_entry.ffn8_ws)(T, k, E, H, I));
+  const Tensor po = buffer(a[13], "pair_out", ScalarType::Half, {T * k, H});
+  const Tensor ps = buffer(a[14], "pair_scale", ScalarType::Float, {T * k});
+  const Tensor ws = workspace(a[15], (BITS == 4 ? g_entry.ffn_ws : g_entry.ffn8_ws)(T, k, E, H, I));
   check((BITS == 4 ? g_entry.ffn : g_entry.ffn8)(ptr<uint8_t>(xc), ptr<uint8_t>(xs), T, H, ptr<uint8_t>(c13), ptr<uint8_t>(s13), ptr<uint8_t>(c2),
                     ptr<uint8_t>(s2), ptr<int32_t>(m2), E, I, k, ptr<int32_t>(off), ptr<int32_t>(srt), ptr<float>(tw),
                     ptr<uint16_t>(po), ptr<float>(ps), ptr<void>(ws), (size_t)ws.numel(), st.get()),
@@ -383,10 +412,10 @@ PyObject* layer(PyObject* const* a) {
   const Tensor& s2 = need(a[8], "w2_scales", ScalarType::Byte, {E, G2, K2, 64, 4});
   if (k < 1 || k > E) raise(PyExc_ValueError, "need 1 <= k <= E, got k = %lld, E = %lld", (long long)k, (long long)E);
   const OnStream st(a[14], x.t);
-  const Tensor y = buffer(a[10], "y", x.t, float_type(type), {T, H});
-  const Tensor ids = buffer(a[11], "topk_ids", x.t, ScalarType::Int, {T, k});
-  const Tensor tw = buffer(a[12], "topk_w", x.t, ScalarType::Float, {T, k});
-  const Tensor ws = workspace(a[13], x.t, g_entry.layer_ws(T, H, E, k, I));
+  const Tensor y = buffer(a[10], "y", float_type(type), {T, H});
+  const Tensor ids = buffer(a[11], "topk_ids", ScalarType::Int, {T, k});
+  const Tensor tw = buffer(a[12], "topk_w", ScalarType::Float, {T, k});
+  const Tensor ws = workspace(a[13], g_entry.layer_ws(T, H, E, k, I));
   check(g_entry.layer(ptr<uint16_t>(x.t), T, H, x.ld, ptr<uint16_t>(wr), ptr<float>(bias), E, k, (float)real(a[4]),
                       ptr<uint8_t>(c13), ptr<uint8_t>(s13), ptr<uint8_t>(c2), ptr<uint8_t>(s2), I, (int32_t)type,
                       y.data_ptr(), ptr<int32_t>(ids), ptr<float>(tw), ptr<void>(ws), (size_t)ws.numel(), st.get()),
@@ -399,11 +428,11 @@ struct Normed {
   Out n;
   Codes q;
 };
-Normed norm_output(PyObject* n, bool quantize, PyObject* codes, PyObject* scales, const Tensor& like, int64_t T,
-                   int64_t H, int bits) {
+Normed norm_output(PyObject* n, bool quantize, PyObject* codes, PyObject* scales, int64_t T, int64_t H,
+                   int bits) {
   Normed r{{Tensor(), H}, {}};
-  if (n != Py_False) r.n = output(n, "n", like, ScalarType::BFloat16, T, H);
-  if (quantize || given(codes) || given(scales)) r.q = mx_output(codes, scales, like, T, H, bits);
+  if (n != Py_False) r.n = output(n, "n", ScalarType::BFloat16, T, H);
+  if (quantize || given(codes) || given(scales)) r.q = mx_output(codes, scales, T, H, bits);
   return r;
 }
 
@@ -413,7 +442,7 @@ PyObject* norm_in(PyObject* const* a) {
   const Rows x = matrix(a[0], "x");
   const Tensor& w = need(a[1], "w", ScalarType::BFloat16, {x.cols});
   const OnStream st(a[7], x.t);
-  const Normed r = norm_output(a[3], truth(a[4]), a[5], a[6], x.t, x.rows, x.cols, BITS);
+  const Normed r = norm_output(a[3], truth(a[4]), a[5], a[6], x.rows, x.cols, BITS);
   check((BITS == 4 ? g_entry.norm_in : g_entry.norm_in8)(ptr<uint16_t>(x.t), x.rows, x.cols, x.ld, ptr<uint16_t>(w), (float)real(a[2]), ptr<uint16_t>(r.n.t),
                         r.n.ld, ptr<uint8_t>(r.q.codes), ptr<uint8_t>(r.q.scales), st.get()),
         BITS == 4 ? "moe_norm_in" : "moe_norm_in_mxfp8");
@@ -440,10 +469,10 @@ PyObject* norm_out(PyObject* const* a) {
     gcs = g.size(1) == 1 ? 0 : g.stride(1);
   }
   const OnStream st(a[12], y.t);
-  const Out ro = output(a[7], "out", y.t, ScalarType::BFloat16, T, H);
+  const Out ro = output(a[7], "out", ScalarType::BFloat16, T, H);
   Normed q{{Tensor(), H}, {}};
   if (wn.defined())
-    q = norm_output(a[8], truth(a[9]), a[10], a[11], y.t, T, H, BITS);
+    q = norm_output(a[8], truth(a[9]), a[10], a[11], T, H, BITS);
   else if (given(a[8]) || truth(a[9]) || given(a[10]) || given(a[11]))
     raise(PyExc_ValueError, "n and its quantization need w_next");
   check((BITS == 4 ? g_entry.norm_out : g_entry.norm_out8)(y.t.data_ptr(), y.t.scalar_type() == ScalarType::Float, T, H, y.ld, ptr<uint16_t>(r.t), r.ld,
@@ -475,7 +504,7 @@ PyObject* combine(PyObject* const* a) {
       raise(PyExc_ValueError, "y must hold T*H = %lld * %lld elements, got %lld", (long long)T, (long long)po.size(1),
             (long long)y.numel());
   } else {
-    y = fresh(po, float_type(type), {T, po.size(1)});
+    y = fresh(float_type(type), {T, po.size(1)});
   }
   check(g_entry.combine(ptr<uint16_t>(po), ptr<float>(ps), T, k, po.size(1), (int32_t)type, y.data_ptr(), st.get()),
         "moe_combine");
